@@ -68,6 +68,14 @@ SIGNATURES = {
                                            _f32, _vp, _i64, _vp, _sz, _vp, _vp]),
     "dlrm_int4_row_bytes": (_i64, [_i32]),
     "dlrm_quantize_int4": (_i32, [_vp, _i32, _i64, _i32, _vp, _vp]),
+    "dlrm_qk_norm_rope_fwd": (_i32, [_vp, _vp, _i64, _i32, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "dlrm_qk_norm_rope_bwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32]),
+    "dlrm_qk_norm_rope_bwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _sz, _vp, _vp]),
+    "dlrm_kv_append": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _vp, _f32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "dlrm_kv_attn_workspace_size": (_sz, [_i64, _i64, _i32, _i32, _i32, _i64, _i64]),
+    "dlrm_kv_attn_fwd": (_i32, [_vp, _vp, _vp, _i32, _i32, _f32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp,
+                                _vp]),
     "dlrm_read_error": (_i32, [_vp, _vp]),
     "dlrm_clear_error": (_i32, [_vp, _vp]),
     "dlrm_status_string": (ctypes.c_char_p, [_i32]),
