@@ -82,7 +82,7 @@ typedef struct dlrm_kv_batch {
     const int64_t *offsets;    /* device [S + 1] */
     const int64_t *lengths;    /* device [S] */
     const int32_t *page_table; /* device, rows of table_width page numbers */
-    int64_t table_stride, table_width; /* table_width * page_size < 2^31 */
+    int64_t table_stride, table_width; /* at most 2^30 positions in a row */
 } dlrm_kv_batch;
 
 /*

@@ -132,9 +132,27 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float x, float y)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
 // The attention's launch: which kernel, rows (token, head of a group) of a
 // tile, and how the positions are split.
-enum AttnKernel { kAttnGeneral, kAttnFew, kAttnTile };
+enum AttnKernel { kAttnGeneral, kAttnTile };
+constexpr int kTileRows = 256;
 struct AttnPlan {
     AttnKernel kernel;
     int rows;        // rows of a tile
@@ -156,6 +174,7 @@ struct AttnParams {
     int rows, split_len, splits;
     int64_t tiles;
     float *part_o, *part_lse;  // [splits][n][q heads]([d]): partial rows, log2 of their sums
+    int64_t *prefix;           // few rows: units before each sequence
     int32_t *err;
 };
 

@@ -16,7 +16,7 @@ int launch_kv_append(const HeadsView &, const HeadsView &, const BatchView &, co
 size_t attn_workspace(int64_t, int64_t, int, int, int, int64_t, int64_t);
 int launch_kv_attn(AttnParams &, int, void *, cudaStream_t);
 
-static const int64_t kMaxTokens = 0x7fffffffLL, kMaxSequences = (int64_t)1 << 24;
+static const int64_t kMaxTokens = 0x7fffffffLL, kMaxPositions = (int64_t)1 << 30, kMaxSequences = (int64_t)1 << 24;
 static const int kMaxHeads = 65536;
 
 static bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -80,7 +80,7 @@ static int check_batch(const dlrm_kv_batch *b, int page_size, BatchView &v)
 {
     if (!b || b->S < 0 || b->n < 0 || b->table_stride < 0 || b->table_width < 0 || (b->S == 0 && b->n > 0))
         return DLRM_ERR_INVALID_ARG;
-    if (b->S > kMaxSequences || b->n > kMaxTokens || b->table_width > kMaxTokens / page_size)
+    if (b->S > kMaxSequences || b->n > kMaxTokens || b->table_width > kMaxPositions / page_size)
         return DLRM_ERR_UNSUPPORTED;
     if (b->n > 0 && (!b->offsets || !b->lengths || (b->table_width > 0 && !b->page_table)))
         return DLRM_ERR_INVALID_ARG;
@@ -201,7 +201,7 @@ size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_hea
 {
     if (S < 0 || S > kMaxSequences || n < 0 || n > kMaxTokens || kv_heads < 1 || kv_heads > kMaxHeads ||
         q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads != 0 || d < 1 || d > DLRM_MAX_HEAD_DIM ||
-        max_new < 0 || max_new > kMaxTokens || max_len < 0 || max_len > kMaxTokens)
+        max_new < 0 || max_new > kMaxTokens || max_len < 0 || max_len > kMaxPositions)
         return 0;
     return attn_workspace(S, n, q_heads, kv_heads, d, max_new, max_len);
 }
@@ -225,7 +225,7 @@ int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm
         return DLRM_ERR_INVALID_ARG;
     p.group = p.q.heads / p.cache.heads;
     p.max_new = max_new < n ? max_new : n;
-    if (max_len > kMaxTokens || p.max_new * p.group > kMaxTokens)
+    if (max_len > kMaxPositions || p.max_new * p.group > kMaxTokens)
         return DLRM_ERR_UNSUPPORTED;
     if (n > 0 && max_new == 0)
         return DLRM_ERR_INVALID_ARG;
@@ -237,7 +237,7 @@ int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm
     p.d = d;
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.causal = causal != 0;
-    p.window = window < kMaxTokens ? (int)window : 0;  // as wide as any history: none
+    p.window = window < kMaxPositions ? (int)window : 0;  // as wide as any history: none
     p.lse = lse;
     p.err = err_flag;
     return launch_kv_attn(p, dtype, workspace, static_cast<cudaStream_t>(stream));

@@ -13,7 +13,9 @@
 
 namespace dlrm {
 
-constexpr float kLn2 = 0.69314718055994530942f;
+size_t few_workspace(int64_t, int64_t, int, int64_t);
+int launch_kv_attn_few(AttnParams &, int, void *, cudaStream_t);
+int launch_kv_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
 
 // ---------------------------------------------------------------- general kernel
 
@@ -210,7 +212,7 @@ static AttnPlan plan_splits(AttnKernel kernel, int rows, int64_t S, int kv_heads
     a.tiles = ceil_div(max_new * group, rows);
     const int64_t have = S * kv_heads * a.tiles, longest = max_len + 127;
     int64_t want = ceil_div(ctas, have < 1 ? 1 : have);
-    want = want < kMaxSplits ? want : kMaxSplits;
+    want = want < 1 ? 1 : (want < kMaxSplits ? want : kMaxSplits);
     int64_t len = ceil_div(ceil_div(longest, want), 128) * 128;
     if (len < least)
         len = least;
@@ -221,8 +223,26 @@ static AttnPlan plan_splits(AttnKernel kernel, int rows, int64_t S, int kv_heads
     return a;
 }
 
+// Full tiles run one CTA on an SM: the number of splits that ends soonest, each
+// CTA costing as much as 512 positions beside its share (its start, its end and the join).
+static AttnPlan plan_tile(int64_t S, int kv_heads, int group, int64_t max_new, int64_t max_len)
+{
+    const int64_t have = S * kv_heads * ceil_div(max_new * group, kTileRows), longest = max_len + 127;
+    int64_t best = 1, least = INT64_MAX;
+    for (int64_t s = 1; s <= 64 && (s == 1 || have * s <= 2 * kPlanSms); s++) {
+        const int64_t cost = ceil_div(have * s, kPlanSms) * (ceil_div(longest, s) + 512);
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return plan_splits(kAttnTile, kTileRows, S, kv_heads, group, max_new, max_len, have * best, 512);
+}
+
 static AttnPlan plan(AttnKernel kernel, int64_t S, int kv_heads, int group, int64_t max_new, int64_t max_len)
 {
+    if (kernel == kAttnTile)
+        return plan_tile(S, kv_heads, group, max_new, max_len);
     return plan_splits(kAttnGeneral, kGenRows, S, kv_heads, group, max_new, max_len, kPlanSms * 8, 256);
 }
 
@@ -236,8 +256,12 @@ size_t attn_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, in
 {
     const int group = q_heads / kv_heads;
     max_new = max_new < n ? max_new : n;
-    const size_t f = part_floats(plan(kAttnGeneral, S, kv_heads, group, max_new, max_len), n, q_heads, d);
-    return f * sizeof(float) + 16;
+    size_t most = few_workspace(S, max_new * group, d, max_len);
+    for (AttnKernel k : {kAttnGeneral, kAttnTile}) {
+        const size_t b = part_floats(plan(k, S, kv_heads, group, max_new, max_len), n, q_heads, d) * sizeof(float);
+        most = b > most ? b : most;
+    }
+    return most + 16;
 }
 
 template <typename T>
@@ -253,12 +277,12 @@ static int launch_general(const AttnParams &p, int64_t ctas, cudaStream_t st)
 }
 
 template <typename T>
-static int launch_attn_t(AttnParams &p, const AttnPlan &a, cudaStream_t st)
+static int launch_attn_t(AttnParams &p, const AttnPlan &a, int dtype, cudaStream_t st)
 {
     const int64_t ctas = p.batch.S * a.tiles * a.splits * p.cache.heads;
     if (ctas > 0x7fffffff)
         return DLRM_ERR_UNSUPPORTED;
-    const int s = launch_general<T>(p, ctas, st);
+    const int s = a.kernel == kAttnTile ? launch_kv_attn_tile(p, dtype, ctas, st) : launch_general<T>(p, ctas, st);
     if (s != DLRM_OK)
         return s;
     if (a.splits > 1) {
@@ -269,9 +293,22 @@ static int launch_attn_t(AttnParams &p, const AttnPlan &a, cudaStream_t st)
     return launch_status();
 }
 
+// The tensor-core kernels' copies are 16 bytes wide.
+static bool wide_rows(const AttnParams &p)
+{
+    auto ok = [](const void *ptr, int64_t a, int64_t b) {
+        return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && a % 8 == 0 && b % 8 == 0;
+    };
+    return p.d <= 128 && p.d % 8 == 0 && ok(p.q.ptr, p.q.ts, p.q.hs) && ok(p.out.ptr, p.out.ts, p.out.hs) &&
+           ok(p.cache.k, p.cache.page_stride, p.cache.slot_stride) && ok(p.cache.v, p.cache.head_stride, 0);
+}
+
 int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
 {
-    const AttnPlan a = plan(kAttnGeneral, p.batch.S, p.cache.heads, p.group, p.max_new, p.max_len);
+    const bool cores = dtype != DLRM_F32 && wide_rows(p);
+    if (cores && p.max_new * p.group <= 16)
+        return launch_kv_attn_few(p, dtype, workspace, st);
+    const AttnPlan a = plan(cores ? kAttnTile : kAttnGeneral, p.batch.S, p.cache.heads, p.group, p.max_new, p.max_len);
     p.rows = a.rows;
     p.tiles = a.tiles;
     p.split_len = a.split_len;
@@ -279,10 +316,10 @@ int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     p.part_o = static_cast<float *>(workspace);
     p.part_lse = p.part_o + (size_t)a.splits * p.batch.n * p.cache.heads * p.group * p.d;
     if (dtype == DLRM_F32)
-        return launch_attn_t<float>(p, a, st);
+        return launch_attn_t<float>(p, a, dtype, st);
     if (dtype == DLRM_F16)
-        return launch_attn_t<__half>(p, a, st);
-    return launch_attn_t<__nv_bfloat16>(p, a, st);
+        return launch_attn_t<__half>(p, a, dtype, st);
+    return launch_attn_t<__nv_bfloat16>(p, a, dtype, st);
 }
 
 }  // namespace dlrm
