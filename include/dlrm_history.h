@@ -100,9 +100,9 @@ typedef struct dlrm_kv_batch {
  * eps             >= 0 and finite.
  * rope            NULL: no rotation.
  * A position outside the table raises DLRM_FLAG_INDEX_OOB and that token's
- * outputs are zeros.  Rows of a multiple of 8 elements, 16-byte aligned with
- * strides that are multiples of 16 bytes, take the vector path (rot then a
- * multiple of 16 in the half layout, of 8 interleaved).
+ * outputs are zeros.  Rows of a multiple of 8 elements whose pointers and
+ * strides are multiples of 4 elements, with rot a multiple of 8 and a 16-byte
+ * aligned table, take the vector path.
  */
 int dlrm_qk_norm_rope_fwd(const dlrm_heads *q, const dlrm_heads *k, int64_t n, int d, int dtype,
                           const float *q_weight, const float *k_weight, float eps, const dlrm_rope *rope,

@@ -6,13 +6,26 @@
 // Turning is orthogonal, so the gradient turns dy back (dz), and with
 // g = dz w:  dx = r (g - x r^2 mean(g x)),  dw = sum of dz x r over all rows.
 //
-// Row kernels: a warp per row, lane l holds the elements l, l + 32, ...
-#include "history.cuh"
+// The row kernels here serve every width, stride and alignment: a warp per row,
+// lane l holds the elements l, l + 32, ...  Rows that can be moved as 4-element pieces
+// take the vector path (head_norm.cuh).
+#include <initializer_list>
+
+#include "head_norm.cuh"
 
 namespace dlrm {
 
+size_t norm_bwd_vec_workspace(int64_t, int, int, int);
+int launch_norm_rope_vec(const HeadsView &, const HeadsView &, int64_t, int, int, const float *, const float *, float,
+                         const RopeView &, const HeadsView &, const HeadsView &, int32_t *, cudaStream_t);
+int launch_norm_rope_bwd_vec(const HeadsView &, const HeadsView &, const HeadsView &, const HeadsView &, int64_t, int,
+                             int, const float *, const float *, float, const RopeView &, const HeadsView &,
+                             const HeadsView &, float *, float *, float *, int32_t *, cudaStream_t);
+int launch_kv_append_vec(const HeadsView &, const HeadsView &, const BatchView &, const CacheView &, int, int,
+                         const float *, float, const RopeView &, const HeadsView &, const float *, const HeadsView &,
+                         int32_t *, cudaStream_t);
+
 constexpr int kRowElems = DLRM_MAX_HEAD_DIM / 32;  // elements of a lane
-constexpr int kWarps = 8;                          // of a CTA
 
 // The partner of element e in its pair and whether e is the pair's first; -1
 // for elements that are not turned.
@@ -32,17 +45,6 @@ __device__ __forceinline__ int angle_of(const RopeView &rope, int e)
 {
     const int half = rope.rot >> 1;
     return rope.interleaved ? e >> 1 : (e < half ? e : e - half);
-}
-
-// The rope row of a position, or null with the flag raised where it is
-// outside the table.
-__device__ __forceinline__ const float *rope_row(const RopeView &rope, int64_t position, int32_t *err)
-{
-    if (position < 0 || position >= rope.length) {
-        raise_flag(err, DLRM_FLAG_INDEX_OOB);
-        return nullptr;
-    }
-    return rope.table + position * rope.rot;
 }
 
 // 1/sqrt(mean x^2 + eps) of a row, from every lane's sum of squares.
@@ -188,21 +190,31 @@ norm_rope_bwd_rows_kernel(HeadsView dqo, HeadsView dko, HeadsView q, HeadsView k
     }
 }
 
-// The CTAs' sums of one weight's gradient added up: a warp per element.
+// The CTAs' sums of the weights' gradients added up: a warp per element.
+// part: q_parts rows of d sums of the queries', then k_parts of the keys'.
 __global__ void __launch_bounds__(kWarps * 32)
-norm_weight_sum_kernel(const float *__restrict__ part, int ctas, int d, float *__restrict__ dqw,
-                       float *__restrict__ dkw)
+norm_weight_sum_kernel(const float *__restrict__ part, int64_t q_parts, int64_t k_parts, int d,
+                       float *__restrict__ dqw, float *__restrict__ dkw)
 {
     float *out = blockIdx.y == 0 ? dqw : dkw;
+    const int64_t from = blockIdx.y == 0 ? 0 : q_parts, to = blockIdx.y == 0 ? q_parts : q_parts + k_parts;
     const int e = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (!out || e >= d)
         return;
     float s = 0.f;
-    for (int c = threadIdx.x & 31; c < ctas; c += 32)
-        s += part[((int64_t)blockIdx.y * ctas + c) * d + e];
+    for (int64_t c = from + (threadIdx.x & 31); c < to; c += 32)
+        s += part[c * d + e];
     s = warp_sum(s);
     if ((threadIdx.x & 31) == 0)
         out[e] = s;
+}
+
+void launch_norm_weight_sum(const float *part, int64_t q_parts, int64_t k_parts, int d, float *dqw, float *dkw,
+                            cudaStream_t st)
+{
+    norm_weight_sum_kernel<<<dim3((d + kWarps - 1) / kWarps, k_parts > 0 ? 2 : 1), kWarps * 32, 0, st>>>(
+        part, q_parts, k_parts, d, dqw, dkw);
+    count_launch(st);
 }
 
 // One warp per new token.
@@ -256,18 +268,29 @@ constexpr int64_t kBwdCtas = 608;  // four for each of 152 SMs
 
 static int64_t bwd_ctas(int64_t n, int heads)
 {
-    const int64_t rows = n * heads, need = (rows + kWarps - 1) / kWarps;
+    const int64_t need = div_up(n * heads, kWarps);
     return need < 1 ? 1 : (need < kBwdCtas ? need : kBwdCtas);
 }
 
 size_t norm_bwd_workspace(int64_t n, int qh, int kh, int d)
 {
-    return 2 * (size_t)bwd_ctas(n, qh > kh ? qh : kh) * d * sizeof(float);
+    const size_t rows = 2 * (size_t)bwd_ctas(n, qh > kh ? qh : kh) * d * sizeof(float);
+    const size_t vec = norm_bwd_vec_workspace(n, qh, kh, d);
+    return rows > vec ? rows : vec;
+}
+
+// Whether the vector path takes these rows.
+static bool vec_ok(int d, int dtype, const RopeView &rope, std::initializer_list<const HeadsView *> heads)
+{
+    bool ok = d % 8 == 0 && rope_pieces_ok(rope);
+    for (const HeadsView *h : heads)
+        ok = ok && pieces_ok(*h, dtype == DLRM_F32 ? 4 : 2);
+    return ok;
 }
 
 static int64_t row_ctas(int64_t rows)
 {
-    const int64_t need = (rows + kWarps - 1) / kWarps;
+    const int64_t need = div_up(rows, kWarps);
     return need < 65536 ? need : 65536;
 }
 
@@ -286,6 +309,8 @@ int launch_norm_rope(const HeadsView &q, const HeadsView &k, int64_t n, int d, i
                      const float *kw, float eps, const RopeView &rope, const HeadsView &qo, const HeadsView &ko,
                      int32_t *err, cudaStream_t st)
 {
+    if (vec_ok(d, dtype, rope, {&q, &k, &qo, &ko}))
+        return launch_norm_rope_vec(q, k, n, d, dtype, qw, kw, eps, rope, qo, ko, err, st);
     if (dtype == DLRM_F32)
         return norm_fwd<float>(q, k, n, d, qw, kw, eps, rope, qo, ko, err, st);
     if (dtype == DLRM_F16)
@@ -303,11 +328,8 @@ static int norm_bwd(const HeadsView &dqo, const HeadsView &dko, const HeadsView 
     norm_rope_bwd_rows_kernel<T><<<dim3((unsigned)ctas, sides), kWarps * 32, 0, st>>>(dqo, dko, q, k, n, d, qw, kw,
                                                                                       eps, rope, dq, dk, part, err);
     count_launch(st);
-    if (dqw || dkw) {
-        norm_weight_sum_kernel<<<dim3((d + kWarps - 1) / kWarps, sides), kWarps * 32, 0, st>>>(part, (int)ctas, d,
-                                                                                               dqw, dkw);
-        count_launch(st);
-    }
+    if (dqw || dkw)
+        launch_norm_weight_sum(part, ctas, sides == 2 ? ctas : 0, d, dqw, dkw, st);
     return launch_status();
 }
 
@@ -316,6 +338,9 @@ int launch_norm_rope_bwd(const HeadsView &dqo, const HeadsView &dko, const Heads
                          const RopeView &rope, const HeadsView &dq, const HeadsView &dk, float *dqw, float *dkw,
                          float *part, int32_t *err, cudaStream_t st)
 {
+    if (vec_ok(d, dtype, rope, {&dqo, &dko, &q, &k, &dq, &dk}))
+        return launch_norm_rope_bwd_vec(dqo, dko, q, k, n, d, dtype, qw, kw, eps, rope, dq, dk, dqw, dkw, part, err,
+                                        st);
     if (dtype == DLRM_F32)
         return norm_bwd<float>(dqo, dko, q, k, n, d, qw, kw, eps, rope, dq, dk, dqw, dkw, part, err, st);
     if (dtype == DLRM_F16)
@@ -338,6 +363,9 @@ int launch_kv_append(const HeadsView &k, const HeadsView &v, const BatchView &ba
                      int dtype, const float *kw, float eps, const RopeView &rope, const HeadsView &q,
                      const float *qw, const HeadsView &qo, int32_t *err, cudaStream_t st)
 {
+    const HeadsView kc = {cache.k, cache.page_stride, cache.slot_stride, 0}, vc = {cache.v, cache.head_stride, 0, 0};
+    if (vec_ok(d, dtype, rope, {&k, &v, &q, &qo, &kc, &vc}))
+        return launch_kv_append_vec(k, v, batch, cache, d, dtype, kw, eps, rope, q, qw, qo, err, st);
     if (dtype == DLRM_F32)
         return append<float>(k, v, batch, cache, d, kw, eps, rope, q, qw, qo, err, st);
     if (dtype == DLRM_F16)
