@@ -6,12 +6,32 @@ import pytest
 import torch
 
 import sparse_dense_interaction_gb300 as sdi
-from sparse_dense_interaction_gb300 import _history as H
-from sparse_dense_interaction_gb300 import _native, build
+from sparse_dense_interaction_gb300 import _history, _native, build
 
 FAKE = 0x10000  # never dereferenced: every call below fails its host checks first
 BAD, UNSUPPORTED, SMALL, OK = (_native.ERR_INVALID_ARG, _native.ERR_UNSUPPORTED, _native.ERR_WORKSPACE_TOO_SMALL,
                                _native.OK)
+
+
+_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("ptr", _vp), ("token_stride", _i64), ("head_stride", _i64), ("heads", _i32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("table", _vp), ("length", _i64), ("positions", _vp), ("rot", _i32), ("layout", _i32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("pages", _i64), ("page_stride", _i64), ("slot_stride", _i64),
+                ("head_stride", _i64), ("page_size", _i32), ("heads", _i32)]
+
+
+class Batch(ctypes.Structure):
+    _fields_ = [("S", _i64), ("n", _i64), ("offsets", _vp), ("lengths", _vp), ("page_table", _vp),
+                ("table_stride", _i64), ("table_width", _i64)]
 
 
 @pytest.fixture(scope="module")
@@ -21,19 +41,19 @@ def lib():
 
 
 def heads(ptr=FAKE, token=256, head=64, n=4):
-    return H._Heads(ptr, token, head, n)
+    return Heads(ptr, token, head, n)
 
 
 def rope(table=FAKE, length=10, positions=FAKE, rot=64, layout=0):
-    return H._Rope(table, length, positions, rot, layout)
+    return Rope(table, length, positions, rot, layout)
 
 
 def batch(S=2, n=8, offsets=FAKE, lengths=FAKE, table=FAKE, stride=4, width=4):
-    return H._Batch(S, n, offsets, lengths, table, stride, width)
+    return Batch(S, n, offsets, lengths, table, stride, width)
 
 
 def cache(k=FAKE, v=FAKE, pages=9, page=4096, slot=256, head=64, size=16, n=4):
-    return H._Cache(k, v, pages, page, slot, head, size, n)
+    return Cache(k, v, pages, page, slot, head, size, n)
 
 
 ref = lambda x: None if x is None else ctypes.byref(x)
@@ -120,6 +140,15 @@ def test_attention_checks(lib, want, kw):
                                 a["window"], a["max_new"], a["max_len"], ref(a["out"]), a["lse"], a["ws"],
                                 need - a["short"], None, None) == want
     assert lib.dlrm_kernel_launch_count() == 0
+
+
+def test_packed_structs_match_the_header():
+    for pack, struct, values in ((_history._HEADS, Heads, (5, 6, 7, 8)), (_history._ROPE, Rope, (5, 6, 7, 8, 1)),
+                                 (_history._CACHE, Cache, (5, 6, 7, 8, 9, 10, 11, 12)),
+                                 (_history._BATCH, Batch, (5, 6, 7, 8, 9, 10, 11))):
+        packed = struct.from_buffer_copy(pack(*values))
+        assert len(pack(*values)) == ctypes.sizeof(struct)
+        assert tuple(getattr(packed, name) for name, _ in struct._fields_) == values
 
 
 def test_workspace_sizes_of_invalid_sizes(lib):
