@@ -294,19 +294,20 @@ static int launch_attn_t(AttnParams &p, const AttnPlan &a, int dtype, cudaStream
 }
 
 // The tensor-core kernels' copies are 16 bytes wide.
-static bool wide_rows(const AttnParams &p)
+static bool wide_rows(const AttnParams &p, int dtype)
 {
-    auto ok = [](const void *ptr, int64_t a, int64_t b) {
-        return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && a % 8 == 0 && b % 8 == 0;
+    const int e = dtype == DLRM_F32 ? 4 : 8;
+    auto ok = [e](const void *ptr, int64_t a, int64_t b) {
+        return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && a % e == 0 && b % e == 0;
     };
-    return p.d <= 128 && p.d % 8 == 0 && ok(p.q.ptr, p.q.ts, p.q.hs) && ok(p.out.ptr, p.out.ts, p.out.hs) &&
+    return p.d <= 128 && p.d % e == 0 && ok(p.q.ptr, p.q.ts, p.q.hs) && ok(p.out.ptr, p.out.ts, p.out.hs) &&
            ok(p.cache.k, p.cache.page_stride, p.cache.slot_stride) && ok(p.cache.v, p.cache.head_stride, 0);
 }
 
 int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
 {
-    const bool cores = dtype != DLRM_F32 && wide_rows(p);
-    if (cores && p.max_new * p.group <= 16)
+    const bool cores = wide_rows(p, dtype);
+    if (cores && (dtype == DLRM_F32 || p.max_new * p.group <= 16))
         return launch_kv_attn_few(p, dtype, workspace, st);
     const AttnPlan a = plan(cores ? kAttnTile : kAttnGeneral, p.batch.S, p.cache.heads, p.group, p.max_new, p.max_len);
     p.rows = a.rows;
