@@ -6,15 +6,21 @@
 // tile of 16 packed rows of one sequence and cache head; the positions of all
 // items are laid end to end in units of four warp blocks, a CTA takes an equal
 // run of units, whatever the lengths, and its warps stream their blocks through
-// rings of asynchronous 16-byte copies that do not stop between items.  Every
-// lane reads back exactly the chunks it copied itself, so the rings need no barrier:
-//  - scores: MMAs of 16 rows x 8 tokens (m16n8k16; fp32: m16n8k8).  The order of
-//    the summed elements is free, so a lane's 16-byte chunk of a key serves two
-//    MMA steps as it is, with the query's chunks in the same order.
-//  - output: MMAs of 16 rows x 8 columns, 16 (fp32: 8) tokens deep.  Which columns
-//    form an MMA's 8 is free too: a lane's chunks of the same columns of two tokens,
-//    interleaved by byte permutes, are the operands of 8 MMAs (fp32: 4, as they
-//    are); and the order of the tokens is the one that the scores come out in.
+// rings that do not stop between items.  Pages of a multiple of 8 slots are
+// copied by bulk tensor copies through the page table, in boxes of 8 or 16
+// rows: keys in columns of 64 bytes, values in columns of 128 bytes swizzled, so that the reads
+// below meet no bank twice.  Other page sizes take asynchronous 16-byte copies, row by row, where
+// every lane reads back exactly the chunks it copied itself; they share the load/store
+// pipe with the reads (256 users: 444 us against 3xx us).
+//  - scores: MMAs of 16 tokens x 8 rows (m16n8k16; fp32: 16 rows x 8 tokens,
+//    m16n8k8).  The order of the summed elements is free, so a lane's 16-byte chunk
+//    of a key serves two MMA steps as it is, with the query's chunks in the same order.
+//  - output: MMAs of 16 columns x 8 rows, 16 tokens deep (fp32: 16 rows x 8
+//    columns, 8 deep).  Which columns form an MMA's 16 is free too: a lane's chunks of
+//    the same columns of four tokens, interleaved by byte permutes, are the operands
+//    of 4 MMAs (fp32: of two tokens, 4 MMAs, as they are).  The weights, whose tokens
+//    are in the lanes that hold rows next, are transposed by movmatrix (fp32: the order
+//    of the tokens is the one that the scores come out in).
 // fp32 runs on TF32 MMAs: an operand is its upper 19 bits, which are what the MMA reads, plus the rest,
 // exactly, and the three products of the split that matter carry each product of
 // two elements to about 2^-20 of its magnitude; sums are fp32.
@@ -68,9 +74,10 @@ __device__ __forceinline__ void mma_fp32(float *c, const float *a, const float *
 // [first, last).
 struct FewItem {
     Sequence seq;
-    int64_t s, first, last;
+    int64_t s;
+    int first, last;
     int head, tile, tiles;
-    int lo, hi;  // positions that the sequence's queries see
+    int lo, hi, lo_seen;  // positions that the sequence's queries see, lo down to a multiple of 16
     const int32_t *pages;
 };
 
@@ -83,7 +90,7 @@ __device__ __forceinline__ int few_units(const AttnParams &p, const Sequence &q,
         return 0;
     hi = seen_hi(q, p.causal, q.count - 1);
     lo = seen_lo(seen_hi(q, p.causal, 0), p.window);
-    return hi > lo ? (hi - lo + unit - 1) / unit : 1;
+    return hi > lo ? (hi - (lo & ~15) + unit - 1) / unit : 1;
 }
 
 __device__ __forceinline__ int few_tiles(const AttnParams &p, const Sequence &q)
@@ -93,11 +100,12 @@ __device__ __forceinline__ int few_tiles(const AttnParams &p, const Sequence &q)
 
 // Sets the item to sequence s's first, from unit `first`; false where the
 // sequence has no units.
-__device__ __forceinline__ bool few_sequence(const AttnParams &p, FewItem &w, int64_t s, int64_t first, int unit)
+__device__ __forceinline__ bool few_sequence(const AttnParams &p, FewItem &w, int64_t s, int first, int unit)
 {
     if (!read_sequence(p.batch, s, p.max_new, p.max_len, w.seq, nullptr))
         return false;
-    const int units = few_units(p, w.seq, unit, w.lo, w.hi);
+    const int units = few_units(p, w.seq, unit, w.lo_seen, w.hi);
+    w.lo = w.lo_seen & ~15;
     w.s = s;
     w.head = w.tile = 0;
     w.tiles = few_tiles(p, w.seq);
@@ -114,16 +122,16 @@ __device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int un
         w.head++;
     }
     if (w.head < p.cache.heads) {
-        const int64_t units = w.last - w.first;
+        const int units = w.last - w.first;
         w.first = w.last;
         w.last += units;
         return;
     }
-    const int64_t first = w.last;
+    const int first = w.last;
     for (int64_t s = w.s + 1; s < p.batch.S; s++)
         if (few_sequence(p, w, s, first, unit))
             return;
-    w.last = INT64_MAX;  // not reached: a CTA's units end with the last item's
+    w.last = 0x7fffffff;  // not reached: a CTA's units end with the last item's
 }
 
 // Units of a CTA when `total` are shared out.
@@ -136,7 +144,7 @@ __host__ __device__ __forceinline__ int64_t few_quota(int64_t total)
 // The CTA's share of all units: sums every sequence's units (each thread a run
 // of sequences), finds the item that holds the first unit of the share.  CTA
 // 0 leaves the sums before each sequence in p.prefix for the join.
-__device__ bool few_share(const AttnParams &p, FewItem &w, int64_t &u0, int64_t &u1, int unit)
+__device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int unit)
 {
     __shared__ int64_t sums[kFewWarps], found[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -164,55 +172,102 @@ __device__ bool few_share(const AttnParams &p, FewItem &w, int64_t &u0, int64_t 
         total += sums[i];
     }
     const int64_t quota = few_quota(total);
-    u0 = min(blockIdx.x * quota, total);
-    u1 = min(u0 + quota, total);
-    const bool here = u0 < u1 && u0 >= before && u0 < before + mine;
+    const int64_t u0 = min(blockIdx.x * quota, total);
+    units = (int)(min(u0 + quota, total) - u0);
+    const bool here = units > 0 && u0 >= before && u0 < before + mine;
     if (here || blockIdx.x == 0) {
         for (int64_t s = from; s < to; s++) {
-            int64_t units = 0;
+            int64_t here_units = 0;
             if (read_sequence(p.batch, s, p.max_new, p.max_len, q, nullptr))
-                units = (int64_t)few_units(p, q, unit, lo, hi) * few_tiles(p, q) * p.cache.heads;
-            if (here && u0 >= before && u0 < before + units) {
+                here_units = (int64_t)few_units(p, q, unit, lo, hi) * few_tiles(p, q) * p.cache.heads;
+            if (here && u0 >= before && u0 < before + here_units) {
                 found[0] = s;
                 found[1] = before;
             }
             if (blockIdx.x == 0)
                 p.prefix[s] = before;
-            before += units;
+            before += here_units;
         }
         if (blockIdx.x == 0 && threadIdx.x == 0)
             p.prefix[p.batch.S] = total;
     }
     __syncthreads();
-    if (u0 >= u1)
+    if (units == 0)
         return false;
-    few_sequence(p, w, found[0], found[1], unit);
-    while (u0 >= w.last)
-        few_next(p, w, unit);
+    // the sequence's items before it may be many: their units are counted from the share's
+    // first in 64 bits, the item's own fit in 32
+    few_sequence(p, w, found[0], 0, unit);
+    const int64_t each = w.last, skip = (u0 - found[1]) / each;
+    w.tile = (int)(skip % w.tiles);
+    w.head = (int)(skip / w.tiles);
+    w.first = (int)(found[1] + skip * each - u0);
+    w.last = w.first + (int)each;
     return true;
 }
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kFewWarps * 32, 2)
-kv_attn_few_kernel(const __grid_constant__ AttnParams p)
+// Rows of a lane's softmax statistics and the layout of its output registers.
+// 16-bit types: the tokens are the MMAs' 16 rows and the query rows their 8
+// columns, kGroups of 8 (narrow tiles do half the work); fp32: the query rows
+// are the 16 rows.
+template <typename T, int DP, int kGroups, bool kBulk>
+struct FewShape {
+    static constexpr bool kWide = sizeof(T) == 4;
+    static constexpr int E = 16 / sizeof(T);                     // elements of a chunk
+    static constexpr int MG = kWide ? 8 : 16;                    // tokens of an MMA group
+    static constexpr int KT = MG / 8, VT = MG / 4;               // a lane's key and value rows of a group
+    static constexpr int KG = DP / (4 * E), VS = DP / (8 * E);   // its chunks of a key row, of a value row
+    static constexpr int TB = kFewStageBytes / (2 * DP * (int)sizeof(T)), NB = TB / MG, UT = kFewWarps * TB;
+    static constexpr int kChunks = KT * KG + VT * VS;            // of a group
+    static constexpr int kStats = kWide ? 2 : 2 * kGroups;       // rows whose statistics a lane holds
+    static constexpr int kOut = kWide ? VS * 16 : kGroups * VS * 16;  // output registers
+    static constexpr int kSmem = 1024 + kFewWarps * kFewStages * kFewStageBytes + 2 * kOut * 32 * 4;
+    static constexpr int kKeyBox = MG * 64, kValueBox = MG * 128;  // bytes of a column of a group's keys, values
+    static constexpr int kGroupBytes = KG * kKeyBox + VS * kValueBox;
+
+    // the row of a lane's statistic i, and the statistic of its output register o
+    __device__ __forceinline__ static int row(int i, int g, int q)
+    {
+        return kWide ? g + 8 * i : 2 * q + (i & 1) + 8 * (i >> 1);
+    }
+    __device__ __forceinline__ static constexpr int stat(int o)
+    {
+        return kWide ? (o & 3) >> 1 : (o & 1) + 2 * (o / (VS * 16));
+    }
+};
+
+// The cache as bulk tensor copies see it: (element, slot, head, page).
+struct FewMaps {
+    CUtensorMap k, v;
+    int rows;  // of a box
+};
+
+// Transposes an 8 x 8 matrix of 16-bit elements over a warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
-    constexpr bool kWide = sizeof(T) == 4;
-    constexpr int E = 16 / sizeof(T);                    // elements of a chunk
-    constexpr int MG = kWide ? 8 : 16, KT = MG / 8, VT = MG / 4;  // tokens of an MMA group; a lane's key and value rows
-    constexpr int KG = DP / (4 * E), VS = DP / (8 * E);  // a lane's chunks of a key row, of a value row
-    constexpr int TB = kFewStageBytes / (2 * DP * (int)sizeof(T)), NB = TB / MG, UT = kFewWarps * TB;
-    constexpr int kChunks = KT * KG + VT * VS, kOut = VS * E * 4;  // chunks of a group; output registers
-    extern __shared__ __align__(16) uint8_t smem[];
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <typename T, int DP, int kGroups, bool kBulk>
+__global__ void __launch_bounds__(kFewWarps * 32, 2)
+kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FewMaps maps)
+{
+    using Sh = FewShape<T, DP, kGroups, kBulk>;
+    constexpr int E = Sh::E, KT = Sh::KT, VT = Sh::VT, KG = Sh::KG, VS = Sh::VS, NB = Sh::NB, UT = Sh::UT;
+    extern __shared__ uint8_t raw[];
     __shared__ float s_m[kFewWarps][kFewRows], s_l[kFewWarps][kFewRows];
+    __shared__ uint64_t bars[kFewWarps][kFewStages];
+    __shared__ int aborted;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    uint8_t *ring = smem + warp * kFewStages * kFewStageBytes + lane * 16;
+    uint8_t *smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
+    uint8_t *ring = smem + warp * kFewStages * kFewStageBytes;
     float *merge = reinterpret_cast<float *>(smem + kFewWarps * kFewStages * kFewStageBytes);  // [2][kOut][32]
 
     FewItem it;  // of the unit being computed; `is`: of the unit whose addresses come next
-    int64_t u0 = 0, u1;
-    bool split = p.splits > 1;
-    if (split) {
-        if (!few_share(p, it, u0, u1, UT))
+    int units;   // of this CTA; the items' are counted from its first
+    if (p.splits > 1) {
+        if (!few_share(p, it, units, UT))
             return;
     } else {
         const int64_t most = (p.max_new * p.group + kFewRows - 1) / kFewRows, of = blockIdx.x / most;
@@ -223,27 +278,52 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p)
         it.tile = (int)(blockIdx.x - of * most);
         if (it.tile >= it.tiles)
             return;
-        u1 = it.last;
+        units = it.last;
     }
     FewItem is = it;
 
-    // this lane's token of the warp's block of unit u: its page number and slot,
-    // no slot for a position that no query sees; and its place in the cache, -1
-    // there and in an invalid page
+    // What this lane copies of the warp's block of unit u -- a box of its own, or
+    // the row of token `lane` -- as a page number and slot; no slot where no
+    // query sees it.
+    const int boxes = Sh::MG / maps.rows * (KG + VS);  // of a group: its keys' columns, then its values'
+    const int my_group = kBulk ? lane / boxes : lane / Sh::MG, my_box = kBulk ? lane - my_group * boxes : 0;
+    const int my_part = kBulk ? my_box % (Sh::MG / maps.rows) : 0, my_column = kBulk ? my_box / (Sh::MG / maps.rows) : 0;
+    const int my_token = kBulk ? my_group * Sh::MG + my_part * maps.rows : lane;
+    const bool copies = my_group < NB;
     int page_id = 0, page_slot = -1;
-    auto find = [&](int64_t u) {
+    auto find = [&](int u) {
         page_slot = -1;
-        if (u >= u1)
+        if (u >= units)
             return;
         while (u >= is.last)
             few_next(p, is, UT);
-        const int at = is.lo + (int)(u - is.first) * UT + warp * TB + lane;
-        if (lane < TB && at < is.hi) {
+        const int at = is.lo + (u - is.first) * UT + warp * Sh::TB + my_token;
+        if (copies && at < is.hi && at + (kBulk ? maps.rows : 1) > is.lo_seen) {
             const uint32_t page = p.cache.page.div((uint32_t)at);
             page_slot = at - (int)(page * p.cache.page.d);
             page_id = __ldg(is.pages + page);
         }
     };
+    const uint32_t ring_at = tc::smem_u32(ring);
+    auto copy_boxes = [&](int stage) {
+        if (lane == 0)
+            tc::mbar_expect_tx(&bars[warp][stage], kFewStageBytes);
+        __syncwarp();
+        if (!copies)
+            return;
+        if (page_slot >= 0 && (uint32_t)page_id >= p.cache.pages)
+            raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+        // a page number outside the cache, and -1 for what no query sees, is outside the map: zeros
+        const int page = page_slot >= 0 && (uint32_t)page_id < p.cache.pages ? page_id : -1, slot = max(page_slot, 0);
+        const uint32_t to = ring_at + stage * kFewStageBytes + my_group * Sh::kGroupBytes;
+        if (my_column < KG)
+            tc::tma_load_4d(to + my_column * Sh::kKeyBox + my_part * maps.rows * 64, &maps.k, my_column * 4 * E, slot,
+                            is.head, page, &bars[warp][stage]);
+        else
+            tc::tma_load_4d(to + KG * Sh::kKeyBox + (my_column - KG) * Sh::kValueBox + my_part * maps.rows * 128,
+                            &maps.v, (my_column - KG) * 8 * E, slot, is.head, page, &bars[warp][stage]);
+    };
+    // the lane's row: its place in the cache, -1 where there is none
     auto place = [&]() -> int64_t {
         if (page_slot < 0)
             return -1;
@@ -254,62 +334,83 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p)
         return (page_id * p.cache.page_stride + page_slot * p.cache.slot_stride + is.head * p.cache.head_stride) *
                (int64_t)sizeof(T);
     };
-    auto copy = [&](int stage, int64_t mine) {
-        uint8_t *to = ring + stage * kFewStageBytes;
+    auto copy_rows = [&](int stage, int64_t mine) {
+        uint32_t to = ring_at + stage * kFewStageBytes + lane * 16;
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
-            for (int t = 0; t < KT; t++) {
-                const int64_t o = __shfl_sync(0xffffffffu, mine, nb * MG + t * 8 + g);
+            for (int t = 0; t < KT + VT; t++) {
+                const bool key = t < KT;
+                const int v = t - KT, token = key ? t * 8 + g : 2 * q + (v & 1) + (v >> 1) * 8;
+                const int64_t at = __shfl_sync(0xffffffffu, mine, nb * Sh::MG + token);
+                const char *from = (key ? p.cache.k + q * 16 : p.cache.v + g * 16) + (at >= 0 ? at : 0);
 #pragma unroll
-                for (int i = 0; i < KG; i++) {
-                    const int e = (4 * i + q) * E;
-                    const bool ok = o >= 0 && e < p.d;
-                    tc::cp_async16(to, p.cache.k + (ok ? o + e * (int)sizeof(T) : 0), ok);
-                    to += 512;
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < VT; t++) {
-                const int64_t o = __shfl_sync(0xffffffffu, mine, nb * MG + 2 * q + (t & 1) + (t >> 1) * 8);
-#pragma unroll
-                for (int i = 0; i < VS; i++) {
-                    const int e = (8 * i + g) * E;
-                    const bool ok = o >= 0 && e < p.d;
-                    tc::cp_async16(to, p.cache.v + (ok ? o + e * (int)sizeof(T) : 0), ok);
+                for (int i = 0; i < (key ? KG : VS); i++) {
+                    const bool there = at >= 0 && (key ? 4 * i + q : 8 * i + g) * E < p.d;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                                 "l"(there ? from + i * (key ? 64 : 128) : p.cache.k), "r"(there ? 16 : 0)
+                                 : "memory");
                     to += 512;
                 }
             }
         }
     };
-    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-
-    find(u0);
-#pragma unroll
-    for (int i = 0; i < kFewStages - 1; i++) {
-        const int64_t mine = place();
-        find(u0 + i + 1);
-        if (u0 + i < u1)
-            copy(i, mine);
-        commit();
+    // copies of unit u, whose page numbers were asked for a unit before, into a stage; then asks for the next
+    bool dead = false;  // a wait ran out: nothing more is copied, the results are invalid
+    auto copy = [&](int u, int stage) {
+        if constexpr (kBulk) {
+            if (u < units && !dead)
+                copy_boxes(stage);
+            find(u + 1);
+        } else {
+            const int64_t row = place();
+            find(u + 1);
+            if (u < units)
+                copy_rows(stage, row);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    if constexpr (kBulk) {
+        if (lane == 0)
+            for (int i = 0; i < kFewStages; i++)
+                tc::mbar_init(&bars[warp][i], 1);
+        if (threadIdx.x == 0)
+            aborted = 0;
+        tc::mbar_init_fence();
+        __syncthreads();
     }
+    find(0);
+#pragma unroll
+    for (int i = 0; i < kFewStages - (kBulk ? 0 : 1); i++)
+        copy(i, i);
 
-    uint4 qa[KG][2];         // the queries' chunks: rows g and g + 8
-    float qlo[kWide ? KG : 1][2][4];  // fp32: their low parts
-    float o[VS][E][4], m[2], l[2];
-    int lo[2], hi[2], rows = 0;  // rows: of the sequence
+    constexpr int kQ = Sh::kWide ? 2 : kGroups;
+    uint4 qa[KG][kQ];        // the queries' chunks of rows g, g + 8
+    float qlo[Sh::kWide ? KG : 1][2][4];  // fp32: their low parts
+    float o[Sh::kOut], m[Sh::kStats], l[Sh::kStats];
+    int lo[Sh::kStats], hi[Sh::kStats], rows = 0;  // rows: of the sequence
+    int all_lo = 0, all_hi = 0;  // positions that every row of the tile sees
     bool fresh = true, first_item = true;
     int stage = 0;
-    for (int64_t u = u0; u < u1; u++) {
+    uint32_t phase = 0;
+#pragma unroll 1
+    for (int u = 0; u < units; u++) {
         if (fresh) {
+            const int row0 = it.tile * kFewRows;
             rows = it.seq.count * p.group;
+            all_hi = seen_hi(it.seq, p.causal, row0 / p.group);
+            all_lo = seen_lo(seen_hi(it.seq, p.causal, (min(rows, row0 + kFewRows) - 1) / p.group), p.window);
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int r = it.tile * kFewRows + g + 8 * h, t = r / p.group;
-                m[h] = -INFINITY;
-                l[h] = 0.f;
-                hi[h] = r < rows ? seen_hi(it.seq, p.causal, t) : 0;
-                lo[h] = seen_lo(hi[h], p.window);
+            for (int i = 0; i < Sh::kStats; i++) {
+                const int r = row0 + Sh::row(i, g, q);
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+                hi[i] = r < rows ? seen_hi(it.seq, p.causal, r / p.group) : 0;
+                lo[i] = seen_lo(hi[i], p.window);
+            }
+#pragma unroll
+            for (int h = 0; h < kQ; h++) {
+                const int r = row0 + g + 8 * h, t = r / p.group;
                 const T *src = p.q.row<T>(it.seq.first + (r < rows ? t : 0),
                                           r < rows ? it.head * p.group + r - t * p.group : 0);
 #pragma unroll
@@ -318,7 +419,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p)
                     qa[i][h] = make_uint4(0, 0, 0, 0);
                     if (r < rows && e < p.d)
                         qa[i][h] = *reinterpret_cast<const uint4 *>(src + e);
-                    if (kWide) {
+                    if (Sh::kWide) {
                         qlo[i][h][0] = low_part(__uint_as_float(qa[i][h].x));
                         qlo[i][h][1] = low_part(__uint_as_float(qa[i][h].y));
                         qlo[i][h][2] = low_part(__uint_as_float(qa[i][h].z));
@@ -327,230 +428,291 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p)
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kOut; i++)
-                (&o[0][0][0])[i] = 0.f;
+            for (int i = 0; i < Sh::kOut; i++)
+                o[i] = 0.f;
             fresh = false;
         }
-        {
-            const int into = stage == 0 ? kFewStages - 1 : stage - 1;
-            const int64_t mine = place();  // of unit u + kFewStages - 1, whose page numbers were asked for a unit ago
-            find(u + kFewStages);
-            if (u + kFewStages - 1 < u1)
-                copy(into, mine);
-            commit();
+        if constexpr (kBulk) {
+            if (!dead && !tc::mbar_wait(&bars[warp][stage], phase, &aborted))
+                dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+        } else {
+            copy(u + kFewStages - 1, stage == 0 ? kFewStages - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 1) : "memory");
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 1) : "memory");
-        const uint4 *chunk = reinterpret_cast<const uint4 *>(ring + stage * kFewStageBytes);
-        const int at = it.lo + (int)(u - it.first) * UT + warp * TB;
-        float s[NB][KT][4];
+        const uint8_t *block = ring + stage * kFewStageBytes;
+        // chunk i of a group's key row t * 8 + g, and of its value row 2q + (t & 1) + 8 (t >> 1)
+        auto key_chunk = [&](int nb, int t, int i) {
+            return *reinterpret_cast<const uint4 *>(
+                kBulk ? block + nb * Sh::kGroupBytes + i * Sh::kKeyBox + (t * 8 + g) * 64 + q * 16
+                      : block + (nb * Sh::kChunks + t * KG + i) * 512 + lane * 16);
+        };
+        auto value_chunk = [&](int nb, int t, int i) {
+            const int row = 2 * q + (t & 1);
+            return *reinterpret_cast<const uint4 *>(
+                kBulk ? block + nb * Sh::kGroupBytes + KG * Sh::kKeyBox + i * Sh::kValueBox + (t >> 1) * 1024 +
+                            row * 128 + ((g ^ row) << 4)
+                      : block + (nb * Sh::kChunks + KT * KG + t * VS + i) * 512 + lane * 16);
+        };
+        const int at = it.lo + (u - it.first) * UT + warp * Sh::TB;
+
+        // scores: s[nb][x][j] is of token token_of(nb, x, j) and statistic stat_of(x, j)
+        constexpr int kS = Sh::kWide ? 1 : kGroups;
+        float s[NB][kS][4];
+        auto token_of = [&](int nb, int j) {
+            return nb * Sh::MG + (Sh::kWide ? 2 * q + (j & 1) : g + 8 * (j >> 1));
+        };
+        auto stat_of = [](int x, int j) { return Sh::kWide ? j >> 1 : 2 * x + (j & 1); };
 #pragma unroll
-        for (int nb = 0; nb < NB; nb++)
+        for (int nb = 0; nb < NB; nb++) {
+            float other[kS][4];  // every second MMA's sum: two chains, half as long
 #pragma unroll
-            for (int t = 0; t < KT; t++) {
+            for (int x = 0; x < kS; x++)
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    s[nb][t][j] = 0.f;
+                    s[nb][x][j] = other[x][j] = 0.f;
 #pragma unroll
-                for (int i = 0; i < KG; i++) {
-                    const uint4 k = chunk[(nb * kChunks + t * KG + i) * 32];
+            for (int i = 0; i < KG; i++) {
+                const uint4 k = key_chunk(nb, 0, i);
+                if constexpr (Sh::kWide) {
                     const uint4 &a = qa[i][0], &b = qa[i][1];
-                    if constexpr (kWide) {
-                        const float x[4] = {__uint_as_float(a.x), __uint_as_float(b.x), __uint_as_float(a.y), __uint_as_float(b.y)};
-                        const float y[4] = {__uint_as_float(a.z), __uint_as_float(b.z), __uint_as_float(a.w), __uint_as_float(b.w)};
-                        const float xl[4] = {qlo[i][0][0], qlo[i][1][0], qlo[i][0][1], qlo[i][1][1]};
-                        const float yl[4] = {qlo[i][0][2], qlo[i][1][2], qlo[i][0][3], qlo[i][1][3]};
-                        mma_fp32(s[nb][t], x, xl, __uint_as_float(k.x), __uint_as_float(k.y));
-                        mma_fp32(s[nb][t], y, yl, __uint_as_float(k.z), __uint_as_float(k.w));
-                    } else {
-                        const uint32_t x[4] = {a.x, b.x, a.y, b.y}, y[4] = {a.z, b.z, a.w, b.w};
-                        mma16816<T>(s[nb][t], x, k.x, k.y);
-                        mma16816<T>(s[nb][t], y, k.z, k.w);
+                    const float x[4] = {__uint_as_float(a.x), __uint_as_float(b.x), __uint_as_float(a.y),
+                                        __uint_as_float(b.y)};
+                    const float y[4] = {__uint_as_float(a.z), __uint_as_float(b.z), __uint_as_float(a.w),
+                                        __uint_as_float(b.w)};
+                    const float xl[4] = {qlo[i][0][0], qlo[i][1][0], qlo[i][0][1], qlo[i][1][1]};
+                    const float yl[4] = {qlo[i][0][2], qlo[i][1][2], qlo[i][0][3], qlo[i][1][3]};
+                    mma_fp32(s[nb][0], x, xl, __uint_as_float(k.x), __uint_as_float(k.y));
+                    mma_fp32(other[0], y, yl, __uint_as_float(k.z), __uint_as_float(k.w));
+                } else {
+                    const uint4 k8 = key_chunk(nb, 1, i);
+                    const uint32_t x[4] = {k.x, k8.x, k.y, k8.y}, y[4] = {k.z, k8.z, k.w, k8.w};
+#pragma unroll
+                    for (int n = 0; n < kGroups; n++) {
+                        mma16816<T>(s[nb][n], x, qa[i][n].x, qa[i][n].y);
+                        mma16816<T>(other[n], y, qa[i][n].z, qa[i][n].w);
                     }
                 }
             }
-        // rows g (elements 0, 1) and g + 8 (elements 2, 3), tokens 2q and 2q + 1 of each 8
-        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int nb = 0; nb < NB; nb++)
+            for (int x = 0; x < kS; x++)
 #pragma unroll
-            for (int t = 0; t < KT; t++)
+                for (int j = 0; j < 4; j++)
+                    s[nb][x][j] += other[x][j];
+        }
+        const bool edge = at < all_lo || at + Sh::TB > all_hi;
+        if (edge) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int pos = at + nb * MG + t * 8 + 2 * q + (j & 1), h = j >> 1;
-                    const float x = pos >= lo[h] && pos < hi[h] ? s[nb][t][j] * p.scale_log2 : -INFINITY;
-                    s[nb][t][j] = x;
-                    top[h] = fmaxf(top[h], x);
-                }
-        float base[2];
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int x = 0; x < kS; x++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int pos = at + token_of(nb, j), i = stat_of(x, j);
+                        s[nb][x][j] = pos >= lo[i] && pos < hi[i] ? s[nb][x][j] : -INFINITY;
+                    }
+        }
+        float top[Sh::kStats], base[Sh::kStats];
         bool moved = false;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-            top[h] = fmaxf(top[h], m[h]);
-            base[h] = top[h] == -INFINITY ? 0.f : top[h];
-            moved |= top[h] > m[h];
+        for (int i = 0; i < Sh::kStats; i++) {
+            top[i] = -INFINITY;
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int x = 0; x < kS; x++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (stat_of(x, j) == i)
+                            top[i] = fmaxf(top[i], s[nb][x][j]);
+#pragma unroll
+            for (int step = Sh::kWide ? 1 : 4; step < (Sh::kWide ? 4 : 32); step *= 2)
+                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], step));
+            top[i] = fmaxf(top[i] * p.scale_log2, m[i]);
+            base[i] = top[i] == -INFINITY ? 0.f : top[i];
+            moved |= top[i] > m[i];
         }
         if (__any_sync(0xffffffffu, moved)) {
+            float f[Sh::kStats];
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const float f = exp2_approx(m[h] - base[h]);
-                l[h] *= f;
-                m[h] = top[h];
-#pragma unroll
-                for (int i = 0; i < VS; i++)
-#pragma unroll
-                    for (int j = 0; j < E; j++) {
-                        o[i][j][2 * h] *= f;
-                        o[i][j][2 * h + 1] *= f;
-                    }
+            for (int i = 0; i < Sh::kStats; i++) {
+                f[i] = exp2_approx(m[i] - base[i]);
+                l[i] *= f[i];
+                m[i] = top[i];
             }
+#pragma unroll
+            for (int i = 0; i < Sh::kOut; i++)
+                o[i] *= f[Sh::stat(i)];
         }
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
-            for (int t = 0; t < KT; t++)
+            for (int x = 0; x < kS; x++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    s[nb][t][j] = exp2_approx(s[nb][t][j] - base[j >> 1]);
-                    l[j >> 1] += s[nb][t][j];
+                    const int i = stat_of(x, j);
+                    s[nb][x][j] = exp2_approx(fmaf(s[nb][x][j], p.scale_log2, -base[i]));
+                    l[i] += s[nb][x][j];
                 }
-            const uint4 *values = chunk + (nb * kChunks + KT * KG) * 32;
-            if constexpr (kWide) {
+            // a box's rows that no query sees may hold anything: a zero weight would not do
+            auto value = [&](int t, int i) {
+                uint4 v = value_chunk(nb, t, i);
+                if (kBulk && edge) {
+                    const int pos = at + nb * Sh::MG + 2 * q + (t & 1) + 8 * (t >> 1);
+                    if (pos < it.lo_seen || pos >= it.hi)
+                        v = make_uint4(0, 0, 0, 0);
+                }
+                return v;
+            };
+            if constexpr (Sh::kWide) {
                 const float *w = s[nb][0];
                 const float pa[4] = {w[0], w[2], w[1], w[3]};
                 const float pl[4] = {low_part(w[0]), low_part(w[2]), low_part(w[1]), low_part(w[3])};
 #pragma unroll
                 for (int i = 0; i < VS; i++) {
-                    const uint4 v0 = values[i * 32], v1 = values[(VS + i) * 32];
-                    mma_fp32(o[i][0], pa, pl, __uint_as_float(v0.x), __uint_as_float(v1.x));
-                    mma_fp32(o[i][1], pa, pl, __uint_as_float(v0.y), __uint_as_float(v1.y));
-                    mma_fp32(o[i][2], pa, pl, __uint_as_float(v0.z), __uint_as_float(v1.z));
-                    mma_fp32(o[i][3], pa, pl, __uint_as_float(v0.w), __uint_as_float(v1.w));
+                    const uint4 v0 = value(0, i), v1 = value(1, i);
+                    mma_fp32(o + 16 * i, pa, pl, __uint_as_float(v0.x), __uint_as_float(v1.x));
+                    mma_fp32(o + 16 * i + 4, pa, pl, __uint_as_float(v0.y), __uint_as_float(v1.y));
+                    mma_fp32(o + 16 * i + 8, pa, pl, __uint_as_float(v0.z), __uint_as_float(v1.z));
+                    mma_fp32(o + 16 * i + 12, pa, pl, __uint_as_float(v0.w), __uint_as_float(v1.w));
                 }
             } else {
-                uint32_t pa[4];  // the weights, rounded to the type; their sum is of the unrounded ones
+                // the weights, rounded to the type (their sum is of the unrounded ones), rows to columns
+                uint32_t b[kGroups][2];
 #pragma unroll
-                for (int t = 0; t < KT; t++) {
-                    pa[2 * t] = pack2<T>(s[nb][t][0], s[nb][t][1]);
-                    pa[2 * t + 1] = pack2<T>(s[nb][t][2], s[nb][t][3]);
+                for (int n = 0; n < kGroups; n++) {
+                    b[n][0] = transpose8x8(pack2<T>(s[nb][n][0], s[nb][n][1]));
+                    b[n][1] = transpose8x8(pack2<T>(s[nb][n][2], s[nb][n][3]));
                 }
 #pragma unroll
                 for (int i = 0; i < VS; i++) {
                     uint4 v[VT];
 #pragma unroll
                     for (int t = 0; t < VT; t++)
-                        v[t] = values[(t * VS + i) * 32];
+                        v[t] = value(t, i);
                     const uint32_t *w0 = &v[0].x, *w1 = &v[1].x, *w2 = &v[2].x, *w3 = &v[3].x;
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        mma16816<T>(o[i][2 * j], pa, __byte_perm(w0[j], w1[j], 0x5410),
-                                    __byte_perm(w2[j], w3[j], 0x5410));
-                        mma16816<T>(o[i][2 * j + 1], pa, __byte_perm(w0[j], w1[j], 0x7632),
-                                    __byte_perm(w2[j], w3[j], 0x7632));
+                    for (int j = 0; j < 4; j++) {  // columns 2j and 2j + 1 of each lane's eight
+                        const uint32_t a[4] = {__byte_perm(w0[j], w1[j], 0x5410), __byte_perm(w0[j], w1[j], 0x7632),
+                                               __byte_perm(w2[j], w3[j], 0x5410), __byte_perm(w2[j], w3[j], 0x7632)};
+#pragma unroll
+                        for (int n = 0; n < kGroups; n++)
+                            mma16816<T>(o + ((n * VS + i) * 4 + j) * 4, a, b[n][0], b[n][1]);
                     }
                 }
             }
         }
-        stage = stage + 1 == kFewStages ? 0 : stage + 1;
-        if (u + 1 < it.last && u + 1 < u1)
+        if constexpr (kBulk) {
+            __syncwarp();  // every lane has read the stage that is filled next: unit u's own
+            copy(u + kFewStages, stage);
+        }
+        stage++;
+        if (stage == kFewStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+        if (u + 1 < it.last && u + 1 < units)
             continue;
 
         // the item's (or the CTA's) last unit: join the warps
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (q == 0) {
-                s_m[warp][g + 8 * h] = m[h];
-                s_l[warp][g + 8 * h] = l[h];
+        for (int i = 0; i < Sh::kStats; i++) {
+#pragma unroll
+            for (int step = Sh::kWide ? 1 : 4; step < (Sh::kWide ? 4 : 32); step *= 2)
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], step);
+            if (Sh::kWide ? q == 0 : g == 0) {
+                s_m[warp][Sh::row(i, g, q)] = m[i];
+                s_l[warp][Sh::row(i, g, q)] = l[i];
             }
         }
         __syncthreads();
-        float lse[2];
+        float lse[Sh::kStats], f[Sh::kStats];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int i = 0; i < Sh::kStats; i++) {
+            const int r = Sh::row(i, g, q);
             float all = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kFewWarps; i++)
-                all = fmaxf(all, s_m[i][g + 8 * h]);
+            for (int w = 0; w < kFewWarps; w++)
+                all = fmaxf(all, s_m[w][r]);
             const float b = all == -INFINITY ? 0.f : all;
 #pragma unroll
-            for (int i = 0; i < kFewWarps; i++)
-                sum = fmaf(s_l[i][g + 8 * h], exp2_approx(s_m[i][g + 8 * h] - b), sum);
-            const float f = sum > 0.f ? exp2_approx(m[h] - b) / sum : 0.f;
-            lse[h] = sum > 0.f ? all + log2f(sum) : -INFINITY;
-#pragma unroll
-            for (int i = 0; i < VS; i++)
-#pragma unroll
-                for (int j = 0; j < E; j++) {
-                    o[i][j][2 * h] *= f;
-                    o[i][j][2 * h + 1] *= f;
-                }
+            for (int w = 0; w < kFewWarps; w++)
+                sum = fmaf(s_l[w][r], exp2_approx(s_m[w][r] - b), sum);
+            f[i] = sum > 0.f ? exp2_approx(m[i] - b) / sum : 0.f;
+            lse[i] = sum > 0.f ? all + log2f(sum) : -INFINITY;
         }
-        float *flat = &o[0][0][0];
+#pragma unroll
+        for (int i = 0; i < Sh::kOut; i++)
+            o[i] *= f[Sh::stat(i)];
         if (warp >= 2)
 #pragma unroll
-            for (int i = 0; i < kOut; i++)
-                merge[((warp - 2) * kOut + i) * 32 + lane] = flat[i];
+            for (int i = 0; i < Sh::kOut; i++)
+                merge[((warp - 2) * Sh::kOut + i) * 32 + lane] = o[i];
         __syncthreads();
         if (warp < 2)
 #pragma unroll
-            for (int i = 0; i < kOut; i++)
-                flat[i] += merge[(warp * kOut + i) * 32 + lane];
+            for (int i = 0; i < Sh::kOut; i++)
+                o[i] += merge[(warp * Sh::kOut + i) * 32 + lane];
         if (warp == 1)
 #pragma unroll
-            for (int i = 0; i < kOut; i++)
-                merge[(kOut + i) * 32 + lane] = flat[i];
+            for (int i = 0; i < Sh::kOut; i++)
+                merge[(Sh::kOut + i) * 32 + lane] = o[i];
         __syncthreads();
         if (warp == 0) {
-            const bool whole = it.first >= u0 && it.last <= u1;
+            const bool whole = it.first >= 0 && it.last <= units;
             const int heads = p.cache.heads * p.group, slot = blockIdx.x * 2 + (first_item ? 0 : 1);
 #pragma unroll
-            for (int i = 0; i < kOut; i++)
-                flat[i] += merge[(kOut + i) * 32 + lane];
+            for (int i = 0; i < Sh::kOut; i++)
+                o[i] += merge[(Sh::kOut + i) * 32 + lane];
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int in = g + 8 * h, r = it.tile * kFewRows + in, t = r / p.group;
+            for (int i = 0; i < Sh::kStats; i++) {
+                const int in = Sh::row(i, g, q), r = it.tile * kFewRows + in, t = r / p.group;
                 const int head = it.head * p.group + r - t * p.group;
                 if (r >= rows)
                     continue;
-                if (q == 0) {
+                if (Sh::kWide ? q == 0 : g == 0) {
                     if (!whole)
-                        p.part_lse[slot * p.rows + in] = lse[h];
+                        p.part_lse[slot * p.rows + in] = lse[i];
                     else if (p.lse)
-                        p.lse[(it.seq.first + t) * heads + head] = lse[h] * kLn2;
+                        p.lse[(it.seq.first + t) * heads + head] = lse[i] * kLn2;
                 }
+                // the lane's runs of E columns of this row: one of each set, fp32: two
 #pragma unroll
-                for (int i = 0; i < VS; i++)
+                for (int c = 0; c < VS * (Sh::kWide ? 2 : 1); c++) {
+                    const int e = (Sh::kWide ? 8 * (c >> 1) + 2 * q + (c & 1) : 8 * c + g) * E;
+                    if (e >= p.d)
+                        continue;
+                    float x[E];
 #pragma unroll
-                    for (int c = 0; c < 2; c++) {  // columns e .. e + E - 1
-                        const int e = (8 * i + 2 * q + c) * E;
-                        if (e >= p.d)
-                            continue;
-                        float x[E];
+                    for (int j = 0; j < E; j++)
+                        x[j] = o[Sh::kWide ? 16 * (c >> 1) + 4 * j + 2 * i + (c & 1)
+                                           : (((i >> 1) * VS + c) * 4 + (j >> 1)) * 4 + 2 * (j & 1) + (i & 1)];
+                    T *out = p.out.row<T>(it.seq.first + t, head) + e;
+                    float4 *part = reinterpret_cast<float4 *>(p.part_o + ((int64_t)slot * p.rows + in) * p.d + e);
+                    if (!whole) {
 #pragma unroll
-                        for (int j = 0; j < E; j++)
-                            x[j] = o[i][j][2 * h + c];
-                        T *out = p.out.row<T>(it.seq.first + t, head) + e;
-                        float4 *part = reinterpret_cast<float4 *>(p.part_o + ((int64_t)slot * p.rows + in) * p.d + e);
-                        if (!whole) {
-#pragma unroll
-                            for (int j = 0; j < E; j += 4)
-                                part[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-                        } else if constexpr (kWide) {
-                            *reinterpret_cast<float4 *>(out) = make_float4(x[0], x[1], x[2], x[3]);
-                        } else {
-                            *reinterpret_cast<uint4 *>(out) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
-                                                                         pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-                        }
+                        for (int j = 0; j < E; j += 4)
+                            part[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                    } else if constexpr (Sh::kWide) {
+                        *reinterpret_cast<float4 *>(out) = make_float4(x[0], x[1], x[2], x[3]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(out) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
+                                                                     pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
                     }
+                }
             }
         }
         fresh = true;
         first_item = false;
-        if (u + 1 < u1)
+        if (u + 1 < units)
             few_next(p, it, UT);
+    }
+    if (kBulk && dead) {  // no copy may be in flight when the memory is given back
+        int never = 0;
+        for (int i = 0; i < kFewStages; i++)
+            tc::mbar_wait(&bars[warp][i], i < stage ? phase ^ 1 : phase, &never);
+        if (lane == 0)
+            raise_flag(p.err, DLRM_FLAG_WAIT_TIMEOUT);
     }
 }
 
@@ -621,12 +783,37 @@ size_t few_workspace(int64_t S, int64_t rows, int d, int64_t max_len)
     return (size_t)2 * kFewCtas * few_rows(rows) * (d + 1) * sizeof(float) + (size_t)(S + 2) * sizeof(int64_t);
 }
 
-template <typename T, int DP>
-static int launch_few(AttnParams &p, void *workspace, cudaStream_t st)
+// Maps of the cache with boxes of `rows` slots; false where it cannot be
+// described so.
+static bool few_maps(const AttnParams &p, int dtype, int rows, FewMaps &m)
 {
-    constexpr int smem = kFewWarps * kFewStages * kFewStageBytes + DP * 32 * 4;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc)
+        return false;
+    const int es = dtype == DLRM_F32 ? 4 : 2;
+    const CUtensorMapDataType type = dtype == DLRM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == DLRM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.d, p.cache.page.d, (cuuint64_t)p.cache.heads, p.cache.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.cache.slot_stride * es, (cuuint64_t)p.cache.head_stride * es,
+                                   (cuuint64_t)p.cache.page_stride * es};
+    const cuuint32_t k_box[4] = {(cuuint32_t)(64 / es), (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t v_box[4] = {(cuuint32_t)(128 / es), (cuuint32_t)rows, 1, 1};
+    m.rows = rows;
+    return enc(&m.k, type, 4, p.cache.k, dims, strides, k_box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+               CUDA_SUCCESS &&
+           enc(&m.v, type, 4, p.cache.v, dims, strides, v_box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+               CUDA_SUCCESS;
+}
+
+template <typename T, int DP, int kGroups, bool kBulk>
+static int launch_few(AttnParams &p, const FewMaps &maps, void *workspace, cudaStream_t st)
+{
+    constexpr int smem = FewShape<T, DP, kGroups, kBulk>::kSmem;
     static std::atomic<unsigned long long> done{0};
-    const int s = allow_dynamic_smem((const void *)kv_attn_few_kernel<T, DP>, smem, &done);
+    const int s = allow_dynamic_smem((const void *)kv_attn_few_kernel<T, DP, kGroups, kBulk>, smem, &done);
     if (s != DLRM_OK)
         return s;
     const bool split = few_splits(p.max_len);
@@ -638,7 +825,8 @@ static int launch_few(AttnParams &p, void *workspace, cudaStream_t st)
     const int64_t items = p.batch.S * p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows);
     if (items > 0x7fffffff)
         return DLRM_ERR_UNSUPPORTED;
-    kv_attn_few_kernel<T, DP><<<(unsigned)(split ? kFewCtas : items), kFewWarps * 32, smem, st>>>(p);
+    kv_attn_few_kernel<T, DP, kGroups, kBulk>
+        <<<(unsigned)(split ? kFewCtas : items), kFewWarps * 32, smem, st>>>(p, maps);
     count_launch(st);
     if (split) {
         const int64_t need = (p.batch.S * p.cache.heads * p.max_new * p.group + 3) / 4;
@@ -648,14 +836,29 @@ static int launch_few(AttnParams &p, void *workspace, cudaStream_t st)
     return launch_status();
 }
 
+template <typename T, int kGroups>
+static int launch_few_width(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
+{
+    FewMaps maps = {};
+    maps.rows = sizeof(T) == 2 && p.cache.page.d % 16 == 0 ? 16 : 8;
+    const bool bulk = p.cache.page.d % 8 == 0 && few_maps(p, dtype, maps.rows, maps);
+    if (p.d <= 64)
+        return bulk ? launch_few<T, 64, kGroups, true>(p, maps, workspace, st)
+                    : launch_few<T, 64, kGroups, false>(p, maps, workspace, st);
+    return bulk ? launch_few<T, 128, kGroups, true>(p, maps, workspace, st)
+                : launch_few<T, 128, kGroups, false>(p, maps, workspace, st);
+}
+
 int launch_kv_attn_few(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
 {
+    const bool narrow = p.max_new * p.group <= 8;
     if (dtype == DLRM_F32)
-        return p.d <= 64 ? launch_few<float, 64>(p, workspace, st) : launch_few<float, 128>(p, workspace, st);
+        return launch_few_width<float, 1>(p, dtype, workspace, st);
     if (dtype == DLRM_F16)
-        return p.d <= 64 ? launch_few<__half, 64>(p, workspace, st) : launch_few<__half, 128>(p, workspace, st);
-    return p.d <= 64 ? launch_few<__nv_bfloat16, 64>(p, workspace, st)
-                     : launch_few<__nv_bfloat16, 128>(p, workspace, st);
+        return narrow ? launch_few_width<__half, 1>(p, dtype, workspace, st)
+                      : launch_few_width<__half, 2>(p, dtype, workspace, st);
+    return narrow ? launch_few_width<__nv_bfloat16, 1>(p, dtype, workspace, st)
+                  : launch_few_width<__nv_bfloat16, 2>(p, dtype, workspace, st);
 }
 
 }  // namespace dlrm
