@@ -161,6 +161,14 @@ struct AttnPlan {
     int splits;      // at most
 };
 
+// An item of up to 16 rows that a CTA began and the ones after it went on with.
+struct FewJoin {
+    int64_t token;         // the sequence's first new token
+    int head, row, rows;   // its first query head, first row and rows (0: there is no such item)
+    int first, last;       // the CTA's own part; the last CTA
+    int unused;
+};
+
 struct AttnParams {
     HeadsView q, out;
     BatchView batch;
@@ -174,7 +182,7 @@ struct AttnParams {
     int rows, split_len, splits;
     int64_t tiles;
     float *part_o, *part_lse;  // [splits][n][q heads]([d]): partial rows, log2 of their sums
-    int64_t *prefix;           // few rows: units before each sequence
+    FewJoin *joins;            // rows of 16: an item that each CTA left unfinished
     int32_t *err;
 };
 

@@ -13,7 +13,7 @@
 
 namespace dlrm {
 
-size_t few_workspace(int64_t, int64_t, int, int64_t);
+size_t few_workspace(int64_t, int, int64_t);
 int launch_kv_attn_few(AttnParams &, int, void *, cudaStream_t);
 int launch_kv_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
 
@@ -256,7 +256,7 @@ size_t attn_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, in
 {
     const int group = q_heads / kv_heads;
     max_new = max_new < n ? max_new : n;
-    size_t most = few_workspace(S, max_new * group, d, max_len);
+    size_t most = few_workspace(max_new * group, d, max_len);
     for (AttnKernel k : {kAttnGeneral, kAttnTile}) {
         const size_t b = part_floats(plan(k, S, kv_heads, group, max_new, max_len), n, q_heads, d) * sizeof(float);
         most = b > most ? b : most;

@@ -11,7 +11,7 @@
 // rows: keys in columns of 64 bytes, values in columns of 128 bytes swizzled, so that the reads
 // below meet no bank twice.  Other page sizes take asynchronous 16-byte copies, row by row, where
 // every lane reads back exactly the chunks it copied itself; they share the load/store
-// pipe with the reads (256 users: 444 us against 3xx us).
+// pipe with the reads (256 users of up to 8192 events: 444 us against 328).
 //  - scores: MMAs of 16 tokens x 8 rows (m16n8k16; fp32: 16 rows x 8 tokens,
 //    m16n8k8).  The order of the summed elements is free, so a lane's 16-byte chunk
 //    of a key serves two MMA steps as it is, with the query's chunks in the same order.
@@ -142,9 +142,8 @@ __host__ __device__ __forceinline__ int64_t few_quota(int64_t total)
 }
 
 // The CTA's share of all units: sums every sequence's units (each thread a run
-// of sequences), finds the item that holds the first unit of the share.  CTA
-// 0 leaves the sums before each sequence in p.prefix for the join.
-__device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int unit)
+// of sequences), finds the item that holds the first unit of the share.
+__device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int &quota_units, int unit)
 {
     __shared__ int64_t sums[kFewWarps], found[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -174,22 +173,17 @@ __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int unit)
     const int64_t quota = few_quota(total);
     const int64_t u0 = min(blockIdx.x * quota, total);
     units = (int)(min(u0 + quota, total) - u0);
+    quota_units = (int)quota;
     const bool here = units > 0 && u0 >= before && u0 < before + mine;
-    if (here || blockIdx.x == 0) {
-        for (int64_t s = from; s < to; s++) {
-            int64_t here_units = 0;
-            if (read_sequence(p.batch, s, p.max_new, p.max_len, q, nullptr))
-                here_units = (int64_t)few_units(p, q, unit, lo, hi) * few_tiles(p, q) * p.cache.heads;
-            if (here && u0 >= before && u0 < before + here_units) {
-                found[0] = s;
-                found[1] = before;
-            }
-            if (blockIdx.x == 0)
-                p.prefix[s] = before;
-            before += here_units;
+    for (int64_t s = from; here && s < to; s++) {
+        int64_t here_units = 0;
+        if (read_sequence(p.batch, s, p.max_new, p.max_len, q, nullptr))
+            here_units = (int64_t)few_units(p, q, unit, lo, hi) * few_tiles(p, q) * p.cache.heads;
+        if (u0 >= before && u0 < before + here_units) {
+            found[0] = s;
+            found[1] = before;
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            p.prefix[p.batch.S] = total;
+        before += here_units;
     }
     __syncthreads();
     if (units == 0)
@@ -265,9 +259,12 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     float *merge = reinterpret_cast<float *>(smem + kFewWarps * kFewStages * kFewStageBytes);  // [2][kOut][32]
 
     FewItem it;  // of the unit being computed; `is`: of the unit whose addresses come next
-    int units;   // of this CTA; the items' are counted from its first
+    int units, quota = 0;  // of this CTA; the items' are counted from its first
     if (p.splits > 1) {
-        if (!few_share(p, it, units, UT))
+        const bool any = few_share(p, it, units, quota, UT);
+        if (threadIdx.x == 0)
+            p.joins[blockIdx.x].rows = 0;  // until an item is left unfinished
+        if (!any)
             return;
     } else {
         const int64_t most = (p.max_new * p.group + kFewRows - 1) / kFewRows, of = blockIdx.x / most;
@@ -702,6 +699,17 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                 }
             }
         }
+        if (threadIdx.x == 0 && it.first >= 0 && it.last > units) {  // the CTAs after this one go on with it
+            const int row0 = it.tile * kFewRows;
+            FewJoin j;
+            j.token = it.seq.first;
+            j.head = it.head * p.group;
+            j.row = row0;
+            j.rows = min(rows - row0, kFewRows);
+            j.first = blockIdx.x * 2 + (first_item ? 0 : 1);
+            j.last = blockIdx.x + (it.last - 1) / quota;
+            p.joins[blockIdx.x] = j;
+        }
         fresh = true;
         first_item = false;
         if (u + 1 < units)
@@ -716,57 +724,66 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     }
 }
 
-// Joins the items that span CTAs: a warp per row of an item.
+// Joins the items that span CTAs: CTA x of this kernel the item that the
+// main kernel's CTA x began and did not end, row blockIdx.y of it.  A warp
+// sums every eighth part, 4 columns a lane.
+constexpr int kJoinWarps = 8;
+
 template <typename T>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
 {
-    const int lane = threadIdx.x & 31, heads = p.cache.heads * p.group;
-    const int64_t quota = few_quota(p.prefix[p.batch.S]), most = p.max_new * p.group;
-    const int64_t all = p.batch.S * p.cache.heads * most;
-    for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); i < all; i += (int64_t)gridDim.x * 4) {
-        const int64_t of = i / most, s = of / p.cache.heads;
-        const int r = (int)(i - of * most), head = (int)(of - s * p.cache.heads), t = r / p.group;
-        const int64_t before = p.prefix[s], all_units = p.prefix[s + 1] - before;
-        const int64_t from = p.batch.offsets[s], token = from + t;
-        if (all_units == 0 || token >= p.batch.offsets[s + 1])
-            continue;
-        const int64_t tiles = ((p.batch.offsets[s + 1] - from) * p.group + kFewRows - 1) / kFewRows;
-        const int64_t units = all_units / (p.cache.heads * tiles);
-        const int64_t first = before + (head * tiles + r / kFewRows) * units;
-        const int64_t c0 = first / quota, c1 = (first + units - 1) / quota;
-        if (c0 == c1)
-            continue;
-        // the first CTA's part is its last item's unless the item begins with it
-        auto row = [&](int64_t c) {
-            return (c * 2 + (c == c0 && c0 * quota < first ? 1 : 0)) * p.rows + r % kFewRows;
-        };
-        float top = -INFINITY;
-        for (int64_t c = c0 + lane; c <= c1; c += 32)
-            top = fmaxf(top, p.part_lse[row(c)]);
-        top = warp_max(top);
-        const float base = top == -INFINITY ? 0.f : top;
-        float total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    __shared__ float4 sums[kJoinWarps][32];
+    __shared__ float weights[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = p.cache.heads * p.group;
+    const FewJoin j = p.joins[blockIdx.x];
+    if ((int)blockIdx.y >= j.rows)
+        return;
+    // its parts: of the first CTA the one it says, of the others their first
+    const int c0 = blockIdx.x, c1 = j.last;
+    auto row = [&](int c) { return (int64_t)(c == c0 ? j.first : c * 2) * p.rows + blockIdx.y; };
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32)
+        top = fmaxf(top, p.part_lse[row(c)]);
+    top = warp_max(top);
+    const float base = top == -INFINITY ? 0.f : top;
+    float weight = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int64_t c = c0; c <= c1; c++) {
-            const float f = exp2_approx(p.part_lse[row(c)] - base);
-            const float *o = p.part_o + row(c) * p.d;
-            total += f;
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (lane + 32 * j < p.d)
-                    acc[j] = fmaf(o[lane + 32 * j], f, acc[j]);
+    for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+        const float f = exp2_approx(p.part_lse[row(c)] - base);
+        weight += f;
+        if (lane * 4 < p.d) {
+            const float4 x = *reinterpret_cast<const float4 *>(p.part_o + row(c) * p.d + lane * 4);
+            sum = make_float4(fmaf(x.x, f, sum.x), fmaf(x.y, f, sum.y), fmaf(x.z, f, sum.z), fmaf(x.w, f, sum.w));
         }
-        const float inv = total > 0.f ? 1.f / total : 0.f;
-        const int h = head * p.group + r - t * p.group;
-        T *out = p.out.row<T>(token, h);
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (lane + 32 * j < p.d)
-                out[lane + 32 * j] = from_f32<T>(acc[j] * inv);
-        if (p.lse && lane == 0)
-            p.lse[token * heads + h] = total > 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
     }
+    sums[warp][lane] = sum;
+    if (lane == 0)
+        weights[warp] = weight;
+    __syncthreads();
+    if (warp != 0)
+        return;
+    weight = 0.f;
+    sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; w++) {
+        const float4 x = sums[w][lane];
+        weight += weights[w];
+        sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+    }
+    const float inv = weight > 0.f ? 1.f / weight : 0.f;
+    const int r = j.row + blockIdx.y, t = r / p.group, h = j.head + r - t * p.group;
+    const int64_t token = j.token + t;
+    if (lane * 4 < p.d) {
+        T *out = p.out.row<T>(token, h) + lane * 4;
+        out[0] = from_f32<T>(sum.x * inv);
+        out[1] = from_f32<T>(sum.y * inv);
+        out[2] = from_f32<T>(sum.z * inv);
+        out[3] = from_f32<T>(sum.w * inv);
+    }
+    if (p.lse && lane == 0)
+        p.lse[token * heads + h] = weight > 0.f ? (top + log2f(weight)) * kLn2 : -INFINITY;
 }
 
 // Histories longer than this are shared out over CTAs in equal runs.
@@ -776,11 +793,11 @@ bool few_splits(int64_t max_len) { return max_len > kFewWhole; }
 
 static int64_t few_rows(int64_t rows) { return rows < kFewRows ? rows : kFewRows; }
 
-size_t few_workspace(int64_t S, int64_t rows, int d, int64_t max_len)
+size_t few_workspace(int64_t rows, int d, int64_t max_len)
 {
     if (!few_splits(max_len))
         return 0;
-    return (size_t)2 * kFewCtas * few_rows(rows) * (d + 1) * sizeof(float) + (size_t)(S + 2) * sizeof(int64_t);
+    return (size_t)2 * kFewCtas * few_rows(rows) * (d + 1) * sizeof(float) + kFewCtas * sizeof(FewJoin);
 }
 
 // Maps of the cache with boxes of `rows` slots; false where it cannot be
@@ -816,10 +833,12 @@ static int launch_few(AttnParams &p, const FewMaps &maps, void *workspace, cudaS
     const int s = allow_dynamic_smem((const void *)kv_attn_few_kernel<T, DP, kGroups, kBulk>, smem, &done);
     if (s != DLRM_OK)
         return s;
-    const bool split = few_splits(p.max_len);
+    // a window bounds what an item's rows see, whatever the history's length
+    const int64_t seen = p.window > 0 ? p.window + (p.causal ? p.max_new : 0) : p.max_len;
+    const bool split = few_splits(seen < p.max_len ? seen : p.max_len);
     p.splits = split ? 2 : 1;
-    p.prefix = static_cast<int64_t *>(workspace);
-    p.part_o = reinterpret_cast<float *>(p.prefix + ((p.batch.S + 2) & ~(int64_t)1));
+    p.joins = static_cast<FewJoin *>(workspace);
+    p.part_o = reinterpret_cast<float *>(p.joins + kFewCtas);
     p.rows = (int)few_rows(p.max_new * p.group);
     p.part_lse = p.part_o + (size_t)2 * kFewCtas * p.rows * p.d;
     const int64_t items = p.batch.S * p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows);
@@ -829,8 +848,7 @@ static int launch_few(AttnParams &p, const FewMaps &maps, void *workspace, cudaS
         <<<(unsigned)(split ? kFewCtas : items), kFewWarps * 32, smem, st>>>(p, maps);
     count_launch(st);
     if (split) {
-        const int64_t need = (p.batch.S * p.cache.heads * p.max_new * p.group + 3) / 4;
-        kv_attn_few_join_kernel<T><<<(unsigned)(need < 65536 ? need : 65536), 128, 0, st>>>(p);
+        kv_attn_few_join_kernel<T><<<dim3(kFewCtas - 1, (unsigned)p.rows), kJoinWarps * 32, 0, st>>>(p);
         count_launch(st);
     }
     return launch_status();
