@@ -3,15 +3,18 @@
 //
 // A CTA holds two query tiles of 128 packed rows and walks the positions in
 // tiles of 128.  Warp roles:
-//  - warps 8 and 9 copy: a thread resolves one position's slot through the page
-//    table, and the warp copies rows with asynchronous 16-byte copies
-//    into a ring of key and value tiles in the 128-byte swizzle -- any page
-//    size and layout, and rows that no query sees are filled with zeros
-//    without being read, so nothing stale meets a zero weight;
-//  - one thread of warp 10 issues the MMAs: S = Q K^T (both operands in
+//  - warp 16 copies keys and values into a ring of tiles in the 128-byte swizzle,
+//    by bulk tensor copies through the page table where pages are multiples of
+//    8 slots, in boxes of the largest power of two up to 128 that divides a page; the rows of
+//    a value tile that no query sees may hold anything, so it overwrites
+//    them with zeros before it hands the tile over.  Other page sizes: two warps copy row by
+//    row in asynchronous 16-byte copies and fill such rows with zeros
+//    without reading them;
+//  - one thread of the last warp issues the MMAs: S = Q K^T (both operands in
 //    shared memory, K-major) and O += P V (P in tensor memory, V MN-major as it lies);
-//  - warps 0-3 and 4-7 are the softmax of one query tile each: a thread owns a
-//    row, reads its 128 scores, and writes the weights over them, in 16 bits.
+//  - warps 0-7 and 8-15 are the softmax of one query tile each: a thread owns half
+//    of a row's 128 scores, agrees on the row's maximum with the thread that owns the
+//    other half, and writes the weights over the scores, in 16 bits.
 // The two tiles take turns: while one's scores are exponentiated the other's
 // MMAs run.  The running maximum a row is scaled by lags: the output (in
 // tensor memory) and the sum are rescaled only when the maximum has grown by more than
@@ -25,8 +28,10 @@
 
 namespace dlrm {
 
-// Eleven warps leave a thread 184 registers: a softmax row's 128 scores stay in them.
-constexpr int kTileThreads = 352, kTilePos = 128, kCopyThreads = 64;
+// With one thread to a row (8 softmax warps) the long chunks take 354 us instead of 342.
+constexpr int kTilePos = 128, kSoftmaxThreads = 512;
+__host__ __device__ constexpr int copy_threads(bool bulk) { return bulk ? 32 : 64; }
+__host__ __device__ constexpr int tile_threads(bool bulk) { return kSoftmaxThreads + copy_threads(bulk) + 32; }
 constexpr int kTileLag = 3;         // copied tiles that may be in flight before one is waited for
 constexpr float kTileSlack = 8.f;   // log2 of the growth of a maximum that is let pass
 
@@ -34,15 +39,28 @@ template <int DP>
 struct TileShape {
     static constexpr int kTileBytes = kTilePos * DP * 2;  // of keys or values; a query tile too
     static constexpr int kSlots = DP == 128 ? 5 : 8;
-    static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kTileBytes;
+    static constexpr int kTiles = 2 * kTileBytes + kSlots * kTileBytes;
     static constexpr int kBlock = kTilePos * 128;         // bytes between 64-column blocks of a tile
     static constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
 };
 
+// Keys and values as bulk tensor copies see them: (element, slot, head, page).
+struct TileMaps {
+    CUtensorMap k, v;
+    int rows;  // of a box
+};
+
+// A wait by a whole warp, whose lanes go on or give up together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *aborted)
+{
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, aborted));
+}
+
 struct TileBars {
-    uint64_t full[8], empty[8], q_full, s_full[2], p_ready[2], o_full[2], drained;
+    uint64_t full[8], empty[8], landed, q_full, s_full[2], p_ready[2], o_full[2], drained;
     uint32_t tmem;
     int aborted;
+    float agree[2][2][128];  // [query tile][half][row]: a maximum of half a row's scores; at the end its sum
 };
 
 // Copies 32 rows (this warp's) of a tile: lane t of the warp knows row t's
@@ -62,24 +80,107 @@ __device__ __forceinline__ void copy_rows(uint8_t *tile, const char *base, int64
     }
 }
 
-template <typename T, int DP>
-__device__ void tile_copy(const AttnParams &p, const AttnWork &w, uint8_t *sq, uint8_t *ring, TileBars &b, int tiles)
+// Copies the queries' rows (rows of zeros past the last).
+template <int DP, int kThreads>
+__device__ __forceinline__ void copy_queries(const AttnParams &p, const AttnWork &w, uint8_t *sq)
 {
-    using Sh = TileShape<DP>;
-    const int tid = threadIdx.x - 256, row0 = tid & ~31;
-#pragma unroll
-    for (int t = 0; t < 4; t++) {
-        const int r = t * 64 + tid, row = w.row0 + r, token = row / p.group;
+    const int tid = threadIdx.x - kSoftmaxThreads, row0 = tid & ~31;
+#pragma unroll 1
+    for (int r0 = 0; r0 < kTileRows; r0 += kThreads) {
+        const int r = r0 + tid, row = w.row0 + r, token = row / p.group;
         const int64_t o = r < w.rows ? ((w.seq.first + token) * p.q.ts +
                                         (int64_t)(w.head * p.group + row - token * p.group) * p.q.hs) * 2
                                      : -1;
-        copy_rows<DP>(sq + (t >> 1) * Sh::kTileBytes, p.q.ptr, o, (t & 1) * 64 + row0, p.d);
+        copy_rows<DP>(sq + (r0 >> 7) * TileShape<DP>::kTileBytes, p.q.ptr, o, (r0 & 127) + row0, p.d);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// The copy warp, by bulk tensor copies.  A tile begins at a multiple of 128
+// positions; lane i copies box i % boxes of the tile, if there are as many.
+template <typename T, int DP>
+__device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const TileMaps &maps, uint8_t *sq,
+                               uint8_t *ring, TileBars &b, int tiles)
+{
+    using Sh = TileShape<DP>;
+    constexpr int kColumns = DP / 64;
+    const int lane = threadIdx.x & 31, start = w.lo & ~127, parts = kTilePos / maps.rows;
+    const int32_t *pages = p.batch.table + w.s * p.batch.table_stride;
+    // part i of tile j: its page number (-1: nothing of it is seen) and slot
+    auto find = [&](int j, int i, int &page, int &slot) {
+        const int at = start + j * kTilePos + i * maps.rows;
+        page = -1;
+        slot = 0;
+        if (i < parts && at < w.hi && at + maps.rows > w.lo) {
+            const uint32_t n = p.cache.page.div((uint32_t)at);
+            slot = at - (int)(n * p.cache.page.d);
+            page = __ldg(pages + n);
+        }
+    };
+    int page, slot, next_page, next_slot;
+    uint32_t patched = 0;  // value tiles mended so far, modulo 2
+    find(0, lane, next_page, next_slot);
+    copy_queries<DP, 32>(p, w, sq);
+    for (int j = 0; j < tiles; j++) {
+        page = next_page;
+        slot = next_slot;
+        find(j + 1, lane, next_page, next_slot);
+        const int at = start + j * kTilePos;
+        const bool seen = at + lane * maps.rows < w.hi && at + (lane + 1) * maps.rows > w.lo;
+        if (lane < parts && seen && (uint32_t)page >= p.cache.pages)
+            raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+        page = (uint32_t)page < p.cache.pages ? page : -1;  // outside the map: zeros
+#pragma unroll
+        for (int kv = 0; kv < 2; kv++) {
+            const int i = 2 * j + kv, ring_slot = i % Sh::kSlots;
+            uint8_t *tile = ring + ring_slot * Sh::kTileBytes;
+            if (i >= Sh::kSlots && !warp_wait(&b.empty[ring_slot], (i / Sh::kSlots - 1) & 1, &b.aborted))
+                return;
+            const bool mend = kv == 1 && (at < w.lo || at + kTilePos > w.hi);
+            uint64_t *bar = mend ? &b.landed : &b.full[ring_slot];
+            if (lane == 0)
+                tc::mbar_expect_tx(bar, Sh::kTileBytes);
+            __syncwarp();
+            if (lane < parts)
+#pragma unroll
+                for (int c = 0; c < kColumns; c++)
+                    tc::tma_load_4d(tc::smem_u32(tile) + c * Sh::kBlock + lane * maps.rows * 128,
+                                    kv ? &maps.v : &maps.k, c * 64, slot, w.head, page, bar);
+            if (i == 0) {  // the queries follow the first keys
+                tc::cp_async_wait_all();
+                tc::fence_async_smem();
+                tc::mbar_arrive(&b.q_full);
+            }
+            if (mend) {
+                if (!warp_wait(&b.landed, patched & 1, &b.aborted))
+                    return;
+                patched++;
+                for (int r = 0; r < kTilePos; r++)
+                    if (at + r < w.lo || at + r >= w.hi)
+                        for (int c = lane; c < Sh::kChunks; c += 32)
+                            *reinterpret_cast<uint4 *>(tile + (c >> 3) * Sh::kBlock + r * 128 + ((c & 7) << 4)) =
+                                make_uint4(0, 0, 0, 0);
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&b.full[ring_slot]);
+            }
+        }
+    }
+}
+
+// The copy warps, row by row.
+template <typename T, int DP>
+__device__ void tile_copy_rows(const AttnParams &p, const AttnWork &w, uint8_t *sq, uint8_t *ring, TileBars &b,
+                               int tiles)
+{
+    using Sh = TileShape<DP>;
+    const int tid = threadIdx.x - kSoftmaxThreads, row0 = tid & ~31, start = w.lo & ~127;
+    copy_queries<DP, 64>(p, w, sq);
     const int32_t *pages = p.batch.table + w.s * p.batch.table_stride;
     auto place = [&](int j, int half) -> int64_t {
-        const int at = w.lo + j * kTilePos + half * 64 + tid;
-        if (j >= tiles || at >= w.hi)
+        const int at = start + j * kTilePos + half * 64 + tid;
+        if (j >= tiles || at >= w.hi || at < w.lo)
             return -1;
         const int64_t o = slot_offset<T>(p.cache, pages, at, w.head);
         if (o < 0)
@@ -125,50 +226,62 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
     using Sh = TileShape<DP>;
     constexpr int kType = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
     constexpr uint32_t kScores = tc::f16_idesc(kType, 128, kTilePos, false), kOut = tc::f16_idesc(kType, 128, DP, true);
-    const uint32_t q = tc::smem_u32(sq), kv = tc::smem_u32(ring);
+    // all lanes run this; one issues.  Descriptors of a later place are the first plus its distance / 16.
+    const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
+    const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(sq)), k_desc = tc::sw128_desc(tc::smem_u32(ring));
+    const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(ring), Sh::kBlock);
     auto scores = [&](int t, int j) {
-        const uint32_t k = kv + (2 * j % Sh::kSlots) * Sh::kTileBytes;
+        const uint64_t q = q_desc + t * (Sh::kTileBytes >> 4), k = k_desc + (2 * j % Sh::kSlots) * (Sh::kTileBytes >> 4);
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int e = 0; e < DP / 16; e++) {
-            const uint32_t at = (e >> 2) * Sh::kBlock + (e & 3) * 32;
-            tc::mma_f16(b.tmem + t * 128, tc::sw128_desc(q + t * Sh::kTileBytes + at), tc::sw128_desc(k + at), kScores,
-                        e > 0);
+            for (int e = 0; e < DP / 16; e++) {
+                const int at = ((e >> 2) * Sh::kBlock + (e & 3) * 32) >> 4;
+                tc::mma_f16(tmem + t * 128, q + at, k + at, kScores, e > 0);
+            }
+            tc::mma_commit(&b.s_full[t]);
         }
-        tc::mma_commit(&b.s_full[t]);
+        __syncwarp();
     };
     auto output = [&](int t, int j) {
-        const uint32_t v = kv + ((2 * j + 1) % Sh::kSlots) * Sh::kTileBytes;
+        const uint64_t v = v_desc + ((2 * j + 1) % Sh::kSlots) * (Sh::kTileBytes >> 4);
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int e = 0; e < kTilePos / 16; e++)
-            tc::mma_f16_ta(b.tmem + 256 + t * DP, b.tmem + t * 128 + e * 8, tc::sw128_mn_desc(v + e * 2048, Sh::kBlock),
-                           kOut, j > 0 || e > 0);
+            for (int e = 0; e < kTilePos / 16; e++)
+                tc::mma_f16_ta(tmem + 256 + t * DP, tmem + t * 128 + e * 8, v + e * (2048 >> 4), kOut, j > 0 || e > 0);
+        }
+        __syncwarp();
     };
-    auto ready = [&](int i) { return tc::mbar_wait(&b.full[i % Sh::kSlots], (i / Sh::kSlots) & 1, &b.aborted); };
-    if (!tc::mbar_wait(&b.q_full, 0, &b.aborted) || !ready(0))
+    auto commit = [&](uint64_t *bar) {
+        if (tc::elect_one())
+            tc::mma_commit(bar);
+        __syncwarp();
+    };
+    auto ready = [&](int i) { return warp_wait(&b.full[i % Sh::kSlots], (i / Sh::kSlots) & 1, &b.aborted); };
+    if (!warp_wait(&b.q_full, 0, &b.aborted) || !ready(0))
         return;
     tc::fence_after_sync();
     scores(0, 0);
     if (two)
         scores(1, 0);
-    tc::mma_commit(&b.empty[0]);
+    commit(&b.empty[0]);
     for (int j = 0; j < tiles; j++) {
         for (int t = 0; t < (two ? 2 : 1); t++) {
             if (t == 0 && !ready(2 * j + 1))
                 return;
-            if (!tc::mbar_wait(&b.p_ready[t], j & 1, &b.aborted))
+            if (!warp_wait(&b.p_ready[t], j & 1, &b.aborted))
                 return;
             tc::fence_after_sync();
             output(t, j);
             if (t == (two ? 1 : 0))
-                tc::mma_commit(&b.empty[(2 * j + 1) % Sh::kSlots]);
+                commit(&b.empty[(2 * j + 1) % Sh::kSlots]);
             if (j + 1 < tiles) {
                 if (t == 0 && !ready(2 * j + 2))
                     return;
                 scores(t, j + 1);
                 if (t == (two ? 1 : 0))
-                    tc::mma_commit(&b.empty[(2 * j + 2) % Sh::kSlots]);
+                    commit(&b.empty[(2 * j + 2) % Sh::kSlots]);
             } else {
-                tc::mma_commit(&b.o_full[t]);
+                commit(&b.o_full[t]);
             }
         }
     }
@@ -177,168 +290,188 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
 template <typename T, int DP>
 __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, TileBars &b, int tiles)
 {
-    const int t = threadIdx.x >> 7, tid = threadIdx.x & 127, r = t * 128 + tid;
-    const uint32_t lanes = b.tmem + ((uint32_t)(tid & ~31) << 16);
-    const uint32_t s_at = lanes + t * 128, o_at = lanes + 256 + t * DP;
+    constexpr int kHalf = kTilePos / 2, kCols = DP / 2;  // scores, output columns of a thread
+    const int warp = threadIdx.x >> 5, t = warp >> 3, half = (warp >> 2) & 1;
+    const int in = (warp & 3) * 32 + (threadIdx.x & 31), r = t * 128 + in, pair = 1 + t * 4 + (warp & 3);
+    const uint32_t lanes = b.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_at = lanes + t * 128 + half * kHalf, p_at = lanes + t * 128 + half * (kHalf / 2);
+    const uint32_t o_at = lanes + 256 + t * DP + half * kCols;
     const int row = w.row0 + r, token = row / p.group;
     const bool mine = r < w.rows;
     // a row past the last sees everything: it needs no mask, and nothing of it is written
     const int hi = mine ? min(seen_hi(w.seq, p.causal, token), w.hi) : 0x7fffffff;
-    const int lo = mine ? seen_lo(seen_hi(w.seq, p.causal, token), p.window) : 0;
+    const int lo = mine ? max(seen_lo(seen_hi(w.seq, p.causal, token), p.window), w.lo) : 0;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < tiles; j++) {
-        if (!tc::mbar_wait(&b.s_full[t], j & 1, &b.aborted))
-            return;
+        // a wait that runs out is seen at the end; the pair's barriers below want every warp
+        tc::mbar_wait(&b.s_full[t], j & 1, &b.aborted);
+        __syncwarp();
         tc::fence_after_sync();
-        uint32_t s[128];
-        const int at = w.lo + j * kTilePos;
-        const bool plain = __all_sync(0xffffffffu, at >= lo && at + kTilePos <= hi);
-        auto load = [&] {
+        uint32_t s[kHalf];
+        const int at = (w.lo & ~127) + j * kTilePos + half * kHalf;
+        tc::tmem_ld32_async(s_at, s);
+        tc::tmem_ld32_async(s_at + 32, s + 32);
+        tc::tmem_ld_wait(s);
+        tc::tmem_ld_wait(s + 32);
+        if (!__all_sync(0xffffffffu, at >= lo && at + kHalf <= hi)) {
 #pragma unroll
-            for (int c = 0; c < 4; c++)
-                tc::tmem_ld32_async(s_at + c * 32, s + c * 32);
-#pragma unroll
-            for (int c = 0; c < 4; c++)
-                tc::tmem_ld_wait(s + c * 32);
-            if (!plain) {
-#pragma unroll
-                for (int i = 0; i < kTilePos; i++)
-                    s[i] = at + i >= lo && at + i < hi ? s[i] : 0xff800000u;
-            }
-        };
-        load();
+            for (int i = 0; i < kHalf; i++)
+                s[i] = at + i >= lo && at + i < hi ? s[i] : 0xff800000u;
+        }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kTilePos; i++)
+        for (int i = 0; i < kHalf; i++)
             top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i]));
-        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+        float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+        b.agree[t][half][in] = now;
+        tc::named_sync(pair, 64);
+        now = fmaxf(now, b.agree[t][1 - half][in]);
         if (__any_sync(0xffffffffu, now > m + kTileSlack)) {
             // also from -infinity; the output of the tiles before is complete: the scores' MMA came after it
             const float next = fmaxf(m, now), f = next == -INFINITY ? 1.f : exp2_approx(m - next);
             m = next;
             l *= f;
             if (j > 0) {
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 16) {
+                    uint32_t o[16];
+                    tc::tmem_ld16(o_at + c, o);
 #pragma unroll
-                for (int c = 0; c < DP; c += 32) {
-                    float o[32];
-                    tc::tmem_ld32(o_at + c, o);
-#pragma unroll
-                    for (int i = 0; i < 32; i++)
-                        o[i] *= f;
-                    tc::tmem_st32(o_at + c, o);
+                    for (int i = 0; i < 16; i++)
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tc::tmem_st16(o_at + c, o);
                 }
-                load();  // the scores' registers held the output
             }
         }
         const float base = m == -INFINITY ? 0.f : m;
         const float2 scale = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-            float packed[32];
+        for (int c = 0; c < kHalf / 32; c++) {
+            uint32_t packed[16];
 #pragma unroll
-            for (int i = 0; i < 32; i++) {
-                const int k = c * 64 + 2 * i;
+            for (int i = 0; i < 16; i++) {
+                const int k = c * 32 + 2 * i;
                 const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale, off);
                 const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                 sum[i & 1] = __fadd2_rn(sum[i & 1], e);
-                packed[i] = __uint_as_float(pack2<T>(e.x, e.y));
+                packed[i] = pack2<T>(e.x, e.y);
             }
-            tc::tmem_st32(s_at + c * 32, packed);
+            tc::tmem_st16(p_at + c * 16, packed);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         tc::mbar_arrive(&b.p_ready[t]);
     }
+    tc::named_sync(pair, 64);  // the last maxima have been read
+    b.agree[t][half][in] = l;
+    tc::named_sync(pair, 64);
+    l = b.agree[t][0][in] + b.agree[t][1][in];
     float inv = 0.f, lse = -INFINITY;
     if (l > 0.f) {
         inv = 1.f / l;
         lse = m + log2f(l);
     }
     if (tiles > 0) {
-        if (!tc::mbar_wait(&b.o_full[t], 0, &b.aborted))
-            return;
+        tc::mbar_wait(&b.o_full[t], 0, &b.aborted);
+        __syncwarp();
         tc::fence_after_sync();
     }
     const int heads = p.cache.heads * p.group, h = w.head * p.group + row - token * p.group;
     const int64_t part = ((int64_t)w.split * p.batch.n + w.seq.first + token) * heads + h;
-    if (mine) {
+    if (mine && half == 0) {
         if (!w.whole)
             p.part_lse[part] = lse;
         else if (p.lse)
             p.lse[(w.seq.first + token) * heads + h] = lse * kLn2;
     }
 #pragma unroll
-    for (int c = 0; c < DP; c += 32) {
-        float o[32];
+    for (int c = 0; c < kCols; c += 16) {
+        uint32_t x[16];
+        float o[16];
         __syncwarp();
         if (tiles > 0)
-            tc::tmem_ld32(o_at + c, o);
+            tc::tmem_ld16(o_at + c, x);
 #pragma unroll
-        for (int i = 0; i < 32; i++)
-            o[i] = inv > 0.f ? o[i] * inv : 0.f;
+        for (int i = 0; i < 16; i++)
+            o[i] = inv > 0.f ? __uint_as_float(x[i]) * inv : 0.f;
+        const int e = half * kCols + c;
         if (mine && w.whole) {
-            T *out = p.out.row<T>(w.seq.first + token, h) + c;
+            T *out = p.out.row<T>(w.seq.first + token, h) + e;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-                if (c + i < p.d)
+            for (int i = 0; i < 16; i += 8)
+                if (e + i < p.d)
                     *reinterpret_cast<uint4 *>(out + i) =
                         make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]), pack2<T>(o[i + 4], o[i + 5]),
                                    pack2<T>(o[i + 6], o[i + 7]));
         } else if (mine) {
-            float *out = p.part_o + part * p.d + c;
+            float *out = p.part_o + part * p.d + e;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-                if (c + i < p.d)
+            for (int i = 0; i < 16; i += 4)
+                if (e + i < p.d)
                     *reinterpret_cast<float4 *>(out + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
     }
 }
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kTileThreads, 1)
-kv_attn_tile_kernel(const __grid_constant__ AttnParams p)
+template <typename T, int DP, bool kBulk>
+__global__ void __launch_bounds__(tile_threads(kBulk), 1)
+kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TileMaps maps)
 {
     using Sh = TileShape<DP>;
-    extern __shared__ uint8_t raw[];
-    __shared__ TileBars b;
-    uint8_t *sq = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023), *ring = sq + 2 * Sh::kTileBytes;
+    constexpr int kLast = tile_threads(kBulk) / 32 - 1;
+    extern __shared__ __align__(1024) uint8_t sq[];  // query tiles, the ring, then the rest: all that an SM has
+    uint8_t *ring = sq + 2 * Sh::kTileBytes;
+    TileBars &b = *reinterpret_cast<TileBars *>(sq + Sh::kTiles);
     const int warp = threadIdx.x >> 5;
     AttnWork w;
     if (!attn_work(p, blockIdx.x, w))
         return;
-    const int tiles = (w.hi - w.lo + kTilePos - 1) / kTilePos;  // 0: rows that see nothing
+    const int tiles = w.hi > w.lo ? (w.hi - (w.lo & ~127) + kTilePos - 1) / kTilePos : 0;  // 0: rows that see nothing
     const bool two = w.rows > 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kSlots; i++) {
-            tc::mbar_init(&b.full[i], kCopyThreads);
+            tc::mbar_init(&b.full[i], kBulk ? 1 : copy_threads(false));
             tc::mbar_init(&b.empty[i], 1);
         }
-        tc::mbar_init(&b.q_full, kCopyThreads);
+        tc::mbar_init(&b.q_full, copy_threads(kBulk));
         tc::mbar_init(&b.drained, 1);
+        tc::mbar_init(&b.landed, 1);
         for (int t = 0; t < 2; t++) {
             tc::mbar_init(&b.s_full[t], 1);
-            tc::mbar_init(&b.p_ready[t], 128);
+            tc::mbar_init(&b.p_ready[t], 256);
             tc::mbar_init(&b.o_full[t], 1);
         }
         b.aborted = 0;
         tc::mbar_init_fence();
     }
-    if (warp == 10)
+    if (warp == kLast)
         tc::tmem_alloc<512>(&b.tmem);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp < 8) {
-        if (warp < 4 || two)
+    if (warp < kSoftmaxThreads / 32) {
+        if (warp < 8 || two)
             tile_softmax<T, DP>(p, w, b, tiles);
-    } else if (warp < 10) {
-        if (tiles > 0)
-            tile_copy<T, DP>(p, w, sq, ring, b, tiles);
-    } else if ((threadIdx.x & 31) == 0 && tiles > 0) {
+    } else if (warp < kLast) {
+        if (tiles > 0) {
+            if constexpr (kBulk) {
+                tile_copy_bulk<T, DP>(p, w, maps, sq, ring, b, tiles);
+                if (*reinterpret_cast<volatile int *>(&b.aborted)) {  // no copy may be in flight at the end
+                    int never = 0;
+                    for (int i = 0; i < Sh::kSlots; i++)
+                        for (int parity = 0; parity < 2; parity++)
+                            tc::mbar_wait(&b.full[i], parity, &never);
+                }
+            } else {
+                tile_copy_rows<T, DP>(p, w, sq, ring, b, tiles);
+            }
+        }
+    } else if (tiles > 0) {
         tile_mma<T, DP>(sq, ring, b, tiles, two);
-        if (b.aborted) {  // no MMA may be in flight when the memory is given back
+        __syncwarp();
+        if (tc::elect_one() && *reinterpret_cast<volatile int *>(&b.aborted)) {  // no MMA may be in flight when the memory is given back
             int never = 0;
             tc::mma_commit(&b.drained);
             tc::mbar_wait(&b.drained, 0, &never);
@@ -349,27 +482,59 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p)
     tc::fence_after_sync();
     if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(&b.aborted))
         raise_flag(p.err, DLRM_FLAG_WAIT_TIMEOUT);
-    if (warp == 10)
+    if (warp == kLast)
         tc::tmem_free<512>(b.tmem);
 }
 
-template <typename T, int DP>
-static int launch_tile(const AttnParams &p, int64_t ctas, cudaStream_t st)
+// Maps of the cache; false where it cannot be described so.
+static bool tile_maps(const AttnParams &p, int dtype, TileMaps &m)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc || p.cache.page.d % 8 != 0)
+        return false;
+    m.rows = 8;
+    while (m.rows < kTilePos && p.cache.page.d % (2 * m.rows) == 0)
+        m.rows *= 2;
+    const CUtensorMapDataType type = dtype == DLRM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.d, p.cache.page.d, (cuuint64_t)p.cache.heads, p.cache.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.cache.slot_stride * 2, (cuuint64_t)p.cache.head_stride * 2,
+                                   (cuuint64_t)p.cache.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)m.rows, 1, 1}, one[4] = {1, 1, 1, 1};
+    for (int kv = 0; kv < 2; kv++)
+        if (enc(kv ? &m.v : &m.k, type, 4, kv ? p.cache.v : p.cache.k, dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
+template <typename T, int DP, bool kBulk>
+static int launch_tile(const AttnParams &p, const TileMaps &maps, int64_t ctas, cudaStream_t st)
 {
     static std::atomic<unsigned long long> done{0};
-    const int s = allow_dynamic_smem((const void *)kv_attn_tile_kernel<T, DP>, TileShape<DP>::kSmem, &done);
+    constexpr int smem = TileShape<DP>::kTiles + sizeof(TileBars);
+    const int s = allow_dynamic_smem((const void *)kv_attn_tile_kernel<T, DP, kBulk>, smem, &done);
     if (s != DLRM_OK)
         return s;
-    kv_attn_tile_kernel<T, DP><<<(unsigned)ctas, kTileThreads, TileShape<DP>::kSmem, st>>>(p);
+    kv_attn_tile_kernel<T, DP, kBulk><<<(unsigned)ctas, tile_threads(kBulk), smem, st>>>(p, maps);
     count_launch(st);
     return DLRM_OK;
 }
 
+template <typename T>
+static int launch_tile_width(const AttnParams &p, int dtype, int64_t ctas, cudaStream_t st)
+{
+    TileMaps maps = {};
+    const bool bulk = tile_maps(p, dtype, maps);
+    if (p.d <= 64)
+        return bulk ? launch_tile<T, 64, true>(p, maps, ctas, st) : launch_tile<T, 64, false>(p, maps, ctas, st);
+    return bulk ? launch_tile<T, 128, true>(p, maps, ctas, st) : launch_tile<T, 128, false>(p, maps, ctas, st);
+}
+
 int launch_kv_attn_tile(const AttnParams &p, int dtype, int64_t ctas, cudaStream_t st)
 {
-    if (dtype == DLRM_F16)
-        return p.d <= 64 ? launch_tile<__half, 64>(p, ctas, st) : launch_tile<__half, 128>(p, ctas, st);
-    return p.d <= 64 ? launch_tile<__nv_bfloat16, 64>(p, ctas, st) : launch_tile<__nv_bfloat16, 128>(p, ctas, st);
+    return dtype == DLRM_F16 ? launch_tile_width<__half>(p, dtype, ctas, st)
+                             : launch_tile_width<__nv_bfloat16>(p, dtype, ctas, st);
 }
 
 }  // namespace dlrm
