@@ -44,10 +44,13 @@ struct TileShape {
     static constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
 };
 
-// Keys and values as bulk tensor copies see them: (element, slot, head, page).
+// Bulk tensor copies: keys and values as (element, slot, head, page) in boxes
+// of `rows` slots; queries as (element, head, token) in boxes of one group's heads
+// and 128 / group tokens, where a group divides 128 (q_rows: else row by row).
 struct TileMaps {
-    CUtensorMap k, v;
-    int rows;  // of a box
+    CUtensorMap k, v, q;
+    int rows;
+    bool q_rows;
 };
 
 // A wait by a whole warp, whose lanes go on or give up together.
@@ -120,7 +123,16 @@ __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const Til
     int page, slot, next_page, next_slot;
     uint32_t patched = 0;  // value tiles mended so far, modulo 2
     find(0, lane, next_page, next_slot);
-    copy_queries<DP, 32>(p, w, sq);
+    if (maps.q_rows) {
+        copy_queries<DP, 32>(p, w, sq);
+    } else if (lane == 0) {
+        const int n = w.rows > 128 ? 2 : 1;
+        tc::mbar_expect_tx(&b.q_full, n * Sh::kTileBytes);
+        for (int t = 0; t < n; t++)
+            for (int c = 0; c < kColumns; c++)
+                tc::tma_load_3d(sq + t * Sh::kTileBytes + c * Sh::kBlock, &maps.q, c * 64, w.head * p.group,
+                                (int)w.seq.first + (w.row0 + t * 128) / p.group, &b.q_full);
+    }
     for (int j = 0; j < tiles; j++) {
         page = next_page;
         slot = next_slot;
@@ -146,10 +158,12 @@ __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const Til
                 for (int c = 0; c < kColumns; c++)
                     tc::tma_load_4d(tc::smem_u32(tile) + c * Sh::kBlock + lane * maps.rows * 128,
                                     kv ? &maps.v : &maps.k, c * 64, slot, w.head, page, bar);
-            if (i == 0) {  // the queries follow the first keys
+            if (i == 0 && maps.q_rows) {
                 tc::cp_async_wait_all();
                 tc::fence_async_smem();
-                tc::mbar_arrive(&b.q_full);
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&b.q_full);
             }
             if (mend) {
                 if (!warp_wait(&b.landed, patched & 1, &b.aborted))
@@ -228,6 +242,8 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
     constexpr uint32_t kScores = tc::f16_idesc(kType, 128, kTilePos, false), kOut = tc::f16_idesc(kType, 128, DP, true);
     // all lanes run this; one issues.  Descriptors of a later place are the first plus its distance / 16.
     const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
+    tiles = __shfl_sync(0xffffffffu, tiles, 0);  // known to be the warp's: the loop's values are uniform
+    two = __shfl_sync(0xffffffffu, two, 0);
     const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(sq)), k_desc = tc::sw128_desc(tc::smem_u32(ring));
     const uint64_t v_desc = tc::sw128_mn_desc(tc::smem_u32(ring), Sh::kBlock);
     auto scores = [&](int t, int j) {
@@ -320,8 +336,8 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, TileBars &b
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kHalf; i++)
-            top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i]));
+        for (int i = 0; i < kHalf; i += 2)
+            top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
         float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
         b.agree[t][half][in] = now;
         tc::named_sync(pair, 64);
@@ -362,7 +378,9 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, TileBars &b
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::tmem_st_wait();
         tc::fence_before_sync();
-        tc::mbar_arrive(&b.p_ready[t]);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            tc::mbar_arrive(&b.p_ready[t]);
     }
     tc::named_sync(pair, 64);  // the last maxima have been read
     b.agree[t][half][in] = l;
@@ -435,12 +453,12 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             tc::mbar_init(&b.full[i], kBulk ? 1 : copy_threads(false));
             tc::mbar_init(&b.empty[i], 1);
         }
-        tc::mbar_init(&b.q_full, copy_threads(kBulk));
+        tc::mbar_init(&b.q_full, kBulk ? 1 : copy_threads(false));
         tc::mbar_init(&b.drained, 1);
         tc::mbar_init(&b.landed, 1);
         for (int t = 0; t < 2; t++) {
             tc::mbar_init(&b.s_full[t], 1);
-            tc::mbar_init(&b.p_ready[t], 256);
+            tc::mbar_init(&b.p_ready[t], 8);  // the tile's warps
             tc::mbar_init(&b.o_full[t], 1);
         }
         b.aborted = 0;
@@ -460,9 +478,12 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 tile_copy_bulk<T, DP>(p, w, maps, sq, ring, b, tiles);
                 if (*reinterpret_cast<volatile int *>(&b.aborted)) {  // no copy may be in flight at the end
                     int never = 0;
-                    for (int i = 0; i < Sh::kSlots; i++)
-                        for (int parity = 0; parity < 2; parity++)
+                    for (int parity = 0; parity < 2; parity++) {
+                        for (int i = 0; i < Sh::kSlots; i++)
                             tc::mbar_wait(&b.full[i], parity, &never);
+                        tc::mbar_wait(&b.landed, parity, &never);
+                    }
+                    tc::mbar_wait(&b.q_full, 0, &never);
                 }
             } else {
                 tile_copy_rows<T, DP>(p, w, sq, ring, b, tiles);
@@ -496,15 +517,23 @@ static bool tile_maps(const AttnParams &p, int dtype, TileMaps &m)
     while (m.rows < kTilePos && p.cache.page.d % (2 * m.rows) == 0)
         m.rows *= 2;
     const CUtensorMapDataType type = dtype == DLRM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    auto encode = [&](CUtensorMap *map, int rank, void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+                      const cuuint32_t *box) {
+        const cuuint32_t one[4] = {1, 1, 1, 1};
+        return enc(map, type, rank, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
     const cuuint64_t dims[4] = {(cuuint64_t)p.d, p.cache.page.d, (cuuint64_t)p.cache.heads, p.cache.pages};
     const cuuint64_t strides[3] = {(cuuint64_t)p.cache.slot_stride * 2, (cuuint64_t)p.cache.head_stride * 2,
                                    (cuuint64_t)p.cache.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)m.rows, 1, 1}, one[4] = {1, 1, 1, 1};
-    for (int kv = 0; kv < 2; kv++)
-        if (enc(kv ? &m.v : &m.k, type, 4, kv ? p.cache.v : p.cache.k, dims, strides, box, one,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return false;
+    const cuuint32_t box[4] = {64, (cuuint32_t)m.rows, 1, 1};
+    if (!encode(&m.k, 4, p.cache.k, dims, strides, box) || !encode(&m.v, 4, p.cache.v, dims, strides, box))
+        return false;
+    const cuuint64_t q_dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.q.heads, (cuuint64_t)p.batch.n};
+    const cuuint64_t q_strides[2] = {(cuuint64_t)p.q.hs * 2, (cuuint64_t)p.q.ts * 2};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(128 / (p.group <= 128 ? p.group : 128))};
+    m.q_rows = p.group > 128 || 128 % p.group != 0 || !encode(&m.q, 3, p.q.ptr, q_dims, q_strides, q_box);
     return true;
 }
 
