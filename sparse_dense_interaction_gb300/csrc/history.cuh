@@ -152,7 +152,12 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // The attention's launch: which kernel, rows (token, head of a group) of a
 // tile, and how the positions are split.
 enum AttnKernel { kAttnGeneral, kAttnTile };
-constexpr int kTileRows = 256;
+
+// Rows of the tensor-core tiles: two query tiles of 128 on an SM of their own;
+// with heads of 64 and at most 256 rows in all (the candidates of a user) one, and two CTAs on an SM, so that
+// one starts and ends while the other computes.
+inline int tile_rows(int64_t rows, int d) { return d <= 64 && rows <= 256 ? 128 : 256; }
+
 struct AttnPlan {
     AttnKernel kernel;
     int rows;        // rows of a tile
@@ -202,19 +207,23 @@ __device__ __forceinline__ int split_base(const Sequence &q, bool causal, int wi
     return seen_lo(seen_hi(q, causal, token), window) & ~127;
 }
 
-// Decodes the CTA's number (head fastest, then split, then tile, then
-// sequence); false where there is nothing to do.
-__device__ __forceinline__ bool attn_work(const AttnParams &p, int64_t cta, AttnWork &w)
+// The CTA's number: head fastest, then split, then tile, then sequence (or its
+// rank); returns the last, sets the head and the split.
+__device__ __forceinline__ int64_t attn_number(const AttnParams &p, int64_t cta, AttnWork &w, int64_t &tile)
 {
     const int hk = p.cache.heads;
     w.head = (int)(cta % hk);
     cta /= hk;
     w.split = (int)(cta % p.splits);
     cta /= p.splits;
-    const int64_t tile = p.tiles - 1 - cta % p.tiles;  // the longest rows of a causal chunk first
-    w.s = cta / p.tiles;
-    if (!read_sequence(p.batch, w.s, p.max_new, p.max_len, w.seq, p.err))
-        return false;
+    tile = p.tiles - 1 - cta % p.tiles;  // the longest rows of a causal chunk first
+    return cta / p.tiles;
+}
+
+// The rows and positions of a tile of the sequence w.seq; false where there is
+// nothing to do.
+__device__ __forceinline__ bool attn_rows(const AttnParams &p, int64_t tile, AttnWork &w)
+{
     const int64_t row0 = tile * p.rows, all = (int64_t)w.seq.count * p.group;
     if (row0 >= all)
         return false;
@@ -230,6 +239,13 @@ __device__ __forceinline__ bool attn_work(const AttnParams &p, int64_t cta, Attn
     w.lo = from > lo ? (int)from : lo;
     w.hi = to < hi ? (int)to : hi;
     return true;
+}
+
+__device__ __forceinline__ bool attn_work(const AttnParams &p, int64_t cta, AttnWork &w)
+{
+    int64_t tile;
+    w.s = attn_number(p, cta, w, tile);
+    return read_sequence(p.batch, w.s, p.max_new, p.max_len, w.seq, p.err) && attn_rows(p, tile, w);
 }
 
 // Byte offset of a position's slot row in the cache (head's own offset

@@ -223,26 +223,28 @@ static AttnPlan plan_splits(AttnKernel kernel, int rows, int64_t S, int kv_heads
     return a;
 }
 
-// Full tiles run one CTA on an SM: the number of splits that ends soonest, each
+// The number of splits that ends soonest, each
 // CTA costing as much as 512 positions beside its share (its start, its end and the join).
-static AttnPlan plan_tile(int64_t S, int kv_heads, int group, int64_t max_new, int64_t max_len)
+static AttnPlan plan_tile(int64_t S, int kv_heads, int group, int d, int64_t max_new, int64_t max_len)
 {
-    const int64_t have = S * kv_heads * ceil_div(max_new * group, kTileRows), longest = max_len + 127;
+    const int rows = tile_rows(max_new * group, d);
+    const int64_t have = S * kv_heads * ceil_div(max_new * group, rows), longest = max_len + 127;
+    const int64_t places = rows == 128 ? 2 * kPlanSms : kPlanSms;
     int64_t best = 1, least = INT64_MAX;
-    for (int64_t s = 1; s <= 64 && (s == 1 || have * s <= 2 * kPlanSms); s++) {
-        const int64_t cost = ceil_div(have * s, kPlanSms) * (ceil_div(longest, s) + 512);
+    for (int64_t s = 1; s <= 64 && (s == 1 || have * s <= 2 * places); s++) {
+        const int64_t cost = ceil_div(have * s, places) * (ceil_div(longest, s) + 512);
         if (cost < least) {
             least = cost;
             best = s;
         }
     }
-    return plan_splits(kAttnTile, kTileRows, S, kv_heads, group, max_new, max_len, have * best, 512);
+    return plan_splits(kAttnTile, rows, S, kv_heads, group, max_new, max_len, have * best, 512);
 }
 
-static AttnPlan plan(AttnKernel kernel, int64_t S, int kv_heads, int group, int64_t max_new, int64_t max_len)
+static AttnPlan plan(AttnKernel kernel, int64_t S, int kv_heads, int group, int d, int64_t max_new, int64_t max_len)
 {
     if (kernel == kAttnTile)
-        return plan_tile(S, kv_heads, group, max_new, max_len);
+        return plan_tile(S, kv_heads, group, d, max_new, max_len);
     return plan_splits(kAttnGeneral, kGenRows, S, kv_heads, group, max_new, max_len, kPlanSms * 8, 256);
 }
 
@@ -258,7 +260,7 @@ size_t attn_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, in
     max_new = max_new < n ? max_new : n;
     size_t most = few_workspace(max_new * group, d, max_len);
     for (AttnKernel k : {kAttnGeneral, kAttnTile}) {
-        const size_t b = part_floats(plan(k, S, kv_heads, group, max_new, max_len), n, q_heads, d) * sizeof(float);
+        const size_t b = part_floats(plan(k, S, kv_heads, group, d, max_new, max_len), n, q_heads, d) * sizeof(float);
         most = b > most ? b : most;
     }
     return most + 16;
@@ -309,7 +311,8 @@ int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     const bool cores = wide_rows(p, dtype);
     if (cores && (dtype == DLRM_F32 || p.max_new * p.group <= 16))
         return launch_kv_attn_few(p, dtype, workspace, st);
-    const AttnPlan a = plan(cores ? kAttnTile : kAttnGeneral, p.batch.S, p.cache.heads, p.group, p.max_new, p.max_len);
+    const AttnPlan a = plan(cores ? kAttnTile : kAttnGeneral, p.batch.S, p.cache.heads, p.group, p.d, p.max_new,
+                            p.max_len);
     p.rows = a.rows;
     p.tiles = a.tiles;
     p.split_len = a.split_len;

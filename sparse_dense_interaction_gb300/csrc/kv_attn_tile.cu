@@ -3,7 +3,7 @@
 //
 // A CTA holds two query tiles of 128 packed rows and walks the positions in
 // tiles of 128.  Warp roles:
-//  - warp 16 copies keys and values into a ring of tiles in the 128-byte swizzle,
+//  - the warp after the softmax's copies keys and values into a ring of tiles in the 128-byte swizzle,
 //    by bulk tensor copies through the page table where pages are multiples of
 //    8 slots, in boxes of the largest power of two up to 128 that divides a page; the rows of
 //    a value tile that no query sees may hold anything, so it overwrites
@@ -12,7 +12,7 @@
 //    without reading them;
 //  - one thread of the last warp issues the MMAs: S = Q K^T (both operands in
 //    shared memory, K-major) and O += P V (P in tensor memory, V MN-major as it lies);
-//  - warps 0-7 and 8-15 are the softmax of one query tile each: a thread owns half
+//  - the first 8 warps for each query tile are its softmax: a thread owns half
 //    of a row's 128 scores, agrees on the row's maximum with the thread that owns the
 //    other half, and writes the weights over the scores, in 16 bits.
 // The two tiles take turns: while one's scores are exponentiated the other's
@@ -29,17 +29,21 @@
 namespace dlrm {
 
 // With one thread to a row (8 softmax warps) the long chunks take 354 us instead of 342.
-constexpr int kTilePos = 128, kSoftmaxThreads = 512;
+constexpr int kTilePos = 128;
 __host__ __device__ constexpr int copy_threads(bool bulk) { return bulk ? 32 : 64; }
-__host__ __device__ constexpr int tile_threads(bool bulk) { return kSoftmaxThreads + copy_threads(bulk) + 32; }
 constexpr int kTileLag = 3;         // copied tiles that may be in flight before one is waited for
 constexpr float kTileSlack = 8.f;   // log2 of the growth of a maximum that is let pass
 
-template <int DP>
+// kTwo: two query tiles of a CTA that has the SM, else one, and two CTAs share the SM.
+template <int DP, bool kTwo>
 struct TileShape {
+    static constexpr int kRows = kTwo ? 256 : 128;
+    static constexpr int kSoftmaxThreads = 2 * kRows, kSoftmaxWarps = kSoftmaxThreads / 32;
+    static constexpr int kScoreCols = kRows, kTmem = 2 * kRows;  // tensor-memory columns: scores, all
+    __host__ __device__ static constexpr int threads(bool bulk) { return kSoftmaxThreads + copy_threads(bulk) + 32; }
     static constexpr int kTileBytes = kTilePos * DP * 2;  // of keys or values; a query tile too
-    static constexpr int kSlots = DP == 128 ? 5 : 8;
-    static constexpr int kTiles = 2 * kTileBytes + kSlots * kTileBytes;
+    static constexpr int kSlots = DP == 128 || !kTwo ? 5 : 8;
+    static constexpr int kTiles = kRows / 128 * kTileBytes + kSlots * kTileBytes;
     static constexpr int kBlock = kTilePos * 128;         // bytes between 64-column blocks of a tile
     static constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
 };
@@ -68,44 +72,44 @@ struct TileBars {
 
 // Copies 32 rows (this warp's) of a tile: lane t of the warp knows row t's
 // byte offset from `base`, -1 for a row of zeros.
-template <int DP>
+template <typename Sh>
 __device__ __forceinline__ void copy_rows(uint8_t *tile, const char *base, int64_t mine, int row0, int d)
 {
-    constexpr int C = TileShape<DP>::kChunks, kRows = 32 / C;  // rows of a step
+    constexpr int C = Sh::kChunks, kRows = 32 / C;  // rows of a step
     const int lane = threadIdx.x & 31, c = lane % C;
 #pragma unroll
     for (int i = 0; i < C; i++) {
         const int r = i * kRows + lane / C;
         const int64_t o = __shfl_sync(0xffffffffu, mine, r);
         const bool ok = o >= 0 && c * 8 < d;
-        tc::cp_async16(tile + (c >> 3) * TileShape<DP>::kBlock + (row0 + r) * 128 + (((c & 7) ^ (r & 7)) << 4),
+        tc::cp_async16(tile + (c >> 3) * Sh::kBlock + (row0 + r) * 128 + (((c & 7) ^ (r & 7)) << 4),
                        base + (ok ? o + c * 16 : 0), ok);
     }
 }
 
 // Copies the queries' rows (rows of zeros past the last).
-template <int DP, int kThreads>
+template <typename Sh, int kThreads>
 __device__ __forceinline__ void copy_queries(const AttnParams &p, const AttnWork &w, uint8_t *sq)
 {
-    const int tid = threadIdx.x - kSoftmaxThreads, row0 = tid & ~31;
+    const int tid = threadIdx.x - Sh::kSoftmaxThreads, row0 = tid & ~31;
 #pragma unroll 1
-    for (int r0 = 0; r0 < kTileRows; r0 += kThreads) {
+    for (int r0 = 0; r0 < Sh::kRows; r0 += kThreads) {
         const int r = r0 + tid, row = w.row0 + r, token = row / p.group;
         const int64_t o = r < w.rows ? ((w.seq.first + token) * p.q.ts +
                                         (int64_t)(w.head * p.group + row - token * p.group) * p.q.hs) * 2
                                      : -1;
-        copy_rows<DP>(sq + (r0 >> 7) * TileShape<DP>::kTileBytes, p.q.ptr, o, (r0 & 127) + row0, p.d);
+        copy_rows<Sh>(sq + (r0 >> 7) * Sh::kTileBytes, p.q.ptr, o, (r0 & 127) + row0, p.d);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 // The copy warp, by bulk tensor copies.  A tile begins at a multiple of 128
 // positions; lane i copies box i % boxes of the tile, if there are as many.
-template <typename T, int DP>
+template <typename T, int DP, bool kTwo>
 __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const TileMaps &maps, uint8_t *sq,
                                uint8_t *ring, TileBars &b, int tiles)
 {
-    using Sh = TileShape<DP>;
+    using Sh = TileShape<DP, kTwo>;
     constexpr int kColumns = DP / 64;
     const int lane = threadIdx.x & 31, start = w.lo & ~127, parts = kTilePos / maps.rows;
     const int32_t *pages = p.batch.table + w.s * p.batch.table_stride;
@@ -124,7 +128,7 @@ __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const Til
     uint32_t patched = 0;  // value tiles mended so far, modulo 2
     find(0, lane, next_page, next_slot);
     if (maps.q_rows) {
-        copy_queries<DP, 32>(p, w, sq);
+        copy_queries<Sh, 32>(p, w, sq);
     } else if (lane == 0) {
         const int n = w.rows > 128 ? 2 : 1;
         tc::mbar_expect_tx(&b.q_full, n * Sh::kTileBytes);
@@ -184,13 +188,13 @@ __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const Til
 }
 
 // The copy warps, row by row.
-template <typename T, int DP>
+template <typename T, int DP, bool kTwo>
 __device__ void tile_copy_rows(const AttnParams &p, const AttnWork &w, uint8_t *sq, uint8_t *ring, TileBars &b,
                                int tiles)
 {
-    using Sh = TileShape<DP>;
-    const int tid = threadIdx.x - kSoftmaxThreads, row0 = tid & ~31, start = w.lo & ~127;
-    copy_queries<DP, 64>(p, w, sq);
+    using Sh = TileShape<DP, kTwo>;
+    const int tid = threadIdx.x - Sh::kSoftmaxThreads, row0 = tid & ~31, start = w.lo & ~127;
+    copy_queries<Sh, 64>(p, w, sq);
     const int32_t *pages = p.batch.table + w.s * p.batch.table_stride;
     auto place = [&](int j, int half) -> int64_t {
         const int at = start + j * kTilePos + half * 64 + tid;
@@ -212,8 +216,8 @@ __device__ void tile_copy_rows(const AttnParams &p, const AttnWork &w, uint8_t *
             const int i = 2 * j + kv, slot = i % Sh::kSlots;
             if (i >= Sh::kSlots && !tc::mbar_wait(&b.empty[slot], (i / Sh::kSlots - 1) & 1, &b.aborted))
                 return tc::cp_async_wait_all();
-            copy_rows<DP>(ring + slot * Sh::kTileBytes, kv ? p.cache.v : p.cache.k, mine0, row0, p.d);
-            copy_rows<DP>(ring + slot * Sh::kTileBytes, kv ? p.cache.v : p.cache.k, mine1, 64 + row0, p.d);
+            copy_rows<Sh>(ring + slot * Sh::kTileBytes, kv ? p.cache.v : p.cache.k, mine0, row0, p.d);
+            copy_rows<Sh>(ring + slot * Sh::kTileBytes, kv ? p.cache.v : p.cache.k, mine1, 64 + row0, p.d);
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (i == 1) {  // the queries and the first keys are wanted at once
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -234,10 +238,10 @@ __device__ void tile_copy_rows(const AttnParams &p, const AttnWork &w, uint8_t *
         tc::mbar_arrive(&b.full[done++ % Sh::kSlots]);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kTwo>
 __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, bool two)
 {
-    using Sh = TileShape<DP>;
+    using Sh = TileShape<DP, kTwo>;
     constexpr int kType = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
     constexpr uint32_t kScores = tc::f16_idesc(kType, 128, kTilePos, false), kOut = tc::f16_idesc(kType, 128, DP, true);
     // all lanes run this; one issues.  Descriptors of a later place are the first plus its distance / 16.
@@ -263,7 +267,7 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
         if (tc::elect_one()) {
 #pragma unroll
             for (int e = 0; e < kTilePos / 16; e++)
-                tc::mma_f16_ta(tmem + 256 + t * DP, tmem + t * 128 + e * 8, v + e * (2048 >> 4), kOut, j > 0 || e > 0);
+                tc::mma_f16_ta(tmem + Sh::kScoreCols + t * DP, tmem + t * 128 + e * 8, v + e * (2048 >> 4), kOut, j > 0 || e > 0);
         }
         __syncwarp();
     };
@@ -303,15 +307,16 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
     }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kTwo>
 __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, TileBars &b, int tiles)
 {
+    using Sh = TileShape<DP, kTwo>;
     constexpr int kHalf = kTilePos / 2, kCols = DP / 2;  // scores, output columns of a thread
     const int warp = threadIdx.x >> 5, t = warp >> 3, half = (warp >> 2) & 1;
     const int in = (warp & 3) * 32 + (threadIdx.x & 31), r = t * 128 + in, pair = 1 + t * 4 + (warp & 3);
     const uint32_t lanes = b.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lanes + t * 128 + half * kHalf, p_at = lanes + t * 128 + half * (kHalf / 2);
-    const uint32_t o_at = lanes + 256 + t * DP + half * kCols;
+    const uint32_t o_at = lanes + Sh::kScoreCols + t * DP + half * kCols;
     const int row = w.row0 + r, token = row / p.group;
     const bool mine = r < w.rows;
     // a row past the last sees everything: it needs no mask, and nothing of it is written
@@ -433,21 +438,69 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, TileBars &b
     }
 }
 
-template <typename T, int DP, bool kBulk>
-__global__ void __launch_bounds__(tile_threads(kBulk), 1)
+// The CTA's work.  In batches of up to kRanked sequences the longest come
+// first, so that the last to start are the shortest: every CTA ranks the lengths
+// (64 users with up to 200 candidates: 63 us in the
+// batch's order, 55 ranked).  `room`: shared
+// memory for kRanked lengths and one sequence.
+constexpr int kRanked = 256;
+
+__device__ bool tile_work(const AttnParams &p, int *room, AttnWork &w)
+{
+    if (p.batch.S > kRanked)
+        return attn_work(p, blockIdx.x, w);
+    int64_t tile;
+    const int64_t rank = attn_number(p, blockIdx.x, w, tile);
+    const int t = threadIdx.x, S = (int)p.batch.S, padded = (S + 3) & ~3;
+    int *found = room + kRanked;  // sequence, first new token, new tokens, stored tokens
+    Sequence seq = {0, 0, 0};
+    int key = -1;  // of a sequence without work, and past the last
+    if (t < S && read_sequence(p.batch, t, p.max_new, p.max_len, seq, blockIdx.x == 0 ? p.err : nullptr) &&
+        seq.count > 0)
+        key = seq.length;
+    if (t < padded)
+        room[t] = key;
+    if (t == 0)
+        found[2] = 0;
+    __syncthreads();
+    if (key >= 0) {
+        int before = 0;
+        for (int i = 0; i < padded; i += 4) {
+            const int4 other = *reinterpret_cast<const int4 *>(room + i);
+            before += (other.x > key || (other.x == key && i < t)) + (other.y > key || (other.y == key && i + 1 < t)) +
+                      (other.z > key || (other.z == key && i + 2 < t)) + (other.w > key || (other.w == key && i + 3 < t));
+        }
+        if (before == rank) {
+            found[0] = t;
+            found[1] = (int)seq.first;
+            found[2] = seq.count;
+            found[3] = seq.length;
+        }
+    }
+    __syncthreads();
+    w.s = found[0];
+    w.seq.first = found[1];
+    w.seq.count = found[2];
+    w.seq.length = found[3];
+    tc::fence_async_smem();  // the room is overwritten by bulk copies, after the barrier that follows
+    return w.seq.count > 0 && attn_rows(p, tile, w);
+}
+
+template <typename T, int DP, bool kBulk, bool kTwo>
+__global__ void __launch_bounds__(TileShape<DP, kTwo>::threads(kBulk), kTwo ? 1 : 2)
 kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TileMaps maps)
 {
-    using Sh = TileShape<DP>;
-    constexpr int kLast = tile_threads(kBulk) / 32 - 1;
+    using Sh = TileShape<DP, kTwo>;
+    constexpr int kLast = Sh::threads(kBulk) / 32 - 1;
     extern __shared__ __align__(1024) uint8_t sq[];  // query tiles, the ring, then the rest: all that an SM has
-    uint8_t *ring = sq + 2 * Sh::kTileBytes;
+    uint8_t *ring = sq + Sh::kRows / 128 * Sh::kTileBytes;
     TileBars &b = *reinterpret_cast<TileBars *>(sq + Sh::kTiles);
     const int warp = threadIdx.x >> 5;
     AttnWork w;
-    if (!attn_work(p, blockIdx.x, w))
+    if (!tile_work(p, reinterpret_cast<int *>(sq), w))
         return;
     const int tiles = w.hi > w.lo ? (w.hi - (w.lo & ~127) + kTilePos - 1) / kTilePos : 0;  // 0: rows that see nothing
-    const bool two = w.rows > 128;
+    const bool two = kTwo && w.rows > 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kSlots; i++) {
             tc::mbar_init(&b.full[i], kBulk ? 1 : copy_threads(false));
@@ -465,17 +518,17 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         tc::mbar_init_fence();
     }
     if (warp == kLast)
-        tc::tmem_alloc<512>(&b.tmem);
+        tc::tmem_alloc<Sh::kTmem>(&b.tmem);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp < kSoftmaxThreads / 32) {
+    if (warp < Sh::kSoftmaxWarps) {
         if (warp < 8 || two)
-            tile_softmax<T, DP>(p, w, b, tiles);
+            tile_softmax<T, DP, kTwo>(p, w, b, tiles);
     } else if (warp < kLast) {
         if (tiles > 0) {
             if constexpr (kBulk) {
-                tile_copy_bulk<T, DP>(p, w, maps, sq, ring, b, tiles);
+                tile_copy_bulk<T, DP, kTwo>(p, w, maps, sq, ring, b, tiles);
                 if (*reinterpret_cast<volatile int *>(&b.aborted)) {  // no copy may be in flight at the end
                     int never = 0;
                     for (int parity = 0; parity < 2; parity++) {
@@ -486,11 +539,11 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     tc::mbar_wait(&b.q_full, 0, &never);
                 }
             } else {
-                tile_copy_rows<T, DP>(p, w, sq, ring, b, tiles);
+                tile_copy_rows<T, DP, kTwo>(p, w, sq, ring, b, tiles);
             }
         }
     } else if (tiles > 0) {
-        tile_mma<T, DP>(sq, ring, b, tiles, two);
+        tile_mma<T, DP, kTwo>(sq, ring, b, tiles, two);
         __syncwarp();
         if (tc::elect_one() && *reinterpret_cast<volatile int *>(&b.aborted)) {  // no MMA may be in flight when the memory is given back
             int never = 0;
@@ -504,7 +557,7 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(&b.aborted))
         raise_flag(p.err, DLRM_FLAG_WAIT_TIMEOUT);
     if (warp == kLast)
-        tc::tmem_free<512>(b.tmem);
+        tc::tmem_free<Sh::kTmem>(b.tmem);
 }
 
 // Maps of the cache; false where it cannot be described so.
@@ -537,33 +590,41 @@ static bool tile_maps(const AttnParams &p, int dtype, TileMaps &m)
     return true;
 }
 
-template <typename T, int DP, bool kBulk>
+template <typename T, int DP, bool kBulk, bool kTwo>
 static int launch_tile(const AttnParams &p, const TileMaps &maps, int64_t ctas, cudaStream_t st)
 {
+    using Sh = TileShape<DP, kTwo>;
+    constexpr int smem = Sh::kTiles + sizeof(TileBars);
     static std::atomic<unsigned long long> done{0};
-    constexpr int smem = TileShape<DP>::kTiles + sizeof(TileBars);
-    const int s = allow_dynamic_smem((const void *)kv_attn_tile_kernel<T, DP, kBulk>, smem, &done);
+    const int s = allow_dynamic_smem((const void *)kv_attn_tile_kernel<T, DP, kBulk, kTwo>, smem, &done);
     if (s != DLRM_OK)
         return s;
-    kv_attn_tile_kernel<T, DP, kBulk><<<(unsigned)ctas, tile_threads(kBulk), smem, st>>>(p, maps);
+    kv_attn_tile_kernel<T, DP, kBulk, kTwo><<<(unsigned)ctas, Sh::threads(kBulk), smem, st>>>(p, maps);
     count_launch(st);
     return DLRM_OK;
 }
 
+template <typename T, bool kBulk>
+static int launch_tile_shape(const AttnParams &p, const TileMaps &maps, int64_t ctas, cudaStream_t st)
+{
+    if (p.d > 64)
+        return launch_tile<T, 128, kBulk, true>(p, maps, ctas, st);
+    return p.rows > 128 ? launch_tile<T, 64, kBulk, true>(p, maps, ctas, st)
+                        : launch_tile<T, 64, kBulk, false>(p, maps, ctas, st);
+}
+
 template <typename T>
-static int launch_tile_width(const AttnParams &p, int dtype, int64_t ctas, cudaStream_t st)
+static int launch_tile_type(const AttnParams &p, int dtype, int64_t ctas, cudaStream_t st)
 {
     TileMaps maps = {};
-    const bool bulk = tile_maps(p, dtype, maps);
-    if (p.d <= 64)
-        return bulk ? launch_tile<T, 64, true>(p, maps, ctas, st) : launch_tile<T, 64, false>(p, maps, ctas, st);
-    return bulk ? launch_tile<T, 128, true>(p, maps, ctas, st) : launch_tile<T, 128, false>(p, maps, ctas, st);
+    return tile_maps(p, dtype, maps) ? launch_tile_shape<T, true>(p, maps, ctas, st)
+                                     : launch_tile_shape<T, false>(p, maps, ctas, st);
 }
 
 int launch_kv_attn_tile(const AttnParams &p, int dtype, int64_t ctas, cudaStream_t st)
 {
-    return dtype == DLRM_F16 ? launch_tile_width<__half>(p, dtype, ctas, st)
-                             : launch_tile_width<__nv_bfloat16>(p, dtype, ctas, st);
+    return dtype == DLRM_F16 ? launch_tile_type<__half>(p, dtype, ctas, st)
+                             : launch_tile_type<__nv_bfloat16>(p, dtype, ctas, st);
 }
 
 }  // namespace dlrm
