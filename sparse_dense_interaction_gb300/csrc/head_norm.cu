@@ -230,7 +230,7 @@ kv_append_rows_kernel(HeadsView k, HeadsView v, BatchView batch, CacheView cache
         const int64_t s = find_sequence(batch, token);
         Sequence seq;
         if (s < 0 || !read_sequence(batch, s, batch.n, batch.capacity, seq, err) ||
-            token >= seq.first + seq.count || seq.count > seq.length) {
+            !seq.has(token) || seq.count > seq.length) {
             raise_flag(err, DLRM_FLAG_BAD_OFFSETS);
             continue;
         }

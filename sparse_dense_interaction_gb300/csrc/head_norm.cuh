@@ -302,12 +302,15 @@ static inline bool rope_pieces_ok(const RopeView &r)
 
 static inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tokens of a warp, such that the CTAs fill the GPU (152 SMs of `resident`
-// CTAs) at most `waves` times over: the last of them ends with the others.
-static inline int64_t run_tokens(int64_t n, int64_t chunks, int64_t resident, int64_t waves)
+// Tokens of a warp: as many as make one wave of CTAs (152 SMs of `resident`), so
+// that a CTA's start and end are paid for once, or as few waves as keep them
+// at `most`.
+static inline int64_t run_tokens(int64_t n, int64_t chunks, int64_t resident, int64_t most)
 {
-    const int64_t run = div_up(n * chunks, kWarps * 152 * resident * waves);
-    return run < 1 ? 1 : (run < kMaxRun ? run : kMaxRun);
+    const int64_t places = kWarps * 152 * resident, work = n * chunks;
+    const int64_t waves = div_up(div_up(work, places), most);
+    const int64_t run = div_up(work, places * (waves < 1 ? 1 : waves));
+    return run < 1 ? 1 : run;
 }
 
 // f<T, GL, interleaved>(...) of the call's type, width and layout.

@@ -11,8 +11,9 @@
 
 namespace dlrm {
 
-// CTAs of an SM and times that they fill it: 3 CTAs take 231 us, 2 in two waves 198.
-constexpr int kBwdResident = 2, kBwdWaves = 4;
+// CTAs of an SM: 3 take 231 us, 2 take 191.  Tokens of a warp at most: 21 in four
+// waves take 191 us, 41 in two 198.
+constexpr int kBwdResident = 2, kBwdRun = 24;
 
 struct NormBwdParams {
     NormSide side[2];
@@ -172,7 +173,7 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
     }
 }
 
-static int64_t bwd_run(int64_t n, int64_t chunks) { return run_tokens(n, chunks, kBwdResident, kBwdWaves); }
+static int64_t bwd_run(int64_t n, int64_t chunks) { return run_tokens(n, chunks, kBwdResident, kBwdRun); }
 
 size_t norm_bwd_vec_workspace(int64_t n, int qh, int kh, int d)
 {

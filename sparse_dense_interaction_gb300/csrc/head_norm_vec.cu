@@ -10,10 +10,10 @@
 
 namespace dlrm {
 
-// CTAs of an SM and times that they fill it: with 4 CTAs the forward above takes
-// 133 us (more rows of memory open at once), with 2 it takes 130; one wave
-// ends unevenly (130 us), four start too often (119).
-constexpr int kResident = 3, kWaves = 2;
+// CTAs of an SM: with 4 the forward above takes 133 us (more rows of memory
+// open at once), with 2 it takes 130.  Tokens of a warp at most: 27 in two waves
+// take 116 us, 54 in one (which ends unevenly) 130.
+constexpr int kResident = 3, kRun = kMaxRun;
 
 struct NormParams {
     NormSide side[3];  // queries, keys, values; out: not of keys and values that go to the cache
@@ -25,20 +25,26 @@ struct NormParams {
     int32_t *err;
 };
 
-// The sequence of token i: by the warp for its first token; for the others by
-// each lane, between that sequence and the last.
-__device__ __forceinline__ int64_t lane_sequence(const BatchView &b, int64_t first, int64_t i)
+// The sequences of up to 32 neighbouring tokens, lane l's token being first + l
+// and s0 the first's: the 32 sequence starts after s0 are read at once; beyond
+// them (many sequences without tokens) a lane searches.  All lanes call it.
+__device__ __forceinline__ int64_t lane_sequence(const BatchView &b, int64_t s0, int64_t i)
 {
-    int64_t lo = first, hi = b.S;  // offsets[lo] <= i < offsets[hi]
-    if (lo + 1 < hi && b.offsets[lo + 1] > i)
-        hi = lo + 1;
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (b.offsets[mid] <= i)
-            lo = mid;
-        else
-            hi = mid;
-    }
+    const int64_t next = s0 + 1 + (threadIdx.x & 31);
+    const int64_t start = next <= b.S ? b.offsets[next] : INT64_MAX;
+    int count = 0;
+#pragma unroll 8
+    for (int j = 0; j < 32; j++)
+        count += __shfl_sync(0xffffffffu, start, j) <= i;
+    int64_t lo = min(s0 + count, b.S - 1), hi = b.S;
+    if (count == 32)
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (b.offsets[mid] <= i)
+                lo = mid;
+            else
+                hi = mid;
+        }
     return lo;
 }
 
@@ -68,21 +74,19 @@ norm_rope_vec_kernel(const __grid_constant__ NormParams p)
     const float *my_angles = nullptr;
     int64_t my_to = 0;
     const int64_t my_token = first + lane;
-    int64_t s0 = -1;
-    if (kAppend && tokens > 0)
+    int64_t s0 = -1, s = 0;
+    if (kAppend && tokens > 0) {
         s0 = find_sequence(p.batch, first);
+        if (s0 >= 0)
+            s = lane_sequence(p.batch, s0, my_token);
+    }
     if (lane < tokens) {
         int64_t position = -1;
         bool good = true;
         Sequence seq = {0, 0, 0};
-        int64_t s = 0;
         if (kAppend) {
-            good = s0 >= 0;
-            if (good) {
-                s = lane_sequence(p.batch, s0, my_token);
-                good = read_sequence(p.batch, s, p.batch.n, p.batch.capacity, seq, p.err) &&
-                       my_token < seq.first + seq.count && seq.count <= seq.length;
-            }
+            good = s0 >= 0 && read_sequence(p.batch, s, p.batch.n, p.batch.capacity, seq, p.err) &&
+                   seq.has(my_token) && seq.count <= seq.length;
             position = seq.length - seq.count + my_token - seq.first;
             if (!good)
                 raise_flag(p.err, DLRM_FLAG_BAD_OFFSETS);
@@ -181,7 +185,7 @@ static int norm_launch(NormParams &p, cudaStream_t st)
     int64_t chunks = 0;
     for (NormSide &side : p.side)
         chunks += side.chunks = (int)div_up(side.x.heads, kSlots * (32 / GL));
-    p.run = (int)run_tokens(p.batch.n, chunks, kResident, kWaves);
+    p.run = (int)run_tokens(p.batch.n, chunks, kResident, kRun);
     norm_rope_vec_kernel<T, GL, kInterleaved, kAppend>
         <<<dim3((unsigned)div_up(p.batch.n, kWarps * p.run), (unsigned)chunks), kWarps * 32, smem, st>>>(p);
     count_launch(st);

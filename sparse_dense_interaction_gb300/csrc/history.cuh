@@ -63,6 +63,9 @@ struct BatchView {
 struct Sequence {
     int64_t first;
     int count, length;
+
+    // offsets that are not monotone lead the searches below anywhere
+    __device__ __forceinline__ bool has(int64_t token) const { return token >= first && token < first + count; }
 };
 
 // Reads sequence s; false (with the flag raised) where the batch's numbers

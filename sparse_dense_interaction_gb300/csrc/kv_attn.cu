@@ -159,7 +159,7 @@ kv_attn_join_kernel(const __grid_constant__ AttnParams p)
         const int64_t token = i / heads, s = find_sequence(p.batch, token);
         const int h = (int)(i - token * heads);
         Sequence seq;
-        if (s < 0 || !read_sequence(p.batch, s, p.max_new, p.max_len, seq, nullptr) || token >= seq.first + seq.count)
+        if (s < 0 || !read_sequence(p.batch, s, p.max_new, p.max_len, seq, nullptr) || !seq.has(token))
             continue;
         // the tile that held this row, and whether it was split
         const int t = (int)(token - seq.first), row = t * p.group + h % p.group, row0 = row / p.rows * p.rows;
