@@ -18,8 +18,10 @@
  * checks before any launch, data-dependent errors as bits in an optional
  * device flag (read with dlrm_read_error), no kernel faults on bad data.
  * The structs below are host structs, read during the call.  Strides are in
- * elements; the d elements of a head row are contiguous.  Outputs must not
- * overlap inputs unless a call says so.
+ * elements; the d elements of a head row are contiguous.  Inputs may share
+ * rows (a stride of 0); the rows of an output lie apart (strides of at least d
+ * where there is more than one; DLRM_ERR_INVALID_ARG otherwise) and must not
+ * overlap the inputs.
  */
 #ifndef DLRM_HISTORY_H
 #define DLRM_HISTORY_H
@@ -187,13 +189,16 @@ size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_hea
  * number outside the cache in the seen range reads as a page of zeros and
  * raises DLRM_FLAG_INDEX_OOB.
  *
- * Scores, the softmax's maxima and sums and the output's sums are fp32.  With
- * 16-bit types the products run on the tensor cores, with each weight p
- * (relative to the row's running maximum) rounded to that type, as large
- * as the rounding of the output itself; fp32 tensors use fp32 arithmetic.
- * Results are the same bits from run to run.  16-bit tensors of at most 128
- * elements a head, with heads, strides and pointers that are multiples of 16
- * bytes, take the tensor cores; others the general kernel.
+ * Scores, the softmax's maxima and sums and the output's sums are fp32.  The
+ * products run on the tensor cores for heads of at most 128 elements whose
+ * widths, strides and pointers are multiples of 16 bytes; others take a general
+ * kernel in fp32.  16-bit types: each weight p (relative to the row's running
+ * maximum) is rounded to that type, an error as large as the rounding of the
+ * output itself.  fp32: operands are split in two TF32 parts, which carries
+ * each product to about 2^-20 of its magnitude.  Results are the same bits from
+ * run to run of one batch; a sequence's last bits may depend on which other
+ * sequences are in its batch.  Every wait inside a kernel is bounded; one that
+ * runs out raises DLRM_FLAG_WAIT_TIMEOUT (results then invalid).
  */
 int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm_kv_cache *cache, int d, int dtype,
                      float scale, int causal, int64_t window, int64_t max_new, int64_t max_len,

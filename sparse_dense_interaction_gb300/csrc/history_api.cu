@@ -44,8 +44,12 @@ static int check_heads(const dlrm_heads *h, int64_t n, int dtype, HeadsView &v)
     return DLRM_OK;
 }
 
+// Rows that are written lie apart (an input's may be the same: a stride of 0).
+static bool apart(int64_t count, int64_t stride, int d) { return count <= 1 || stride >= d; }
+
 // An input and an output of the same heads; both null: no heads.
-static int check_pair(const dlrm_heads *in, const dlrm_heads *out, int64_t n, int dtype, HeadsView &vi, HeadsView &vo)
+static int check_pair(const dlrm_heads *in, const dlrm_heads *out, int64_t n, int d, int dtype, HeadsView &vi,
+                      HeadsView &vo)
 {
     vi = vo = HeadsView{nullptr, 0, 0, 0};
     if (!in && !out)
@@ -53,7 +57,9 @@ static int check_pair(const dlrm_heads *in, const dlrm_heads *out, int64_t n, in
     int s = check_heads(in, n, dtype, vi);
     if (s == DLRM_OK)
         s = check_heads(out, n, dtype, vo);
-    return s == DLRM_OK && vi.heads != vo.heads ? DLRM_ERR_INVALID_ARG : s;
+    return s == DLRM_OK && (vi.heads != vo.heads || !apart(n, vo.ts, d) || !apart(vo.heads, vo.hs, d))
+               ? DLRM_ERR_INVALID_ARG
+               : s;
 }
 
 static int check_rope(const dlrm_rope *r, int64_t n, int d, bool needs_positions, RopeView &v)
@@ -118,9 +124,9 @@ int dlrm_qk_norm_rope_fwd(const dlrm_heads *q, const dlrm_heads *k, int64_t n, i
     int s = check_row_type(n, d, dtype);
     if (s != DLRM_OK)
         return s;
-    if (!q || (s = check_pair(q, q_out, n, dtype, vq, vqo)) != DLRM_OK)
+    if (!q || (s = check_pair(q, q_out, n, d, dtype, vq, vqo)) != DLRM_OK)
         return s != DLRM_OK ? s : DLRM_ERR_INVALID_ARG;
-    if ((s = check_pair(k, k_out, n, dtype, vk, vko)) != DLRM_OK ||
+    if ((s = check_pair(k, k_out, n, d, dtype, vk, vko)) != DLRM_OK ||
         (s = check_weights(q_weight, k_weight, eps)) != DLRM_OK || (s = check_rope(rope, n, d, true, vr)) != DLRM_OK)
         return s;
     if (n == 0)
@@ -143,18 +149,20 @@ int dlrm_qk_norm_rope_bwd(const dlrm_heads *dq_out, const dlrm_heads *dk_out, co
                           const dlrm_heads *dk, float *dq_weight, float *dk_weight, void *workspace,
                           size_t workspace_bytes, int32_t *err_flag, dlrm_stream_t stream)
 {
-    HeadsView vq, vk, vdq, vdk, vdqo, vdko;
+    HeadsView vq, vk, vdq, vdk, vdqo, vdko = {nullptr, 0, 0, 0};
     RopeView vr;
     int s = check_row_type(n, d, dtype);
     if (s != DLRM_OK)
         return s;
-    if (!q || (s = check_pair(q, dq, n, dtype, vq, vdq)) != DLRM_OK)
+    if (!q || (s = check_pair(q, dq, n, d, dtype, vq, vdq)) != DLRM_OK)
         return s != DLRM_OK ? s : DLRM_ERR_INVALID_ARG;
-    if ((s = check_pair(q, dq_out, n, dtype, vq, vdqo)) != DLRM_OK ||
-        (s = check_pair(k, dk, n, dtype, vk, vdk)) != DLRM_OK ||
-        (s = check_pair(k, dk_out, n, dtype, vk, vdko)) != DLRM_OK ||
+    if ((s = check_heads(dq_out, n, dtype, vdqo)) != DLRM_OK ||
+        (s = check_pair(k, dk, n, d, dtype, vk, vdk)) != DLRM_OK ||
+        (k && (s = check_heads(dk_out, n, dtype, vdko)) != DLRM_OK) ||
         (s = check_weights(q_weight, k_weight, eps)) != DLRM_OK || (s = check_rope(rope, n, d, true, vr)) != DLRM_OK)
         return s;
+    if (vdqo.heads != vq.heads || !k != !dk_out || (k && vdko.heads != vk.heads))
+        return DLRM_ERR_INVALID_ARG;
     if ((dq_weight && !q_weight) || (dk_weight && (!k_weight || !k)) || !aligned(dq_weight, 4) ||
         !aligned(dk_weight, 4) || !workspace || !aligned(workspace, 16))
         return DLRM_ERR_INVALID_ARG;
@@ -185,10 +193,11 @@ int dlrm_kv_append(const dlrm_heads *k, const dlrm_heads *v, const dlrm_kv_batch
     int s = check_row_type(n, d, dtype);
     if (s != DLRM_OK || (s = check_cache(cache, dtype, vc)) != DLRM_OK ||
         (s = check_batch(batch, cache->page_size, vb)) != DLRM_OK || (s = check_heads(k, n, dtype, vk)) != DLRM_OK ||
-        (s = check_heads(v, n, dtype, vv)) != DLRM_OK || (s = check_pair(q, q_out, n, dtype, vq, vqo)) != DLRM_OK ||
+        (s = check_heads(v, n, dtype, vv)) != DLRM_OK || (s = check_pair(q, q_out, n, d, dtype, vq, vqo)) != DLRM_OK ||
         (s = check_weights(q_weight, k_weight, eps)) != DLRM_OK || (s = check_rope(rope, n, d, false, vr)) != DLRM_OK)
         return s;
-    if (vk.heads != vc.heads || vv.heads != vc.heads)
+    if (vk.heads != vc.heads || vv.heads != vc.heads || !apart(cache->pages, vc.page_stride, d) ||
+        !apart(cache->page_size, vc.slot_stride, d) || !apart(vc.heads, vc.head_stride, d))
         return DLRM_ERR_INVALID_ARG;
     if (n == 0)
         return DLRM_OK;
@@ -218,7 +227,7 @@ int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm
     int s = check_row_type(n, d, dtype);
     if (s != DLRM_OK || (s = check_cache(cache, dtype, p.cache)) != DLRM_OK ||
         (s = check_batch(batch, cache->page_size, p.batch)) != DLRM_OK ||
-        (s = check_pair(q, out, n, dtype, p.q, p.out)) != DLRM_OK)
+        (s = check_pair(q, out, n, d, dtype, p.q, p.out)) != DLRM_OK)
         return s;
     if (p.q.heads % p.cache.heads != 0 || !(scale > 0.f) || !(scale <= 3.0e38f) || (causal != 0 && causal != 1) ||
         window < 0 || max_new < 0 || max_len < 0 || !aligned(lse, 4) || !workspace || !aligned(workspace, 16))

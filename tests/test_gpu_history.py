@@ -159,6 +159,61 @@ def test_norm_rope_positions_outside_the_table(dtype, d):
     close(dw, ws_, R.weight_tolerance(wm, 64), "weight")
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 18)])
+def test_norm_rope_of_broadcast_inputs(dtype, d):
+    # one row for all heads, one gradient for all tokens: strides of 0
+    n, h = 9, 3
+    row, dy = randn(1, (n, 1, d), dtype, 1.5), randn(2, (1, h, d), dtype)
+    x, dyx = row.expand(n, h, d), dy.expand(n, h, d)
+    w, table, at = 1 + 0.3 * randn(3, (d,), "f32"), rope_table(20, 16), torch.arange(n, device=DEV)
+    out, dx, dw = torch.empty((n, h, d), dtype=DT[dtype], device=DEV), torch.empty((n, h, d), dtype=DT[dtype], device=DEV), torch.empty(d, device=DEV)
+    sdi.dlrm_qk_norm_rope_fwd(x, None, w, None, EPS, table, at, out, None)
+    y, mag = R.norm_rope(np64(x), np64(w), EPS, np64(table), at.cpu().numpy())
+    close(out, y, R.rows_tolerance(y, mag, dtype), "broadcast rows")
+    ws = torch.empty(sdi.dlrm_qk_norm_rope_bwd_workspace_size(n, h, 0, d), dtype=torch.uint8, device=DEV)
+    sdi.dlrm_qk_norm_rope_bwd(dyx, None, x, None, w, None, EPS, table, at, dx, None, dw, None, ws)
+    want, mag, wsum, wmag = R.norm_rope_bwd(np64(dyx), np64(x), np64(w), EPS, np64(table), at.cpu().numpy())
+    close(dx, want, R.rows_tolerance(want, mag, dtype, 32), "broadcast gradients")
+    close(dw, wsum, R.weight_tolerance(wmag, 64 + n * h // 64), "weight")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_of_many_empty_sequences(dtype):
+    # tokens whose sequences lie more than 32 apart, and several in one
+    counts = [1] + [0] * 40 + [2] + [0] * 100 + [1, 1] + [0] * 7 + [3, 0]
+    lengths = [c + 4 * (c > 0) for c in counts]
+    table, table_d, offsets, lens, pages = make_batch(counts, lengths, 8)
+    d, hk, n = 64, 2, sum(counts)
+    kc, vc = (make_cache(s, pages, 8, hk, d, dtype, False) for s in (1, 2))
+    k, v = randn(3, (n, hk, d), dtype), randn(4, (n, hk, d), dtype)
+    f = flag()
+    sdi.dlrm_kv_append(k, v, offsets, lens, table_d, kc, vc, err_flag=f)
+    assert sdi.dlrm_read_error(f) == 0
+    at = np.concatenate([np.arange(m - c, m) for c, m in zip(counts, lengths)])
+    pg = table[np.repeat(np.arange(len(counts)), counts), at // 8]
+    assert np.array_equal(np64(kc)[pg, at % 8], np64(k)) and np.array_equal(np64(vc)[pg, at % 8], np64(v))
+
+
+@pytest.mark.parametrize("dtype,c", [("bf16", 1), ("f16", 40), ("f32", 2)])
+def test_offsets_that_are_not_monotone_do_no_harm(dtype, c):
+    # whatever the offsets say, only the batch's own rows and slots are touched
+    case = ([c] * 4, [40] * 4, 4, 2, 64, 16, False, True, 0, dtype)
+    table, table_d, offsets, lens, kc, vc, q = attention_inputs(case, stale=0.0)
+    good_out, _ = attend(case, q, offsets, lens, table_d, kc, vc, 0.125)
+    for bad in ([0, 3 * c, c, 2 * c, 4 * c], [4 * c, 3 * c, 2 * c, c, 0], [-5, c, 2 * c, 1 << 40, 4 * c], [1, 1, 1, 1, 1]):
+        o, f = torch.tensor(bad, device=DEV), flag()
+        out, _ = attend(case, q, o, lens, table_d, kc, vc, 0.125, f)
+        kc2, vc2 = kc.clone(), vc.clone()
+        sdi.dlrm_kv_append(q[:, :2], q[:, 2:], o, lens, table_d, kc2, vc2, err_flag=f)
+        torch.cuda.synchronize()
+        if bad != [1, 1, 1, 1, 1]:
+            assert sdi.dlrm_read_error(f) == _native.ERR_BAD_OFFSETS
+        live = torch.from_numpy(table[:, :3]).long().to(DEV).flatten()
+        other = torch.ones(kc.shape[0], dtype=torch.bool, device=DEV)
+        other[live] = False
+        assert torch.equal(kc2[other], kc[other])
+
+
 def test_norm_rope_of_no_tokens_and_zero_rows():
     x = torch.zeros(0, 2, 64, device=DEV)
     w, dw = torch.ones(64, device=DEV), torch.full((64,), 7.0, device=DEV)
@@ -294,6 +349,15 @@ ATTN = [
     ([1, 30], [100, 260], 2, 2, 17, 5, False, True, 0, "bf16"),
     ([3, 20], [100, 200], 2, 1, 256, 16, False, True, 0, "bf16"),
     ([3, 20], [100, 200], 2, 1, 200, 16, True, False, 50, "f32"),
+    ([5 + i % 30 for i in range(270)], [3 + 37 * i % 200 for i in range(270)], 4, 2, 64, 16, False, True, 0, "f16"),
+    ([300], [5000], 2, 1, 64, 16, True, True, 0, "bf16"),
+    ([200, 5], [333, 64], 2, 1, 128, 7, False, True, 0, "f16"),  # pages that end inside a tile, two query tiles
+    ([140], [3001], 3, 1, 56, 3, False, False, 700, "bf16"),
+    ([1] * 40, [(i * i * 7) % 3001 for i in range(40)], 8, 2, 64, 16, False, True, 0, "bf16"),
+    ([i % 3 for i in range(300)], [(i * 61) % 1300 for i in range(300)], 2, 1, 64, 64, True, False, 0, "f16"),
+    ([16, 3], [1500, 2000], 1, 1, 128, 24, False, True, 0, "bf16"),
+    ([2, 1], [2500, 3], 2, 1, 20, 5, False, True, 0, "f32"),
+    ([60, 1], [1100, 700], 3, 1, 64, 16, True, True, 0, "f32"),
 ]
 
 
