@@ -21,9 +21,11 @@
 //    of 4 MMAs (fp32: of two tokens, 4 MMAs, as they are).  The weights, whose tokens
 //    are in the lanes that hold rows next, are transposed by movmatrix (fp32: the order
 //    of the tokens is the one that the scores come out in).
-// fp32 runs on TF32 MMAs: an operand is its upper 19 bits, which are what the MMA reads, plus the rest,
-// exactly, and the three products of the split that matter carry each product of
-// two elements to about 2^-20 of its magnitude; sums are fp32.
+// fp32 runs on TF32 MMAs: an operand is itself rounded to TF32 plus the rest (of
+// which the MMA reads 11 bits), and the three products of the split that matter carry each
+// product of two elements to about 2^-22 of its magnitude.  An MMA starts from zero and its sum is
+// added in fp32: the MMA's own additions are cut off, which leaves 1e-5 of the
+// output after 20000 events where a chain of MMAs runs on (4e-7 so, at 10 % more time).
 // A warp keeps its own running maximum, sum and output; the four are joined
 // in shared memory at an item's end.  An item that spans CTAs leaves
 // normalised partial rows and log2 of their sums, which a second kernel joins.
@@ -54,7 +56,7 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float *c, const uint32_t
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The same in fp32, 8 deep, as three TF32 MMAs: x = its upper bits + lo.
+// The same in fp32, 8 deep, as three TF32 MMAs: x = x rounded to TF32 + lo.
 __device__ __forceinline__ void mma1688(float *c, const float *a, float b0, float b1)
 {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -62,12 +64,23 @@ __device__ __forceinline__ void mma1688(float *c, const float *a, float b0, floa
         : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
           "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
-__device__ __forceinline__ float low_part(float x) { return x - tc::tf32_trunc(x); }
-__device__ __forceinline__ void mma_fp32(float *c, const float *a, const float *a_lo, float b0, float b1)
+struct Split {
+    float hi, lo;
+
+    __device__ __forceinline__ Split() {}
+    __device__ __forceinline__ Split(float x) : hi(tc::tf32_round(x)), lo(x - hi) {}
+};
+// The MMA's own sums are cut off, not rounded: it adds up 8 products, the rest is added in fp32.
+__device__ __forceinline__ void mma_fp32(float *c, const Split *a, Split b0, Split b1)
 {
-    mma1688(c, a_lo, b0, b1);
-    mma1688(c, a, low_part(b0), low_part(b1));
-    mma1688(c, a, b0, b1);
+    const float hi[4] = {a[0].hi, a[1].hi, a[2].hi, a[3].hi}, lo[4] = {a[0].lo, a[1].lo, a[2].lo, a[3].lo};
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    mma1688(t, lo, b0.hi, b1.hi);
+    mma1688(t, hi, b0.lo, b1.lo);
+    mma1688(t, hi, b0.hi, b1.hi);
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        c[i] += t[i];
 }
 
 // One item -- row tile `tile` of a sequence and head -- and its units
@@ -382,8 +395,8 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         copy(i, i);
 
     constexpr int kQ = Sh::kWide ? 2 : kGroups;
-    uint4 qa[KG][kQ];        // the queries' chunks of rows g, g + 8
-    float qlo[Sh::kWide ? KG : 1][2][4];  // fp32: their low parts
+    uint4 qa[Sh::kWide ? 1 : KG][kQ];         // the queries' chunks of rows g, g + 8
+    Split qs[Sh::kWide ? KG : 1][2][4];       // fp32: split
     float o[Sh::kOut], m[Sh::kStats], l[Sh::kStats];
     int lo[Sh::kStats], hi[Sh::kStats], rows = 0;  // rows: of the sequence
     int all_lo = 0, all_hi = 0;  // positions that every row of the tile sees
@@ -413,14 +426,16 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
                 for (int i = 0; i < KG; i++) {
                     const int e = (4 * i + q) * E;
-                    qa[i][h] = make_uint4(0, 0, 0, 0);
+                    uint4 x = make_uint4(0, 0, 0, 0);
                     if (r < rows && e < p.d)
-                        qa[i][h] = *reinterpret_cast<const uint4 *>(src + e);
-                    if (Sh::kWide) {
-                        qlo[i][h][0] = low_part(__uint_as_float(qa[i][h].x));
-                        qlo[i][h][1] = low_part(__uint_as_float(qa[i][h].y));
-                        qlo[i][h][2] = low_part(__uint_as_float(qa[i][h].z));
-                        qlo[i][h][3] = low_part(__uint_as_float(qa[i][h].w));
+                        x = *reinterpret_cast<const uint4 *>(src + e);
+                    if constexpr (Sh::kWide) {
+                        qs[i][h][0] = Split(__uint_as_float(x.x));
+                        qs[i][h][1] = Split(__uint_as_float(x.y));
+                        qs[i][h][2] = Split(__uint_as_float(x.z));
+                        qs[i][h][3] = Split(__uint_as_float(x.w));
+                    } else {
+                        qa[i][h] = x;
                     }
                 }
             }
@@ -472,15 +487,10 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             for (int i = 0; i < KG; i++) {
                 const uint4 k = key_chunk(nb, 0, i);
                 if constexpr (Sh::kWide) {
-                    const uint4 &a = qa[i][0], &b = qa[i][1];
-                    const float x[4] = {__uint_as_float(a.x), __uint_as_float(b.x), __uint_as_float(a.y),
-                                        __uint_as_float(b.y)};
-                    const float y[4] = {__uint_as_float(a.z), __uint_as_float(b.z), __uint_as_float(a.w),
-                                        __uint_as_float(b.w)};
-                    const float xl[4] = {qlo[i][0][0], qlo[i][1][0], qlo[i][0][1], qlo[i][1][1]};
-                    const float yl[4] = {qlo[i][0][2], qlo[i][1][2], qlo[i][0][3], qlo[i][1][3]};
-                    mma_fp32(s[nb][0], x, xl, __uint_as_float(k.x), __uint_as_float(k.y));
-                    mma_fp32(other[0], y, yl, __uint_as_float(k.z), __uint_as_float(k.w));
+                    const Split x[4] = {qs[i][0][0], qs[i][1][0], qs[i][0][1], qs[i][1][1]};
+                    const Split y[4] = {qs[i][0][2], qs[i][1][2], qs[i][0][3], qs[i][1][3]};
+                    mma_fp32(s[nb][0], x, __uint_as_float(k.x), __uint_as_float(k.y));
+                    mma_fp32(other[0], y, __uint_as_float(k.z), __uint_as_float(k.w));
                 } else {
                     const uint4 k8 = key_chunk(nb, 1, i);
                     const uint32_t x[4] = {k.x, k8.x, k.y, k8.y}, y[4] = {k.z, k8.z, k.w, k8.w};
@@ -563,15 +573,14 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             };
             if constexpr (Sh::kWide) {
                 const float *w = s[nb][0];
-                const float pa[4] = {w[0], w[2], w[1], w[3]};
-                const float pl[4] = {low_part(w[0]), low_part(w[2]), low_part(w[1]), low_part(w[3])};
+                const Split pa[4] = {w[0], w[2], w[1], w[3]};
 #pragma unroll
                 for (int i = 0; i < VS; i++) {
                     const uint4 v0 = value(0, i), v1 = value(1, i);
-                    mma_fp32(o + 16 * i, pa, pl, __uint_as_float(v0.x), __uint_as_float(v1.x));
-                    mma_fp32(o + 16 * i + 4, pa, pl, __uint_as_float(v0.y), __uint_as_float(v1.y));
-                    mma_fp32(o + 16 * i + 8, pa, pl, __uint_as_float(v0.z), __uint_as_float(v1.z));
-                    mma_fp32(o + 16 * i + 12, pa, pl, __uint_as_float(v0.w), __uint_as_float(v1.w));
+                    mma_fp32(o + 16 * i, pa, __uint_as_float(v0.x), __uint_as_float(v1.x));
+                    mma_fp32(o + 16 * i + 4, pa, __uint_as_float(v0.y), __uint_as_float(v1.y));
+                    mma_fp32(o + 16 * i + 8, pa, __uint_as_float(v0.z), __uint_as_float(v1.z));
+                    mma_fp32(o + 16 * i + 12, pa, __uint_as_float(v0.w), __uint_as_float(v1.w));
                 }
             } else {
                 // the weights, rounded to the type (their sum is of the unrounded ones), rows to columns
