@@ -12,15 +12,14 @@
 // below meet no bank twice.  Other page sizes take asynchronous 16-byte copies, row by row, where
 // every lane reads back exactly the chunks it copied itself; they share the load/store
 // pipe with the reads (256 users of up to 8192 events: 444 us against 328).
-//  - scores: MMAs of 16 tokens x 8 rows (m16n8k16; fp32: 16 rows x 8 tokens,
-//    m16n8k8).  The order of the summed elements is free, so a lane's 16-byte chunk
-//    of a key serves two MMA steps as it is, with the query's chunks in the same order.
-//  - output: MMAs of 16 columns x 8 rows, 16 tokens deep (fp32: 16 rows x 8
-//    columns, 8 deep).  Which columns form an MMA's 16 is free too: a lane's chunks of
-//    the same columns of four tokens, interleaved by byte permutes, are the operands
-//    of 4 MMAs (fp32: of two tokens, 4 MMAs, as they are).  The weights, whose tokens
-//    are in the lanes that hold rows next, are transposed by movmatrix (fp32: the order
-//    of the tokens is the one that the scores come out in).
+//  - scores: MMAs of 16 tokens x 8 rows (m16n8k16; fp32: m16n8k8).  The order of the
+//    summed elements is free, so a lane's 16-byte chunk of a key serves two MMA
+//    steps as it is, with the query's chunks in the same order.
+//  - output: MMAs of 16 columns x 8 rows, 16 tokens deep (fp32: 8).  Which columns form an MMA's
+//    16 is free too: a lane's chunks of the same columns of four tokens, interleaved
+//    by byte permutes, are the operands of 4 MMAs (fp32: of two tokens, 2 MMAs, as they
+//    are).  The weights, whose tokens are in the lanes that hold rows next, are
+//    transposed by movmatrix (fp32: each half of their bits).
 // fp32 runs on TF32 MMAs: an operand is itself rounded to TF32 plus the rest (of
 // which the MMA reads 11 bits), and the three products of the split that matter carry each
 // product of two elements to about 2^-22 of its magnitude.  An MMA starts from zero and its sum is
@@ -70,14 +69,22 @@ struct Split {
     __device__ __forceinline__ Split() {}
     __device__ __forceinline__ Split(float x) : hi(tc::tf32_round(x)), lo(x - hi) {}
 };
-// The MMA's own sums are cut off, not rounded: it adds up 8 products, the rest is added in fp32.
-__device__ __forceinline__ void mma_fp32(float *c, const Split *a, Split b0, Split b1)
+// Two steps.  The MMA's own sums are cut off, not rounded: it adds up 16 products, small terms first, and the
+// rest is added in fp32.
+__device__ __forceinline__ void mma_fp32(float *c, const Split *a, const Split *b)
 {
-    const float hi[4] = {a[0].hi, a[1].hi, a[2].hi, a[3].hi}, lo[4] = {a[0].lo, a[1].lo, a[2].lo, a[3].lo};
     float t[4] = {0.f, 0.f, 0.f, 0.f};
-    mma1688(t, lo, b0.hi, b1.hi);
-    mma1688(t, hi, b0.lo, b1.lo);
-    mma1688(t, hi, b0.hi, b1.hi);
+#pragma unroll
+    for (int pass = 0; pass < 3; pass++)
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const Split *x = a + 4 * k, *y = b + 2 * k;
+            float ax[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                ax[i] = pass == 0 ? x[i].lo : x[i].hi;
+            mma1688(t, ax, pass == 1 ? y[0].lo : y[0].hi, pass == 1 ? y[1].lo : y[1].hi);
+        }
 #pragma unroll
     for (int i = 0; i < 4; i++)
         c[i] += t[i];
@@ -213,33 +220,33 @@ __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int &quot
 }
 
 // Rows of a lane's softmax statistics and the layout of its output registers.
-// 16-bit types: the tokens are the MMAs' 16 rows and the query rows their 8
-// columns, kGroups of 8 (narrow tiles do half the work); fp32: the query rows
-// are the 16 rows.
+// The tokens are the MMAs' 16 rows and the query rows their 8 columns, kGroups
+// of 8 (narrow tiles do half the work).
 template <typename T, int DP, int kGroups, bool kBulk>
 struct FewShape {
     static constexpr bool kWide = sizeof(T) == 4;
     static constexpr int E = 16 / sizeof(T);                     // elements of a chunk
-    static constexpr int MG = kWide ? 8 : 16;                    // tokens of an MMA group
+    static constexpr int MG = 16;                                // tokens of an MMA group
     static constexpr int KT = MG / 8, VT = MG / 4;               // a lane's key and value rows of a group
     static constexpr int KG = DP / (4 * E), VS = DP / (8 * E);   // its chunks of a key row, of a value row
-    static constexpr int TB = kFewStageBytes / (2 * DP * (int)sizeof(T)), NB = TB / MG, UT = kFewWarps * TB;
-    static constexpr int kChunks = KT * KG + VT * VS;            // of a group
-    static constexpr int kStats = kWide ? 2 : 2 * kGroups;       // rows whose statistics a lane holds
-    static constexpr int kOut = kWide ? VS * 16 : kGroups * VS * 16;  // output registers
+    static constexpr int kTokenBytes = 2 * DP * (int)sizeof(T);  // keys and values
+    // A group that fills two stages has its keys in one and its values in the next.
+    static constexpr int kParts = MG * kTokenBytes / kFewStageBytes > 1 ? 2 : 1;
+    static constexpr int TB = kParts * kFewStageBytes / kTokenBytes, NB = TB / MG, UT = kFewWarps * TB;
+    static constexpr int kChunks = kParts > 1 ? 0 : KT * KG + VT * VS;  // from a group to the next
+    static constexpr int kStats = 2 * kGroups;                   // rows whose statistics a lane holds
+    static constexpr int kOutMmas = E / 2;                       // of a set of output columns
+    static constexpr int kOut = kGroups * VS * kOutMmas * 4;     // output registers
     static constexpr int kSmem = 1024 + kFewWarps * kFewStages * kFewStageBytes + 2 * kOut * 32 * 4;
     static constexpr int kKeyBox = MG * 64, kValueBox = MG * 128;  // bytes of a column of a group's keys, values
+    static constexpr int kKeyBytes = kParts > 1 ? 0 : KG * kKeyBox;  // before a group's values
+    static constexpr int kKeyChunks = kParts > 1 ? 0 : KT * KG;
     static constexpr int kGroupBytes = KG * kKeyBox + VS * kValueBox;
+    static_assert(NB * MG == TB && (kParts == 1 || NB == 1), "a stage holds whole groups");
 
     // the row of a lane's statistic i, and the statistic of its output register o
-    __device__ __forceinline__ static int row(int i, int g, int q)
-    {
-        return kWide ? g + 8 * i : 2 * q + (i & 1) + 8 * (i >> 1);
-    }
-    __device__ __forceinline__ static constexpr int stat(int o)
-    {
-        return kWide ? (o & 3) >> 1 : (o & 1) + 2 * (o / (VS * 16));
-    }
+    __device__ __forceinline__ static int row(int i, int q) { return 2 * q + (i & 1) + 8 * (i >> 1); }
+    __device__ __forceinline__ static constexpr int stat(int o) { return (o & 1) + 2 * (o / (VS * kOutMmas * 4)); }
 };
 
 // The cache as bulk tensor copies see it: (element, slot, head, page).
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
 kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FewMaps maps)
 {
     using Sh = FewShape<T, DP, kGroups, kBulk>;
-    constexpr int E = Sh::E, KT = Sh::KT, VT = Sh::VT, KG = Sh::KG, VS = Sh::VS, NB = Sh::NB, UT = Sh::UT;
+    constexpr int E = Sh::E, KT = Sh::KT, VT = Sh::VT, KG = Sh::KG, VS = Sh::VS, NB = Sh::NB, UT = Sh::UT, kParts = Sh::kParts;
     extern __shared__ uint8_t raw[];
     __shared__ float s_m[kFewWarps][kFewRows], s_l[kFewWarps][kFewRows];
     __shared__ uint64_t bars[kFewWarps][kFewStages];
@@ -315,11 +322,11 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
     };
     const uint32_t ring_at = tc::smem_u32(ring);
-    auto copy_boxes = [&](int stage) {
+    auto copy_boxes = [&](int stage, int part) {
         if (lane == 0)
             tc::mbar_expect_tx(&bars[warp][stage], kFewStageBytes);
         __syncwarp();
-        if (!copies)
+        if (!copies || (kParts > 1 && (my_column >= KG) != part))
             return;
         if (page_slot >= 0 && (uint32_t)page_id >= p.cache.pages)
             raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
@@ -330,7 +337,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             tc::tma_load_4d(to + my_column * Sh::kKeyBox + my_part * maps.rows * 64, &maps.k, my_column * 4 * E, slot,
                             is.head, page, &bars[warp][stage]);
         else
-            tc::tma_load_4d(to + KG * Sh::kKeyBox + (my_column - KG) * Sh::kValueBox + my_part * maps.rows * 128,
+            tc::tma_load_4d(to + Sh::kKeyBytes + (my_column - KG) * Sh::kValueBox + my_part * maps.rows * 128,
                             &maps.v, (my_column - KG) * 8 * E, slot, is.head, page, &bars[warp][stage]);
     };
     // the lane's row: its place in the cache, -1 where there is none
@@ -344,13 +351,15 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         return (page_id * p.cache.page_stride + page_slot * p.cache.slot_stride + is.head * p.cache.head_stride) *
                (int64_t)sizeof(T);
     };
-    auto copy_rows = [&](int stage, int64_t mine) {
+    auto copy_rows = [&](int stage, int part, int64_t mine) {
         uint32_t to = ring_at + stage * kFewStageBytes + lane * 16;
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
             for (int t = 0; t < KT + VT; t++) {
                 const bool key = t < KT;
+                if (kParts > 1 && key == part)
+                    continue;
                 const int v = t - KT, token = key ? t * 8 + g : 2 * q + (v & 1) + (v >> 1) * 8;
                 const int64_t at = __shfl_sync(0xffffffffu, mine, nb * Sh::MG + token);
                 const char *from = (key ? p.cache.k + q * 16 : p.cache.v + g * 16) + (at >= 0 ? at : 0);
@@ -365,18 +374,21 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             }
         }
     };
-    // copies of unit u, whose page numbers were asked for a unit before, into a stage; then asks for the next
+    // copies of unit u (of its keys or values), whose page numbers were asked for a unit before, into a stage; then
+    // asks for the next
     bool dead = false;  // a wait ran out: nothing more is copied, the results are invalid
-    auto copy = [&](int u, int stage) {
+    auto copy = [&](int u, int part, int stage) {
         if constexpr (kBulk) {
             if (u < units && !dead)
-                copy_boxes(stage);
-            find(u + 1);
+                copy_boxes(stage, part);
+            if (part == kParts - 1)
+                find(u + 1);
         } else {
             const int64_t row = place();
-            find(u + 1);
+            if (part == kParts - 1)
+                find(u + 1);
             if (u < units)
-                copy_rows(stage, row);
+                copy_rows(stage, part, row);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
@@ -392,17 +404,40 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     find(0);
 #pragma unroll
     for (int i = 0; i < kFewStages - (kBulk ? 0 : 1); i++)
-        copy(i, i);
+        copy(i / kParts, i % kParts, i);
 
-    constexpr int kQ = Sh::kWide ? 2 : kGroups;
-    uint4 qa[Sh::kWide ? 1 : KG][kQ];         // the queries' chunks of rows g, g + 8
-    Split qs[Sh::kWide ? KG : 1][2][4];       // fp32: split
+    uint4 qa[Sh::kWide ? 1 : KG][kGroups];     // the queries' chunks of rows g, g + 8
+    Split qs[Sh::kWide ? KG : 1][kGroups][4];  // fp32: split
     float o[Sh::kOut], m[Sh::kStats], l[Sh::kStats];
     int lo[Sh::kStats], hi[Sh::kStats], rows = 0;  // rows: of the sequence
     int all_lo = 0, all_hi = 0;  // positions that every row of the tile sees
     bool fresh = true, first_item = true;
     int stage = 0;
     uint32_t phase = 0;
+    // waits for a part of unit u; goes on to the next stage when it has been read
+    auto arrived = [&](int u, int part) {
+        if constexpr (kBulk) {
+            if (!dead && !tc::mbar_wait(&bars[warp][stage], phase, &aborted))
+                dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+        } else {
+            const int next = part + kFewStages - 1;
+            copy(u + next / kParts, next % kParts, stage == 0 ? kFewStages - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 1) : "memory");
+        }
+    };
+    auto read = [&](int u, int part) {
+        if constexpr (kBulk) {
+            __syncwarp();  // every lane has read the stage that is filled next
+            const int next = part + kFewStages;
+            copy(u + next / kParts, next % kParts, stage);
+        }
+        stage++;
+        if (stage == kFewStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
 #pragma unroll 1
     for (int u = 0; u < units; u++) {
         if (fresh) {
@@ -412,14 +447,14 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             all_lo = seen_lo(seen_hi(it.seq, p.causal, (min(rows, row0 + kFewRows) - 1) / p.group), p.window);
 #pragma unroll
             for (int i = 0; i < Sh::kStats; i++) {
-                const int r = row0 + Sh::row(i, g, q);
+                const int r = row0 + Sh::row(i, q);
                 m[i] = -INFINITY;
                 l[i] = 0.f;
                 hi[i] = r < rows ? seen_hi(it.seq, p.causal, r / p.group) : 0;
                 lo[i] = seen_lo(hi[i], p.window);
             }
 #pragma unroll
-            for (int h = 0; h < kQ; h++) {
+            for (int h = 0; h < kGroups; h++) {
                 const int r = row0 + g + 8 * h, t = r / p.group;
                 const T *src = p.q.row<T>(it.seq.first + (r < rows ? t : 0),
                                           r < rows ? it.head * p.group + r - t * p.group : 0);
@@ -444,14 +479,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                 o[i] = 0.f;
             fresh = false;
         }
-        if constexpr (kBulk) {
-            if (!dead && !tc::mbar_wait(&bars[warp][stage], phase, &aborted))
-                dead = true;
-            dead = __any_sync(0xffffffffu, dead);
-        } else {
-            copy(u + kFewStages - 1, stage == 0 ? kFewStages - 1 : stage - 1);
-            asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 1) : "memory");
-        }
+        arrived(u, 0);
         const uint8_t *block = ring + stage * kFewStageBytes;
         // chunk i of a group's key row t * 8 + g, and of its value row 2q + (t & 1) + 8 (t >> 1)
         auto key_chunk = [&](int nb, int t, int i) {
@@ -462,37 +490,35 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         auto value_chunk = [&](int nb, int t, int i) {
             const int row = 2 * q + (t & 1);
             return *reinterpret_cast<const uint4 *>(
-                kBulk ? block + nb * Sh::kGroupBytes + KG * Sh::kKeyBox + i * Sh::kValueBox + (t >> 1) * 1024 +
+                kBulk ? block + nb * Sh::kGroupBytes + Sh::kKeyBytes + i * Sh::kValueBox + (t >> 1) * 1024 +
                             row * 128 + ((g ^ row) << 4)
-                      : block + (nb * Sh::kChunks + KT * KG + t * VS + i) * 512 + lane * 16);
+                      : block + (nb * Sh::kChunks + Sh::kKeyChunks + t * VS + i) * 512 + lane * 16);
         };
         const int at = it.lo + (u - it.first) * UT + warp * Sh::TB;
 
         // scores: s[nb][x][j] is of token token_of(nb, x, j) and statistic stat_of(x, j)
-        constexpr int kS = Sh::kWide ? 1 : kGroups;
-        float s[NB][kS][4];
-        auto token_of = [&](int nb, int j) {
-            return nb * Sh::MG + (Sh::kWide ? 2 * q + (j & 1) : g + 8 * (j >> 1));
-        };
-        auto stat_of = [](int x, int j) { return Sh::kWide ? j >> 1 : 2 * x + (j & 1); };
+        float s[NB][kGroups][4];
+        auto token_of = [&](int nb, int j) { return nb * Sh::MG + g + 8 * (j >> 1); };
+        auto stat_of = [](int x, int j) { return 2 * x + (j & 1); };
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
-            float other[kS][4];  // every second MMA's sum: two chains, half as long
+            float other[kGroups][4];  // every second MMA's sum: two chains, half as long
 #pragma unroll
-            for (int x = 0; x < kS; x++)
+            for (int x = 0; x < kGroups; x++)
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     s[nb][x][j] = other[x][j] = 0.f;
 #pragma unroll
             for (int i = 0; i < KG; i++) {
-                const uint4 k = key_chunk(nb, 0, i);
+                const uint4 k = key_chunk(nb, 0, i), k8 = key_chunk(nb, 1, i);
                 if constexpr (Sh::kWide) {
-                    const Split x[4] = {qs[i][0][0], qs[i][1][0], qs[i][0][1], qs[i][1][1]};
-                    const Split y[4] = {qs[i][0][2], qs[i][1][2], qs[i][0][3], qs[i][1][3]};
-                    mma_fp32(s[nb][0], x, __uint_as_float(k.x), __uint_as_float(k.y));
-                    mma_fp32(other[0], y, __uint_as_float(k.z), __uint_as_float(k.w));
+                    const Split x[8] = {__uint_as_float(k.x), __uint_as_float(k8.x), __uint_as_float(k.y),
+                                        __uint_as_float(k8.y), __uint_as_float(k.z), __uint_as_float(k8.z),
+                                        __uint_as_float(k.w), __uint_as_float(k8.w)};
+#pragma unroll
+                    for (int n = 0; n < kGroups; n++)
+                        mma_fp32(i & 1 ? other[n] : s[nb][n], x, qs[i][n]);
                 } else {
-                    const uint4 k8 = key_chunk(nb, 1, i);
                     const uint32_t x[4] = {k.x, k8.x, k.y, k8.y}, y[4] = {k.z, k8.z, k.w, k8.w};
 #pragma unroll
                     for (int n = 0; n < kGroups; n++) {
@@ -502,17 +528,22 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                 }
             }
 #pragma unroll
-            for (int x = 0; x < kS; x++)
+            for (int x = 0; x < kGroups; x++)
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     s[nb][x][j] += other[x][j];
+        }
+        if constexpr (kParts > 1) {
+            read(u, 0);
+            arrived(u, 1);
+            block = ring + stage * kFewStageBytes;
         }
         const bool edge = at < all_lo || at + Sh::TB > all_hi;
         if (edge) {
 #pragma unroll
             for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-                for (int x = 0; x < kS; x++)
+                for (int x = 0; x < kGroups; x++)
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
                         const int pos = at + token_of(nb, j), i = stat_of(x, j);
@@ -527,13 +558,13 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
             for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-                for (int x = 0; x < kS; x++)
+                for (int x = 0; x < kGroups; x++)
 #pragma unroll
                     for (int j = 0; j < 4; j++)
                         if (stat_of(x, j) == i)
                             top[i] = fmaxf(top[i], s[nb][x][j]);
 #pragma unroll
-            for (int step = Sh::kWide ? 1 : 4; step < (Sh::kWide ? 4 : 32); step *= 2)
+            for (int step = 4; step < 32; step *= 2)
                 top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], step));
             top[i] = fmaxf(top[i] * p.scale_log2, m[i]);
             base[i] = top[i] == -INFINITY ? 0.f : top[i];
@@ -554,7 +585,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
-            for (int x = 0; x < kS; x++)
+            for (int x = 0; x < kGroups; x++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     const int i = stat_of(x, j);
@@ -572,15 +603,36 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                 return v;
             };
             if constexpr (Sh::kWide) {
-                const float *w = s[nb][0];
-                const Split pa[4] = {w[0], w[2], w[1], w[3]};
+                // the weights, rows to columns: b[n] of tokens 2q, 2q + 1 and of those + 8
+                Split b[kGroups][4];
+#pragma unroll
+                for (int n = 0; n < kGroups; n++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t w0 = __float_as_uint(s[nb][n][2 * h]), w1 = __float_as_uint(s[nb][n][2 * h + 1]);
+                        const uint32_t lower = transpose8x8(__byte_perm(w0, w1, 0x5410));
+                        const uint32_t upper = transpose8x8(__byte_perm(w0, w1, 0x7632));
+                        b[n][2 * h] = __uint_as_float(__byte_perm(lower, upper, 0x5410));
+                        b[n][2 * h + 1] = __uint_as_float(__byte_perm(lower, upper, 0x7632));
+                    }
 #pragma unroll
                 for (int i = 0; i < VS; i++) {
-                    const uint4 v0 = value(0, i), v1 = value(1, i);
-                    mma_fp32(o + 16 * i, pa, __uint_as_float(v0.x), __uint_as_float(v1.x));
-                    mma_fp32(o + 16 * i + 4, pa, __uint_as_float(v0.y), __uint_as_float(v1.y));
-                    mma_fp32(o + 16 * i + 8, pa, __uint_as_float(v0.z), __uint_as_float(v1.z));
-                    mma_fp32(o + 16 * i + 12, pa, __uint_as_float(v0.w), __uint_as_float(v1.w));
+                    uint4 v[VT];
+#pragma unroll
+                    for (int t = 0; t < VT; t++)
+                        v[t] = value(t, i);
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {  // columns 2j and 2j + 1 of each lane's four
+                        Split a[8];
+#pragma unroll
+                        for (int t = 0; t < VT; t++) {
+                            a[(t >> 1) * 4 + 2 * (t & 1)] = __uint_as_float(j ? v[t].z : v[t].x);
+                            a[(t >> 1) * 4 + 2 * (t & 1) + 1] = __uint_as_float(j ? v[t].w : v[t].y);
+                        }
+#pragma unroll
+                        for (int n = 0; n < kGroups; n++)
+                            mma_fp32(o + ((n * VS + i) * 2 + j) * 4, a, b[n]);
+                    }
                 }
             } else {
                 // the weights, rounded to the type (their sum is of the unrounded ones), rows to columns
@@ -608,15 +660,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                 }
             }
         }
-        if constexpr (kBulk) {
-            __syncwarp();  // every lane has read the stage that is filled next: unit u's own
-            copy(u + kFewStages, stage);
-        }
-        stage++;
-        if (stage == kFewStages) {
-            stage = 0;
-            phase ^= 1;
-        }
+        read(u, kParts - 1);
         if (u + 1 < it.last && u + 1 < units)
             continue;
 
@@ -624,18 +668,18 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
         for (int i = 0; i < Sh::kStats; i++) {
 #pragma unroll
-            for (int step = Sh::kWide ? 1 : 4; step < (Sh::kWide ? 4 : 32); step *= 2)
+            for (int step = 4; step < 32; step *= 2)
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], step);
-            if (Sh::kWide ? q == 0 : g == 0) {
-                s_m[warp][Sh::row(i, g, q)] = m[i];
-                s_l[warp][Sh::row(i, g, q)] = l[i];
+            if (g == 0) {
+                s_m[warp][Sh::row(i, q)] = m[i];
+                s_l[warp][Sh::row(i, q)] = l[i];
             }
         }
         __syncthreads();
         float lse[Sh::kStats], f[Sh::kStats];
 #pragma unroll
         for (int i = 0; i < Sh::kStats; i++) {
-            const int r = Sh::row(i, g, q);
+            const int r = Sh::row(i, q);
             float all = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kFewWarps; w++)
@@ -672,27 +716,26 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                 o[i] += merge[(Sh::kOut + i) * 32 + lane];
 #pragma unroll
             for (int i = 0; i < Sh::kStats; i++) {
-                const int in = Sh::row(i, g, q), r = it.tile * kFewRows + in, t = r / p.group;
+                const int in = Sh::row(i, q), r = it.tile * kFewRows + in, t = r / p.group;
                 const int head = it.head * p.group + r - t * p.group;
                 if (r >= rows)
                     continue;
-                if (Sh::kWide ? q == 0 : g == 0) {
+                if (g == 0) {
                     if (!whole)
                         p.part_lse[slot * p.rows + in] = lse[i];
                     else if (p.lse)
                         p.lse[(it.seq.first + t) * heads + head] = lse[i] * kLn2;
                 }
-                // the lane's runs of E columns of this row: one of each set, fp32: two
+                // the lane's runs of E columns of this row: one of each set
 #pragma unroll
-                for (int c = 0; c < VS * (Sh::kWide ? 2 : 1); c++) {
-                    const int e = (Sh::kWide ? 8 * (c >> 1) + 2 * q + (c & 1) : 8 * c + g) * E;
+                for (int c = 0; c < VS; c++) {
+                    const int e = (8 * c + g) * E;
                     if (e >= p.d)
                         continue;
                     float x[E];
 #pragma unroll
                     for (int j = 0; j < E; j++)
-                        x[j] = o[Sh::kWide ? 16 * (c >> 1) + 4 * j + 2 * i + (c & 1)
-                                           : (((i >> 1) * VS + c) * 4 + (j >> 1)) * 4 + 2 * (j & 1) + (i & 1)];
+                        x[j] = o[(((i >> 1) * VS + c) * Sh::kOutMmas + (j >> 1)) * 4 + 2 * (j & 1) + (i & 1)];
                     T *out = p.out.row<T>(it.seq.first + t, head) + e;
                     float4 *part = reinterpret_cast<float4 *>(p.part_o + ((int64_t)slot * p.rows + in) * p.d + e);
                     if (!whole) {
@@ -867,7 +910,7 @@ template <typename T, int kGroups>
 static int launch_few_width(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
 {
     FewMaps maps = {};
-    maps.rows = sizeof(T) == 2 && p.cache.page.d % 16 == 0 ? 16 : 8;
+    maps.rows = p.cache.page.d % 16 == 0 ? 16 : 8;
     const bool bulk = p.cache.page.d % 8 == 0 && few_maps(p, dtype, maps.rows, maps);
     if (p.d <= 64)
         return bulk ? launch_few<T, 64, kGroups, true>(p, maps, workspace, st)
@@ -880,7 +923,8 @@ int launch_kv_attn_few(AttnParams &p, int dtype, void *workspace, cudaStream_t s
 {
     const bool narrow = p.max_new * p.group <= 8;
     if (dtype == DLRM_F32)
-        return launch_few_width<float, 1>(p, dtype, workspace, st);
+        return narrow ? launch_few_width<float, 1>(p, dtype, workspace, st)
+                      : launch_few_width<float, 2>(p, dtype, workspace, st);
     if (dtype == DLRM_F16)
         return narrow ? launch_few_width<__half, 1>(p, dtype, workspace, st)
                       : launch_few_width<__half, 2>(p, dtype, workspace, st);
