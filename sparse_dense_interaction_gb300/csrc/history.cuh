@@ -157,8 +157,10 @@ constexpr float kLn2 = 0.69314718055994530942f;
 enum AttnKernel { kAttnGeneral, kAttnTile };
 
 // Rows of the tensor-core tiles: two query tiles of 128 on an SM of their own;
-// with heads of 64 and at most 256 rows in all (the candidates of a user) one, and two CTAs on an SM, so that
-// one starts and ends while the other computes.
+// with heads of 64 and at most 256 rows in all (the candidates of a user) one,
+// and two CTAs on an SM, so that one starts and ends while the other computes
+// (up to 200 candidates of each of 64 users: 55 us against 69).  More rows keep
+// the pair, which reads keys and values once for both tiles.
 inline int tile_rows(int64_t rows, int d) { return d <= 64 && rows <= 256 ? 128 : 256; }
 
 struct AttnPlan {

@@ -223,8 +223,8 @@ static AttnPlan plan_splits(AttnKernel kernel, int rows, int64_t S, int kv_heads
     return a;
 }
 
-// The number of splits that ends soonest, each
-// CTA costing as much as 512 positions beside its share (its start, its end and the join).
+// The number of splits that ends soonest, each CTA costing as much as 512
+// positions beside its share (its start, its end and the join).
 static AttnPlan plan_tile(int64_t S, int kv_heads, int group, int d, int64_t max_new, int64_t max_len)
 {
     const int rows = tile_rows(max_new * group, d);

@@ -2,32 +2,43 @@
 // and fp32 tensors of every length.
 //
 // Such a call reads every key and value once and does little with each, so
-// memory bounds it, and the design keeps loads in flight.  An item is a
-// tile of 16 packed rows of one sequence and cache head; the positions of all
-// items are laid end to end in units of four warp blocks, a CTA takes an equal
-// run of units, whatever the lengths, and its warps stream their blocks through
-// rings that do not stop between items.  Pages of a multiple of 8 slots are
-// copied by bulk tensor copies through the page table, in boxes of 8 or 16
-// rows: keys in columns of 64 bytes, values in columns of 128 bytes swizzled, so that the reads
-// below meet no bank twice.  Other page sizes take asynchronous 16-byte copies, row by row, where
-// every lane reads back exactly the chunks it copied itself; they share the load/store
-// pipe with the reads (256 users of up to 8192 events: 444 us against 328).
-//  - scores: MMAs of 16 tokens x 8 rows (m16n8k16; fp32: m16n8k8).  The order of the
-//    summed elements is free, so a lane's 16-byte chunk of a key serves two MMA
-//    steps as it is, with the query's chunks in the same order.
-//  - output: MMAs of 16 columns x 8 rows, 16 tokens deep (fp32: 8).  Which columns form an MMA's
-//    16 is free too: a lane's chunks of the same columns of four tokens, interleaved
-//    by byte permutes, are the operands of 4 MMAs (fp32: of two tokens, 2 MMAs, as they
-//    are).  The weights, whose tokens are in the lanes that hold rows next, are
-//    transposed by movmatrix (fp32: each half of their bits).
+// memory bounds it, and the design keeps loads in flight.  An item is a tile of
+// 16 packed rows of one sequence and cache head; the positions of all items are
+// laid end to end in units of four warp blocks, a CTA takes an equal run of
+// units, whatever the lengths, and its warps stream their blocks through rings
+// that do not stop between items.  Pages of a multiple of 8 slots are copied by
+// bulk tensor copies through the page table, in boxes of 8 or 16 rows: keys in
+// columns of 64 bytes, values in columns of 128 bytes swizzled, so that the
+// reads below meet no bank twice.  Other page sizes take asynchronous 16-byte
+// copies, row by row, where every lane reads back exactly the chunks it copied
+// itself; they share the load/store pipe with the reads (256 users of up to
+// 8192 events: 444 us against 328).
+//  - scores: MMAs of 16 tokens x 8 rows (m16n8k16; fp32: m16n8k8).  The order
+//    of the summed elements is free, so a lane's 16-byte chunk of a key serves
+//    two MMA steps as it is, with the query's chunks in the same order.
+//  - output: MMAs of 16 columns x 8 rows, 16 tokens deep (fp32: 8).  Which
+//    columns form an MMA's 16 is free too: a lane's chunks of the same columns
+//    of four tokens, interleaved by byte permutes, are the operands of 4 MMAs
+//    (fp32: of two tokens, 2 MMAs, as they are).  The weights, whose tokens are
+//    in the lanes that hold rows next, are transposed by movmatrix (fp32: each
+//    half of their bits).
+// These are the warp's own MMAs, not those of tensor memory: 16 rows would fill
+// an eighth of such a tile, and the tensor pipe is 10 % busy as it is.
 // fp32 runs on TF32 MMAs: an operand is itself rounded to TF32 plus the rest (of
-// which the MMA reads 11 bits), and the three products of the split that matter carry each
-// product of two elements to about 2^-22 of its magnitude.  An MMA starts from zero and its sum is
-// added in fp32: the MMA's own additions are cut off, which leaves 1e-5 of the
-// output after 20000 events where a chain of MMAs runs on (4e-7 so, at 10 % more time).
-// A warp keeps its own running maximum, sum and output; the four are joined
-// in shared memory at an item's end.  An item that spans CTAs leaves
-// normalised partial rows and log2 of their sums, which a second kernel joins.
+// which the MMA reads 11 bits), and the three products of the split that matter
+// carry each product of two elements to about 2^-22 of its magnitude.  An MMA
+// starts from zero and its sum is added in fp32: the MMA's own additions are
+// cut off, which leaves 1e-5 of the output after 20000 events where a chain of
+// MMAs runs on (4e-7 so).
+// A warp keeps its own running maximum, sum and output; the four are joined in
+// shared memory at an item's end.  An item that spans CTAs leaves normalised
+// partial rows and log2 of their sums, which a second kernel joins.
+//
+// One event each of 256 users with up to 8192 events (16 heads on 4, 128 bf16
+// elements): 328 us, 6.2 TB/s, 0.92 of a plain copy.  One history of 262143:
+// 101 us, 5.3 TB/s, of which the join and its launch take 10.  fp32, 128 users
+// who see 512 events (4 heads on 2 of 64): 21 us, 2.5 TB/s; there a CTA has 9 units, and
+// its start, its end and the uneven spread of 256 items over 304 places count.
 #include "history.cuh"
 #include "tc.cuh"
 
