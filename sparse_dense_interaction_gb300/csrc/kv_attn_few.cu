@@ -248,7 +248,9 @@ struct FewShape {
     static constexpr int kStats = 2 * kGroups;                   // rows whose statistics a lane holds
     static constexpr int kOutMmas = E / 2;                       // of a set of output columns
     static constexpr int kOut = kGroups * VS * kOutMmas * 4;     // output registers
-    static constexpr int kSmem = 1024 + kFewWarps * kFewStages * kFewStageBytes + 2 * kOut * 32 * 4;
+    // registers joined at a time: with all 64 of them two CTAs would not fit on an SM
+    static constexpr int kMerge = kOut < 32 ? kOut : 32;
+    static constexpr int kSmem = 1024 + kFewWarps * kFewStages * kFewStageBytes + 2 * kMerge * 32 * 4;
     static constexpr int kKeyBox = MG * 64, kValueBox = MG * 128;  // bytes of a column of a group's keys, values
     static constexpr int kKeyBytes = kParts > 1 ? 0 : KG * kKeyBox;  // before a group's values
     static constexpr int kKeyChunks = kParts > 1 ? 0 : KT * KG;
@@ -287,7 +289,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     uint8_t *smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
     uint8_t *ring = smem + warp * kFewStages * kFewStageBytes;
-    float *merge = reinterpret_cast<float *>(smem + kFewWarps * kFewStages * kFewStageBytes);  // [2][kOut][32]
+    float *merge = reinterpret_cast<float *>(smem + kFewWarps * kFewStages * kFewStageBytes);  // [2][kMerge][32]
 
     FewItem it;  // of the unit being computed; `is`: of the unit whose addresses come next
     int units, quota = 0;  // of this CTA; the items' are counted from its first
@@ -705,26 +707,32 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
         for (int i = 0; i < Sh::kOut; i++)
             o[i] *= f[Sh::stat(i)];
-        if (warp >= 2)
 #pragma unroll
-            for (int i = 0; i < Sh::kOut; i++)
-                merge[((warp - 2) * Sh::kOut + i) * 32 + lane] = o[i];
-        __syncthreads();
-        if (warp < 2)
+        for (int r = 0; r < Sh::kOut; r += Sh::kMerge) {
+            if (r > 0)
+                __syncthreads();
+            if (warp >= 2)
 #pragma unroll
-            for (int i = 0; i < Sh::kOut; i++)
-                o[i] += merge[(warp * Sh::kOut + i) * 32 + lane];
-        if (warp == 1)
+                for (int i = 0; i < Sh::kMerge; i++)
+                    merge[((warp - 2) * Sh::kMerge + i) * 32 + lane] = o[r + i];
+            __syncthreads();
+            if (warp < 2)
 #pragma unroll
-            for (int i = 0; i < Sh::kOut; i++)
-                merge[(Sh::kOut + i) * 32 + lane] = o[i];
-        __syncthreads();
+                for (int i = 0; i < Sh::kMerge; i++)
+                    o[r + i] += merge[(warp * Sh::kMerge + i) * 32 + lane];
+            if (warp == 1)
+#pragma unroll
+                for (int i = 0; i < Sh::kMerge; i++)
+                    merge[(Sh::kMerge + i) * 32 + lane] = o[r + i];
+            __syncthreads();
+            if (warp == 0)
+#pragma unroll
+                for (int i = 0; i < Sh::kMerge; i++)
+                    o[r + i] += merge[(Sh::kMerge + i) * 32 + lane];
+        }
         if (warp == 0) {
             const bool whole = it.first >= 0 && it.last <= units;
             const int heads = p.cache.heads * p.group, slot = blockIdx.x * 2 + (first_item ? 0 : 1);
-#pragma unroll
-            for (int i = 0; i < Sh::kOut; i++)
-                o[i] += merge[(Sh::kOut + i) * 32 + lane];
 #pragma unroll
             for (int i = 0; i < Sh::kStats; i++) {
                 const int in = Sh::row(i, q), r = it.tile * kFewRows + in, t = r / p.group;
@@ -849,16 +857,28 @@ kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
         p.lse[token * heads + h] = weight > 0.f ? (top + log2f(weight)) * kLn2 : -INFINITY;
 }
 
-// Histories longer than this are shared out over CTAs in equal runs.
-constexpr int64_t kFewWhole = 1024;
+// Whether the positions are shared out in equal runs, or an item is a CTA's
+// whole.  Runs keep every CTA busy whatever the lengths; whole items need no
+// search for the CTA's share and no join, their CTAs start and end beside one
+// another, and an SM that is faster takes more of them.  Against that stands
+// the last CTAs' unevenness, a part of the time in which a CTA reads the
+// longest item.  So short items stay whole, and longer ones where there are
+// more to even them out.  bf16, whole against runs: 64 users with up to 2000
+// events, 8 heads of 64: 35 and 48 us; 256 users 98 and 128; 512 users with up to
+// 4000, 4 heads of 128: 326 and 352; 256 with up to 8192: 335 and 328; 64 users with
+// up to 8000, 2 heads of 64: 65 and 39; one with 3000: 26 and 16.
+constexpr int64_t kFewWholeBytes = 384 << 10, kFewWholeBytesPerItem = 3 << 10;
 
-bool few_splits(int64_t max_len) { return max_len > kFewWhole; }
+static bool few_splits(int64_t seen, int d, int es, int64_t items)
+{
+    return seen * d * 2 * es > kFewWholeBytes + items * kFewWholeBytesPerItem;
+}
 
 static int64_t few_rows(int64_t rows) { return rows < kFewRows ? rows : kFewRows; }
 
 size_t few_workspace(int64_t rows, int d, int64_t max_len)
 {
-    if (!few_splits(max_len))
+    if (!few_splits(max_len, d, 4, 0))
         return 0;
     return (size_t)2 * kFewCtas * few_rows(rows) * (d + 1) * sizeof(float) + kFewCtas * sizeof(FewJoin);
 }
@@ -879,12 +899,16 @@ static bool few_maps(const AttnParams &p, int dtype, int rows, FewMaps &m)
                                    (cuuint64_t)p.cache.page_stride * es};
     const cuuint32_t k_box[4] = {(cuuint32_t)(64 / es), (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
     const cuuint32_t v_box[4] = {(cuuint32_t)(128 / es), (cuuint32_t)rows, 1, 1};
+    // lines of 256 bytes where a head's rows fill them; else they would be its neighbours' (8
+    // interleaved heads of 64 16-bit elements: 146 us, 126 with 128)
+    const CUtensorMapL2promotion lines = p.d * es >= 256 || p.cache.slot_stride == p.d ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                                                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
     m.rows = rows;
     return enc(&m.k, type, 4, p.cache.k, dims, strides, k_box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+               CU_TENSOR_MAP_SWIZZLE_NONE, lines, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
                CUDA_SUCCESS &&
            enc(&m.v, type, 4, p.cache.v, dims, strides, v_box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+               CU_TENSOR_MAP_SWIZZLE_128B, lines, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
                CUDA_SUCCESS;
 }
 
@@ -898,13 +922,13 @@ static int launch_few(AttnParams &p, const FewMaps &maps, void *workspace, cudaS
         return s;
     // a window bounds what an item's rows see, whatever the history's length
     const int64_t seen = p.window > 0 ? p.window + (p.causal ? p.max_new : 0) : p.max_len;
-    const bool split = few_splits(seen < p.max_len ? seen : p.max_len);
+    const int64_t items = p.batch.S * p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows);
+    const bool split = few_splits(seen < p.max_len ? seen : p.max_len, p.d, sizeof(T), items);
     p.splits = split ? 2 : 1;
     p.joins = static_cast<FewJoin *>(workspace);
     p.part_o = reinterpret_cast<float *>(p.joins + kFewCtas);
     p.rows = (int)few_rows(p.max_new * p.group);
     p.part_lse = p.part_o + (size_t)2 * kFewCtas * p.rows * p.d;
-    const int64_t items = p.batch.S * p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows);
     if (items > 0x7fffffff)
         return DLRM_ERR_UNSUPPORTED;
     kv_attn_few_kernel<T, DP, kGroups, kBulk>
