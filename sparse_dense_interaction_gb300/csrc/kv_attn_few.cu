@@ -35,17 +35,17 @@
 // partial rows and log2 of their sums, which a second kernel joins.
 //
 // One event each of 256 users with up to 8192 events (16 heads on 4, 128 bf16
-// elements): 328 us, 6.2 TB/s, 0.92 of a plain copy.  One history of 262143:
-// 101 us, 5.3 TB/s, of which the join and its launch take 10.  fp32, 128 users
-// who see 512 events (4 heads on 2 of 64): 21 us, 2.5 TB/s; there a CTA has 9 units, and
-// its start, its end and the uneven spread of 256 items over 304 places count.
+// elements): 320 us, 6.4 TB/s, 0.94 of a plain copy.  One history of 262143:
+// 98 us, 5.5 TB/s, of which the join and its launch take 10.  fp32, 128 users who see
+// 512 events (4 heads on 2 of 64): 21 us, 2.5 TB/s; there a CTA has 9 units, and its
+// start, its end and the uneven spread of 256 items over 304 places count.
 #include "history.cuh"
 #include "tc.cuh"
 
 namespace dlrm {
 
-constexpr int kFewWarps = 4, kFewRows = 16, kFewStages = 3;
-constexpr int kFewCtas = 304;      // two for each of 152 SMs
+constexpr int kFewWarps = 4, kFewRows = 16;
+constexpr int kFewSms = 152, kFewMaxCtas = 3 * kFewSms;
 constexpr int kFewStageBytes = 8192;  // of a warp: keys and values of a block (16 tokens of 128 16-bit elements)
 constexpr int kFewMinUnits = 4;    // of a CTA: less is not worth a join
 
@@ -166,9 +166,9 @@ __device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int un
 }
 
 // Units of a CTA when `total` are shared out.
-__host__ __device__ __forceinline__ int64_t few_quota(int64_t total)
+__host__ __device__ __forceinline__ int64_t few_quota(int64_t total, int ctas)
 {
-    const int64_t q = (total + kFewCtas - 1) / kFewCtas;
+    const int64_t q = (total + ctas - 1) / ctas;
     return q < kFewMinUnits ? kFewMinUnits : q;
 }
 
@@ -201,7 +201,7 @@ __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int &quot
         before += i < warp ? sums[i] : 0;
         total += sums[i];
     }
-    const int64_t quota = few_quota(total);
+    const int64_t quota = few_quota(total, gridDim.x);
     const int64_t u0 = min(blockIdx.x * quota, total);
     units = (int)(min(u0 + quota, total) - u0);
     quota_units = (int)quota;
@@ -249,8 +249,13 @@ struct FewShape {
     static constexpr int kOutMmas = E / 2;                       // of a set of output columns
     static constexpr int kOut = kGroups * VS * kOutMmas * 4;     // output registers
     // registers joined at a time: with all 64 of them two CTAs would not fit on an SM
+    // CTAs of an SM and stages of a warp's ring: where 3 CTAs have the registers, two stages each keep as many bytes in
+    // flight as three of 2, and an item's start and end hide behind two others (256 users of up to 8192 events
+    // 329 -> 320 us, 512 users of up to 1000 with 8 heads of 64 117 -> 94)
+    static constexpr int kResident = kBulk && !kWide && kGroups == 1 ? 3 : 2, kStages = kResident == 3 ? 2 : 3;
+    static constexpr int kCtas = kResident * kFewSms;
     static constexpr int kMerge = kOut < 32 ? kOut : 32;
-    static constexpr int kSmem = 1024 + kFewWarps * kFewStages * kFewStageBytes + 2 * kMerge * 32 * 4;
+    static constexpr int kSmem = 1024 + kFewWarps * kStages * kFewStageBytes + 2 * kMerge * 32 * 4;
     static constexpr int kKeyBox = MG * 64, kValueBox = MG * 128;  // bytes of a column of a group's keys, values
     static constexpr int kKeyBytes = kParts > 1 ? 0 : KG * kKeyBox;  // before a group's values
     static constexpr int kKeyChunks = kParts > 1 ? 0 : KT * KG;
@@ -277,11 +282,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 }
 
 template <typename T, int DP, int kGroups, bool kBulk>
-__global__ void __launch_bounds__(kFewWarps * 32, 2)
+__global__ void __launch_bounds__(kFewWarps * 32, FewShape<T, DP, kGroups, kBulk>::kResident)
 kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FewMaps maps)
 {
     using Sh = FewShape<T, DP, kGroups, kBulk>;
-    constexpr int E = Sh::E, KT = Sh::KT, VT = Sh::VT, KG = Sh::KG, VS = Sh::VS, NB = Sh::NB, UT = Sh::UT, kParts = Sh::kParts;
+    constexpr int E = Sh::E, KT = Sh::KT, VT = Sh::VT, KG = Sh::KG, VS = Sh::VS, NB = Sh::NB, UT = Sh::UT, kParts = Sh::kParts, kFewStages = Sh::kStages;
     extern __shared__ uint8_t raw[];
     __shared__ float s_m[kFewWarps][kFewRows], s_l[kFewWarps][kFewRows];
     __shared__ uint64_t bars[kFewWarps][kFewStages];
@@ -880,7 +885,7 @@ size_t few_workspace(int64_t rows, int d, int64_t max_len)
 {
     if (!few_splits(max_len, d, 4, 0))
         return 0;
-    return (size_t)2 * kFewCtas * few_rows(rows) * (d + 1) * sizeof(float) + kFewCtas * sizeof(FewJoin);
+    return (size_t)2 * kFewMaxCtas * few_rows(rows) * (d + 1) * sizeof(float) + kFewMaxCtas * sizeof(FewJoin);
 }
 
 // Maps of the cache with boxes of `rows` slots; false where it cannot be
@@ -926,16 +931,16 @@ static int launch_few(AttnParams &p, const FewMaps &maps, void *workspace, cudaS
     const bool split = few_splits(seen < p.max_len ? seen : p.max_len, p.d, sizeof(T), items);
     p.splits = split ? 2 : 1;
     p.joins = static_cast<FewJoin *>(workspace);
-    p.part_o = reinterpret_cast<float *>(p.joins + kFewCtas);
+    p.part_o = reinterpret_cast<float *>(p.joins + kFewMaxCtas);
     p.rows = (int)few_rows(p.max_new * p.group);
-    p.part_lse = p.part_o + (size_t)2 * kFewCtas * p.rows * p.d;
+    p.part_lse = p.part_o + (size_t)2 * kFewMaxCtas * p.rows * p.d;
     if (items > 0x7fffffff)
         return DLRM_ERR_UNSUPPORTED;
     kv_attn_few_kernel<T, DP, kGroups, kBulk>
-        <<<(unsigned)(split ? kFewCtas : items), kFewWarps * 32, smem, st>>>(p, maps);
+        <<<(unsigned)(split ? FewShape<T, DP, kGroups, kBulk>::kCtas : items), kFewWarps * 32, smem, st>>>(p, maps);
     count_launch(st);
     if (split) {
-        kv_attn_few_join_kernel<T><<<dim3(kFewCtas - 1, (unsigned)p.rows), kJoinWarps * 32, 0, st>>>(p);
+        kv_attn_few_join_kernel<T><<<dim3(FewShape<T, DP, kGroups, kBulk>::kCtas - 1, (unsigned)p.rows), kJoinWarps * 32, 0, st>>>(p);
         count_launch(st);
     }
     return launch_status();
