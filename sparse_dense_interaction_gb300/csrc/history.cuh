@@ -162,6 +162,7 @@ enum AttnKernel { kAttnGeneral, kAttnTile };
 // (up to 200 candidates of each of 64 users: 55 us against 69).  More rows keep
 // the pair, which reads keys and values once for both tiles.
 inline int tile_rows(int64_t rows, int d) { return d <= 64 && rows <= 256 ? 128 : 256; }
+__host__ __device__ constexpr int tile_places(int rows) { return rows == 128 ? 2 * 152 : 152; }  // CTAs that run at once
 
 struct AttnPlan {
     AttnKernel kernel;
@@ -214,15 +215,15 @@ __device__ __forceinline__ int split_base(const Sequence &q, bool causal, int wi
 
 // The CTA's number: head fastest, then split, then tile, then sequence (or its
 // rank); returns the last, sets the head and the split.
-__device__ __forceinline__ int64_t attn_number(const AttnParams &p, int64_t cta, AttnWork &w, int64_t &tile)
+__device__ __forceinline__ int64_t attn_number(const AttnParams &p, uint32_t cta, AttnWork &w, int64_t &tile)
 {
-    const int hk = p.cache.heads;
+    const uint32_t hk = p.cache.heads, splits = p.splits, tiles = (uint32_t)p.tiles;
     w.head = (int)(cta % hk);
     cta /= hk;
-    w.split = (int)(cta % p.splits);
-    cta /= p.splits;
-    tile = p.tiles - 1 - cta % p.tiles;  // the longest rows of a causal chunk first
-    return cta / p.tiles;
+    w.split = (int)(cta % splits);
+    cta /= splits;
+    tile = tiles - 1 - cta % tiles;  // the longest rows of a causal chunk first
+    return cta / tiles;
 }
 
 // The rows and positions of a tile of the sequence w.seq; false where there is
@@ -246,7 +247,7 @@ __device__ __forceinline__ bool attn_rows(const AttnParams &p, int64_t tile, Att
     return true;
 }
 
-__device__ __forceinline__ bool attn_work(const AttnParams &p, int64_t cta, AttnWork &w)
+__device__ __forceinline__ bool attn_work(const AttnParams &p, uint32_t cta, AttnWork &w)
 {
     int64_t tile;
     w.s = attn_number(p, cta, w, tile);

@@ -173,15 +173,22 @@ kv_attn_join_kernel(const __grid_constant__ AttnParams p)
         for (int k = first + lane; k <= last; k += 32)
             top = fmaxf(top, p.part_lse[(int64_t)k * all + i]);
         top = warp_max(top);
+        const float base_top = top == -INFINITY ? 0.f : top;
         float total = 0.f, acc[DLRM_MAX_HEAD_DIM / 32] = {};
-        for (int k = first; k <= last; k++) {
-            const float f = exp2_approx(p.part_lse[(int64_t)k * all + i] - top);
-            total += f;
-            const float *o = p.part_o + ((int64_t)k * all + i) * p.d;
+        for (int k0 = first; k0 <= last; k0 += 32) {
+            // the weights by a lane each, then the parts, whose loads do not wait for one another
+            const int n = min(last - k0 + 1, 32);
+            const float mine = lane < n ? exp2_approx(p.part_lse[(int64_t)(k0 + lane) * all + i] - base_top) : 0.f;
+            total += warp_sum(mine);
+#pragma unroll 8
+            for (int k = 0; k < n; k++) {
+                const float f = __shfl_sync(0xffffffffu, mine, k);
+                const float *o = p.part_o + ((int64_t)(k0 + k) * all + i) * p.d;
 #pragma unroll
-            for (int j = 0; j < DLRM_MAX_HEAD_DIM / 32; j++)
-                if (lane + 32 * j < p.d)
-                    acc[j] = fmaf(o[lane + 32 * j], f, acc[j]);
+                for (int j = 0; j < DLRM_MAX_HEAD_DIM / 32; j++)
+                    if (lane + 32 * j < p.d)
+                        acc[j] = fmaf(o[lane + 32 * j], f, acc[j]);
+            }
         }
         const float inv = total > 0.f ? 1.f / total : 0.f;
         T *out = p.out.row<T>(token, h);
@@ -223,22 +230,29 @@ static AttnPlan plan_splits(AttnKernel kernel, int rows, int64_t S, int kv_heads
     return a;
 }
 
-// The number of splits that ends soonest, each CTA costing as much as 512
-// positions beside its share (its start, its end and the join).
-static AttnPlan plan_tile(int64_t S, int kv_heads, int group, int d, int64_t max_new, int64_t max_len)
+// The number of splits that ends soonest, for lengths that are all the longest
+// (rounds of CTAs) and for lengths of any size up to it (the CTAs' positions
+// shared out evenly, then the last CTA's own): the sum of both.  A CTA costs as
+// much as 512 positions beside its share (its start and its end), 704 where its
+// rows go through the join, which itself costs 512.  (24 sequences of up to 333
+// rows on up to 95129 positions: 213 us with 16 splits, 401 with the 3 that one
+// round takes; 8 of 1024 rows on 8192 each: 95 and 77, on up to 8192: 53 and 69.)
+static AttnPlan plan_tile(int64_t S, int kv_heads, int group, int d, int64_t max_new, int64_t seen)
 {
     const int rows = tile_rows(max_new * group, d);
-    const int64_t have = S * kv_heads * ceil_div(max_new * group, rows), longest = max_len + 127;
-    const int64_t places = rows == 128 ? 2 * kPlanSms : kPlanSms;
+    const int64_t have = S * kv_heads * ceil_div(max_new * group, rows), longest = seen + 127;
+    const int64_t places = tile_places(rows);
     int64_t best = 1, least = INT64_MAX;
-    for (int64_t s = 1; s <= 64 && (s == 1 || have * s <= 2 * places); s++) {
-        const int64_t cost = ceil_div(have * s, places) * (ceil_div(longest, s) + 512);
+    for (int64_t s = 1; s <= 64 && (s == 1 || (have < 2 * places && have * s <= 16 * places)); s++) {
+        const int64_t cta = s > 1 ? 704 : 512, own = ceil_div(longest, s) + cta;
+        const int64_t cost = ceil_div(have * s, places) * own + have * (longest / 2 + s * cta) / places + own +
+                             (s > 1 ? 1024 : 0);
         if (cost < least) {
             least = cost;
             best = s;
         }
     }
-    return plan_splits(kAttnTile, rows, S, kv_heads, group, max_new, max_len, have * best, 512);
+    return plan_splits(kAttnTile, rows, S, kv_heads, group, max_new, seen, best > 1 ? have * best : 1, 512);
 }
 
 static AttnPlan plan(AttnKernel kernel, int64_t S, int kv_heads, int group, int d, int64_t max_new, int64_t max_len)
@@ -309,10 +323,21 @@ static bool wide_rows(const AttnParams &p, int dtype)
 int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
 {
     const bool cores = wide_rows(p, dtype);
-    if (cores && (dtype == DLRM_F32 || p.max_new * p.group <= 16))
+    // a window bounds what a row sees, and a sequence's rows, whatever the history's length
+    const int64_t rows = p.max_new * p.group, bound = p.window + (p.causal ? p.max_new : 0);
+    const int64_t seen = p.window > 0 && bound < p.max_len ? bound : p.max_len;
+    // Rows of 16: for few of them the keys and values are read as often as by one tile of 256, and more CTAs
+    // fit on an SM.  150 users, 8 heads of 128, 32 rows: up to 100 events 51 us against 73, up to 1000
+    // 105 and 113, up to 2000 101 and 37 (64 users); 48 rows, up to 400: 90 and 88; heads of 64, 32 rows, up to 100: 42 and 40.
+    if (cores && (dtype == DLRM_F32 || rows <= 16 || (p.d > 64 && rows <= 32 && seen <= 1024)))
         return launch_kv_attn_few(p, dtype, workspace, st);
-    const AttnPlan a = plan(cores ? kAttnTile : kAttnGeneral, p.batch.S, p.cache.heads, p.group, p.d, p.max_new,
-                            p.max_len);
+    const AttnKernel kernel = cores ? kAttnTile : kAttnGeneral;
+    AttnPlan a = plan(kernel, p.batch.S, p.cache.heads, p.group, p.d, p.max_new, p.max_len);
+    if (seen < p.max_len) {  // never more parts than the workspace, whose size knows no window
+        const AttnPlan b = plan(kernel, p.batch.S, p.cache.heads, p.group, p.d, p.max_new, seen);
+        if (b.splits <= a.splits)
+            a = b;
+    }
     p.rows = a.rows;
     p.tiles = a.tiles;
     p.split_len = a.split_len;

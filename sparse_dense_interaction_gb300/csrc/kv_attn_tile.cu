@@ -97,13 +97,14 @@ __device__ __forceinline__ void copy_rows(uint8_t *tile, const char *base, int64
     }
 }
 
-// Copies the queries' rows (rows of zeros past the last).
+// Copies the queries' rows (in groups of this call's threads: rows of zeros
+// past the last; what lies in the groups after that reaches no output).
 template <typename Sh, int kThreads>
 __device__ __forceinline__ void copy_queries(const AttnParams &p, const AttnWork &w, uint8_t *sq)
 {
     const int tid = threadIdx.x - Sh::kSoftmaxThreads, row0 = tid & ~31;
 #pragma unroll 1
-    for (int r0 = 0; r0 < Sh::kRows; r0 += kThreads) {
+    for (int r0 = 0; r0 < w.rows; r0 += kThreads) {
         const int r = r0 + tid, row = w.row0 + r, token = row / p.group;
         const int64_t o = r < w.rows ? ((w.seq.first + token) * p.q.ts +
                                         (int64_t)(w.head * p.group + row - token * p.group) * p.q.hs) * 2
@@ -451,13 +452,14 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, TileBars &b
 // The CTA's work.  In batches of up to kRanked sequences the longest come
 // first, so that the last to start are the shortest: every CTA ranks the
 // lengths (64 users with up to 200 candidates: 63 us in the batch's order, 55
-// ranked).  Larger batches have enough CTAs to even out.  `room`: shared memory
-// for kRanked lengths and one sequence.
+// ranked).  More CTAs even out by themselves and would pay for the ranking (77
+// users' own up to 439 events, 64 heads on 8 of 64: 300 us against 353).
+// `room`: shared memory for kRanked lengths and one sequence.
 constexpr int kRanked = 256;
 
 __device__ bool tile_work(const AttnParams &p, int *room, AttnWork &w)
 {
-    if (p.batch.S > kRanked)
+    if (p.batch.S > kRanked || gridDim.x > 5 * tile_places(p.rows))
         return attn_work(p, blockIdx.x, w);
     int64_t tile;
     const int64_t rank = attn_number(p, blockIdx.x, w, tile);
