@@ -26,7 +26,7 @@
 // 2 x DP.
 //
 // 4 sequences of 2048 new events on 8192 (16 heads on 4, 128 bf16 elements):
-// 347 us, 1390 TFLOP/s, 0.73 of a large matrix product's rate (0.81 of the rate
+// 342 us, 1410 TFLOP/s, 0.74 of a large matrix product's rate (0.82 of the rate
 // that one keeps up for seconds): inside a CTA the tensor pipe is busy 80 % of
 // the time, and the chip draws all the power it may.  Up to 200 candidates of
 // each of 64 users with up to 2000 events (8 heads of 64 f16 elements): 55 us,
@@ -319,7 +319,7 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
 }
 
 template <typename T, int DP, bool kTwo>
-__device__ void tile_softmax(const AttnParams &p, const AttnWork &w, TileBars &b, int tiles)
+__device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq, TileBars &b, int tiles)
 {
     using Sh = TileShape<DP, kTwo>;
     constexpr int kHalf = kTilePos / 2, kCols = DP / 2;  // scores, output columns of a thread
@@ -420,33 +420,61 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, TileBars &b
         else if (p.lse)
             p.lse[(w.seq.first + token) * heads + h] = lse * kLn2;
     }
+    // Through the queries' tiles (their MMAs are done), so that a row's lines are
+    // written whole: a warp's 32 half rows, chunks of a row turned by its number
+    // against bank conflicts.  Partial rows are fp32 and take two passes.  (Written
+    // from the registers, a thread a row: 93 us instead of 88 for up to 300 new
+    // tokens of each of 64 sequences on up to 1000, 16 heads on 4 of 128.)
+    constexpr int kRowBytes = kCols * 2, kRowChunks = kRowBytes / 16;
+    uint8_t *room = sq + warp * 32 * kRowBytes;
+    const int lane = threadIdx.x & 31;
+    auto at = [&](int r, int c) {
+        return reinterpret_cast<uint4 *>(room + r * kRowBytes + ((c ^ (kRowChunks == 8 ? r & 7 : r >> 1 & 3)) << 4));
+    };
+    char *to = nullptr;
+    if (mine)
+        to = w.whole ? reinterpret_cast<char *>(p.out.row<T>(w.seq.first + token, h))
+                     : reinterpret_cast<char *>(p.part_o + part * p.d);
+    auto write = [&](auto whole) {
+        constexpr int es = decltype(whole)::value ? 2 : 4, cols = kRowBytes / es;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kCols; c0 += cols) {
+            __syncwarp();
 #pragma unroll
-    for (int c = 0; c < kCols; c += 16) {
-        uint32_t x[16];
-        float o[16];
-        __syncwarp();
-        if (tiles > 0)
-            tc::tmem_ld16(o_at + c, x);
+            for (int c = 0; c < cols; c += 16) {
+                uint32_t x[16];
+                float o[16];
+                if (tiles > 0)
+                    tc::tmem_ld16(o_at + c0 + c, x);
 #pragma unroll
-        for (int i = 0; i < 16; i++)
-            o[i] = inv > 0.f ? __uint_as_float(x[i]) * inv : 0.f;
-        const int e = half * kCols + c;
-        if (mine && w.whole) {
-            T *out = p.out.row<T>(w.seq.first + token, h) + e;
+                for (int i = 0; i < 16; i++)
+                    o[i] = inv > 0.f ? __uint_as_float(x[i]) * inv : 0.f;
+                if constexpr (es == 2)
 #pragma unroll
-            for (int i = 0; i < 16; i += 8)
-                if (e + i < p.d)
-                    *reinterpret_cast<uint4 *>(out + i) =
-                        make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]), pack2<T>(o[i + 4], o[i + 5]),
-                                   pack2<T>(o[i + 6], o[i + 7]));
-        } else if (mine) {
-            float *out = p.part_o + part * p.d + e;
+                    for (int i = 0; i < 16; i += 8)
+                        *at(lane, (c + i) / 8) = make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]),
+                                                            pack2<T>(o[i + 4], o[i + 5]), pack2<T>(o[i + 6], o[i + 7]));
+                else
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                if (e + i < p.d)
-                    *reinterpret_cast<float4 *>(out + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 16; i += 4)
+                        *at(lane, (c + i) / 4) = make_uint4(__float_as_uint(o[i]), __float_as_uint(o[i + 1]),
+                                                            __float_as_uint(o[i + 2]), __float_as_uint(o[i + 3]));
+            }
+            __syncwarp();
+            const int e = half * kCols + c0, c = lane % kRowChunks;
+#pragma unroll
+            for (int i = 0; i < kRowChunks; i++) {
+                const int r = (i * 32 + lane) / kRowChunks;
+                char *row_to = reinterpret_cast<char *>(__shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(to), r));
+                if (row_to && e + c * (16 / es) < p.d)
+                    *reinterpret_cast<uint4 *>(row_to + e * es + c * 16) = *at(r, c);
+            }
         }
-    }
+    };
+    if (w.whole)
+        write(std::true_type{});
+    else
+        write(std::false_type{});
 }
 
 // The CTA's work.  In batches of up to kRanked sequences the longest come
@@ -508,6 +536,12 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     uint8_t *ring = sq + Sh::kRows / 128 * Sh::kTileBytes;
     TileBars &b = *reinterpret_cast<TileBars *>(sq + Sh::kTiles);
     const int warp = threadIdx.x >> 5;
+    if (kBulk && threadIdx.x == Sh::kSoftmaxThreads) {  // on their way while the CTA finds its work
+        if (!maps.q_rows)
+            tc::prefetch_map(&maps.q);
+        tc::prefetch_map(&maps.k);
+        tc::prefetch_map(&maps.v);
+    }
     AttnWork w;
     if (!tile_work(p, reinterpret_cast<int *>(sq), w))
         return;
@@ -536,7 +570,7 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     tc::fence_after_sync();
     if (warp < Sh::kSoftmaxWarps) {
         if (warp < 8 || two)
-            tile_softmax<T, DP, kTwo>(p, w, b, tiles);
+            tile_softmax<T, DP, kTwo>(p, w, sq, b, tiles);
     } else if (warp < kLast) {
         if (tiles > 0) {
             if constexpr (kBulk) {

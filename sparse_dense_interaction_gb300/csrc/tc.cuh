@@ -287,6 +287,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Fetches a tensor map ahead of the first copy that uses it.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // x with the 13 bits below TF32 precision cleared: the value a TF32 MMA reads
 // from an fp32 operand in shared memory (it ignores those bits).
 __device__ __forceinline__ float tf32_trunc(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
