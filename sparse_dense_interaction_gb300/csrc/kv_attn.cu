@@ -243,7 +243,12 @@ static AttnPlan plan_tile(int64_t S, int kv_heads, int group, int d, int64_t max
     const int64_t have = S * kv_heads * ceil_div(max_new * group, rows), longest = seen + 127;
     const int64_t places = tile_places(rows);
     int64_t best = 1, least = INT64_MAX;
-    for (int64_t s = 1; s <= 64 && (s == 1 || (have < 2 * places && have * s <= 16 * places)); s++) {
+    // one, or as many as fill 1 to 16 rounds of places
+    for (int64_t round = 0, last = 0; round <= (have < 2 * places ? 16 : 0); round++) {
+        const int64_t most = round * places / (have < 1 ? 1 : have), s = most < 1 ? 1 : (most < 64 ? most : 64);
+        if (s == last)
+            continue;
+        last = s;
         const int64_t cta = s > 1 ? 704 : 512, own = ceil_div(longest, s) + cta;
         const int64_t cost = ceil_div(have * s, places) * own + have * (longest / 2 + s * cta) / places + own +
                              (s > 1 ? 1024 : 0);
