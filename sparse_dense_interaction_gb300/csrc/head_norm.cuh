@@ -1,14 +1,15 @@
 // Shared by the kernels over rows of heads: the scalar helpers and the vector
 // path's row layout.
 //
-// Vector path: GL lanes (8, 16 or 32) hold a row of up to 8 GL elements, 8 a
-// lane in two pieces of 4, chosen so that the elements that turn together are
+// Vector path: GL lanes (4, 8, 16 or 32) hold a row of up to 8 GL elements, 8
+// a lane in two pieces of 4, chosen so that the elements that turn together are
 // one lane's.  A warp takes a chunk of the heads of `run` tokens (32 at most), a
-// row for each lane group at a time; such slots stream through a ring in
-// shared memory by asynchronous copies, several ahead of the one that is computed:
-// a lane reads back what it copied itself.  What a token needs beside its
-// rows (its angles' row, where its rows go) one lane finds out for each token
-// before the first.
+// row for each lane group at a time, of one token or, where a token has at most
+// half as many heads as there are groups, of 2, 4 or 8; such slots stream through a
+// ring in shared memory by asynchronous copies, several ahead of the one that is
+// computed: a lane reads back what it copied itself.  What a token needs beside
+// its rows (its angles' row, where its rows go) one lane finds out for each
+// token before the first.
 #pragma once
 
 #include "history.cuh"
@@ -22,12 +23,12 @@ constexpr int kSlots = 4;  // of a chunk of a token's heads: a row for each lane
 constexpr int kMaxRun = 32;
 
 // The ring of a warp: slots of kIn rows for each lane group, and the angles of
-// as many tokens.
+// their tokens (`fold` to a slot).
 template <typename T, int GL, int kIn>
 struct Ring {
     static constexpr int kPiece = 4 * sizeof(T), kSlot = kIn * 2 * 32 * kPiece, kAngles = GL * 32;
     static constexpr int kDepth = kSlot <= 512 ? 6 : (kSlot <= 1024 ? 5 : 3);  // deeper rings measured no faster
-    static constexpr int kBytes = kDepth * (kSlot + kAngles);
+    __host__ __device__ static constexpr int bytes(int fold) { return kDepth * (kSlot + kAngles * fold); }
 };
 
 // The rope row of a position, or null with the flag raised where it is
@@ -177,13 +178,13 @@ struct Angles {
 };
 
 // Copies a token's angles to shared memory: 8 floats for each lane of a group,
-// by the first group.
+// by the token's first group (`mine`).
 template <int GL>
-__device__ __forceinline__ void copy_angles(uint8_t *to, const float *row, int half, const RowLane<GL> &at)
+__device__ __forceinline__ void copy_angles(uint8_t *to, const float *row, int half, const RowLane<GL> &at, bool mine)
 {
-    if (at.group == 0 && at.angle >= 0 && row) {
-        copy_piece<16>(to + (threadIdx.x & 31) * 32, row + at.angle, true);
-        copy_piece<16>(to + (threadIdx.x & 31) * 32 + 16, row + half + at.angle, true);
+    if (mine && at.angle >= 0 && row) {
+        copy_piece<16>(to + threadIdx.x % GL * 32, row + at.angle, true);
+        copy_piece<16>(to + threadIdx.x % GL * 32 + 16, row + half + at.angle, true);
     }
 }
 
@@ -194,6 +195,32 @@ struct NormSide {
     HeadsView x, dy, out;  // dy: of the gradient alone
     const float *w;
     int chunks;            // of a token's heads; the CTAs of chunk blockIdx.y
+    int fold;              // tokens of a slot
+
+    // 195312 tokens of 4 query heads and one key head of 64 bf16 elements: 81 us, 107 with one token a slot; 488281 of
+    // one and one: 108 and 243
+    void lay_out(int groups)
+    {
+        chunks = (x.heads + kSlots * groups - 1) / (kSlots * groups);
+        for (fold = 1; x.heads > 0 && x.heads * fold * 2 <= groups;)
+            fold *= 2;
+    }
+};
+
+// Where a lane group works: its token of a slot, the first head of its chunk
+// and its own, the slots of a token.
+struct Fold {
+    int token, head, slots;
+    bool first;  // the token's first group
+
+    __device__ __forceinline__ Fold(const NormSide &side, int chunk, int group, int groups)
+    {
+        const int per = groups / side.fold, base = chunk * kSlots * groups;
+        token = group / per;
+        head = base + group % per;
+        first = group % per == 0;
+        slots = min(kSlots, (side.x.heads - base + groups - 1) / groups);
+    }
 };
 
 // The side of chunk `chunk`, which becomes the chunk's number within it.
@@ -313,7 +340,9 @@ static inline int64_t run_tokens(int64_t n, int64_t chunks, int64_t resident, in
     return run < 1 ? 1 : run;
 }
 
-// f<T, GL, interleaved>(...) of the call's type, width and layout.
+// f<T, GL, interleaved>(...) of the call's type, width and layout: the fewest
+// lanes that hold a row (97656 tokens of 16 and 4 heads of 32 bf16 elements: 53
+// us with 4 lanes, 87 with 8).
 #define DLRM_HEAD_DISPATCH(f, d, dtype, interleaved, ...)                                                             \
     do {                                                                                                              \
         if (dtype == DLRM_F32)                                                                                        \
@@ -324,6 +353,8 @@ static inline int64_t run_tokens(int64_t n, int64_t chunks, int64_t resident, in
     } while (0)
 #define DLRM_HEAD_WIDTH(f, T, d, interleaved, ...)                                                                    \
     do {                                                                                                              \
+        if (d <= 32)                                                                                                  \
+            return interleaved ? f<T, 4, true>(__VA_ARGS__) : f<T, 4, false>(__VA_ARGS__);                            \
         if (d <= 64)                                                                                                  \
             return interleaved ? f<T, 8, true>(__VA_ARGS__) : f<T, 8, false>(__VA_ARGS__);                            \
         if (d <= 128)                                                                                                 \

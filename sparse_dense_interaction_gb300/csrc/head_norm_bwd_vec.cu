@@ -17,6 +17,7 @@ constexpr int kBwdResident = 2, kBwdRun = 24;
 
 struct NormBwdParams {
     NormSide side[2];
+    int fold;  // the larger of theirs
     RopeView rope;
     int64_t n;
     int d, run;
@@ -38,37 +39,39 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
     const RowLane<GL> at(p.d, p.rope);
     int chunk = blockIdx.y;
     const NormSide &me = p.side[side_of(p.side, chunk)];
-    const int head = chunk * kSlots * at.kGroups + at.group;
-    const int slots = min(kSlots, (me.x.heads - head + at.group + at.kGroups - 1) / at.kGroups);
+    const Fold my(me, chunk, at.group, at.kGroups);
+    const int fold = me.fold, head = my.head, slots = my.slots;
     const int rows = at.active ? me.x.heads - head : 0;  // from this lane's group on
     const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.run;
     const int tokens = (int)max(min((int64_t)p.run, p.n - first), (int64_t)0);
-    uint8_t *ring = smem + (threadIdx.x >> 5) * R::kBytes, *angle_ring = ring + R::kDepth * R::kSlot;
-    uint8_t *mine = ring + lane * R::kPiece;
+    const int steps = (tokens + fold - 1) / fold, angle_bytes = R::kAngles * fold;
+    uint8_t *ring = smem + (threadIdx.x >> 5) * R::bytes(p.fold);
+    uint8_t *angle_ring = ring + R::kDepth * R::kSlot + my.token * R::kAngles, *mine = ring + lane * R::kPiece;
 
     const float *my_angles = nullptr;  // lane i: token i's
     if (p.rope.table && lane < tokens)
         my_angles = rope_row(p.rope, __ldg(p.rope.positions + first + lane), p.err);
 
     // the copies run kDepth - 1 slots ahead
-    const T *x_row = me.x.row<T>(first, head), *y_row = me.dy.row<T>(first, head);
+    const T *x_row = me.x.row<T>(first + my.token, head), *y_row = me.dy.row<T>(first + my.token, head);
     const int64_t x_step = at.kGroups * me.x.hs, y_step = at.kGroups * me.dy.hs;
-    int ahead_token = 0, ahead_slot = 0, ahead = 0;
+    int ahead_step = 0, ahead_slot = 0, ahead = 0;
     auto copy = [&] {
-        if (ahead_token < tokens) {
+        if (ahead_step < steps) {
+            const int token = ahead_step * fold + my.token;
             if (ahead_slot == 0) {
                 const float *a = reinterpret_cast<const float *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), ahead_token));
-                copy_angles<GL>(angle_ring + ahead_token % R::kDepth * R::kAngles, a, p.rope.rot >> 1, at);
+                    __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), token));
+                copy_angles<GL>(angle_ring + ahead_step % R::kDepth * angle_bytes, a, p.rope.rot >> 1, at, my.first);
             }
-            const bool there = ahead_slot * at.kGroups < rows;
+            const bool there = ahead_slot * at.kGroups < rows && token < tokens;
             copy_row<T, GL>(mine + ahead * R::kSlot, x_row, me.x.ptr, there, at);
             copy_row<T, GL>(mine + ahead * R::kSlot + R::kSlot / 2, y_row, me.x.ptr, there, at);
             const bool last = ahead_slot + 1 == slots;
-            x_row += last ? me.x.ts - (slots - 1) * x_step : x_step;
-            y_row += last ? me.dy.ts - (slots - 1) * y_step : y_step;
+            x_row += last ? fold * me.x.ts - (slots - 1) * x_step : x_step;
+            y_row += last ? fold * me.dy.ts - (slots - 1) * y_step : y_step;
             ahead_slot = last ? 0 : ahead_slot + 1;
-            ahead_token += last;
+            ahead_step += last;
         }
         ahead = ahead + 1 == R::kDepth ? 0 : ahead + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -81,16 +84,17 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
     const float inv_d = 1.f / (float)p.d;
     const float2 *wa = sw[lane % GL], *wb = wa + 2;
     float2 da[2] = {}, db[2] = {};
-    T *to = me.out.row<T>(first, head);
-    const int64_t to_step = at.kGroups * me.out.hs, to_wrap = me.out.ts - slots * to_step;
+    T *to = me.out.row<T>(first + my.token, head);
+    const int64_t to_step = at.kGroups * me.out.hs, to_wrap = fold * me.out.ts - slots * to_step;
     int slot = 0;
 #pragma unroll 1
-    for (int i = 0; i < tokens; i++, to += to_wrap) {
-        const bool bad = p.rope.table && !__shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), i);
+    for (int i = 0; i < steps; i++, to += to_wrap) {
+        const int token = i * fold + my.token;
+        const bool bad = p.rope.table && !__shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), token);
         copy();
         asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
         __syncwarp();
-        const Angles t(reinterpret_cast<const float4 *>(angle_ring + i % R::kDepth * R::kAngles + lane % GL * 32),
+        const Angles t(reinterpret_cast<const float4 *>(angle_ring + i % R::kDepth * angle_bytes + lane % GL * 32),
                        at.angle >= 0 && !bad);
         const float2 c[2] = {make_float2(t.c.x, t.c.y), make_float2(t.c.z, t.c.w)};
         const float2 s[2] = {make_float2(t.s.x, t.s.y), make_float2(t.s.z, t.s.w)};
@@ -104,6 +108,9 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
             read_row<T>(mine + slot * R::kSlot, x);
             read_row<T>(mine + slot * R::kSlot + R::kSlot / 2, y);
             slot = slot + 1 == R::kDepth ? 0 : slot + 1;
+            const bool there = u * at.kGroups < rows && token < tokens, counts = there && !bad;
+            if (!counts)  // gives zeros, and adds nothing
+                x[0] = x[1] = y[0] = y[1] = Raw{};
             float2 a[2], b[2], ga[2], gb[2];
             widen_row<T, kInterleaved>(x, a, b);
             widen_row<T, kInterleaved>(y, ga, gb);
@@ -113,8 +120,8 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
                 ga[i] = __ffma2_rn(f, c[i], __fmul2_rn(g, s[i]));
                 gb[i] = __ffma2_rn(g, c[i], __fmul2_rn(make_float2(-f.x, -f.y), s[i]));
             }
-            Raw z[2] = {Raw{}, Raw{}};
-            if (me.w && !bad) {
+            Raw z[2];
+            if (me.w) {
                 float2 va[2], vb[2], sq = make_float2(0.f, 0.f), gx = sq;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
@@ -129,7 +136,7 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
                     s1 += __shfl_xor_sync(0xffffffffu, s1, o);
                     s2 += __shfl_xor_sync(0xffffffffu, s2, o);
                 }
-                const float r = rsqrt_approx(fmaf(s1, inv_d, p.eps)), m = -s2 * inv_d * r * r;
+                const float r = counts ? rsqrt_approx(fmaf(s1, inv_d, p.eps)) : 0.f, m = -s2 * inv_d * r * r;
                 const float2 rr = make_float2(r, r), mm = make_float2(m, m);
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
@@ -141,9 +148,8 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
                     gb[i] = __ffma2_rn(vb[i], rr, __fmul2_rn(b[i], mm));
                 }
             }
-            if (!bad)
-                narrow_row<T, kInterleaved>(ga, gb, z);
-            store_row<T, GL>(to, u * at.kGroups < rows, at, z);
+            narrow_row<T, kInterleaved>(ga, gb, z);
+            store_row<T, GL>(to, there, at, z);
             to += to_step;
         }
     }
@@ -177,7 +183,7 @@ static int64_t bwd_run(int64_t n, int64_t chunks) { return run_tokens(n, chunks,
 
 size_t norm_bwd_vec_workspace(int64_t n, int qh, int kh, int d)
 {
-    const int64_t heads = kSlots * (d <= 64 ? 4 : (d <= 128 ? 2 : 1)), chunks = div_up(qh, heads) + div_up(kh, heads);
+    const int64_t heads = kSlots * (d <= 32 ? 8 : (d <= 64 ? 4 : (d <= 128 ? 2 : 1))), chunks = div_up(qh, heads) + div_up(kh, heads);
     return (size_t)(chunks * div_up(n, kWarps * bwd_run(n, chunks))) * d * sizeof(float) + 16;
 }
 
@@ -188,11 +194,15 @@ static int norm_bwd_vec(const HeadsView &dqo, const HeadsView &dko, const HeadsV
                         int d, const float *qw, const float *kw, float eps, const RopeView &rope, const HeadsView &dq,
                         const HeadsView &dk, float *dqw, float *dkw, float *part, int32_t *err, cudaStream_t st)
 {
-    const int64_t heads = kSlots * (32 / GL), qc = div_up(q.heads, heads), kc = div_up(k.heads, heads);
-    const int64_t run = bwd_run(n, qc + kc), x = div_up(n, kWarps * run);
     NormBwdParams p = {};
-    p.side[0] = {q, dqo, dq, qw, (int)qc};
-    p.side[1] = {k, dko, dk, kw, (int)kc};
+    p.side[0] = {q, dqo, dq, qw, 0, 1};
+    p.side[1] = {k, dko, dk, kw, 0, 1};
+    p.fold = 1;
+    for (NormSide &side : p.side) {
+        side.lay_out(32 / GL);
+        p.fold = side.fold > p.fold ? side.fold : p.fold;
+    }
+    const int64_t qc = p.side[0].chunks, kc = p.side[1].chunks, run = bwd_run(n, qc + kc), x = div_up(n, kWarps * run);
     p.rope = rope;
     p.n = n;
     p.d = d;
@@ -200,12 +210,13 @@ static int norm_bwd_vec(const HeadsView &dqo, const HeadsView &dko, const HeadsV
     p.eps = eps;
     p.part = part;
     p.err = err;
-    constexpr int smem = kWarps * Ring<T, GL, 2>::kBytes;
     static std::atomic<unsigned long long> done{0};
-    const int s = allow_dynamic_smem((const void *)norm_rope_bwd_vec_kernel<T, GL, kInterleaved>, smem, &done);
+    const int s = allow_dynamic_smem((const void *)norm_rope_bwd_vec_kernel<T, GL, kInterleaved>,
+                                     kWarps * Ring<T, GL, 2>::bytes(32 / GL), &done);
     if (s != DLRM_OK)
         return s;
-    norm_rope_bwd_vec_kernel<T, GL, kInterleaved><<<dim3((unsigned)x, (unsigned)(qc + kc)), kWarps * 32, smem, st>>>(p);
+    norm_rope_bwd_vec_kernel<T, GL, kInterleaved><<<dim3((unsigned)x, (unsigned)(qc + kc)), kWarps * 32,
+                                                 kWarps * Ring<T, GL, 2>::bytes(p.fold), st>>>(p);
     count_launch(st);
     if (dqw || dkw)
         launch_norm_weight_sum(part, x * qc, x * kc, d, dqw, dkw, st);

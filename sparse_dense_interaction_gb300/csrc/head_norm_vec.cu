@@ -17,6 +17,7 @@ constexpr int kResident = 3, kRun = kMaxRun;
 
 struct NormParams {
     NormSide side[3];  // queries, keys, values; out: not of keys and values that go to the cache
+    int fold;          // the largest of them
     RopeView rope;
     BatchView batch;   // of the append; else only n
     CacheView cache;
@@ -62,13 +63,14 @@ norm_rope_vec_kernel(const __grid_constant__ NormParams p)
     const int which = side_of(p.side, chunk);
     const NormSide &me = p.side[which];
     const bool is_v = kAppend && which == 2, cached = kAppend && which > 0;
-    const int head = chunk * kSlots * at.kGroups + at.group;
-    const int slots = min(kSlots, (me.x.heads - head + at.group + at.kGroups - 1) / at.kGroups);
+    const Fold my(me, chunk, at.group, at.kGroups);
+    const int fold = me.fold, head = my.head, slots = my.slots;
     const int rows = at.active ? me.x.heads - head : 0;  // from this lane's group on
     const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.run;
     const int tokens = (int)max(min((int64_t)p.run, p.batch.n - first), (int64_t)0);
-    uint8_t *ring = smem + (threadIdx.x >> 5) * R::kBytes, *angle_ring = ring + R::kDepth * R::kSlot;
-    uint8_t *mine = ring + lane * R::kPiece;
+    const int steps = (tokens + fold - 1) / fold, angle_bytes = R::kAngles * fold;
+    uint8_t *ring = smem + (threadIdx.x >> 5) * R::bytes(p.fold);
+    uint8_t *angle_ring = ring + R::kDepth * R::kSlot + my.token * R::kAngles, *mine = ring + lane * R::kPiece;
 
     // lane i: token i's angles, and where its rows go (0: it is left out)
     const float *my_angles = nullptr;
@@ -110,21 +112,23 @@ norm_rope_vec_kernel(const __grid_constant__ NormParams p)
     }
 
     // the copies run kDepth - 1 slots ahead
-    const T *row = me.x.row<T>(first, head);
-    const int64_t step = at.kGroups * me.x.hs, wrap = me.x.ts - (slots - 1) * step;
-    int ahead_token = 0, ahead_slot = 0, ahead = 0;
+    const T *row = me.x.row<T>(first + my.token, head);
+    const int64_t step = at.kGroups * me.x.hs, wrap = fold * me.x.ts - (slots - 1) * step;
+    int ahead_step = 0, ahead_slot = 0, ahead = 0;
     auto copy = [&] {
-        if (ahead_token < tokens) {
+        if (ahead_step < steps) {
+            const int token = ahead_step * fold + my.token;
             if (ahead_slot == 0 && !is_v) {
                 const float *a = reinterpret_cast<const float *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), ahead_token));
-                copy_angles<GL>(angle_ring + ahead_token % R::kDepth * R::kAngles, a, p.rope.rot >> 1, at);
+                    __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), token));
+                copy_angles<GL>(angle_ring + ahead_step % R::kDepth * angle_bytes, a, p.rope.rot >> 1, at, my.first);
             }
-            copy_row<T, GL>(mine + ahead * R::kSlot, row, me.x.ptr, ahead_slot * at.kGroups < rows, at);
+            copy_row<T, GL>(mine + ahead * R::kSlot, row, me.x.ptr,
+                            ahead_slot * at.kGroups < rows && token < tokens, at);
             const bool last = ahead_slot + 1 == slots;
             row += last ? wrap : step;
             ahead_slot = last ? 0 : ahead_slot + 1;
-            ahead_token += last;
+            ahead_step += last;
         }
         ahead = ahead + 1 == R::kDepth ? 0 : ahead + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -139,16 +143,17 @@ norm_rope_vec_kernel(const __grid_constant__ NormParams p)
     const int64_t to_head = head * (cached ? p.cache.head_stride : me.out.hs);
     int slot = 0;
 #pragma unroll 1
-    for (int t = 0; t < tokens; t++) {
-        T *to = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, my_to, t));
+    for (int t = 0; t < steps; t++) {
+        const int token = t * fold + my.token;
+        T *to = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, my_to, token));  // none past the last token
         const bool there = to != nullptr;
         const bool turns = p.rope.table && !is_v;
-        const bool zero = turns && !__shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), t);
+        const bool zero = turns && !__shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), token);
         to += to_head;
         copy();
         asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
         __syncwarp();
-        const Angles angles(reinterpret_cast<const float4 *>(angle_ring + t % R::kDepth * R::kAngles + lane % GL * 32),
+        const Angles angles(reinterpret_cast<const float4 *>(angle_ring + t % R::kDepth * angle_bytes + lane % GL * 32),
                             at.angle >= 0 && turns && !zero);
         const Turn turn(angles, sw[lane % GL]);
 #pragma unroll 1
@@ -177,17 +182,22 @@ norm_rope_vec_kernel(const __grid_constant__ NormParams p)
 template <typename T, int GL, bool kInterleaved, bool kAppend>
 static int norm_launch(NormParams &p, cudaStream_t st)
 {
-    constexpr int smem = kWarps * Ring<T, GL, 1>::kBytes;
     static std::atomic<unsigned long long> done{0};
-    const int s = allow_dynamic_smem((const void *)norm_rope_vec_kernel<T, GL, kInterleaved, kAppend>, smem, &done);
+    const int s = allow_dynamic_smem((const void *)norm_rope_vec_kernel<T, GL, kInterleaved, kAppend>,
+                                     kWarps * Ring<T, GL, 1>::bytes(32 / GL), &done);
     if (s != DLRM_OK)
         return s;
     int64_t chunks = 0;
-    for (NormSide &side : p.side)
-        chunks += side.chunks = (int)div_up(side.x.heads, kSlots * (32 / GL));
+    p.fold = 1;
+    for (NormSide &side : p.side) {
+        side.lay_out(32 / GL);
+        chunks += side.chunks;
+        p.fold = side.fold > p.fold ? side.fold : p.fold;
+    }
     p.run = (int)run_tokens(p.batch.n, chunks, kResident, kRun);
     norm_rope_vec_kernel<T, GL, kInterleaved, kAppend>
-        <<<dim3((unsigned)div_up(p.batch.n, kWarps * p.run), (unsigned)chunks), kWarps * 32, smem, st>>>(p);
+        <<<dim3((unsigned)div_up(p.batch.n, kWarps * p.run), (unsigned)chunks), kWarps * 32,
+           kWarps * Ring<T, GL, 1>::bytes(p.fold), st>>>(p);
     count_launch(st);
     return launch_status();
 }
@@ -202,8 +212,8 @@ int launch_norm_rope_vec(const HeadsView &q, const HeadsView &k, int64_t n, int 
                          int32_t *err, cudaStream_t st)
 {
     NormParams p = {};
-    p.side[0] = {q, {}, qo, qw, 0};
-    p.side[1] = {k, {}, ko, kw, 0};
+    p.side[0] = {q, {}, qo, qw, 0, 1};
+    p.side[1] = {k, {}, ko, kw, 0, 1};
     p.rope = rope;
     p.batch.n = n;
     p.d = d;
@@ -217,9 +227,9 @@ int launch_kv_append_vec(const HeadsView &k, const HeadsView &v, const BatchView
                          const float *qw, const HeadsView &qo, int32_t *err, cudaStream_t st)
 {
     NormParams p = {};
-    p.side[0] = {q, {}, qo, qw, 0};
-    p.side[1] = {k, {}, {}, kw, 0};
-    p.side[2] = {v, {}, {}, nullptr, 0};
+    p.side[0] = {q, {}, qo, qw, 0, 1};
+    p.side[1] = {k, {}, {}, kw, 0, 1};
+    p.side[2] = {v, {}, {}, nullptr, 0, 1};
     p.rope = rope;
     p.batch = batch;
     p.cache = cache;

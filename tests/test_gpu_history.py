@@ -177,6 +177,22 @@ def test_norm_rope_of_broadcast_inputs(dtype, d):
     close(dw, wsum, R.weight_tolerance(wmag, 64 + n * h // 64), "weight")
 
 
+@pytest.mark.parametrize("n,hq,hk,d,dtype", [(5, 3, 1, 64, "f32"), (11, 1, 3, 32, "bf16"), (33, 2, 1, 24, "f16"),
+                                             (70, 5, 1, 32, "f32"), (9, 1, 1, 128, "bf16")])
+def test_norm_gradient_without_an_epsilon(n, hq, hk, d, dtype):
+    # lanes and rows that hold nothing must not turn into 0 * infinity
+    x, dy = randn(1, (n, hq + hk, d), dtype, 1.5), randn(2, (n, hq + hk, d), dtype)
+    w = [1 + 0.3 * randn(3 + i, (d,), "f32") for i in (0, 1)]
+    dx, dw = torch.empty_like(x), [torch.empty(d, device=DEV) for _ in range(2)]
+    ws = torch.full((sdi.dlrm_qk_norm_rope_bwd_workspace_size(n, hq, hk, d),), 255, dtype=torch.uint8, device=DEV)
+    sdi.dlrm_qk_norm_rope_bwd(dy[:, :hq], dy[:, hq:], x[:, :hq], x[:, hq:], w[0], w[1], 0.0, None, None, dx[:, :hq],
+                              dx[:, hq:], dw[0], dw[1], ws)
+    for i, part in enumerate((slice(0, hq), slice(hq, hq + hk))):
+        want, mag, wsum, wmag = R.norm_rope_bwd(np64(dy[:, part]), np64(x[:, part]), np64(w[i]), 0.0, None, None)
+        close(dx[:, part], want, R.rows_tolerance(want, mag, dtype, 32), "inputs")
+        close(dw[i], wsum, R.weight_tolerance(wmag, 64 + n * max(hq, hk)), "weight")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_append_of_many_empty_sequences(dtype):
     # tokens whose sequences lie more than 32 apart, and several in one
