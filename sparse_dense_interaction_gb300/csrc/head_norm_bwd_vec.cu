@@ -48,23 +48,17 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
     uint8_t *ring = smem + (threadIdx.x >> 5) * R::bytes(p.fold);
     uint8_t *angle_ring = ring + R::kDepth * R::kSlot + my.token * R::kAngles, *mine = ring + lane * R::kPiece;
 
-    const float *my_angles = nullptr;  // lane i: token i's
+    int64_t position = 0;  // lane i: token i's
     if (p.rope.table && lane < tokens)
-        my_angles = rope_row(p.rope, __ldg(p.rope.positions + first + lane), p.err);
+        position = __ldg(p.rope.positions + first + lane);
 
-    // the copies run kDepth - 1 slots ahead
+    // the copies run kDepth - 1 slots ahead; the first rows do not wait for the positions
     const T *x_row = me.x.row<T>(first + my.token, head), *y_row = me.dy.row<T>(first + my.token, head);
     const int64_t x_step = at.kGroups * me.x.hs, y_step = at.kGroups * me.dy.hs;
     int ahead_step = 0, ahead_slot = 0, ahead = 0;
-    auto copy = [&] {
+    auto copy_slot = [&] {
         if (ahead_step < steps) {
-            const int token = ahead_step * fold + my.token;
-            if (ahead_slot == 0) {
-                const float *a = reinterpret_cast<const float *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), token));
-                copy_angles<GL>(angle_ring + ahead_step % R::kDepth * angle_bytes, a, p.rope.rot >> 1, at, my.first);
-            }
-            const bool there = ahead_slot * at.kGroups < rows && token < tokens;
+            const bool there = ahead_slot * at.kGroups < rows && ahead_step * fold + my.token < tokens;
             copy_row<T, GL>(mine + ahead * R::kSlot, x_row, me.x.ptr, there, at);
             copy_row<T, GL>(mine + ahead * R::kSlot + R::kSlot / 2, y_row, me.x.ptr, there, at);
             const bool last = ahead_slot + 1 == slots;
@@ -74,11 +68,32 @@ norm_rope_bwd_vec_kernel(const __grid_constant__ NormBwdParams p)
             ahead_step += last;
         }
         ahead = ahead + 1 == R::kDepth ? 0 : ahead + 1;
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
     for (int i = 0; i < R::kDepth - 1; i++)
-        copy();
+        copy_slot();
+    const float *my_angles = nullptr;
+    if (p.rope.table && lane < tokens)
+        my_angles = rope_row(p.rope, position, p.err);
+    auto copy_turn = [&](int step) {
+        if (step < steps) {
+            const float *a = reinterpret_cast<const float *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<int64_t>(my_angles), step * fold + my.token));
+            copy_angles<GL>(angle_ring + step % R::kDepth * angle_bytes, a, p.rope.rot >> 1, at, my.first);
+        }
+    };
+    auto copy = [&] {
+        if (ahead_slot == 0)
+            copy_turn(ahead_step);
+        copy_slot();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; i++) {
+        if (i % slots == 0)
+            copy_turn(i / slots);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
     stage_weights<kInterleaved>(me.w, at, sw);
 
     const float inv_d = 1.f / (float)p.d;
