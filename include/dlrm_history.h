@@ -190,9 +190,9 @@ size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_hea
  * raises DLRM_FLAG_INDEX_OOB.
  *
  * Scores, the softmax's maxima and sums and the output's sums are fp32.  The
- * products run on the tensor cores for heads of at most 128 elements whose
- * widths, strides and pointers are multiples of 16 bytes; others take a general
- * kernel in fp32.  16-bit types: each weight p (relative to the row's running
+ * products run on the tensor cores for heads of at most 256 16-bit or 128 fp32
+ * elements whose widths, strides and pointers are multiples of 16 bytes; others
+ * take a general kernel in fp32.  16-bit types: each weight p (relative to the row's running
  * maximum) is rounded to that type, an error as large as the rounding of the
  * output itself.  fp32: operands are split in two TF32 parts, which carries
  * each product to about 2^-22 of its magnitude.  Results are the same bits from

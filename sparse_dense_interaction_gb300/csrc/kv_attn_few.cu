@@ -1,5 +1,5 @@
 // Attention over the paged cache by rows of 16: single tokens and short chunks,
-// and fp32 tensors of every length.
+// and chunks of every length in fp32 or with 16-bit heads above 128.
 //
 // Such a call reads every key and value once and does little with each, so
 // memory bounds it, and the design keeps loads in flight.  An item is a tile of
@@ -252,7 +252,7 @@ struct FewShape {
     // CTAs of an SM and stages of a warp's ring: where 3 CTAs have the registers, two stages each keep as many bytes in
     // flight as three of 2, and an item's start and end hide behind two others (256 users of up to 8192 events
     // 329 -> 320 us, 512 users of up to 1000 with 8 heads of 64 117 -> 94)
-    static constexpr int kResident = kBulk && !kWide && kGroups == 1 ? 3 : 2, kStages = kResident == 3 ? 2 : 3;
+    static constexpr int kResident = kBulk && !kWide && kGroups == 1 && DP <= 128 ? 3 : 2, kStages = kResident == 3 ? 2 : 3;
     static constexpr int kCtas = kResident * kFewSms;
     static constexpr int kMerge = kOut < 32 ? kOut : 32;
     static constexpr int kSmem = 1024 + kFewWarps * kStages * kFewStageBytes + 2 * kMerge * 32 * 4;
@@ -802,14 +802,14 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 
 // Joins the items that span CTAs: CTA x of this kernel the item that the
 // main kernel's CTA x began and did not end, row blockIdx.y of it.  A warp
-// sums every eighth part, 4 columns a lane.
+// sums every eighth part, 4 columns a lane (and 4 more of wide heads).
 constexpr int kJoinWarps = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
 {
-    __shared__ float4 sums[kJoinWarps][32];
+    __shared__ float4 sums[kJoinWarps][2][32];
     __shared__ float weights[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = p.cache.heads * p.group;
     const FewJoin j = p.joins[blockIdx.x];
@@ -824,40 +824,48 @@ kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
     top = warp_max(top);
     const float base = top == -INFINITY ? 0.f : top;
     float weight = 0.f;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 4
     for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
         const float f = exp2_approx(p.part_lse[row(c)] - base);
         weight += f;
-        if (lane * 4 < p.d) {
-            const float4 x = *reinterpret_cast<const float4 *>(p.part_o + row(c) * p.d + lane * 4);
-            sum = make_float4(fmaf(x.x, f, sum.x), fmaf(x.y, f, sum.y), fmaf(x.z, f, sum.z), fmaf(x.w, f, sum.w));
-        }
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (i * 128 + lane * 4 < p.d) {
+                const float4 x = *reinterpret_cast<const float4 *>(p.part_o + row(c) * p.d + i * 128 + lane * 4);
+                sum[i] = make_float4(fmaf(x.x, f, sum[i].x), fmaf(x.y, f, sum[i].y), fmaf(x.z, f, sum[i].z),
+                                     fmaf(x.w, f, sum[i].w));
+            }
     }
-    sums[warp][lane] = sum;
+    sums[warp][0][lane] = sum[0];
+    sums[warp][1][lane] = sum[1];
     if (lane == 0)
         weights[warp] = weight;
     __syncthreads();
     if (warp != 0)
         return;
     weight = 0.f;
-    sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; w++) {
-        const float4 x = sums[w][lane];
+    for (int w = 0; w < kJoinWarps; w++)
         weight += weights[w];
-        sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
-    }
     const float inv = weight > 0.f ? 1.f / weight : 0.f;
     const int r = j.row + blockIdx.y, t = r / p.group, h = j.head + r - t * p.group;
     const int64_t token = j.token + t;
-    if (lane * 4 < p.d) {
-        T *out = p.out.row<T>(token, h) + lane * 4;
-        out[0] = from_f32<T>(sum.x * inv);
-        out[1] = from_f32<T>(sum.y * inv);
-        out[2] = from_f32<T>(sum.z * inv);
-        out[3] = from_f32<T>(sum.w * inv);
-    }
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        if (i * 128 + lane * 4 < p.d) {
+            float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; w++) {
+                const float4 x = sums[w][i][lane];
+                all = make_float4(all.x + x.x, all.y + x.y, all.z + x.z, all.w + x.w);
+            }
+            T *out = p.out.row<T>(token, h) + i * 128 + lane * 4;
+            out[0] = from_f32<T>(all.x * inv);
+            out[1] = from_f32<T>(all.y * inv);
+            out[2] = from_f32<T>(all.z * inv);
+            out[3] = from_f32<T>(all.w * inv);
+        }
     if (p.lse && lane == 0)
         p.lse[token * heads + h] = weight > 0.f ? (top + log2f(weight)) * kLn2 : -INFINITY;
 }
@@ -955,6 +963,10 @@ static int launch_few_width(AttnParams &p, int dtype, void *workspace, cudaStrea
     if (p.d <= 64)
         return bulk ? launch_few<T, 64, kGroups, true>(p, maps, workspace, st)
                     : launch_few<T, 64, kGroups, false>(p, maps, workspace, st);
+    if constexpr (sizeof(T) == 2)
+        if (p.d > 128)
+            return bulk ? launch_few<T, 256, kGroups, true>(p, maps, workspace, st)
+                        : launch_few<T, 256, kGroups, false>(p, maps, workspace, st);
     return bulk ? launch_few<T, 128, kGroups, true>(p, maps, workspace, st)
                 : launch_few<T, 128, kGroups, false>(p, maps, workspace, st);
 }

@@ -374,6 +374,11 @@ ATTN = [
     ([16, 3], [1500, 2000], 1, 1, 128, 24, False, True, 0, "bf16"),
     ([2, 1], [2500, 3], 2, 1, 20, 5, False, True, 0, "f32"),
     ([60, 1], [1100, 700], 3, 1, 64, 16, True, True, 0, "f32"),
+    ([1, 1, 1], [5000, 0, 77], 8, 2, 256, 16, False, True, 0, "bf16"),
+    ([3, 16], [900, 3300], 2, 2, 192, 24, True, False, 0, "f16"),
+    ([30, 5], [400, 5], 3, 1, 160, 7, False, True, 100, "bf16"),
+    ([5, 1], [700, 200], 4, 2, 136, 8, False, True, 0, "f16"),
+    ([5], [700], 2, 1, 132, 8, False, True, 0, "f16"),
 ]
 
 
