@@ -805,11 +805,11 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 // sums every eighth part, 4 columns a lane (and 4 more of wide heads).
 constexpr int kJoinWarps = 8;
 
-template <typename T>
+template <typename T, int kHalves>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
 {
-    __shared__ float4 sums[kJoinWarps][2][32];
+    __shared__ float4 sums[kJoinWarps][kHalves][32];
     __shared__ float weights[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = p.cache.heads * p.group;
     const FewJoin j = p.joins[blockIdx.x];
@@ -824,21 +824,25 @@ kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
     top = warp_max(top);
     const float base = top == -INFINITY ? 0.f : top;
     float weight = 0.f;
-    float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float4 sum[kHalves];
+#pragma unroll
+    for (int i = 0; i < kHalves; i++)
+        sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
         const float f = exp2_approx(p.part_lse[row(c)] - base);
         weight += f;
 #pragma unroll
-        for (int i = 0; i < 2; i++)
+        for (int i = 0; i < kHalves; i++)
             if (i * 128 + lane * 4 < p.d) {
                 const float4 x = *reinterpret_cast<const float4 *>(p.part_o + row(c) * p.d + i * 128 + lane * 4);
                 sum[i] = make_float4(fmaf(x.x, f, sum[i].x), fmaf(x.y, f, sum[i].y), fmaf(x.z, f, sum[i].z),
                                      fmaf(x.w, f, sum[i].w));
             }
     }
-    sums[warp][0][lane] = sum[0];
-    sums[warp][1][lane] = sum[1];
+#pragma unroll
+    for (int i = 0; i < kHalves; i++)
+        sums[warp][i][lane] = sum[i];
     if (lane == 0)
         weights[warp] = weight;
     __syncthreads();
@@ -852,7 +856,7 @@ kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
     const int r = j.row + blockIdx.y, t = r / p.group, h = j.head + r - t * p.group;
     const int64_t token = j.token + t;
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < kHalves; i++)
         if (i * 128 + lane * 4 < p.d) {
             float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -948,7 +952,8 @@ static int launch_few(AttnParams &p, const FewMaps &maps, void *workspace, cudaS
         <<<(unsigned)(split ? FewShape<T, DP, kGroups, kBulk>::kCtas : items), kFewWarps * 32, smem, st>>>(p, maps);
     count_launch(st);
     if (split) {
-        kv_attn_few_join_kernel<T><<<dim3(FewShape<T, DP, kGroups, kBulk>::kCtas - 1, (unsigned)p.rows), kJoinWarps * 32, 0, st>>>(p);
+        const dim3 grid(FewShape<T, DP, kGroups, kBulk>::kCtas - 1, (unsigned)p.rows);
+        kv_attn_few_join_kernel<T, (DP > 128 ? 2 : 1)><<<grid, kJoinWarps * 32, 0, st>>>(p);
         count_launch(st);
     }
     return launch_status();
