@@ -8,10 +8,10 @@
 //
 // The row kernels here serve every width, stride and alignment: a warp per row,
 // lane l holds the elements l, l + 32, ...  Rows that can be moved as 4-element pieces
-// take the vector path (head_norm.cuh).  A row's loads wait for nothing but are few at a
-// time: 20000 tokens of 8 query and 2 key heads of 250 bf16 elements take 200 us
-// forward, 1.0 TB/s, 374 backward, 0.8 TB/s; 8 and 2 of 17 fp32 elements 87 and 122 us;
-// the append of as many rows of 250 282 us.
+// take the vector path (head_norm.cuh).  Loads of single elements, few at a
+// time, bound them: 20000 tokens of 8 query and 2 key heads of 250 bf16 elements
+// take 200 us forward, 1.0 TB/s, 374 backward, 0.8 TB/s; of 17 fp32 elements 87
+// and 122 us; the append of as many rows of 250 282 us.
 #include <initializer_list>
 
 #include "head_norm.cuh"

@@ -198,7 +198,8 @@ static int64_t bwd_run(int64_t n, int64_t chunks) { return run_tokens(n, chunks,
 
 size_t norm_bwd_vec_workspace(int64_t n, int qh, int kh, int d)
 {
-    const int64_t heads = kSlots * (d <= 32 ? 8 : (d <= 64 ? 4 : (d <= 128 ? 2 : 1))), chunks = div_up(qh, heads) + div_up(kh, heads);
+    const int64_t heads = kSlots * (d <= 32 ? 8 : (d <= 64 ? 4 : (d <= 128 ? 2 : 1)));
+    const int64_t chunks = div_up(qh, heads) + div_up(kh, heads);
     return (size_t)(chunks * div_up(n, kWarps * bwd_run(n, chunks))) * d * sizeof(float) + 16;
 }
 

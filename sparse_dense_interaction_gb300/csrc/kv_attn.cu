@@ -316,16 +316,18 @@ static int launch_attn_t(AttnParams &p, const AttnPlan &a, int dtype, cudaStream
     return launch_status();
 }
 
-// The tensor-core kernels' copies are 16 bytes wide.  Heads of 129 to 256 16-bit elements take
-// rows of 16 for any number of rows (one event of each of 64 users with 2000, 16
-// heads on 4 of 256: 98 us, the general kernel 823; 64 new of 16: 290 and 4499).
+// The tensor-core kernels' copies are 16 bytes wide.  Heads of 129 to 256
+// 16-bit elements take rows of 16 for any number of rows (one event of each of
+// 64 users with 2000, 16 heads on 4 of 256: 98 us, the general kernel 823; 64
+// new of 16: 290 and 4499).
 static bool wide_rows(const AttnParams &p, int dtype)
 {
     const int e = dtype == DLRM_F32 ? 4 : 8;
     auto ok = [e](const void *ptr, int64_t a, int64_t b) {
         return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && a % e == 0 && b % e == 0;
     };
-    return p.d <= (dtype == DLRM_F32 ? 128 : 256) && p.d % e == 0 && ok(p.q.ptr, p.q.ts, p.q.hs) && ok(p.out.ptr, p.out.ts, p.out.hs) &&
+    return p.d <= (dtype == DLRM_F32 ? 128 : 256) && p.d % e == 0 && ok(p.q.ptr, p.q.ts, p.q.hs) &&
+           ok(p.out.ptr, p.out.ts, p.out.hs) &&
            ok(p.cache.k, p.cache.page_stride, p.cache.slot_stride) && ok(p.cache.v, p.cache.head_stride, 0);
 }
 
@@ -335,9 +337,11 @@ int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     // a window bounds what a row sees, and a sequence's rows, whatever the history's length
     const int64_t rows = p.max_new * p.group, bound = p.window + (p.causal ? p.max_new : 0);
     const int64_t seen = p.window > 0 && bound < p.max_len ? bound : p.max_len;
-    // Rows of 16: for few of them the keys and values are read as often as by one tile of 256, and more CTAs
-    // fit on an SM.  150 users, 8 heads of 128, 32 rows: up to 100 events 51 us against 73, up to 1000
-    // 105 and 113, up to 2000 101 and 37 (64 users); 48 rows, up to 400: 90 and 88; heads of 64, 32 rows, up to 100: 42 and 40.
+    // Rows of 16: for few of them a short history's keys and values stay in L2,
+    // and more CTAs fit on an SM.  150 users, 8 heads of 128, 32 rows, rows of 16
+    // against tiles: up to 100 events 51 and 73 us, up to 1000 105 and 113; 64
+    // users, up to 2000: 101 and 37; 48 rows, up to 400: 90 and 88; heads of 64,
+    // 32 rows, up to 100: 42 and 40.
     if (cores && (dtype == DLRM_F32 || p.d > 128 || rows <= 16 || (p.d > 64 && rows <= 32 && seen <= 1024)))
         return launch_kv_attn_few(p, dtype, workspace, st);
     const AttnKernel kernel = cores ? kAttnTile : kAttnGeneral;

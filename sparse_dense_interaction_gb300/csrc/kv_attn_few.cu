@@ -80,8 +80,8 @@ struct Split {
     __device__ __forceinline__ Split() {}
     __device__ __forceinline__ Split(float x) : hi(tc::tf32_round(x)), lo(x - hi) {}
 };
-// Two steps.  The MMA's own sums are cut off, not rounded: it adds up 16 products, small terms first, and the
-// rest is added in fp32.
+// Two steps.  The MMA's own sums are cut off, not rounded: it adds up 16
+// products, small terms first, and the rest is added in fp32.
 __device__ __forceinline__ void mma_fp32(float *c, const Split *a, const Split *b)
 {
     float t[4] = {0.f, 0.f, 0.f, 0.f};
@@ -249,9 +249,10 @@ struct FewShape {
     static constexpr int kOutMmas = E / 2;                       // of a set of output columns
     static constexpr int kOut = kGroups * VS * kOutMmas * 4;     // output registers
     // registers joined at a time: with all 64 of them two CTAs would not fit on an SM
-    // CTAs of an SM and stages of a warp's ring: where 3 CTAs have the registers, two stages each keep as many bytes in
-    // flight as three of 2, and an item's start and end hide behind two others (256 users of up to 8192 events
-    // 329 -> 320 us, 512 users of up to 1000 with 8 heads of 64 117 -> 94)
+    // CTAs of an SM and stages of a warp's ring: where 3 CTAs have the registers,
+    // two stages each keep as many bytes in flight as three of 2, and an item's
+    // start and end hide behind two others (256 users of up to 8192 events 320 us,
+    // 329 with 2; 512 users of up to 1000, 8 heads of 64: 94 and 117)
     static constexpr int kResident = kBulk && !kWide && kGroups == 1 && DP <= 128 ? 3 : 2, kStages = kResident == 3 ? 2 : 3;
     static constexpr int kCtas = kResident * kFewSms;
     static constexpr int kMerge = kOut < 32 ? kOut : 32;
@@ -286,7 +287,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, FewShape<T, DP, kGroups, kBulk
 kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FewMaps maps)
 {
     using Sh = FewShape<T, DP, kGroups, kBulk>;
-    constexpr int E = Sh::E, KT = Sh::KT, VT = Sh::VT, KG = Sh::KG, VS = Sh::VS, NB = Sh::NB, UT = Sh::UT, kParts = Sh::kParts, kFewStages = Sh::kStages;
+    constexpr int E = Sh::E, KT = Sh::KT, VT = Sh::VT, KG = Sh::KG, VS = Sh::VS, NB = Sh::NB, UT = Sh::UT;
+    constexpr int kParts = Sh::kParts, kFewStages = Sh::kStages;
     extern __shared__ uint8_t raw[];
     __shared__ float s_m[kFewWarps][kFewRows], s_l[kFewWarps][kFewRows];
     __shared__ uint64_t bars[kFewWarps][kFewStages];

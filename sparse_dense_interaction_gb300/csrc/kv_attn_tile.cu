@@ -278,7 +278,8 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
         if (tc::elect_one()) {
 #pragma unroll
             for (int e = 0; e < kTilePos / 16; e++)
-                tc::mma_f16_ta(tmem + Sh::kScoreCols + t * DP, tmem + t * 128 + e * 8, v + e * (2048 >> 4), kOut, j > 0 || e > 0);
+                tc::mma_f16_ta(tmem + Sh::kScoreCols + t * DP, tmem + t * 128 + e * 8, v + e * (2048 >> 4), kOut,
+                               j > 0 || e > 0);
         }
         __syncwarp();
     };
@@ -591,7 +592,8 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     } else if (tiles > 0) {
         tile_mma<T, DP, kTwo>(sq, ring, b, tiles, two);
         __syncwarp();
-        if (tc::elect_one() && *reinterpret_cast<volatile int *>(&b.aborted)) {  // no MMA may be in flight when the memory is given back
+        // no MMA may be in flight when the memory is given back
+        if (tc::elect_one() && *reinterpret_cast<volatile int *>(&b.aborted)) {
             int never = 0;
             tc::mma_commit(&b.drained);
             tc::mbar_wait(&b.drained, 0, &never);
