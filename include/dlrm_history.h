@@ -194,7 +194,9 @@ size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_hea
  * elements whose widths, strides and pointers are multiples of 16 bytes; others
  * take a general kernel in fp32.  16-bit types: each weight p (relative to the row's running
  * maximum) is rounded to that type, an error as large as the rounding of the
- * output itself.  fp32: operands are split in two TF32 parts, which carries
+ * output itself; f16 weights are scaled to use that type's range, so this holds
+ * down to 2^-25 of the row's largest weight, and smaller ones are rounded to
+ * steps of at most 2^-35 of it.  fp32: operands are split in two TF32 parts, which carries
  * each product to about 2^-22 of its magnitude.  Results are the same bits from
  * run to run of one batch; a sequence's last bits may depend on which other
  * sequences are in its batch.  Every wait inside a kernel is bounded; one that

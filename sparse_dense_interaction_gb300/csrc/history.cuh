@@ -152,6 +152,17 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y)
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// log2 of the largest weight that the 16-bit kernels keep.  A weight 2^(s - m) of
+// at most 1 wastes half of fp16's range: from 2^-14 on it is subnormal and below
+// 2^-25 it is gone, while the sum still counts it (40000 such weights under one
+// strong key lost all that they gather).  So fp16 weights are lifted to 2^15;
+// sum and output carry the same factor.  bf16 has fp32's range.  The maxima are
+// rounded up and the lifted exponents down, so that no weight exceeds it.
+template <typename T>
+constexpr float kWeightTop = 0.f;
+template <>
+constexpr float kWeightTop<__half> = 15.f;
+
 // The attention's launch: which kernel, rows (token, head of a group) of a
 // tile, and how the positions are split.
 enum AttnKernel { kAttnGeneral, kAttnTile };

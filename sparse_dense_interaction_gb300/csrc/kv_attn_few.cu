@@ -570,7 +570,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                         s[nb][x][j] = pos >= lo[i] && pos < hi[i] ? s[nb][x][j] : -INFINITY;
                     }
         }
-        float top[Sh::kStats], base[Sh::kStats];
+        float top[Sh::kStats], base[Sh::kStats], off[Sh::kStats];
         bool moved = false;
 #pragma unroll
         for (int i = 0; i < Sh::kStats; i++) {
@@ -586,8 +586,9 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
             for (int step = 4; step < 32; step *= 2)
                 top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], step));
-            top[i] = fmaxf(top[i] * p.scale_log2, m[i]);
+            top[i] = fmaxf(__fmul_ru(top[i], p.scale_log2), m[i]);
             base[i] = top[i] == -INFINITY ? 0.f : top[i];
+            off[i] = __fsub_rd(kWeightTop<T>, base[i]);
             moved |= top[i] > m[i];
         }
         if (__any_sync(0xffffffffu, moved)) {
@@ -609,7 +610,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     const int i = stat_of(x, j);
-                    s[nb][x][j] = exp2_approx(fmaf(s[nb][x][j], p.scale_log2, -base[i]));
+                    s[nb][x][j] = exp2_approx(fmaf(s[nb][x][j], p.scale_log2, off[i]));
                     l[i] += s[nb][x][j];
                 }
             // a box's rows that no query sees may hold anything: a zero weight would not do
@@ -709,7 +710,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             for (int w = 0; w < kFewWarps; w++)
                 sum = fmaf(s_l[w][r], exp2_approx(s_m[w][r] - b), sum);
             f[i] = sum > 0.f ? exp2_approx(m[i] - b) / sum : 0.f;
-            lse[i] = sum > 0.f ? all + log2f(sum) : -INFINITY;
+            lse[i] = sum > 0.f ? all + (log2f(sum) - kWeightTop<T>) : -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < Sh::kOut; i++)

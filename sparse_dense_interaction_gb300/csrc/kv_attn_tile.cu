@@ -20,8 +20,9 @@
 // The two tiles take turns: while one's scores are exponentiated the other's
 // MMAs run.  The running maximum a row is scaled by lags: the output (in
 // tensor memory) and the sum are rescaled only when the maximum has grown by
-// more than 2^8, which rarely happens after the first tiles; a weight is then
-// at most 2^8, and sum and output carry the same factor, so nothing is lost.
+// more than 2^8 (fp16: 2^4, which leaves more of its range to the weights), which
+// rarely happens after the first tiles; a weight is then at most that much above
+// 1, and sum and output carry the same factor, so nothing is lost.
 // Tensor memory: scores 2 x 128 columns (the weights on top of them), output
 // 2 x DP.
 //
@@ -42,7 +43,15 @@ namespace dlrm {
 constexpr int kTilePos = 128;
 __host__ __device__ constexpr int copy_threads(bool bulk) { return bulk ? 32 : 64; }
 constexpr int kTileLag = 3;         // copied tiles that may be in flight before one is waited for
-constexpr float kTileSlack = 8.f;   // log2 of the growth of a maximum that is let pass
+
+// log2 of the growth of a maximum that is let pass, and of what is left of the
+// range that weights may use (kWeightTop) to lift them by.
+template <typename T>
+constexpr float kTileSlack = 8.f;
+template <>
+constexpr float kTileSlack<__half> = 4.f;
+template <typename T>
+constexpr float kTileLift = kWeightTop<T> > 0.f ? kWeightTop<T> - kTileSlack<T> : 0.f;
 
 // kTwo: two query tiles of a CTA that has the SM, else one, and two CTAs share the SM.
 template <int DP, bool kTwo>
@@ -355,11 +364,11 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
 #pragma unroll
         for (int i = 0; i < kHalf; i += 2)
             top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-        float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+        float now = __fmul_ru(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), p.scale_log2);
         b.agree[t][half][in] = now;
         tc::named_sync(pair, 64);
         now = fmaxf(now, b.agree[t][1 - half][in]);
-        if (__any_sync(0xffffffffu, now > m + kTileSlack)) {
+        if (__any_sync(0xffffffffu, now - m > kTileSlack<T>)) {
             // also from -infinity; the output of the tiles before is complete: the scores' MMA came after it
             const float next = fmaxf(m, now), f = next == -INFINITY ? 1.f : exp2_approx(m - next);
             m = next;
@@ -376,8 +385,8 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
                 }
             }
         }
-        const float base = m == -INFINITY ? 0.f : m;
-        const float2 scale = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-base, -base);
+        const float lift = __fsub_rd(kTileLift<T>, m == -INFINITY ? 0.f : m);
+        const float2 scale = make_float2(p.scale_log2, p.scale_log2), off = make_float2(lift, lift);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < kHalf / 32; c++) {
@@ -406,7 +415,7 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
     float inv = 0.f, lse = -INFINITY;
     if (l > 0.f) {
         inv = 1.f / l;
-        lse = m + log2f(l);
+        lse = m + (log2f(l) - kTileLift<T>);
     }
     if (tiles > 0) {
         tc::mbar_wait(&b.o_full[t], 0, &b.aborted);
