@@ -171,7 +171,7 @@ size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_hea
  *   lse_i = log sum_j exp(scale * (q_i . k_j))                (natural logarithm)
  *
  * Query head h reads cache head h / (q_heads / cache heads).  A query that
- * sees nothing gets out = 0 and lse = -infinity.
+ * sees nothing gets out = 0 and lse = -infinity; one with a NaN gets NaN in both.
  *
  * q, out     heads a multiple of the cache's; dtype is that of q, out and the
  *            cache.

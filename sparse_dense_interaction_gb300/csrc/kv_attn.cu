@@ -122,7 +122,7 @@ kv_attn_general_kernel(const __grid_constant__ AttnParams p)
     for (int j = 0; j < 2; j++) {
         const int r = warp * 2 + j;
         if (lane == 0) {
-            sf[r] = l[j] > 0.f ? 1.f / l[j] : 0.f;
+            sf[r] = l[j] == 0.f ? 0.f : 1.f / l[j];
             if (r < w.rows) {
                 const int row = w.row0 + r, t = row / p.group, h = w.head * p.group + row - t * p.group;
                 const float lse = m[j] + log2f(l[j]);  // -infinity where nothing was seen
@@ -192,7 +192,7 @@ kv_attn_join_kernel(const __grid_constant__ AttnParams p)
                         acc[j] = fmaf(o[lane + 32 * j], f, acc[j]);
             }
         }
-        const float inv = total > 0.f ? 1.f / total : 0.f;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
         T *out = p.out.row<T>(token, h);
 #pragma unroll
         for (int j = 0; j < DLRM_MAX_HEAD_DIM / 32; j++)

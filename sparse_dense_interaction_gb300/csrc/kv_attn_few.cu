@@ -709,8 +709,9 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
             for (int w = 0; w < kFewWarps; w++)
                 sum = fmaf(s_l[w][r], exp2_approx(s_m[w][r] - b), sum);
-            f[i] = sum > 0.f ? exp2_approx(m[i] - b) / sum : 0.f;
-            lse[i] = sum > 0.f ? all + (log2f(sum) - kWeightTop<T>) : -INFINITY;
+            // no weight at all: nothing is seen; a sum that is not a number stays one
+            f[i] = sum == 0.f ? 0.f : exp2_approx(m[i] - b) / sum;
+            lse[i] = sum == 0.f ? -INFINITY : all + (log2f(sum) - kWeightTop<T>);
         }
 #pragma unroll
         for (int i = 0; i < Sh::kOut; i++)
@@ -855,7 +856,7 @@ kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
     for (int w = 0; w < kJoinWarps; w++)
         weight += weights[w];
-    const float inv = weight > 0.f ? 1.f / weight : 0.f;
+    const float inv = weight == 0.f ? 0.f : 1.f / weight;
     const int r = j.row + blockIdx.y, t = r / p.group, h = j.head + r - t * p.group;
     const int64_t token = j.token + t;
 #pragma unroll
@@ -874,7 +875,7 @@ kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
             out[3] = from_f32<T>(all.w * inv);
         }
     if (p.lse && lane == 0)
-        p.lse[token * heads + h] = weight > 0.f ? (top + log2f(weight)) * kLn2 : -INFINITY;
+        p.lse[token * heads + h] = weight == 0.f ? -INFINITY : (top + log2f(weight)) * kLn2;
 }
 
 // Whether the positions are shared out in equal runs, or an item is a CTA's

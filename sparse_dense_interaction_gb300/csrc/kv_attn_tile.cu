@@ -413,7 +413,7 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
     tc::named_sync(pair, 64);
     l = b.agree[t][0][in] + b.agree[t][1][in];
     float inv = 0.f, lse = -INFINITY;
-    if (l > 0.f) {
+    if (l != 0.f) {  // not a number either: then neither is the row
         inv = 1.f / l;
         lse = m + (log2f(l) - kTileLift<T>);
     }
@@ -458,7 +458,7 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
                     tc::tmem_ld16(o_at + c0 + c, x);
 #pragma unroll
                 for (int i = 0; i < 16; i++)
-                    o[i] = inv > 0.f ? __uint_as_float(x[i]) * inv : 0.f;
+                    o[i] = inv != 0.f ? __uint_as_float(x[i]) * inv : 0.f;
                 if constexpr (es == 2)
 #pragma unroll
                     for (int i = 0; i < 16; i += 8)

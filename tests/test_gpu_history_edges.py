@@ -56,3 +56,22 @@ def test_attention_weights_far_below_the_strongest(case, gap, strong):
     tol = (2 * score + 2.0 ** -18 + weight) * absout + R.U[dtype] * np.abs(want) * 1.01 + R.TINY[dtype]
     close(out, want, tol + (flat * 2.0 ** -33 if dtype == "f16" else 0), case)
     close(lse, wl, R.lse_tolerance(wl, smax, d), (case, "lse"))
+
+
+@pytest.mark.parametrize("case", [
+    ([1, 1], [300, 40], 4, 2, 64, 16, False, True, 0, "f16"), ([1, 1], [40000, 40], 4, 2, 128, 16, True, True, 0, "bf16"),
+    ([3, 2], [3000, 40], 4, 2, 64, 16, True, True, 0, "f32"), ([40, 9], [100, 40], 4, 2, 64, 16, False, False, 0, "bf16"),
+    ([40, 9], [9000, 40], 4, 2, 128, 16, False, True, 0, "f16"), ([40, 9], [900, 40], 4, 2, 128, 5, False, True, 64, "f16"),
+    ([1, 3], [3000, 40], 4, 2, 20, 5, False, True, 0, "f32"), ([1, 3], [40, 90], 4, 2, 20, 5, False, True, 0, "bf16"),
+])
+def test_a_query_of_nan_gives_nan(case):
+    # and not the zeros of a row that sees nothing; no other row knows of it
+    hq = case[2]
+    table, table_d, offsets, lens, kc, vc, q = attention_inputs(case)
+    out, lse = attend(case, q, offsets, lens, table_d, kc, vc, 0.125)
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    bad[0, 1] = bad[-1, hq - 1] = True
+    q[bad, 5] = float("nan")
+    got, got_lse = attend(case, q, offsets, lens, table_d, kc, vc, 0.125)
+    assert got[bad].isnan().all() and got_lse[bad].isnan().all()
+    assert torch.equal(got[~bad], out[~bad]) and torch.equal(got_lse[~bad], lse[~bad])
