@@ -476,7 +476,11 @@ int dlrm_emb_bag_bwd_sgd_noalloc(void *const *tables, const int64_t *rows, int T
  *                    bulk-copy (CUDA-core) interaction forward (negative: the
  *                    default; 0: give up at once).  A CTA that gives up waits,
  *                    with the default limit, for its copies in flight, writes
- *                    NaN into its samples' pair outputs and returns.
+ *                    NaN into its samples' pair outputs and returns.  Also
+ *                    polls of the waits inside the kernels of dlrm_kv_attn_fwd
+ *                    (dlrm_history.h), which then wait
+ *                    for their copies and products in flight in the same way
+ *                    and raise DLRM_FLAG_WAIT_TIMEOUT.
  * Returns DLRM_OK, or DLRM_ERR_INVALID_ARG for a negative sort_first_tile.
  */
 int dlrm_set_wait_test_hooks(int64_t sort_wait_polls, int sort_first_tile, int64_t copy_wait_polls);

@@ -36,7 +36,8 @@ bool interact_tensor_cores();
 // Limits of the kernels' bounded waits for the next launches, as the testing
 // hook dlrm_set_wait_test_hooks left them (defaults when unset): polls of a
 // radix pass's look-back word, the first tile the passes claim, polls of a
-// stage barrier in the main loop of the bulk-copy interaction forward.
+// stage barrier in the main loop of the bulk-copy interaction forward and of the
+// attention kernels' waits.
 struct WaitHooks {
     int sort_polls;
     uint32_t sort_first_tile;

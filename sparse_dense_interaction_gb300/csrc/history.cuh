@@ -205,6 +205,7 @@ struct AttnParams {
     int64_t tiles;
     float *part_o, *part_lse;  // [splits][n][q heads]([d]): partial rows, log2 of their sums
     FewJoin *joins;            // rows of 16: an item that each CTA left unfinished
+    int wait_polls;            // of a wait inside a kernel, before it gives up
     int32_t *err;
 };
 

@@ -1,6 +1,7 @@
 // C ABI of the event-history operators: argument checks and dispatch, all on
 // the host before anything is launched.
 #include "history.cuh"
+#include "tc.cuh"
 
 namespace dlrm {
 
@@ -248,6 +249,7 @@ int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm
     p.causal = causal != 0;
     p.window = window < kMaxPositions ? (int)window : 0;  // as wide as any history: none
     p.lse = lse;
+    p.wait_polls = wait_hooks(0, tc::kSpinLimit).copy_polls;  // the default unless a test shortens it
     p.err = err_flag;
     return launch_kv_attn(p, dtype, workspace, static_cast<cudaStream_t>(stream));
 }

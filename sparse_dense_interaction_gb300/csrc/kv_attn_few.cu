@@ -292,7 +292,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     extern __shared__ uint8_t raw[];
     __shared__ float s_m[kFewWarps][kFewRows], s_l[kFewWarps][kFewRows];
     __shared__ uint64_t bars[kFewWarps][kFewStages];
-    __shared__ int aborted;
+    __shared__ int aborted, died_at[kFewWarps];  // died_at: the part whose wait ran out
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     uint8_t *smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
     uint8_t *ring = smem + warp * kFewStages * kFewStageBytes;
@@ -437,8 +437,10 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     // waits for a part of unit u; goes on to the next stage when it has been read
     auto arrived = [&](int u, int part) {
         if constexpr (kBulk) {
-            if (!dead && !tc::mbar_wait(&bars[warp][stage], phase, &aborted))
+            if (!dead && !tc::mbar_wait(&bars[warp][stage], phase, &aborted, p.wait_polls)) {
                 dead = true;
+                died_at[warp] = u * kParts + part;
+            }
             dead = __any_sync(0xffffffffu, dead);
         } else {
             const int next = part + kFewStages - 1;
@@ -795,10 +797,12 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         if (u + 1 < units)
             few_next(p, it, UT);
     }
-    if (kBulk && dead) {  // no copy may be in flight when the memory is given back
-        int never = 0;
-        for (int i = 0; i < kFewStages; i++)
-            tc::mbar_wait(&bars[warp][i], i < stage ? phase ^ 1 : phase, &never);
+    if (kBulk && dead) {
+        // that part and those copied ahead of it may still be in flight: none may be when the memory is given back
+        __syncwarp();
+        const int first = died_at[warp];
+        for (int i = first; i < min(first + kFewStages, units * kParts); i++)
+            tc::mbar_drain(&bars[warp][i % kFewStages], (i / kFewStages) & 1);
         if (lane == 0)
             raise_flag(p.err, DLRM_FLAG_WAIT_TIMEOUT);
     }

@@ -77,15 +77,16 @@ struct TileMaps {
 };
 
 // A wait by a whole warp, whose lanes go on or give up together.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *aborted)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *aborted, int polls)
 {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, aborted));
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, aborted, polls));
 }
 
 struct TileBars {
     uint64_t full[8], empty[8], landed, q_full, s_full[2], p_ready[2], o_full[2], drained;
     uint32_t tmem;
     int aborted;
+    int copied, landing;  // what the copy warp left behind: tiles copied, parity of a wait for `landed` (-1: none)
     float agree[2][2][128];  // [query tile][half][row]: a maximum of half a row's scores; at the end its sum
 };
 
@@ -145,7 +146,13 @@ __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const Til
         }
     };
     int page, slot, next_page, next_slot;
-    uint32_t patched = 0;  // value tiles mended so far, modulo 2
+    int patched = 0;  // value tiles mended so far
+    auto left_behind = [&](int copied, int landing) {
+        if (lane == 0) {
+            b.copied = copied;
+            b.landing = landing;
+        }
+    };
     find(0, lane, next_page, next_slot);
     if (maps.q_rows) {
         copy_queries<Sh, 32>(p, w, sq);
@@ -170,8 +177,8 @@ __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const Til
         for (int kv = 0; kv < 2; kv++) {
             const int i = 2 * j + kv, ring_slot = i % Sh::kSlots;
             uint8_t *tile = ring + ring_slot * Sh::kTileBytes;
-            if (i >= Sh::kSlots && !warp_wait(&b.empty[ring_slot], (i / Sh::kSlots - 1) & 1, &b.aborted))
-                return;
+            if (i >= Sh::kSlots && !warp_wait(&b.empty[ring_slot], (i / Sh::kSlots - 1) & 1, &b.aborted, p.wait_polls))
+                return left_behind(i, -1);
             const bool mend = kv == 1 && (at < w.lo || at + kTilePos > w.hi);
             uint64_t *bar = mend ? &b.landed : &b.full[ring_slot];
             if (lane == 0)
@@ -190,8 +197,8 @@ __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const Til
                     tc::mbar_arrive(&b.q_full);
             }
             if (mend) {
-                if (!warp_wait(&b.landed, patched & 1, &b.aborted))
-                    return;
+                if (!warp_wait(&b.landed, patched & 1, &b.aborted, p.wait_polls))
+                    return left_behind(i, patched & 1);
                 patched++;
                 for (int r = 0; r < kTilePos; r++)
                     if (at + r < w.lo || at + r >= w.hi)
@@ -205,6 +212,21 @@ __device__ void tile_copy_bulk(const AttnParams &p, const AttnWork &w, const Til
             }
         }
     }
+    left_behind(2 * tiles, -1);
+}
+
+// After a wait was given up: waits for the copies that may still be in flight,
+// the queries' and those of the last tiles.  (A mended tile's have landed, and
+// its barrier has been arrived at, but for the one that was waited for.)
+template <int kSlots>
+__device__ __noinline__ void tile_drain(TileBars &b, bool q_rows)
+{
+    if (!q_rows)
+        tc::mbar_drain(&b.q_full, 0);
+    for (int i = max(b.copied - kSlots, 0); i < b.copied; i++)
+        tc::mbar_drain(&b.full[i % kSlots], (i / kSlots) & 1);
+    if (b.landing >= 0)
+        tc::mbar_drain(&b.landed, b.landing);
 }
 
 // The copy warps, row by row.
@@ -234,7 +256,7 @@ __device__ void tile_copy_rows(const AttnParams &p, const AttnWork &w, uint8_t *
 #pragma unroll
         for (int kv = 0; kv < 2; kv++) {
             const int i = 2 * j + kv, slot = i % Sh::kSlots;
-            if (i >= Sh::kSlots && !tc::mbar_wait(&b.empty[slot], (i / Sh::kSlots - 1) & 1, &b.aborted))
+            if (i >= Sh::kSlots && !tc::mbar_wait(&b.empty[slot], (i / Sh::kSlots - 1) & 1, &b.aborted, p.wait_polls))
                 return tc::cp_async_wait_all();
             copy_rows<Sh>(ring + slot * Sh::kTileBytes, kv ? p.cache.v : p.cache.k, mine0, row0, p.d);
             copy_rows<Sh>(ring + slot * Sh::kTileBytes, kv ? p.cache.v : p.cache.k, mine1, 64 + row0, p.d);
@@ -259,7 +281,7 @@ __device__ void tile_copy_rows(const AttnParams &p, const AttnWork &w, uint8_t *
 }
 
 template <typename T, int DP, bool kTwo>
-__device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, bool two)
+__device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, bool two, int polls)
 {
     using Sh = TileShape<DP, kTwo>;
     constexpr int kType = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
@@ -297,8 +319,8 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
             tc::mma_commit(bar);
         __syncwarp();
     };
-    auto ready = [&](int i) { return warp_wait(&b.full[i % Sh::kSlots], (i / Sh::kSlots) & 1, &b.aborted); };
-    if (!warp_wait(&b.q_full, 0, &b.aborted) || !ready(0))
+    auto ready = [&](int i) { return warp_wait(&b.full[i % Sh::kSlots], (i / Sh::kSlots) & 1, &b.aborted, polls); };
+    if (!warp_wait(&b.q_full, 0, &b.aborted, polls) || !ready(0))
         return;
     tc::fence_after_sync();
     scores(0, 0);
@@ -309,7 +331,7 @@ __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, boo
         for (int t = 0; t < (two ? 2 : 1); t++) {
             if (t == 0 && !ready(2 * j + 1))
                 return;
-            if (!warp_wait(&b.p_ready[t], j & 1, &b.aborted))
+            if (!warp_wait(&b.p_ready[t], j & 1, &b.aborted, polls))
                 return;
             tc::fence_after_sync();
             output(t, j);
@@ -346,7 +368,7 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < tiles; j++) {
         // a wait that runs out is seen at the end; the pair's barriers below want every warp
-        tc::mbar_wait(&b.s_full[t], j & 1, &b.aborted);
+        tc::mbar_wait(&b.s_full[t], j & 1, &b.aborted, p.wait_polls);
         __syncwarp();
         tc::fence_after_sync();
         uint32_t s[kHalf];
@@ -418,7 +440,7 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
         lse = m + (log2f(l) - kTileLift<T>);
     }
     if (tiles > 0) {
-        tc::mbar_wait(&b.o_full[t], 0, &b.aborted);
+        tc::mbar_wait(&b.o_full[t], 0, &b.aborted, p.wait_polls);
         __syncwarp();
         tc::fence_after_sync();
     }
@@ -570,7 +592,8 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             tc::mbar_init(&b.p_ready[t], 8);  // the tile's warps
             tc::mbar_init(&b.o_full[t], 1);
         }
-        b.aborted = 0;
+        b.aborted = b.copied = 0;
+        b.landing = -1;
         tc::mbar_init_fence();
     }
     if (warp == kLast)
@@ -585,34 +608,29 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         if (tiles > 0) {
             if constexpr (kBulk) {
                 tile_copy_bulk<T, DP, kTwo>(p, w, maps, sq, ring, b, tiles);
-                if (*reinterpret_cast<volatile int *>(&b.aborted)) {  // no copy may be in flight at the end
-                    int never = 0;
-                    for (int parity = 0; parity < 2; parity++) {
-                        for (int i = 0; i < Sh::kSlots; i++)
-                            tc::mbar_wait(&b.full[i], parity, &never);
-                        tc::mbar_wait(&b.landed, parity, &never);
-                    }
-                    tc::mbar_wait(&b.q_full, 0, &never);
-                }
             } else {
                 tile_copy_rows<T, DP, kTwo>(p, w, sq, ring, b, tiles);
             }
         }
     } else if (tiles > 0) {
-        tile_mma<T, DP, kTwo>(sq, ring, b, tiles, two);
+        tile_mma<T, DP, kTwo>(sq, ring, b, tiles, two, p.wait_polls);
         __syncwarp();
-        // no MMA may be in flight when the memory is given back
-        if (tc::elect_one() && *reinterpret_cast<volatile int *>(&b.aborted)) {
-            int never = 0;
-            tc::mma_commit(&b.drained);
-            tc::mbar_wait(&b.drained, 0, &never);
-        }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (threadIdx.x == 0 && *reinterpret_cast<volatile int *>(&b.aborted))
-        raise_flag(p.err, DLRM_FLAG_WAIT_TIMEOUT);
+    // Nobody waits any more, so all see the same.  No copy and no MMA may be in flight when the memory is given back.
+    if (*reinterpret_cast<volatile int *>(&b.aborted)) {
+        if (threadIdx.x == 0)
+            raise_flag(p.err, DLRM_FLAG_WAIT_TIMEOUT);
+        if (kBulk && warp == Sh::kSoftmaxWarps && tiles > 0)
+            tile_drain<Sh::kSlots>(b, maps.q_rows);
+        if (warp == kLast && tiles > 0 && tc::elect_one()) {
+            tc::mma_commit(&b.drained);
+            tc::mbar_drain(&b.drained, 0);
+        }
+        __syncthreads();
+    }
     if (warp == kLast)
         tc::tmem_free<Sh::kTmem>(b.tmem);
 }

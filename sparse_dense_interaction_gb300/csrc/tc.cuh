@@ -57,15 +57,15 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
 }
 
 // Waits for the phase of the given parity.  Gives up (false) once another
-// thread of the CTA has raised *aborted, or after kSpinLimit polls, in which
+// thread of the CTA has raised *aborted, or after `polls` polls (0: at once), in which
 // case it raises *aborted itself so the other roles leave their loops too.
 // A phase that has already completed is seen by one non-blocking test (a
 // potentially suspending try_wait costs a few hundred cycles even then).
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *aborted)
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *aborted, int polls = kSpinLimit)
 {
-    if (mbar_test(bar, parity))
+    if (mbar_test(bar, parity) && polls > 0)
         return true;
-    for (int it = 0; it < kSpinLimit; it++) {
+    for (int it = 0; it < polls; it++) {
         if (mbar_try_wait(bar, parity))
             return true;
         if ((it & 255) == 255 && *aborted)
@@ -73,6 +73,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
     *aborted = 1;
     return false;
+}
+
+// The wait for a copy in flight of a kernel that gives up: by itself, with the
+// default limit, whatever else was given up.
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity)
+{
+    int alone = 0;
+    mbar_wait(bar, parity, &alone);
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
