@@ -229,6 +229,7 @@ kv_append_rows_kernel(HeadsView k, HeadsView v, BatchView batch, CacheView cache
                       const float *__restrict__ qw, HeadsView qo, int32_t *err)
 {
     const int lane = threadIdx.x & 31;
+    check_sequences(batch, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x, err);
     for (int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); token < batch.n;
          token += (int64_t)gridDim.x * kWarps) {
         const int64_t s = find_sequence(batch, token);

@@ -136,6 +136,9 @@ norm_rope_vec_kernel(const __grid_constant__ NormParams p)
 #pragma unroll
     for (int i = 0; i < R::kDepth - 1; i++)
         copy();
+    if (kAppend)
+        check_sequences(p.batch, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                        (int64_t)gridDim.y * gridDim.x * blockDim.x, p.err);
     stage_weights<kInterleaved>(me.w, at, sw);
 
     const float inv_d = 1.f / (float)p.d;

@@ -69,7 +69,8 @@ struct Sequence {
 };
 
 // Reads sequence s; false (with the flag raised) where the batch's numbers
-// contradict each other or the bounds.
+// contradict each other or the bounds.  The flag is also raised where the first
+// or the last sequence leaves tokens to nobody.
 __device__ __forceinline__ bool read_sequence(const BatchView &b, int64_t s, int64_t max_new, int64_t max_len,
                                               Sequence &q, int32_t *err)
 {
@@ -78,10 +79,22 @@ __device__ __forceinline__ bool read_sequence(const BatchView &b, int64_t s, int
         raise_flag(err, DLRM_FLAG_BAD_OFFSETS);
         return false;
     }
+    if (err && ((s == 0 && f != 0) || (s == b.S - 1 && e != b.n)))
+        raise_flag(err, DLRM_FLAG_BAD_OFFSETS);
     q.first = f;
     q.count = (int)(e - f);
     q.length = (int)len;
     return true;
+}
+
+// Raises the flag for this thread's share of the sequences, with and without new
+// tokens, if they are to be appended (attention reads every sequence anyway).
+__device__ __forceinline__ void check_sequences(const BatchView &b, int64_t thread, int64_t threads, int32_t *err)
+{
+    Sequence q;
+    for (int64_t s = thread; err && s < b.S; s += threads)
+        if (read_sequence(b, s, b.n, b.capacity, q, err) && q.count > q.length)
+            raise_flag(err, DLRM_FLAG_BAD_OFFSETS);
 }
 
 // The last sequence that starts at or before token i, by one warp: 32 probes

@@ -4,8 +4,10 @@ import numpy as np
 import pytest
 import torch
 
+import sparse_dense_interaction_gb300 as sdi
+from sparse_dense_interaction_gb300 import _native
 from tests import _history_ref as R
-from tests.test_gpu_history import DEV, attend, attention_inputs, close, np64
+from tests.test_gpu_history import DEV, attend, attention_inputs, close, flag, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +77,49 @@ def test_a_query_of_nan_gives_nan(case):
     got, got_lse = attend(case, q, offsets, lens, table_d, kc, vc, 0.125)
     assert got[bad].isnan().all() and got_lse[bad].isnan().all()
     assert torch.equal(got[~bad], out[~bad]) and torch.equal(got_lse[~bad], lse[~bad])
+
+
+# an idle sequence in the middle: rows of 16, whole and shared out; tiles, ranked and in the batch's order; general
+CONTRADICTED = [
+    ([2, 0, 2], [60, 40, 50], 4, 2, 64, 16, False, True, 0, "bf16"), ([2, 0, 2], [9000, 40, 50], 4, 2, 64, 16, True, True, 0, "f16"),
+    ([2, 0, 2], [60, 40, 50], 4, 2, 64, 16, False, True, 0, "f32"), ([40, 0, 40], [60, 40, 50], 4, 2, 64, 16, False, True, 0, "f16"),
+    ([20] + [0] * 300 + [20], [60] + [40] * 300 + [50], 4, 2, 128, 16, True, True, 0, "bf16"),
+    ([2, 0, 2], [60, 40, 50], 4, 2, 20, 7, False, True, 0, "f32"), ([2, 0, 2], [60, 40, 50], 4, 2, 20, 7, False, True, 0, "bf16"),
+]
+
+
+@pytest.mark.parametrize("what", ["idle and negative", "idle and beyond its table", "first token", "last token"])
+@pytest.mark.parametrize("case", CONTRADICTED)
+def test_contradictions_of_a_batch_are_flagged_by_every_call(case, what):
+    counts, lengths, hq, hk, d, page, first, causal, window, dtype = case
+    table, table_d, offsets, lens, kc, vc, q = attention_inputs(case, stale=0.0)
+    n, c, S = q.shape[0], counts[0], len(counts)
+    good, good_lse = attend(case, q, offsets, lens, table_d, kc, vc, 0.125, f := flag())
+    assert sdi.dlrm_read_error(f) == 0
+    k, v = q[:, :hk].contiguous(), q[:, hk:2 * hk].contiguous()
+    kc1, vc1 = kc.clone(), vc.clone()
+    sdi.dlrm_kv_append(k, v, offsets, lens, table_d, kc1, vc1, err_flag=(f := flag()))
+    assert sdi.dlrm_read_error(f) == 0
+    same, left_out = slice(0, n), slice(0, 0)
+    if what == "idle and negative":
+        lens[1] = -1
+    elif what == "idle and beyond its table":
+        lens[1] = table_d.shape[1] * page + 1
+    elif what == "first token":
+        offsets[0], same, left_out = 1, slice(c, n), slice(0, 1)
+    else:
+        offsets[S], same, left_out = n - 1, slice(0, c), slice(n - 1, n)
+    out, lse = attend(case, q, offsets, lens, table_d, kc, vc, 0.125, f := flag())
+    assert sdi.dlrm_read_error(f) == _native.ERR_BAD_OFFSETS
+    assert torch.equal(out[same], good[same]) and torch.equal(lse[same], good_lse[same])
+    assert (out[left_out] == 7).all() and (lse[left_out] == 7).all()
+    kc2, vc2 = kc.clone(), vc.clone()
+    sdi.dlrm_kv_append(k, v, offsets, lens, table_d, kc2, vc2, err_flag=(f := flag()))
+    assert sdi.dlrm_read_error(f) == _native.ERR_BAD_OFFSETS
+    at = np.concatenate([np.arange(m - e, m) for e, m in zip(counts, lengths)])
+    pages = table[np.repeat(np.arange(S), counts), at // page]
+    for got, want, before in ((kc2, kc1, kc), (vc2, vc1, vc)):
+        if what.startswith("idle"):
+            assert torch.equal(got, want)
+        else:  # the other sequences' tokens are stored, the token of nobody is not
+            assert np.array_equal(np64(got)[pages[same], at[same] % page], np64(want)[pages[same], at[same] % page])
