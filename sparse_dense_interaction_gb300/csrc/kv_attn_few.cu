@@ -146,7 +146,16 @@ __device__ __forceinline__ bool few_sequence(const AttnParams &p, FewItem &w, in
     return units > 0;
 }
 
-__device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int unit)
+// Sequences of a thread when the batch's are shared out over a CTA.
+__device__ __forceinline__ int few_run(const AttnParams &p)
+{
+    return (int)((p.batch.S + kFewWarps * 32 - 1) / (kFewWarps * 32));
+}
+
+// The next item, by a whole warp.  Sequences without new tokens (slots of idle users) are passed over 32 at
+// a time, then whole runs of them (busy: the first sequence with some of each run, -1: none).  Two users with
+// 200000 events, 12000 idle ones between them: 103 us, the search for the CTAs' shares; one at a time 4930.
+__device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int unit, const int *busy)
 {
     if (++w.tile == w.tiles) {
         w.tile = 0;
@@ -158,10 +167,23 @@ __device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int un
         w.last += units;
         return;
     }
-    const int first = w.last;
-    for (int64_t s = w.s + 1; s < p.batch.S; s++)
-        if (few_sequence(p, w, s, first, unit))
-            return;
+    const int first = w.last, lane = threadIdx.x & 31;
+    const int S = (int)p.batch.S, run = few_run(p), here = (int)w.s / run, end = min((here + 1) * run, S);
+    int next = -1;
+    for (int s = (int)w.s + 1; s < end && next < 0; s += 32) {
+        Sequence mine;
+        const bool some = s + lane < end && read_sequence(p.batch, s + lane, p.max_new, p.max_len, mine, nullptr) &&
+                          mine.count > 0;
+        const uint32_t found = __ballot_sync(0xffffffffu, some);
+        next = found ? s + __ffs(found) - 1 : -1;
+    }
+    for (int r = here + 1; r < kFewWarps * 32 && next < 0; r += 32) {
+        const int mine = r + lane < kFewWarps * 32 ? busy[r + lane] : -1;
+        const uint32_t found = __ballot_sync(0xffffffffu, mine >= 0);
+        next = found ? __shfl_sync(0xffffffffu, mine, __ffs(found) - 1) : -1;
+    }
+    if (next >= 0 && few_sequence(p, w, next, first, unit))
+        return;
     w.last = 0x7fffffff;  // not reached: a CTA's units end with the last item's
 }
 
@@ -174,18 +196,21 @@ __host__ __device__ __forceinline__ int64_t few_quota(int64_t total, int ctas)
 
 // The CTA's share of all units: sums every sequence's units (each thread a run
 // of sequences), finds the item that holds the first unit of the share.
-__device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int &quota_units, int unit)
+__device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int &quota_units, int unit, int *busy)
 {
     __shared__ int64_t sums[kFewWarps], found[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t run = (p.batch.S + kFewWarps * 32 - 1) / (kFewWarps * 32);
+    const int64_t run = few_run(p);
     const int64_t from = min(threadIdx.x * run, p.batch.S), to = min(from + run, p.batch.S);
     int64_t mine = 0;
     Sequence q;
-    int lo, hi;
+    int lo, hi, first = -1;
     for (int64_t s = from; s < to; s++)
-        if (read_sequence(p.batch, s, p.max_new, p.max_len, q, blockIdx.x == 0 ? p.err : nullptr))
+        if (read_sequence(p.batch, s, p.max_new, p.max_len, q, blockIdx.x == 0 ? p.err : nullptr)) {
             mine += (int64_t)few_units(p, q, unit, lo, hi) * few_tiles(p, q) * p.cache.heads;
+            first = first < 0 && q.count > 0 ? (int)s : first;
+        }
+    busy[threadIdx.x] = first;
     int64_t before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -292,6 +317,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     extern __shared__ uint8_t raw[];
     __shared__ float s_m[kFewWarps][kFewRows], s_l[kFewWarps][kFewRows];
     __shared__ uint64_t bars[kFewWarps][kFewStages];
+    __shared__ int busy[kFewWarps * 32];
     __shared__ int aborted, died_at[kFewWarps];  // died_at: the part whose wait ran out
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     uint8_t *smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
@@ -301,7 +327,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     FewItem it;  // of the unit being computed; `is`: of the unit whose addresses come next
     int units, quota = 0;  // of this CTA; the items' are counted from its first
     if (p.splits > 1) {
-        const bool any = few_share(p, it, units, quota, UT);
+        const bool any = few_share(p, it, units, quota, UT, busy);
         if (threadIdx.x == 0)
             p.joins[blockIdx.x].rows = 0;  // until an item is left unfinished
         if (!any)
@@ -333,7 +359,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         if (u >= units)
             return;
         while (u >= is.last)
-            few_next(p, is, UT);
+            few_next(p, is, UT, busy);
         const int at = is.lo + (u - is.first) * UT + warp * Sh::TB + my_token;
         if (copies && at < is.hi && at + (kBulk ? maps.rows : 1) > is.lo_seen) {
             const uint32_t page = p.cache.page.div((uint32_t)at);
@@ -795,7 +821,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         fresh = true;
         first_item = false;
         if (u + 1 < units)
-            few_next(p, it, UT);
+            few_next(p, it, UT, busy);
     }
     if (kBulk && dead) {
         // that part and those copied ahead of it may still be in flight: none may be when the memory is given back
@@ -947,8 +973,10 @@ static int launch_few(AttnParams &p, const FewMaps &maps, void *workspace, cudaS
         return s;
     // a window bounds what an item's rows see, whatever the history's length
     const int64_t seen = p.window > 0 ? p.window + (p.causal ? p.max_new : 0) : p.max_len;
-    const int64_t items = p.batch.S * p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows);
-    const bool split = few_splits(seen < p.max_len ? seen : p.max_len, p.d, sizeof(T), items);
+    // items, idle sequences' among them; the batch cannot have more busy sequences than tokens
+    const int64_t each = p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows), items = p.batch.S * each;
+    const int64_t busy = (p.batch.S < p.batch.n ? p.batch.S : p.batch.n) * each;
+    const bool split = few_splits(seen < p.max_len ? seen : p.max_len, p.d, sizeof(T), busy);
     p.splits = split ? 2 : 1;
     p.joins = static_cast<FewJoin *>(workspace);
     p.part_o = reinterpret_cast<float *>(p.joins + kFewMaxCtas);

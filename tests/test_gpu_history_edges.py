@@ -7,7 +7,7 @@ import torch
 import sparse_dense_interaction_gb300 as sdi
 from sparse_dense_interaction_gb300 import _native
 from tests import _history_ref as R
-from tests.test_gpu_history import DEV, attend, attention_inputs, close, flag, np64
+from tests.test_gpu_history import DEV, attend, attention_inputs, check_attention, close, flag, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,45 @@ def test_contradictions_of_a_batch_are_flagged_by_every_call(case, what):
             assert torch.equal(got, want)
         else:  # the other sequences' tokens are stored, the token of nobody is not
             assert np.array_equal(np64(got)[pages[same], at[same] % page], np64(want)[pages[same], at[same] % page])
+
+
+def idle_batch(busy, idle, where, length, dtype):
+    """`busy` users with up to `length` events and one new among `idle` slots without."""
+    S = busy + idle
+    at = {"ends": np.linspace(0, S - 1, busy).astype(int), "last": np.arange(idle, S),
+          "anywhere": np.sort(np.random.default_rng(S).permutation(S)[:busy])}[where]
+    counts, lengths = np.zeros(S, int), np.full(S, 5)
+    counts[at] = 1
+    lengths[at] = length - np.arange(busy) * (length // (busy + 1))
+    return counts.tolist(), lengths.tolist(), 4, 1, 64, 16, True, True, 0, dtype
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["ends", "last", "anywhere"])
+@pytest.mark.parametrize("busy,idle,length", [(2, 1, 20000), (2, 31, 20000), (3, 127, 9000), (9, 1500, 9000), (2, 3000, 30000)])
+def test_attention_among_idle_users(busy, idle, length, where, dtype):
+    case = idle_batch(busy, idle, where, length, dtype)
+    table, table_d, offsets, lens, kc, vc, q = attention_inputs(case)
+    f = flag()
+    out, lse = attend(case, q, offsets, lens, table_d, kc, vc, 0.125, f)
+    assert sdi.dlrm_read_error(f) == 0
+    check_attention(case, q, table, kc, vc, 0.125, out, lse)
+
+
+def test_idle_users_cost_little():
+    # 3000 slots between two long histories: 47 us beside 36 without them, 1231 when they were passed one by one
+    def best(idle):
+        case = idle_batch(2, idle, "ends", 200000, "bf16")
+        _, table_d, offsets, lens, kc, vc, q = attention_inputs(case)
+        out = torch.empty_like(q)
+        ws = torch.empty(sdi.dlrm_kv_attn_workspace_size(2 + idle, 2, 4, 1, 64, 1, 200000), dtype=torch.uint8, device=DEV)
+        times = []
+        for _ in range(30):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            sdi.dlrm_kv_attn_fwd(q, offsets, lens, table_d, kc, vc, out, 0.125, ws, 1, 200000)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    assert best(3000) < 5 * best(0)
