@@ -21,7 +21,9 @@
  * elements; the d elements of a head row are contiguous.  Inputs may share
  * rows (a stride of 0); the rows of an output lie apart (strides of at least d
  * where there is more than one; DLRM_ERR_INVALID_ARG otherwise) and must not
- * overlap the inputs.
+ * overlap the inputs, but for the norms, their gradient and the append's queries
+ * in place: q_out may be q and k_out may be k, dq may be q or dq_out and dk may
+ * be k or dk_out, with the same pointer and strides.
  */
 #ifndef DLRM_HISTORY_H
 #define DLRM_HISTORY_H

@@ -56,7 +56,8 @@ __device__ __forceinline__ float inv_rms(float squares, int d, float eps)
     return 1.f / sqrtf(warp_sum(squares) / (float)d + eps);
 }
 
-// One row: norm (weight not null) and rotation (row not null) into y.
+// One row: norm (weight not null) and rotation (row not null) into y, which may
+// be x: it is written when every lane has read.
 template <typename T>
 __device__ __forceinline__ void norm_rope_row(const T *x, T *y, int d, const float *weight, float eps,
                                               const RopeView &rope, const float *angles)
@@ -85,8 +86,13 @@ __device__ __forceinline__ void norm_rope_row(const T *x, T *y, int d, const flo
             const float c = angles[a], s = angles[a + (rope.rot >> 1)];
             z = first ? fmaf(z, c, -zo * s) : fmaf(z, c, zo * s);
         }
-        y[e] = from_f32<T>(z);
+        v[j] = z;
     }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kRowElems; j++)
+        if (lane + 32 * j < d)
+            y[lane + 32 * j] = from_f32<T>(v[j]);
 }
 
 template <typename T>
@@ -175,6 +181,7 @@ norm_rope_bwd_rows_kernel(HeadsView dqo, HeadsView dko, HeadsView q, HeadsView k
                 dz[j] = r * fmaf(-v[j], m, dz[j] * weight[e]);
             }
         }
+        __syncwarp();  // dx may be x or dy
 #pragma unroll
         for (int j = 0; j < kRowElems; j++)
             if (lane + 32 * j < d)

@@ -7,7 +7,9 @@ import torch
 import sparse_dense_interaction_gb300 as sdi
 from sparse_dense_interaction_gb300 import _native
 from tests import _history_ref as R
-from tests.test_gpu_history import DEV, attend, attention_inputs, check_attention, close, flag, np64
+from tests.test_gpu_history import (
+    APPEND, DEV, DT, EPS, NORM, attend, attention_inputs, check_attention, close, flag, heads_of, make_batch, make_cache, norm_inputs,
+    np64, randn, rope_table)
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +167,53 @@ def test_idle_users_cost_little():
             times.append(a.elapsed_time(b))
         return min(times)
     assert best(3000) < 5 * best(0)
+
+
+@pytest.mark.parametrize("case", NORM)
+@pytest.mark.parametrize("normed", [True, False])
+def test_norm_rope_and_gradient_in_place(case, normed):
+    n, hq, hk, d, rot, inter, dtype, pad = case
+    x, w, table, at = norm_inputs(case)
+    if not normed:
+        w = {"q": None, "k": None}
+    copy = lambda t: {a: None if u is None else heads_of(9, n, u.shape[1], d, dtype, pad).copy_(u) for a, u in t.items()}
+    run = lambda x, out: sdi.dlrm_qk_norm_rope_fwd(x["q"], x["k"], w["q"], w["k"], EPS, table, at, out["q"], out["k"],
+                                                   interleaved=inter)
+    want, got = copy(x), copy(x)
+    run(x, want)
+    run(got, got)
+    for a in x:
+        assert x[a] is None or torch.equal(got[a], want[a])
+    dy = {a: heads_of(11, n, t.shape[1], d, dtype, pad, 1.0) if t is not None else None for a, t in x.items()}
+    ws = torch.empty(sdi.dlrm_qk_norm_rope_bwd_workspace_size(n, hq, hk, d), dtype=torch.uint8, device=DEV)
+
+    def back(dy, x, dx):
+        dw = {a: torch.empty(d, device=DEV) if normed and x[a] is not None else None for a in x}
+        sdi.dlrm_qk_norm_rope_bwd(dy["q"], dy["k"], x["q"], x["k"], w["q"], w["k"], EPS, table, at, dx["q"], dx["k"],
+                                  dw["q"], dw["k"], ws, interleaved=inter)
+        return dw
+
+    want, over_dy, over_x = copy(x), copy(dy), copy(x)
+    results = [back(dy, x, want), back(over_dy, x, over_dy), back(dy, over_x, over_x)]
+    for a in x:
+        if x[a] is not None:
+            assert torch.equal(over_dy[a], want[a]) and torch.equal(over_x[a], want[a])
+            assert not normed or all(torch.equal(r[a], results[0][a]) for r in results)
+
+
+@pytest.mark.parametrize("case", [c for c in APPEND if c[2]])
+def test_append_turns_its_queries_in_place(case):
+    counts, lengths, hq, hk, d, rot, page, first, normed, inter, dtype = case
+    n = sum(counts)
+    _, table_d, offsets, lens, pages = make_batch(counts, lengths, page)
+    kc, vc = (make_cache(s, pages, page, hk, d, dtype, first) for s in (21, 22))
+    qkv = randn(23, (n, hq + 2 * hk, d), dtype, 1.5)
+    weight = 1 + 0.3 * randn(3, (d,), "f32") if normed else None
+
+    def run(q, q_out):
+        sdi.dlrm_kv_append(qkv[:, hq:hq + hk], qkv[:, hq + hk:], offsets, lens, table_d, kc, vc, k_weight=weight, eps=EPS,
+                           rope=rope_table(max(lengths), rot), interleaved=inter, q=q, q_weight=weight, q_out=q_out)
+        return q_out
+
+    want = run(qkv[:, :hq], torch.empty((n, hq, d), dtype=DT[dtype], device=DEV))
+    assert torch.equal(run(qkv[:, :hq], qkv[:, :hq]), want)
