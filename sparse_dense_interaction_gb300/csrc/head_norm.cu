@@ -10,8 +10,8 @@
 // lane l holds the elements l, l + 32, ...  Rows that can be moved as 4-element pieces
 // take the vector path (head_norm.cuh).  Loads of single elements, few at a
 // time, bound them: 20000 tokens of 8 query and 2 key heads of 250 bf16 elements
-// take 200 us forward, 1.0 TB/s, 374 backward, 0.8 TB/s; of 17 fp32 elements 87
-// and 122 us; the append of as many rows of 250 282 us.
+// take 180 us forward, 1.1 TB/s, 373 backward, 0.8 TB/s; of 17 fp32 elements 89
+// and 123 us; the append of as many rows of 250 294 us.
 #include <initializer_list>
 
 #include "head_norm.cuh"
@@ -124,8 +124,11 @@ norm_rope_rows_kernel(HeadsView q, HeadsView k, int64_t n, int d, const float *_
 }
 
 // blockIdx.y: 0 the queries, 1 the keys.  part: [2][gridDim.x][d] sums of the
-// weights' gradients.
-template <typename T>
+// weights' gradients.  dx may be x or dy: what is stored depends on sums of all that
+// the warp reads of the row, but for rows that are only turned (kPlain: there are
+// some), which wait for one another (in all rows that takes 418 us instead of 373
+// for the bf16 gradient named above).
+template <typename T, bool kPlain>
 __global__ void __launch_bounds__(kWarps * 32)
 norm_rope_bwd_rows_kernel(HeadsView dqo, HeadsView dko, HeadsView q, HeadsView k, int64_t n, int d,
                           const float *__restrict__ qw, const float *__restrict__ kw, float eps, RopeView rope,
@@ -181,7 +184,8 @@ norm_rope_bwd_rows_kernel(HeadsView dqo, HeadsView dko, HeadsView q, HeadsView k
                 dz[j] = r * fmaf(-v[j], m, dz[j] * weight[e]);
             }
         }
-        __syncwarp();  // dx may be x or dy
+        if (kPlain)
+            __syncwarp();
 #pragma unroll
         for (int j = 0; j < kRowElems; j++)
             if (lane + 32 * j < d)
@@ -337,8 +341,8 @@ static int norm_bwd(const HeadsView &dqo, const HeadsView &dko, const HeadsView 
 {
     const int64_t ctas = bwd_ctas(n, q.heads > k.heads ? q.heads : k.heads);
     const unsigned sides = k.heads > 0 ? 2 : 1;
-    norm_rope_bwd_rows_kernel<T><<<dim3((unsigned)ctas, sides), kWarps * 32, 0, st>>>(dqo, dko, q, k, n, d, qw, kw,
-                                                                                      eps, rope, dq, dk, part, err);
+    const auto kernel = qw && (kw || sides == 1) ? norm_rope_bwd_rows_kernel<T, false> : norm_rope_bwd_rows_kernel<T, true>;
+    kernel<<<dim3((unsigned)ctas, sides), kWarps * 32, 0, st>>>(dqo, dko, q, k, n, d, qw, kw, eps, rope, dq, dk, part, err);
     count_launch(st);
     if (dqw || dkw)
         launch_norm_weight_sum(part, ctas, sides == 2 ? ctas : 0, d, dqw, dkw, st);
