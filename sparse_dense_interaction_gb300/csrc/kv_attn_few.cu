@@ -152,9 +152,31 @@ __device__ __forceinline__ int few_run(const AttnParams &p)
     return (int)((p.batch.S + kFewWarps * 32 - 1) / (kFewWarps * 32));
 }
 
-// The next item, by a whole warp.  Sequences without new tokens (slots of idle users) are passed over 32 at
-// a time, then whole runs of them (busy: the first sequence with some of each run, -1: none).  Two users with
-// 200000 events, 12000 idle ones between them: 103 us, the search for the CTAs' shares; one at a time 4930.
+// The first sequence after `s` that has new tokens, by a whole warp; -1: none.  Idle sequences (slots of users
+// who wait) are passed over 32 at a time, then whole runs of them (busy: the first sequence with new tokens of
+// each run, -1: none).  Two users with 200000 events, 12000 idle ones between them: 103 us, the search for the
+// CTAs' shares; read one by one 4930.  Not inlined: it is rare, and its copies would cost registers.
+__device__ __noinline__ int few_busy_after(const AttnParams &p, int s0, const int *busy)
+{
+    const int lane = threadIdx.x & 31, S = (int)p.batch.S, run = few_run(p), here = s0 / run;
+    const int end = min((here + 1) * run, S);
+    int next = -1;
+    for (int s = s0 + 1; s < end && next < 0; s += 32) {
+        Sequence mine;
+        const bool some = s + lane < end && read_sequence(p.batch, s + lane, p.max_new, p.max_len, mine, nullptr) &&
+                          mine.count > 0;
+        const uint32_t found = __ballot_sync(0xffffffffu, some);
+        next = found ? s + __ffs(found) - 1 : -1;
+    }
+    for (int r = here + 1; r < kFewWarps * 32 && next < 0; r += 32) {
+        const int mine = r + lane < kFewWarps * 32 ? busy[r + lane] : -1;
+        const uint32_t found = __ballot_sync(0xffffffffu, mine >= 0);
+        next = found ? __shfl_sync(0xffffffffu, mine, __ffs(found) - 1) : -1;
+    }
+    return next;
+}
+
+// The next item, by a whole warp.
 __device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int unit, const int *busy)
 {
     if (++w.tile == w.tiles) {
@@ -167,21 +189,7 @@ __device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int un
         w.last += units;
         return;
     }
-    const int first = w.last, lane = threadIdx.x & 31;
-    const int S = (int)p.batch.S, run = few_run(p), here = (int)w.s / run, end = min((here + 1) * run, S);
-    int next = -1;
-    for (int s = (int)w.s + 1; s < end && next < 0; s += 32) {
-        Sequence mine;
-        const bool some = s + lane < end && read_sequence(p.batch, s + lane, p.max_new, p.max_len, mine, nullptr) &&
-                          mine.count > 0;
-        const uint32_t found = __ballot_sync(0xffffffffu, some);
-        next = found ? s + __ffs(found) - 1 : -1;
-    }
-    for (int r = here + 1; r < kFewWarps * 32 && next < 0; r += 32) {
-        const int mine = r + lane < kFewWarps * 32 ? busy[r + lane] : -1;
-        const uint32_t found = __ballot_sync(0xffffffffu, mine >= 0);
-        next = found ? __shfl_sync(0xffffffffu, mine, __ffs(found) - 1) : -1;
-    }
+    const int first = w.last, next = few_busy_after(p, (int)w.s, busy);
     if (next >= 0 && few_sequence(p, w, next, first, unit))
         return;
     w.last = 0x7fffffff;  // not reached: a CTA's units end with the last item's
