@@ -81,7 +81,9 @@ typedef struct dlrm_kv_cache {
  * within 0 .. n, raise DLRM_FLAG_BAD_OFFSETS and that sequence is left out
  * (nothing of it is written), whether it has new tokens or not.  offsets[0] is 0
  * and offsets[S] is n: else the flag is raised too, and what no sequence owns is
- * left out.  (A call with n = 0 launches nothing and checks none of this.) */
+ * left out.  Where offsets fall, a token's sequence may not be found, and sequences
+ * that are sound by themselves may be left out too, in part.  (A call with n = 0
+ * launches nothing and checks none of this.) */
 typedef struct dlrm_kv_batch {
     int64_t S;                 /* sequences, 0 .. 2^24 */
     int64_t n;                 /* new tokens, 0 .. 2^31 - 1 */

@@ -217,3 +217,49 @@ def test_append_turns_its_queries_in_place(case):
 
     want = run(qkv[:, :hq], torch.empty((n, hq, d), dtype=DT[dtype], device=DEV))
     assert torch.equal(run(qkv[:, :hq], qkv[:, :hq]), want)
+
+
+@pytest.mark.parametrize("bad", [[0, 3, 1, 2, 4], [4, 3, 2, 1, 0], [-5, 1, 2, 1 << 40, 4], [1, 1, 1, 1, 1], [0, 1, 2, 1, 4],
+                                 [0, 4, 0, 4, 4], [2, 3, 0, 1, 2], [-(1 << 62), 1 << 62, 0, 1, 2]])
+@pytest.mark.parametrize("c,length,d,dtype", [(1, 40, 64, "bf16"), (1, 9000, 64, "f16"), (40, 40, 64, "f16"), (40, 9000, 128, "bf16"),
+                                              (2, 40, 64, "f32"), (2, 40, 20, "f32"), (1, 5000, 20, "bf16"), (5, 300, 200, "f16")])
+def test_offsets_that_fall_touch_only_what_a_sound_sequence_owns(c, length, d, dtype, bad):
+    """Rows and slots hold what their sequence gives them, or what they held."""
+    hq, hk, page, S, n = 4, 2, 16, 4, 4 * c
+    case = ([c] * S, [length] * S, hq, hk, d, page, False, True, 0, dtype)
+    table, table_d, _, lens, kc, vc, q = attention_inputs(case, stale=0.0)
+    offsets = [o * c if abs(o) <= 5 else o for o in bad]
+    offsets_d = torch.tensor(offsets, device=DEV)
+    guard, size = 1024, n * hq * d
+    buf, lse_buf = torch.full((size + 2 * guard,), 7, dtype=DT[dtype], device=DEV), torch.full((n * hq + 2 * guard,), 7.0, device=DEV)
+    out, lse = buf[guard:guard + size].view(n, hq, d), lse_buf[guard:guard + n * hq].view(n, hq)
+    ws = torch.full((sdi.dlrm_kv_attn_workspace_size(S, n, hq, hk, d, c, length),), 255, dtype=torch.uint8, device=DEV)
+    sdi.dlrm_kv_attn_fwd(q, offsets_d, lens, table_d, kc, vc, out, 0.125, ws, c, length, lse=lse, err_flag=(f := flag()))
+    assert sdi.dlrm_read_error(f) == _native.ERR_BAD_OFFSETS
+    for b in (buf, lse_buf):
+        assert (b[:guard] == 7).all() and (b[-guard:] == 7).all()
+    sound = [s for s in range(S) if 0 <= offsets[s] <= offsets[s + 1] <= n]
+    right = torch.zeros((n, hq), dtype=torch.bool, device=DEV)
+    for s in sound:
+        a, e = offsets[s], offsets[s + 1]
+        if not 0 < e - a <= c:
+            continue
+        want, wl, absout, smax, flat = R.attention(np64(q[a:e]), [e - a], [length], table[s:s + 1], np64(kc), np64(vc), 0.125, True, 0)
+        tol = R.attention_tolerance(want, absout, smax, flat, d, dtype)
+        right[a:e] |= torch.from_numpy((np.abs(np64(out[a:e]) - want) <= tol).all(-1) &
+                                       (np.abs(np64(lse[a:e]) - wl) <= R.lse_tolerance(wl, smax, d))).to(DEV)
+    assert (right | ((out == 7).all(-1) & (lse == 7))).all()
+
+    # the append: a slot may hold a token of a sound sequence that has its place there, or what it held
+    k, v = q[:, :hk].contiguous(), q[:, hk:].contiguous()
+    kc2, vc2 = kc.clone(), vc.clone()
+    sdi.dlrm_kv_append(k, v, offsets_d, lens, table_d, kc2, vc2, err_flag=(f := flag()))
+    assert sdi.dlrm_read_error(f) == _native.ERR_BAD_OFFSETS
+    same = (kc2 == kc).flatten(2).all(-1) & (vc2 == vc).flatten(2).all(-1)
+    for s in sound:
+        a, e = offsets[s], offsets[s + 1]
+        if e - a <= length:
+            at = np.arange(length - (e - a), length)
+            pages, slots = (torch.from_numpy(x).long().to(DEV) for x in (table[s, at // page], at % page))
+            same[pages, slots] |= (kc2[pages, slots] == k[a:e]).flatten(1).all(-1) & (vc2[pages, slots] == v[a:e]).flatten(1).all(-1)
+    assert same.all()
