@@ -50,6 +50,20 @@ def _int64(t, what, n):
     return t.data_ptr()
 
 
+def _workspace(t):
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("a workspace is a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _flag(t):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or not t.is_cuda or t.numel() < 1:
+        raise ValueError("err_flag is an int32 CUDA tensor")
+    return t.data_ptr()
+
+
 def _rope(rope, positions, interleaved, n):
     if rope is None:
         return None
@@ -97,7 +111,7 @@ def dlrm_qk_norm_rope_fwd(q, k, q_weight, k_weight, eps: float, rope, positions,
     _check(load().dlrm_qk_norm_rope_fwd(
         _heads(q, n, d, dtype), None if k is None else _heads(k, n, d, dtype), n, d, _TORCH_DTYPES[dtype],
         _weight(q_weight, d), _weight(k_weight, d), eps, _rope(rope, positions, interleaved, n),
-        _heads(q_out, n, d, dtype), None if k_out is None else _heads(k_out, n, d, dtype), _ptr(err_flag),
+        _heads(q_out, n, d, dtype), None if k_out is None else _heads(k_out, n, d, dtype), _flag(err_flag),
         _stream(stream)), "dlrm_qk_norm_rope_fwd")
 
 
@@ -117,7 +131,7 @@ def dlrm_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, eps: float, 
         None if k is None else _heads(k, n, d, dtype), n, d, _TORCH_DTYPES[dtype], _weight(q_weight, d),
         _weight(k_weight, d), eps, _rope(rope, positions, interleaved, n), _heads(dq, n, d, dtype),
         None if dk is None else _heads(dk, n, d, dtype), _weight(dq_weight, d), _weight(dk_weight, d),
-        workspace.data_ptr(), workspace.nbytes, _ptr(err_flag), _stream(stream)), "dlrm_qk_norm_rope_bwd")
+        _workspace(workspace), workspace.nbytes, _flag(err_flag), _stream(stream)), "dlrm_qk_norm_rope_bwd")
 
 
 def dlrm_kv_append(k, v, offsets, lengths, page_table, k_cache, v_cache, k_weight=None, eps: float = 1e-6, rope=None,
@@ -133,7 +147,7 @@ def dlrm_kv_append(k, v, offsets, lengths, page_table, k_cache, v_cache, k_weigh
         _heads(k, n, d, dtype), _heads(v, n, d, dtype), _batch(offsets, lengths, page_table, n),
         _cache(k_cache, v_cache, d, dtype), d, _TORCH_DTYPES[dtype], _weight(k_weight, d), eps,
         _rope(rope, positions, interleaved, n), None if q is None else _heads(q, n, d, dtype), _weight(q_weight, d),
-        None if q_out is None else _heads(q_out, n, d, dtype), _ptr(err_flag), _stream(stream)), "dlrm_kv_append")
+        None if q_out is None else _heads(q_out, n, d, dtype), _flag(err_flag), _stream(stream)), "dlrm_kv_append")
 
 
 def dlrm_kv_attn_workspace_size(S: int, n: int, q_heads: int, kv_heads: int, d: int, max_new: int,
@@ -159,4 +173,4 @@ def dlrm_kv_attn_fwd(q, offsets, lengths, page_table, k_cache, v_cache, out, sca
     _check(load().dlrm_kv_attn_fwd(
         _heads(q, n, d, dtype), _batch(offsets, lengths, page_table, n), _cache(k_cache, v_cache, d, dtype), d,
         _TORCH_DTYPES[dtype], scale, 1 if causal else 0, window, max_new, max_len, _heads(out, n, d, dtype),
-        _ptr(lse), workspace.data_ptr(), workspace.nbytes, _ptr(err_flag), _stream(stream)), "dlrm_kv_attn_fwd")
+        _ptr(lse), _workspace(workspace), workspace.nbytes, _flag(err_flag), _stream(stream)), "dlrm_kv_attn_fwd")
