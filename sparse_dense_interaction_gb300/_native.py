@@ -127,8 +127,11 @@ def _check(status: int, what: str):
 
 
 def _stream(stream) -> int:
-    if stream is None:  # torch.cuda.current_stream().cuda_stream, without the Stream object (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        try:  # the current stream without its Stream object (3 us); not torch's public interface
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

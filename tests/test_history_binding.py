@@ -82,3 +82,16 @@ def test_flags_are_int32_and_on_the_gpu(lib, call):
         with pytest.raises(ValueError):
             call(err_flag=bad)
     assert len(lib.calls) == 1
+
+
+@pytest.mark.parametrize("gone", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_the_current_stream_by_the_public_interface(monkeypatch, gone):
+    class Stream:
+        cuda_stream = 77
+
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.setattr(torch._C, name, lambda *args: 5, raising=False)
+    assert _native._stream(None) == 5
+    monkeypatch.delattr(torch._C, gone)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream())
+    assert _native._stream(None) == 77 and _native._stream(3) == 3 and _native._stream(Stream()) == 77
