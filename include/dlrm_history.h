@@ -181,7 +181,7 @@ size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_hea
  *
  * q, out     heads a multiple of the cache's; dtype is that of q, out and the
  *            cache.
- * scale      > 0 and finite.
+ * scale      > 0, at most 2e38.
  * causal     0 or 1;  window  >= 0, 0 for none.
  * max_new, max_len  host bounds of the batch's new tokens per sequence and
  *            lengths, for the launch's shape; a sequence beyond them raises

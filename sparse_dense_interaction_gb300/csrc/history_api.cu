@@ -19,6 +19,7 @@ int launch_kv_attn(AttnParams &, int, void *, cudaStream_t);
 
 static const int64_t kMaxTokens = 0x7fffffffLL, kMaxPositions = (int64_t)1 << 30, kMaxSequences = (int64_t)1 << 24;
 static const int kMaxHeads = 65536;
+static const float kMaxScale = 2.0e38f;  // times log2(e) it is still finite
 
 static bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -230,7 +231,7 @@ int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm
         (s = check_batch(batch, cache->page_size, p.batch)) != DLRM_OK ||
         (s = check_pair(q, out, n, d, dtype, p.q, p.out)) != DLRM_OK)
         return s;
-    if (p.q.heads % p.cache.heads != 0 || !(scale > 0.f) || !(scale <= 3.0e38f) || (causal != 0 && causal != 1) ||
+    if (p.q.heads % p.cache.heads != 0 || !(scale > 0.f) || !(scale <= kMaxScale) || (causal != 0 && causal != 1) ||
         window < 0 || max_new < 0 || max_len < 0 || !aligned(lse, 4) || !workspace || !aligned(workspace, 16))
         return DLRM_ERR_INVALID_ARG;
     p.group = p.q.heads / p.cache.heads;
