@@ -198,8 +198,9 @@ size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_hea
  * Scores, the softmax's maxima and sums and the output's sums are fp32.  The
  * products run on the tensor cores for heads of at most 256 16-bit or 128 fp32
  * elements whose widths, strides and pointers are multiples of 16 bytes; others
- * take a general kernel in fp32.  16-bit types: each weight p (relative to the row's running
- * maximum) is rounded to that type, an error as large as the rounding of the
+ * take a general kernel in fp32.  16-bit types: for up to 8 rows (max_new times the query heads
+ * of a cache head) each weight p (relative to the row's running maximum) is carried in two
+ * parts of that type, for more it is rounded to it, an error as large as the rounding of the
  * output itself; f16 weights are scaled to use that type's range, so this holds
  * down to 2^-25 of the row's largest weight, and smaller ones are rounded to
  * steps of at most 2^-35 of it.  fp32: operands are split in two TF32 parts, which carries

@@ -163,6 +163,16 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // log2 of the largest weight that the 16-bit kernels keep.  A weight 2^(s - m) of

@@ -279,6 +279,10 @@ struct FewShape {
     static constexpr int TB = kParts * kFewStageBytes / kTokenBytes, NB = TB / MG, UT = kFewWarps * TB;
     static constexpr int kChunks = kParts > 1 ? 0 : KT * KG + VT * VS;  // from a group to the next
     static constexpr int kStats = 2 * kGroups;                   // rows whose statistics a lane holds
+    // Up to 8 rows a 16-bit weight is carried in two parts, so that the output is rounded once: of 256 users
+    // with up to 8192 events 323 -> 325 us, one of 262143 100.5 -> 100.8.  With 16 rows the
+    // second MMA costs more than one rounding is worth (64 users 44 -> 47 us; 64 new of 256-wide heads 290 -> 319).
+    static constexpr bool kTwoParts = !kWide && kGroups == 1;
     static constexpr int kOutMmas = E / 2;                       // of a set of output columns
     static constexpr int kOut = kGroups * VS * kOutMmas * 4;     // output registers
     // registers joined at a time: with all 64 of them two CTAs would not fit on an SM
@@ -692,13 +696,19 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                     }
                 }
             } else {
-                // the weights, rounded to the type (their sum is of the unrounded ones), rows to columns
-                uint32_t b[kGroups][2];
+                // the weights, rounded to the type, and in narrow tiles what that leaves of them, rows to columns
+                uint32_t b[kGroups][2], rest[kGroups][2];
 #pragma unroll
-                for (int n = 0; n < kGroups; n++) {
-                    b[n][0] = transpose8x8(pack2<T>(s[nb][n][0], s[nb][n][1]));
-                    b[n][1] = transpose8x8(pack2<T>(s[nb][n][2], s[nb][n][3]));
-                }
+                for (int n = 0; n < kGroups; n++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const float x = s[nb][n][2 * h], y = s[nb][n][2 * h + 1];
+                        const uint32_t w = pack2<T>(x, y);
+                        const float2 r = unpack2<T>(w);
+                        b[n][h] = transpose8x8(w);
+                        if (Sh::kTwoParts)
+                            rest[n][h] = transpose8x8(pack2<T>(x - r.x, y - r.y));
+                    }
 #pragma unroll
                 for (int i = 0; i < VS; i++) {
                     uint4 v[VT];
@@ -711,8 +721,12 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                         const uint32_t a[4] = {__byte_perm(w0[j], w1[j], 0x5410), __byte_perm(w0[j], w1[j], 0x7632),
                                                __byte_perm(w2[j], w3[j], 0x5410), __byte_perm(w2[j], w3[j], 0x7632)};
 #pragma unroll
-                        for (int n = 0; n < kGroups; n++)
-                            mma16816<T>(o + ((n * VS + i) * 4 + j) * 4, a, b[n][0], b[n][1]);
+                        for (int n = 0; n < kGroups; n++) {
+                            float *sum = o + ((n * VS + i) * 4 + j) * 4;
+                            if (Sh::kTwoParts)
+                                mma16816<T>(sum, a, rest[n][0], rest[n][1]);
+                            mma16816<T>(sum, a, b[n][0], b[n][1]);
+                        }
                     }
                 }
             }

@@ -263,3 +263,22 @@ def test_offsets_that_fall_touch_only_what_a_sound_sequence_owns(c, length, d, d
             pages, slots = (torch.from_numpy(x).long().to(DEV) for x in (table[s, at // page], at % page))
             same[pages, slots] |= (kc2[pages, slots] == k[a:e]).flatten(1).all(-1) & (vc2[pages, slots] == v[a:e]).flatten(1).all(-1)
     assert same.all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts,lengths,hq,hk,d,page", [
+    ([1] * 20, list(range(10, 2010, 100)), 4, 2, 64, 16), ([1], [20000], 8, 1, 128, 16), ([1] * 6, list(range(50, 350, 50)), 4, 1, 256, 8),
+    ([2, 1], [900, 300], 4, 1, 96, 7), ([4] * 9, [700] * 9, 2, 1, 40, 32)])
+def test_attention_of_few_rows_rounds_its_output_once(counts, lengths, hq, hk, d, page, dtype):
+    """Up to 8 rows carry their weights in two parts: of U of a weight, U is left.
+
+    The sum of p |v| is off by the scores' roundings and by U^2; the output is then
+    rounded to the type (small scores, so that theirs do not hide it)."""
+    case = (counts, lengths, hq, hk, d, page, True, True, 0, dtype)
+    table, table_d, offsets, lens, kc, vc, q = attention_inputs(case)
+    scale = 0.1 / d ** 0.5
+    out, _ = attend(case, q, offsets, lens, table_d, kc, vc, scale)
+    k, v = (np.nan_to_num(np64(t), nan=0.0) for t in (kc, vc))
+    want, _, absout, smax, flat = R.attention(np64(q), counts, lengths, table, k, v, scale, True, 0)
+    score = (d + 4) * 2.0 ** -23 * smax[..., None]
+    close(out, want, (2 * score + 2.0 ** -18 + 2 * R.U[dtype] ** 2) * absout + R.U[dtype] * np.abs(want) * 1.01 + R.TINY[dtype], case)
