@@ -282,3 +282,32 @@ def test_attention_of_few_rows_rounds_its_output_once(counts, lengths, hq, hk, d
     want, _, absout, smax, flat = R.attention(np64(q), counts, lengths, table, k, v, scale, True, 0)
     score = (d + 4) * 2.0 ** -23 * smax[..., None]
     close(out, want, (2 * score + 2.0 ** -18 + 2 * R.U[dtype] ** 2) * absout + R.U[dtype] * np.abs(want) * 1.01 + R.TINY[dtype], case)
+
+
+FORMS = [
+    # fp32 bulk copies of columns that reach past the head's width
+    ([3, 1], [300, 77], 4, 2, 40, 16, False, True, 0, "f32"), ([1, 2], [900, 50], 2, 2, 96, 8, True, False, 0, "f32"),
+    ([5], [200], 3, 1, 24, 32, False, True, 30, "f32"), ([2], [3000], 4, 1, 100, 16, True, True, 0, "f32"),
+    ([1, 1], [40, 90], 2, 1, 4, 8, False, True, 0, "f32"), ([9], [500], 4, 2, 124, 24, False, True, 0, "f32"),
+    # the same in 16 bits, rows of 16 and tiles
+    ([2, 1], [300, 77], 4, 2, 8, 16, False, True, 0, "bf16"), ([1], [5000], 4, 1, 72, 16, True, True, 0, "f16"),
+    ([70, 3], [300, 77], 2, 2, 24, 16, False, True, 0, "f16"), ([40], [1000], 4, 1, 104, 32, True, False, 0, "bf16"),
+    # prompts in fp32 and of 16-bit heads above 128
+    ([300], [300], 2, 1, 64, 16, False, True, 0, "f32"), ([150, 200], [900, 200], 2, 2, 128, 32, True, True, 70, "f32"),
+    ([150, 7], [150, 400], 2, 1, 256, 16, False, True, 0, "bf16"), ([200], [700], 3, 1, 192, 7, True, True, 40, "f16"),
+    ([130], [400], 2, 2, 136, 8, False, False, 0, "bf16"),
+    # tiles in the batch's order by their number: more than five for each place
+    ([9] * 200, [9 + (i * 37) % 120 for i in range(200)], 16, 4, 128, 16, False, True, 0, "bf16"),
+    ([6] * 200, [6 + (i * 37) % 90 for i in range(200)], 32, 8, 64, 16, False, True, 0, "f16"),
+]
+
+
+@pytest.mark.parametrize("case", FORMS)
+def test_attention_of_further_forms(case):
+    table, table_d, offsets, lens, kc, vc, q = attention_inputs(case)
+    f = flag()
+    out, lse = attend(case, q, offsets, lens, table_d, kc, vc, case[4] ** -0.5, f)
+    assert sdi.dlrm_read_error(f) == 0
+    check_attention(case, q, table, kc, vc, case[4] ** -0.5, out, lse)
+    again = attend(case, q, offsets, lens, table_d, kc, vc, case[4] ** -0.5)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
