@@ -105,7 +105,8 @@ typedef struct dlrm_kv_batch {
  * n, d            tokens; head width, 1 .. DLRM_MAX_HEAD_DIM.
  * dtype           DLRM_F32, DLRM_F16 or DLRM_BF16, of q, k, q_out and k_out.
  * q_weight, k_weight  device fp32 [d], or NULL: no norm.
- * eps             >= 0 and finite.
+ * eps             >= 0 and finite.  Without one, rows whose mean square is
+ *                 subnormal in fp32 count as zeros.
  * rope            NULL: no rotation.
  * A position outside the table raises DLRM_FLAG_INDEX_OOB and that token's
  * outputs are zeros.  Rows of a multiple of 8 elements whose pointers and
@@ -185,7 +186,9 @@ size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_hea
  * causal     0 or 1;  window  >= 0, 0 for none.
  * max_new, max_len  host bounds of the batch's new tokens per sequence and
  *            lengths, for the launch's shape; a sequence beyond them raises
- *            DLRM_FLAG_BAD_OFFSETS and its rows are not written.
+ *            DLRM_FLAG_BAD_OFFSETS and its rows are not written.  The shape is
+ *            one for all: long chunks and single tokens are faster in a call each
+ *            (one of 2048 new and 256 of one, on 2000: 480 us, in two calls 236).
  * lse        optional (NULL) device fp32 [n][q_heads].
  * workspace  device, 16-byte aligned, dlrm_kv_attn_workspace_size bytes.
  *

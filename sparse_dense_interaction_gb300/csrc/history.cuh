@@ -192,9 +192,16 @@ enum AttnKernel { kAttnGeneral, kAttnTile };
 
 // Rows of the tensor-core tiles: two query tiles of 128 on an SM of their own;
 // with heads of 64 and at most 256 rows in all (the candidates of a user) one,
-// and two CTAs on an SM, so that one starts and ends while the other computes
-// (up to 200 candidates of each of 64 users: 55 us against 69).  More rows keep
-// the pair, which reads keys and values once for both tiles.
+// and two CTAs on an SM, so that one starts and ends while the other computes.
+// More rows keep the pair, which reads keys and values once for both tiles.  us
+// with one and with two query tiles, f16, 8 heads of 64, users with up to so many events:
+//   64 users    128 rows     256 rows     400 rows     800 rows
+//      500      23.4  33.9   34.0  39.8   47.9  46.6   85.5  83.0
+//     2000      41.2  58.8   57.2  64.1   97.1  91.2    159   146
+//     8000       109   147    160   167    225   204    365   327
+// 256 users of 4 heads and up to 250 events: 48.3 and 50.2, 49.2 and 56.4, 78.9 and 79.0, 127 and 122.  Only
+// where the pairs already fit beside one another is one tile worse at few rows (64 users of 2 heads,
+// 4 query heads each, up to 250 events, 128 rows: 15.8 and 12.5).
 inline int tile_rows(int64_t rows, int d) { return d <= 64 && rows <= 256 ? 128 : 256; }
 __host__ __device__ constexpr int tile_places(int rows) { return rows == 128 ? 2 * 152 : 152; }  // CTAs that run at once
 

@@ -24,7 +24,7 @@ int launch_kv_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
 // takes one position's score for two rows, then each thread sums its output
 // columns.  Its loads wait for its sums and its products for shared memory: one
 // event of each of 64 users with 2000, 16 heads on 4 of 17 fp32 elements, takes
-// 136 us, 0.5 TB/s.
+// 141 us, 0.5 TB/s.
 constexpr int kGenRows = 8, kGenTile = 32, kGenThreads = 128;
 constexpr int kGenCols = kGenRows * DLRM_MAX_HEAD_DIM / kGenThreads;  // output elements of a thread
 
@@ -318,8 +318,8 @@ static int launch_attn_t(AttnParams &p, const AttnPlan &a, int dtype, cudaStream
 
 // The tensor-core kernels' copies are 16 bytes wide.  Heads of 129 to 256
 // 16-bit elements take rows of 16 for any number of rows (one event of each of
-// 64 users with 2000, 16 heads on 4 of 256: 98 us, the general kernel 823; 64
-// new of 16: 290 and 4499).
+// 64 users with 2000, 16 heads on 4 of 256: 100 us, the general kernel 823; 64
+// new of 16: 293 and 4499).
 static bool wide_rows(const AttnParams &p, int dtype)
 {
     const int e = dtype == DLRM_F32 ? 4 : 8;

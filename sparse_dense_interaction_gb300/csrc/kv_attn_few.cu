@@ -35,8 +35,8 @@
 // partial rows and log2 of their sums, which a second kernel joins.
 //
 // One event each of 256 users with up to 8192 events (16 heads on 4, 128 bf16
-// elements): 320 us, 6.4 TB/s, 0.94 of a plain copy.  One history of 262143:
-// 98 us, 5.5 TB/s, of which the join and its launch take 10.  fp32, 128 users who see
+// elements): 322 us, 6.3 TB/s, 0.93 of a plain copy.  One history of 262143:
+// 100 us, 5.4 TB/s, of which the join and its launch take 10.  fp32, 128 users who see
 // 512 events (4 heads on 2 of 64): 21 us, 2.5 TB/s; there a CTA has 9 units, and its
 // start, its end and the uneven spread of 256 items over 304 places count.
 #include "history.cuh"
@@ -102,7 +102,11 @@ __device__ __forceinline__ void mma_fp32(float *c, const Split *a, const Split *
 }
 
 // One item -- row tile `tile` of a sequence and head -- and its units
-// [first, last).
+// [first, last).  Every tile of a sequence has the same units, those of the
+// positions that any of its queries sees, so that a CTA finds its share by
+// division.  That is right for one tile; of a causal chunk of many tiles it is
+// twice what they see, and more with a window (fp32, 4 sequences of 2048 new, 4 heads on
+// 2 of 64: 397 us, with a window of 128 too, where a tile sees 135 of 2176).
 struct FewItem {
     Sequence seq;
     int64_t s;
@@ -288,8 +292,8 @@ struct FewShape {
     // registers joined at a time: with all 64 of them two CTAs would not fit on an SM
     // CTAs of an SM and stages of a warp's ring: where 3 CTAs have the registers,
     // two stages each keep as many bytes in flight as three of 2, and an item's
-    // start and end hide behind two others (256 users of up to 8192 events 320 us,
-    // 329 with 2; 512 users of up to 1000, 8 heads of 64: 94 and 117)
+    // start and end hide behind two others (with weights in one part: 256 users of up to 8192
+    // events 320 us, 329 with 2; 512 users of up to 1000, 8 heads of 64: 94 and 117)
     static constexpr int kResident = kBulk && !kWide && kGroups == 1 && DP <= 128 ? 3 : 2, kStages = kResident == 3 ? 2 : 3;
     static constexpr int kCtas = kResident * kFewSms;
     static constexpr int kMerge = kOut < 32 ? kOut : 32;

@@ -27,11 +27,11 @@
 // 2 x DP.
 //
 // 4 sequences of 2048 new events on 8192 (16 heads on 4, 128 bf16 elements):
-// 342 us, 1410 TFLOP/s, 0.74 of a large matrix product's rate (0.82 of the rate
+// 355 us, 1350 TFLOP/s, 0.71 of a large matrix product's rate (0.79 of the rate
 // that one keeps up for seconds): inside a CTA the tensor pipe is busy 80 % of
 // the time, and the chip draws all the power it may.  Up to 200 candidates of
-// each of 64 users with up to 2000 events (8 heads of 64 f16 elements): 55 us,
-// where a CTA lives for 8 tiles of positions and its start, its end and the
+// each of 64 users with up to 2000 events (8 heads of 64 f16 elements): 53 us,
+// where a CTA lives for 9 tiles of positions and its start, its end and the
 // last CTAs' uneven ends count most.
 #include <type_traits>
 
