@@ -23,7 +23,7 @@
 //    in the lanes that hold rows next, are transposed by movmatrix (fp32: each
 //    half of their bits).
 // These are the warp's own MMAs, not those of tensor memory: 16 rows would fill
-// an eighth of such a tile, and the tensor pipe is 10 % busy as it is.
+// an eighth of such a tile, and the tensor pipe is 15 % busy as it is.
 // fp32 runs on TF32 MMAs: an operand is itself rounded to TF32 plus the rest (of
 // which the MMA reads 11 bits), and the three products of the split that matter
 // carry each product of two elements to about 2^-22 of its magnitude.  An MMA
