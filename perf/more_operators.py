@@ -281,8 +281,9 @@ def _prepare_reserve(c, gen, s):
     ring[at] = order[sum(held):sum(held) + free]
     as64 = lambda v: torch.tensor(v, dtype=torch.int64, device="cuda")
     n = sum(max(x, 0) for x in counts)
-    s.update(counts=as64(counts), lengths=as64(before), page_table=table, ring=ring, state=as64([head, head + free, 0]),
-             n=n, gone=sum(h for x, h in zip(counts, held) if x < 0), new_state=torch.zeros(3, dtype=torch.int64, device="cuda"),
+    s.update(counts=as64(counts), lengths=as64(before), page_table=table, ring=ring, state=as64([head, head + free]),
+             n=n, gone=sum(h for x, h in zip(counts, held) if x < 0),
+             new_state=torch.zeros(2, dtype=torch.int64, device="cuda"),
              offsets=torch.empty(S + 1, dtype=torch.int64, device="cuda"),
              new_lengths=torch.empty(S, dtype=torch.int64, device="cuda"),
              slots=torch.full((n + 5,), -7, dtype=torch.int64, device="cuda"),  # rows behind the last stay as they are
@@ -362,7 +363,6 @@ def _reserve(s):
     ring[(tail + k) % pages] = freed
     s["new_state"][0] = head + torch.where(granted, prefix, 0).max()
     s["new_state"][1] = tail + s["gone"]
-    s["new_state"][2] = 0
     return {k: s[k] for k in _RESERVED}
 
 
