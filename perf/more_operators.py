@@ -361,7 +361,7 @@ def _reserve(s):
     first = got & (at % page == 0)
     table[seq[first], number[first]] = fresh[first]
     ring[(tail + k) % pages] = freed
-    s["new_state"][0] = head + torch.where(granted, prefix, 0).max()
+    s["new_state"][0] = head + torch.where(granted & (need > 0), prefix, 0).max()
     s["new_state"][1] = tail + s["gone"]
     return {k: s[k] for k in _RESERVED}
 
