@@ -11,7 +11,10 @@
  *   2. appending new keys and values to the cache, normed and rotated on the
  *      way (serving);
  *   3. attention of the new tokens over the cache, from one token per
- *      sequence to long chunks.
+ *      sequence to long chunks;
+ *   4. the same cache in 8 bits: an append that encodes, and attention that reads
+ *      the codes;
+ *   5. pages and slots of a step's new tokens, given out on the device.
  *
  * The conventions are those of dlrm_sparse.h: device pointers owned by the
  * caller, no device allocation, asynchronous on the caller's stream, host
@@ -216,6 +219,100 @@ int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm
                      float scale, int causal, int64_t window, int64_t max_new, int64_t max_len,
                      const dlrm_heads *out, float *lse, void *workspace, size_t workspace_bytes,
                      int32_t *err_flag, dlrm_stream_t stream);
+
+/*
+ * A paged cache in 8 bits.  Keys and values are E4M3 codes (a sign, 4 bits of exponent, 3 of
+ * mantissa; at most 448), laid out like those of dlrm_kv_cache, a byte an
+ * element.  For each head, each `block` consecutive slots of a page share one exponent for their
+ * keys and one for their values: the value of slot t's code c is
+ * c * 2^(e - 127), with e the byte at k_exp (or v_exp)
+ * + p*exp_page_stride + (t / block)*exp_block_stride + h*exp_head_stride.  0 stands for a block of zeros;
+ * 248 .. 255 are never written, and what is read with them may overflow.
+ */
+typedef struct dlrm_kv_cache8 {
+    void *k, *v;            /* device, codes */
+    uint8_t *k_exp, *v_exp; /* device, exponents */
+    int64_t pages;          /* 1 .. 2^31 - 1 */
+    int64_t page_stride, slot_stride, head_stride;             /* of the codes */
+    int64_t exp_page_stride, exp_block_stride, exp_head_stride; /* of the exponents */
+    int32_t page_size;      /* slots of a page, 1 .. 65536 */
+    int32_t heads;          /* key/value heads */
+    int32_t block;          /* slots that share an exponent; divides page_size */
+} dlrm_kv_cache8;
+
+/*
+ * Appends the batch's new tokens to a cache in 8 bits, at the places that
+ * dlrm_kv_append says.  Keys are stored as they are given: dlrm_qk_norm_rope_fwd
+ * norms and turns them first (with dlrm_kv_reserve's positions).
+ *
+ * Of each block that new tokens enter, with m the largest finite |x| of its new tokens in a
+ * head and e the smallest exponent, at least 1, with m <= 448 * 2^(e - 127) (0 for m = 0):
+ * - a block whose first slot is among the new ones gets e, whatever it held;
+ * - one that holds older tokens of its sequence keeps the larger of e and its own; where e
+ *   is larger, the older codes are rounded again.
+ * A code is x * 2^(127 - e) rounded to nearest, ties to even.  Infinities become the
+ * largest code and NaN its own code; neither counts for m.  The products with powers of two are exact, so
+ * results are the same bits as those of this definition.
+ *
+ * k, v        [n] tokens, as many heads as the cache; dtype DLRM_F32, DLRM_F16 or DLRM_BF16.
+ * Errors in the data are flagged and left out as by dlrm_kv_append.  Two sequences of a call must not add to
+ * one block (pages that sequences share are read only).  Rows of a multiple of 8 elements, on 16 bytes, with
+ * codes on 8, take the vector path.
+ */
+int dlrm_kv8_append(const dlrm_heads *k, const dlrm_heads *v, const dlrm_kv_batch *batch,
+                    const dlrm_kv_cache8 *cache, int d, int dtype, int32_t *err_flag, dlrm_stream_t stream);
+
+/* Bytes of workspace of dlrm_kv8_attn_fwd for these sizes; 0 for invalid ones. */
+size_t dlrm_kv8_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new,
+                                    int64_t max_len);
+
+/*
+ * dlrm_kv_attn_fwd over a cache in 8 bits: the same masks, rows, outputs, bounds and errors.
+ * dtype is that of q and out.
+ *
+ * Codes are read as they are (fp16 holds every one), their powers of two are
+ * applied to scores and weights in fp32.
+ */
+int dlrm_kv8_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm_kv_cache8 *cache, int d, int dtype,
+                      float scale, int causal, int64_t window, int64_t max_new, int64_t max_len,
+                      const dlrm_heads *out, float *lse, void *workspace, size_t workspace_bytes,
+                      int32_t *err_flag, dlrm_stream_t stream);
+
+/*
+ * Pages and slots for a step's new tokens, for either cache, without the host.
+ * Sequence s stores L = lengths[s] tokens and gets c = counts[s] more; c < 0: it has
+ * ended, and its pages are given back.  The free pages are a ring of `pages` entries:
+ * those at places state[0] .. state[1] - 1 (modulo pages) are free.
+ *
+ * offsets      device [S + 1]: sums of the counts above 0, the batch's offsets.
+ * new_lengths  device [S]: L + c, the batch's lengths; 0 for a sequence that has
+ *              ended; ~L (below 0, so that append and attention leave it out) for one that
+ *              does not get its pages.  A length below 0 is read as its complement, so the next
+ *              call tries again.
+ * page_table   device, rows of table_width entries, table_stride apart (at least table_width):
+ *              the ceil((L + c) / page_size) - ceil(L / page_size) pages that s needs are
+ *              written behind those it has; nothing else is.
+ * ring, state  pages are taken from state[0] on, in the order of sequences and of their
+ *              pages, and given back from state[1] on, in the same order; they can be taken from the
+ *              next call on.  new_state[0 .. 1]: the state afterwards.
+ * slots, positions  device [n] or NULL: of each new token its slot
+ *              (page * page_size + slot of the page) and its place in its history, -1
+ *              where its sequence is left out.  Rows behind the last token are left as they were.
+ * n            new tokens at most: rows of slots and positions.
+ * new_lengths may be lengths and new_state may be state; nothing else may overlap.
+ *
+ * A sequence whose pages, with those that the sequences before it need, are more than the ring has is left
+ * out (DLRM_FLAG_CAPACITY), and so is every later one that needs a page; so is one that does not fit its row
+ * of the table, which takes no pages, or whose tokens go beyond n (DLRM_FLAG_BAD_OFFSETS).  A page number outside 0 .. pages - 1 raises
+ * DLRM_FLAG_INDEX_OOB (its tokens' slots are -1).  A state that is not 0 <= state[0] <= state[1] <=
+ * state[0] + pages raises DLRM_FLAG_BAD_OFFSETS: no page is taken or given back.  More pages given back than the
+ * ring has room for raise DLRM_FLAG_CAPACITY and are dropped.
+ * Every launch sums up all S sequences in each of its CTAs: made for steps of some thousands of them.
+ */
+int dlrm_kv_reserve(const int64_t *counts, const int64_t *lengths, int64_t S, int64_t n, int32_t *page_table,
+                    int64_t table_stride, int64_t table_width, int page_size, int32_t *ring, int64_t pages,
+                    const int64_t *state, int64_t *new_state, int64_t *offsets, int64_t *new_lengths, int64_t *slots,
+                    int64_t *positions, int32_t *err_flag, dlrm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -7,11 +7,14 @@ package is its thin Python binding (same names, torch tensors in, argument
 marshalling only) plus the seeded workload generator used by the tests and
 the benchmark.  The same library holds the event-history operators of
 ``include/dlrm_history.h``: head norms with the position rotation and their
-gradient, the append to a paged key/value cache, and attention over it.
+gradient, the append to a paged key/value cache, and attention over it; the
+same cache in 8 bits; and the pages of a step's new tokens.
 """
 from ._history import (  # noqa: F401
     dlrm_kv_append, dlrm_kv_attn_fwd, dlrm_kv_attn_workspace_size, dlrm_qk_norm_rope_bwd,
     dlrm_qk_norm_rope_bwd_workspace_size, dlrm_qk_norm_rope_fwd)
+from ._history8 import (  # noqa: F401
+    dlrm_kv8_append, dlrm_kv8_attn_fwd, dlrm_kv8_attn_workspace_size, dlrm_kv_reserve)
 from ._native import (  # noqa: F401
     BF16, F16, F32, INT4, INTERACT_KERNEL_AUTO, INTERACT_KERNEL_CUDA_CORE, MAX_TABLES, DlrmError,
     dlrm_clear_error, dlrm_emb_bag_bwd_adagrad, dlrm_emb_bag_bwd_sgd, dlrm_emb_bag_bwd_sgd_atomic,

@@ -76,6 +76,12 @@ SIGNATURES = {
     "dlrm_kv_attn_workspace_size": (_sz, [_i64, _i64, _i32, _i32, _i32, _i64, _i64]),
     "dlrm_kv_attn_fwd": (_i32, [_vp, _vp, _vp, _i32, _i32, _f32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp,
                                 _vp]),
+    "dlrm_kv8_append": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp]),
+    "dlrm_kv8_attn_workspace_size": (_sz, [_i64, _i64, _i32, _i32, _i32, _i64, _i64]),
+    "dlrm_kv8_attn_fwd": (_i32, [_vp, _vp, _vp, _i32, _i32, _f32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp,
+                                 _vp]),
+    "dlrm_kv_reserve": (_i32, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _vp, _vp]),
     "dlrm_read_error": (_i32, [_vp, _vp]),
     "dlrm_clear_error": (_i32, [_vp, _vp]),
     "dlrm_status_string": (ctypes.c_char_p, [_i32]),

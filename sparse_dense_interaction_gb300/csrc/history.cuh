@@ -52,6 +52,13 @@ struct CacheView {
     int heads;
 };
 
+// Exponents of a cache in 8 bits, one for each block of a page's slots and head.
+struct ExpView {
+    uint8_t *k, *v;
+    int64_t page_stride, block_stride, head_stride;
+    FastDiv block;  // divides a slot by the block's size
+};
+
 struct BatchView {
     int64_t S, n;
     const int64_t *offsets, *lengths;
@@ -237,6 +244,7 @@ struct AttnParams {
     FewJoin *joins;            // rows of 16: an item that each CTA left unfinished
     int wait_polls;            // of a wait inside a kernel, before it gives up
     int32_t *err;
+    ExpView exp;               // of a cache in 8 bits
 };
 
 // What one CTA works on: rows of tile `tile` of head `head` of the sequence,

@@ -1,5 +1,7 @@
 // C ABI of the event-history operators: argument checks and dispatch, all on
 // the host before anything is launched.
+#include <algorithm>
+
 #include "history.cuh"
 #include "tc.cuh"
 
@@ -16,6 +18,12 @@ int launch_kv_append(const HeadsView &, const HeadsView &, const BatchView &, co
                      int32_t *, cudaStream_t);
 size_t attn_workspace(int64_t, int64_t, int, int, int, int64_t, int64_t);
 int launch_kv_attn(AttnParams &, int, void *, cudaStream_t);
+int launch_kv8_attn(AttnParams &, int, void *, cudaStream_t);
+int launch_kv_reserve(const int64_t *, const int64_t *, int64_t, int64_t, int32_t *, int64_t, int64_t, int, int32_t *,
+                      int64_t, const int64_t *, int64_t *, int64_t *, int64_t *, int64_t *, int64_t *, int32_t *,
+                      cudaStream_t);
+int launch_kv8_append(const HeadsView &, const HeadsView &, const BatchView &, const CacheView &, const ExpView &, int,
+                      int, int32_t *, cudaStream_t);
 
 static const int64_t kMaxTokens = 0x7fffffffLL, kMaxPositions = (int64_t)1 << 30, kMaxSequences = (int64_t)1 << 24;
 static const int kMaxHeads = 65536;
@@ -108,6 +116,53 @@ static int check_cache(const dlrm_kv_cache *c, int dtype, CacheView &v)
         return DLRM_ERR_UNSUPPORTED;
     v = CacheView{static_cast<char *>(c->k), static_cast<char *>(c->v), c->page_stride, c->slot_stride,
                   c->head_stride, (uint32_t)c->pages, FastDiv::make((uint32_t)c->page_size), c->heads};
+    return DLRM_OK;
+}
+
+// A cache in 8 bits: its codes, as a cache of one byte an element, and its exponents.
+static int check_cache8(const dlrm_kv_cache8 *c, CacheView &v, ExpView &x)
+{
+    if (!c || !c->k || !c->v || !c->k_exp || !c->v_exp || c->pages < 1 || c->page_size < 1 || c->heads < 1 ||
+        c->page_stride < 0 || c->slot_stride < 0 || c->head_stride < 0 || c->exp_page_stride < 0 ||
+        c->exp_block_stride < 0 || c->exp_head_stride < 0 || c->block < 1 || c->page_size % c->block != 0)
+        return DLRM_ERR_INVALID_ARG;
+    if (c->pages > 0x7fffffffLL || c->page_size > 65536 || c->heads > kMaxHeads)
+        return DLRM_ERR_UNSUPPORTED;
+    v = CacheView{static_cast<char *>(c->k), static_cast<char *>(c->v), c->page_stride, c->slot_stride,
+                  c->head_stride, (uint32_t)c->pages, FastDiv::make((uint32_t)c->page_size), c->heads};
+    x = ExpView{c->k_exp, c->v_exp, c->exp_page_stride, c->exp_block_stride, c->exp_head_stride,
+                FastDiv::make((uint32_t)c->block)};
+    return DLRM_OK;
+}
+
+// What both attention calls ask of their other arguments; fills the parameters.
+static int check_attention(const dlrm_heads *q, const dlrm_kv_batch *batch, int d, int dtype, float scale, int causal,
+                           int64_t window, int64_t max_new, int64_t max_len, const dlrm_heads *out, float *lse,
+                           void *workspace, size_t workspace_bytes, int32_t *err_flag, AttnParams &p)
+{
+    const int64_t n = batch->n;
+    const int s = check_pair(q, out, n, d, dtype, p.q, p.out);
+    if (s != DLRM_OK)
+        return s;
+    if (p.q.heads % p.cache.heads != 0 || !(scale > 0.f) || !(scale <= kMaxScale) || (causal != 0 && causal != 1) ||
+        window < 0 || max_new < 0 || max_len < 0 || !aligned(lse, 4) || !workspace || !aligned(workspace, 16))
+        return DLRM_ERR_INVALID_ARG;
+    p.group = p.q.heads / p.cache.heads;
+    p.max_new = max_new < n ? max_new : n;
+    if (max_len > kMaxPositions || p.max_new * p.group > kMaxTokens)
+        return DLRM_ERR_UNSUPPORTED;
+    if (n > 0 && max_new == 0)
+        return DLRM_ERR_INVALID_ARG;
+    if (workspace_bytes < attn_workspace(p.batch.S, n, p.q.heads, p.cache.heads, d, max_new, max_len))
+        return DLRM_ERR_WORKSPACE_TOO_SMALL;
+    p.max_len = max_len;
+    p.d = d;
+    p.scale_log2 = scale * 1.44269504088896340736f;
+    p.causal = causal != 0;
+    p.window = window < kMaxPositions ? (int)window : 0;  // as wide as any history: none
+    p.lse = lse;
+    p.wait_polls = wait_hooks(0, tc::kSpinLimit).copy_polls;  // the default unless a test shortens it
+    p.err = err_flag;
     return DLRM_OK;
 }
 
@@ -225,34 +280,85 @@ int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm
     AttnParams p = {};
     if (!batch || !q)
         return DLRM_ERR_INVALID_ARG;
-    const int64_t n = batch->n;
-    int s = check_row_type(n, d, dtype);
+    int s = check_row_type(batch->n, d, dtype);
     if (s != DLRM_OK || (s = check_cache(cache, dtype, p.cache)) != DLRM_OK ||
         (s = check_batch(batch, cache->page_size, p.batch)) != DLRM_OK ||
-        (s = check_pair(q, out, n, d, dtype, p.q, p.out)) != DLRM_OK)
+        (s = check_attention(q, batch, d, dtype, scale, causal, window, max_new, max_len, out, lse, workspace,
+                             workspace_bytes, err_flag, p)) != DLRM_OK)
         return s;
-    if (p.q.heads % p.cache.heads != 0 || !(scale > 0.f) || !(scale <= kMaxScale) || (causal != 0 && causal != 1) ||
-        window < 0 || max_new < 0 || max_len < 0 || !aligned(lse, 4) || !workspace || !aligned(workspace, 16))
+    return batch->n == 0 ? DLRM_OK : launch_kv_attn(p, dtype, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int dlrm_kv_reserve(const int64_t *counts, const int64_t *lengths, int64_t S, int64_t n, int32_t *page_table,
+                    int64_t table_stride, int64_t table_width, int page_size, int32_t *ring, int64_t pages,
+                    const int64_t *state, int64_t *new_state, int64_t *offsets, int64_t *new_lengths, int64_t *slots,
+                    int64_t *positions, int32_t *err_flag, dlrm_stream_t stream)
+{
+    if (S < 0 || n < 0 || table_stride < 0 || table_width < 0 || page_size < 1 || pages < 1 || !ring || !state ||
+        !new_state || !offsets || (S > 0 && (!counts || !lengths || !new_lengths)) ||
+        (S > 0 && table_width > 0 && !page_table) || !apart(S, table_stride, (int)std::min<int64_t>(table_width, kMaxPositions)))
         return DLRM_ERR_INVALID_ARG;
-    p.group = p.q.heads / p.cache.heads;
-    p.max_new = max_new < n ? max_new : n;
-    if (max_len > kMaxPositions || p.max_new * p.group > kMaxTokens)
+    if (S > kMaxSequences || n > kMaxTokens || page_size > 65536 || pages > 0x7fffffffLL ||
+        table_width > kMaxPositions / page_size)
         return DLRM_ERR_UNSUPPORTED;
-    if (n > 0 && max_new == 0)
+    for (const void *x : {(const void *)counts, (const void *)lengths, (const void *)state, (const void *)new_state,
+                          (const void *)offsets, (const void *)new_lengths, (const void *)slots,
+                          (const void *)positions})
+        if (!aligned(x, 8))
+            return DLRM_ERR_INVALID_ARG;
+    if (!aligned(page_table, 4) || !aligned(ring, 4))
         return DLRM_ERR_INVALID_ARG;
-    if (workspace_bytes < attn_workspace(p.batch.S, n, p.q.heads, p.cache.heads, d, max_new, max_len))
-        return DLRM_ERR_WORKSPACE_TOO_SMALL;
+    return launch_kv_reserve(counts, lengths, S, n, page_table, table_stride, table_width, page_size, ring, pages,
+                             state, new_state, offsets, new_lengths, slots, positions, err_flag,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int dlrm_kv8_append(const dlrm_heads *k, const dlrm_heads *v, const dlrm_kv_batch *batch, const dlrm_kv_cache8 *cache,
+                    int d, int dtype, int32_t *err_flag, dlrm_stream_t stream)
+{
+    HeadsView vk, vv;
+    BatchView vb;
+    CacheView vc;
+    ExpView vx;
+    if (!batch)
+        return DLRM_ERR_INVALID_ARG;
+    const int64_t n = batch->n;
+    int s = check_row_type(n, d, dtype);
+    if (s != DLRM_OK || (s = check_cache8(cache, vc, vx)) != DLRM_OK ||
+        (s = check_batch(batch, cache->page_size, vb)) != DLRM_OK || (s = check_heads(k, n, dtype, vk)) != DLRM_OK ||
+        (s = check_heads(v, n, dtype, vv)) != DLRM_OK)
+        return s;
+    if (vk.heads != vc.heads || vv.heads != vc.heads || !apart(cache->pages, vc.page_stride, d) ||
+        !apart(cache->page_size, vc.slot_stride, d) || !apart(vc.heads, vc.head_stride, d) ||
+        !apart(cache->pages, vx.page_stride, 1) || !apart(cache->page_size / cache->block, vx.block_stride, 1) ||
+        !apart(vc.heads, vx.head_stride, 1))
+        return DLRM_ERR_INVALID_ARG;
     if (n == 0)
         return DLRM_OK;
-    p.max_len = max_len;
-    p.d = d;
-    p.scale_log2 = scale * 1.44269504088896340736f;
-    p.causal = causal != 0;
-    p.window = window < kMaxPositions ? (int)window : 0;  // as wide as any history: none
-    p.lse = lse;
-    p.wait_polls = wait_hooks(0, tc::kSpinLimit).copy_polls;  // the default unless a test shortens it
-    p.err = err_flag;
-    return launch_kv_attn(p, dtype, workspace, static_cast<cudaStream_t>(stream));
+    return launch_kv8_append(vk, vv, vb, vc, vx, d, dtype, err_flag, static_cast<cudaStream_t>(stream));
+}
+
+size_t dlrm_kv8_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new,
+                                    int64_t max_len)
+{
+    return dlrm_kv_attn_workspace_size(S, n, q_heads, kv_heads, d, max_new, max_len);
+}
+
+int dlrm_kv8_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm_kv_cache8 *cache, int d, int dtype,
+                      float scale, int causal, int64_t window, int64_t max_new, int64_t max_len,
+                      const dlrm_heads *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                      dlrm_stream_t stream)
+{
+    AttnParams p = {};
+    if (!batch || !q)
+        return DLRM_ERR_INVALID_ARG;
+    int s = check_row_type(batch->n, d, dtype);
+    if (s != DLRM_OK || (s = check_cache8(cache, p.cache, p.exp)) != DLRM_OK ||
+        (s = check_batch(batch, cache->page_size, p.batch)) != DLRM_OK ||
+        (s = check_attention(q, batch, d, dtype, scale, causal, window, max_new, max_len, out, lse, workspace,
+                             workspace_bytes, err_flag, p)) != DLRM_OK)
+        return s;
+    return batch->n == 0 ? DLRM_OK : launch_kv8_attn(p, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

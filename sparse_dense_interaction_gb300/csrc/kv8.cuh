@@ -1,0 +1,50 @@
+// Shared by the kernels of the cache in 8 bits: E4M3 codes, and a power of two
+// for each block of slots and head.
+#pragma once
+
+#include "history.cuh"
+
+namespace dlrm {
+
+// 2^(e - 127) of an exponent byte; 0 (a block of zeros) gives 0.
+__device__ __forceinline__ float exp_power(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Two codes as fp16 (exact: E4M3's values are fp16 values).
+__device__ __forceinline__ uint32_t decode2(uint16_t codes)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+    return h;
+}
+
+__device__ __forceinline__ float2 decode2_f32(uint16_t codes) { return unpack2<__half>(decode2(codes)); }
+
+// Two values as codes, x in the lower byte: to nearest, ties to even, beyond 448 the largest.
+__device__ __forceinline__ uint16_t encode2(float x, float y)
+{
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(y), "f"(x));
+    return c;
+}
+
+// The smallest exponent whose codes reach `top` (finite, >= 0): 448 = 1.75 * 2^8.
+// The codes carry exponents of their own, so a power of two wastes no bit of
+// them, products with it are exact, and a block whose power grows keeps its
+// codes' bits but for those that fall below the smallest.
+__device__ __forceinline__ int exponent_of(float top)
+{
+    const uint32_t b = __float_as_uint(top);
+    const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return b == 0 ? 0 : (e < 1 ? 1 : e);
+}
+
+// What values are multiplied by before they are encoded: 2^(127 - e), e = 0 .. 247.
+__device__ __forceinline__ float encode_power(int e) { return __uint_as_float((uint32_t)(254 - (e < 1 ? 1 : e)) << 23); }
+
+// Place of the exponent of a page's slot and head.
+__device__ __forceinline__ int64_t exp_offset(const ExpView &x, int64_t page, uint32_t slot, int head)
+{
+    return page * x.page_stride + (int64_t)x.block.div(slot) * x.block_stride + (int64_t)head * x.head_stride;
+}
+
+}  // namespace dlrm

@@ -1,0 +1,270 @@
+// Appends a step's keys and values to the cache in 8 bits.
+//
+// A block (some consecutive slots of a page, one head, keys or values) has one
+// exponent, so what enters it is encoded together: its largest magnitude first,
+// then the codes.  An item is such a block; it belongs to the first new token
+// that enters it, and a warp takes it.  Where the block already holds older
+// tokens its exponent only grows, and only then are their codes read and
+// rounded again; most steps touch no older code.
+//
+// Memory bounds long prompts: 16-bit rows are read once into registers, a
+// chunk of 8 elements each, and written as half as many bytes.
+#include "kv8.cuh"
+
+namespace dlrm {
+
+constexpr int kApWarps = 8, kApMaxSlice = 32;
+
+struct Append8Params {
+    HeadsView k, v;
+    BatchView batch;
+    CacheView cache;
+    ExpView exp;
+    int d;
+    int slice;       // tokens whose blocks a CTA looks after
+    FastDiv chunks;  // divides by the chunks of a row
+    int32_t *err;
+};
+
+// A block's first new token, and what of the block is new and older.
+struct Append8Item {
+    int64_t token;
+    int32_t page;
+    int32_t slot;   // of the token in its page
+    int32_t fresh;  // new tokens in the block
+    int32_t older;  // slots before the token's in the block, all filled
+};
+
+// 8 elements as fp32.
+template <typename T>
+__device__ __forceinline__ void load8(const T *src, float *x);
+template <>
+__device__ __forceinline__ void load8<float>(const float *src, float *x)
+{
+    const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *src, float *x)
+{
+    const uint4 a = *reinterpret_cast<const uint4 *>(src);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 y = unpack2<T>(w[i]);
+        x[2 * i] = y.x;
+        x[2 * i + 1] = y.y;
+    }
+}
+
+// |x| where x is finite, else 0: what is not finite does not count for the exponent.
+__device__ __forceinline__ float finite_size(float x)
+{
+    const float a = fabsf(x);
+    return a <= 3.4028234663852886e38f ? a : 0.f;
+}
+
+// The blocks that the tokens first .. first + slice of the batch begin to fill, by one warp; returns how many.
+__device__ __forceinline__ int append8_items(const Append8Params &p, int64_t i0, Append8Item *items, int32_t *owner)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t i1 = min(i0 + p.slice, p.batch.n);
+    owner[lane] = -1;
+    __syncwarp();
+    // the slice's sequences, 32 at a time, each marks its tokens
+    int64_t s = find_sequence(p.batch, i0);
+    for (bool more = s >= 0; more; s += 32) {
+        const bool there = s + lane < p.batch.S;
+        const int64_t from = there ? p.batch.offsets[s + lane] : i1, to = there ? p.batch.offsets[s + lane + 1] : i1;
+        for (int64_t t = max(from, i0); t < min(to, i1); t++)
+            owner[t - i0] = (int)(s + lane);
+        more = __all_sync(0xffffffffu, there && from < i1);
+    }
+    __syncwarp();
+    const int64_t token = i0 + lane;
+    const int mine = lane < i1 - i0 ? owner[lane] : -1;
+    Append8Item it = {};
+    bool first = false;
+    Sequence q;
+    if (mine >= 0 && read_sequence(p.batch, mine, p.batch.n, p.batch.capacity, q, p.err) && q.has(token) &&
+        q.count <= q.length) {
+        const int at = q.length - q.count + (int)(token - q.first), block = (int)p.exp.block.d;
+        const uint32_t number = p.cache.page.div((uint32_t)at);
+        it.token = token;
+        it.slot = at - (int)(number * p.cache.page.d);
+        it.older = it.slot - (int)p.exp.block.div((uint32_t)it.slot) * block;
+        it.fresh = min(block - it.older, (int)(q.first + q.count - token));
+        first = token == q.first || it.older == 0;
+        if (first) {
+            it.page = p.batch.table[mine * p.batch.table_stride + number];
+            if ((uint32_t)it.page >= p.cache.pages) {
+                raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+                first = false;
+            }
+        }
+    }
+    const uint32_t all = __ballot_sync(0xffffffffu, first);
+    if (first)
+        items[__popc(all & ((1u << lane) - 1))] = it;
+    return __popc(all);
+}
+
+// One block of one head, by a warp.  kVec: chunks of 8 elements that lie on
+// 16 bytes (fp32 too) and whose codes lie on 8; else element by element.
+template <typename T, bool kVec>
+__device__ __forceinline__ void append8_block(const Append8Params &p, const Append8Item &it, int head, bool value)
+{
+    constexpr int kHold = sizeof(T) == 4 ? 4 : 8;  // chunks of a lane that stay in registers
+    const int lane = threadIdx.x & 31;
+    const HeadsView &in = value ? p.v : p.k;
+    uint8_t *exps = (value ? p.exp.v : p.exp.k) + exp_offset(p.exp, it.page, it.slot, head);
+    char *codes = (value ? p.cache.v : p.cache.k) + it.page * p.cache.page_stride + head * p.cache.head_stride;
+    const int before = it.older > 0 ? *exps : 0;
+    const int per_row = kVec ? p.d / 8 : p.d, all = it.fresh * per_row;
+    auto row_of = [&](int c, int &at) {
+        const int r = (int)p.chunks.div((uint32_t)c);
+        at = (c - r * per_row) * (kVec ? 8 : 1);
+        return r;
+    };
+    float top = 0.f;
+    float held[kVec ? kHold : 1][8];
+    if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < kHold; i++) {
+            const int c = i * 32 + lane;
+            if (c < all) {
+                int at;
+                const int r = row_of(c, at);
+                load8<T>(in.row<T>(it.token + r, head) + at, held[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    held[i][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kHold; i++)
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                top = fmaxf(top, finite_size(held[i][e]));
+    }
+    for (int c = (kVec ? kHold * 32 : 0) + lane; c < all; c += 32) {
+        int at;
+        const int r = row_of(c, at);
+        const T *src = in.row<T>(it.token + r, head) + at;
+        if constexpr (kVec) {
+            float x[8];
+            load8<T>(src, x);
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                top = fmaxf(top, finite_size(x[e]));
+        } else {
+            top = fmaxf(top, finite_size(to_f32(*src)));
+        }
+    }
+    const int fresh = exponent_of(warp_max(top)), now = fresh > before ? fresh : before;
+    const float scale = encode_power(now);
+    auto write8 = [&](int c, const float *x) {
+        int at;
+        const int r = row_of(c, at);
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            w[i] = encode2(x[4 * i] * scale, x[4 * i + 1] * scale) |
+                   (uint32_t)encode2(x[4 * i + 2] * scale, x[4 * i + 3] * scale) << 16;
+        *reinterpret_cast<uint2 *>(codes + (it.slot + r) * p.cache.slot_stride + at) = make_uint2(w[0], w[1]);
+    };
+    if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < kHold; i++)
+            if (i * 32 + lane < all)
+                write8(i * 32 + lane, held[i]);
+    }
+    for (int c = (kVec ? kHold * 32 : 0) + lane; c < all; c += 32) {
+        int at;
+        const int r = row_of(c, at);
+        const T *src = in.row<T>(it.token + r, head) + at;
+        if constexpr (kVec) {
+            float x[8];
+            load8<T>(src, x);
+            write8(c, x);
+        } else {
+            codes[(it.slot + r) * p.cache.slot_stride + at] = (char)encode2(to_f32(*src) * scale, 0.f);
+        }
+    }
+    if (it.older > 0 && now > before) {  // older codes under the larger power; below 2^-120 all of them are zeros
+        const float down = __uint_as_float((uint32_t)(127 + max(before - now, -120)) << 23);
+        for (int c = lane; c < it.older * p.d; c += 32) {
+            const int r = c / p.d;
+            char *at = codes + (it.slot - it.older + r) * p.cache.slot_stride + (c - r * p.d);
+            *at = (char)encode2(decode2_f32((uint8_t)*at).x * down, 0.f);
+        }
+    }
+    __syncwarp();  // every lane has read the exponent
+    if (lane == 0)
+        *exps = (uint8_t)now;
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kApWarps * 32)
+kv8_append_kernel(const __grid_constant__ Append8Params p)
+{
+    __shared__ Append8Item items[kApMaxSlice];
+    __shared__ int32_t owner[32];
+    __shared__ int found;
+    const int warp = threadIdx.x >> 5;
+    check_sequences(p.batch, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x, p.err);
+    const int64_t slices = (p.batch.n + p.slice - 1) / p.slice;
+    for (int64_t i = blockIdx.x; i < slices; i += gridDim.x) {
+        __syncthreads();
+        if (warp == 0) {
+            const int n = append8_items(p, i * p.slice, items, owner);
+            if (threadIdx.x == 0)
+                found = n;
+        }
+        __syncthreads();
+        const int heads = p.cache.heads, all = found * heads * 2;
+        for (int x = warp; x < all; x += kApWarps) {
+            const int which = x / (2 * heads), part = x - which * 2 * heads;
+            append8_block<T, kVec>(p, items[which], part >> 1, part & 1);
+        }
+    }
+}
+
+template <typename T>
+static int launch_append8(Append8Params &p, cudaStream_t st)
+{
+    auto even = [](const HeadsView &h) {
+        return reinterpret_cast<uintptr_t>(h.ptr) % 16 == 0 && h.ts * sizeof(T) % 16 == 0 && h.hs * sizeof(T) % 16 == 0;
+    };
+    const CacheView &c = p.cache;
+    const bool vec = p.d % 8 == 0 && even(p.k) && even(p.v) && reinterpret_cast<uintptr_t>(c.k) % 8 == 0 &&
+                     reinterpret_cast<uintptr_t>(c.v) % 8 == 0 && c.page_stride % 8 == 0 && c.slot_stride % 8 == 0 &&
+                     c.head_stride % 8 == 0;
+    p.chunks = FastDiv::make((uint32_t)(vec ? p.d / 8 : p.d));
+    const int64_t places = 4 * 152;
+    p.slice = kApMaxSlice;
+    while (p.slice > 1 && (p.batch.n + p.slice - 1) / p.slice < places)
+        p.slice /= 2;
+    const int64_t slices = (p.batch.n + p.slice - 1) / p.slice;
+    const unsigned grid = (unsigned)(slices < 0x7fffffff ? slices : 0x7fffffff);
+    if (vec)
+        kv8_append_kernel<T, true><<<grid, kApWarps * 32, 0, st>>>(p);
+    else
+        kv8_append_kernel<T, false><<<grid, kApWarps * 32, 0, st>>>(p);
+    count_launch(st);
+    return launch_status();
+}
+
+int launch_kv8_append(const HeadsView &k, const HeadsView &v, const BatchView &batch, const CacheView &cache,
+                      const ExpView &exp, int d, int dtype, int32_t *err, cudaStream_t st)
+{
+    Append8Params p = {k, v, batch, cache, exp, d, 0, {}, err};
+    if (dtype == DLRM_F32)
+        return launch_append8<float>(p, st);
+    if (dtype == DLRM_F16)
+        return launch_append8<__half>(p, st);
+    return launch_append8<__nv_bfloat16>(p, st);
+}
+
+}  // namespace dlrm

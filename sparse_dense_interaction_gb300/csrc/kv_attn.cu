@@ -9,7 +9,9 @@
 // and adds 2^(s - m_new).  Positions are split where there are few rows; a
 // split leaves its normalised output and log2 of its sum, and the join weighs
 // the splits by 2^(lse - max).
-#include "history.cuh"
+#include <type_traits>
+
+#include "kv8.cuh"
 
 namespace dlrm {
 
@@ -36,10 +38,12 @@ static int general_smem(int d)
     return (kGenRows * dp + kGenTile * (dp + 4) + kGenTile * dp + kGenRows * kGenTile + kGenRows) * 4;
 }
 
-template <typename T>
+// kCodes: the cache holds codes of 8 bits.
+template <typename T, bool kCodes>
 __global__ void __launch_bounds__(kGenThreads)
 kv_attn_general_kernel(const __grid_constant__ AttnParams p)
 {
+    using Stored = typename std::conditional<kCodes, uint8_t, T>::type;
     extern __shared__ float4 smem4[];
     const int d = p.d, dp = gen_pad(d), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kGenRows * dp, *sv = sk + kGenTile * (dp + 4);
@@ -72,9 +76,26 @@ kv_attn_general_kernel(const __grid_constant__ AttnParams p)
         for (int t = warp; t < kGenTile; t += kGenThreads / 32) {
             int64_t at = -1;
             if (tile + t < w.hi) {
-                at = slot_offset<T>(p.cache, pages, tile + t, w.head);
+                at = slot_offset<Stored>(p.cache, pages, tile + t, w.head);
                 if (at < 0)
                     raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+            }
+            if constexpr (kCodes) {
+                float kp = 0.f, vp = 0.f;
+                if (at >= 0) {
+                    const uint32_t page = p.cache.page.div((uint32_t)(tile + t));
+                    const int64_t x = exp_offset(p.exp, pages[page], tile + t - page * p.cache.page.d, w.head);
+                    kp = exp_power(p.exp.k[x]);
+                    vp = exp_power(p.exp.v[x]);
+                }
+                for (int e = lane; e < dp; e += 32) {
+                    const bool there = at >= 0 && e < d;
+                    const uint16_t c = there ? (uint8_t)p.cache.k[at + e] | (uint8_t)p.cache.v[at + e] << 8 : 0;
+                    const float2 x = decode2_f32(c);
+                    sk[t * (dp + 4) + e] = x.x * kp;
+                    sv[t * dp + e] = x.y * vp;
+                }
+                continue;
             }
             const T *k = reinterpret_cast<const T *>(p.cache.k + at), *v = reinterpret_cast<const T *>(p.cache.v + at);
             for (int e = lane; e < dp; e += 32) {
@@ -287,14 +308,14 @@ size_t attn_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, in
     return most + 16;
 }
 
-template <typename T>
+template <typename T, bool kCodes>
 static int launch_general(const AttnParams &p, int64_t ctas, cudaStream_t st)
 {
     static std::atomic<unsigned long long> done{0};
-    const int s = allow_dynamic_smem((const void *)kv_attn_general_kernel<T>, general_smem(DLRM_MAX_HEAD_DIM), &done);
+    const int s = allow_dynamic_smem((const void *)kv_attn_general_kernel<T, kCodes>, general_smem(DLRM_MAX_HEAD_DIM), &done);
     if (s != DLRM_OK)
         return s;
-    kv_attn_general_kernel<T><<<(unsigned)ctas, kGenThreads, general_smem(p.d), st>>>(p);
+    kv_attn_general_kernel<T, kCodes><<<(unsigned)ctas, kGenThreads, general_smem(p.d), st>>>(p);
     count_launch(st);
     return DLRM_OK;
 }
@@ -305,7 +326,9 @@ static int launch_attn_t(AttnParams &p, const AttnPlan &a, int dtype, cudaStream
     const int64_t ctas = p.batch.S * a.tiles * a.splits * p.cache.heads;
     if (ctas > 0x7fffffff)
         return DLRM_ERR_UNSUPPORTED;
-    const int s = a.kernel == kAttnTile ? launch_kv_attn_tile(p, dtype, ctas, st) : launch_general<T>(p, ctas, st);
+    const int s = a.kernel == kAttnTile ? launch_kv_attn_tile(p, dtype, ctas, st)
+                  : p.exp.k             ? launch_general<T, true>(p, ctas, st)
+                                        : launch_general<T, false>(p, ctas, st);
     if (s != DLRM_OK)
         return s;
     if (a.splits > 1) {
@@ -331,20 +354,16 @@ static bool wide_rows(const AttnParams &p, int dtype)
            ok(p.cache.k, p.cache.page_stride, p.cache.slot_stride) && ok(p.cache.v, p.cache.head_stride, 0);
 }
 
-int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
+// The part that a row sees at most, whatever the history's length: a window bounds it, and a sequence's rows.
+static int64_t seen_bound(const AttnParams &p)
 {
-    const bool cores = wide_rows(p, dtype);
-    // a window bounds what a row sees, and a sequence's rows, whatever the history's length
-    const int64_t rows = p.max_new * p.group, bound = p.window + (p.causal ? p.max_new : 0);
-    const int64_t seen = p.window > 0 && bound < p.max_len ? bound : p.max_len;
-    // Rows of 16: for few of them a short history's keys and values stay in L2,
-    // and more CTAs fit on an SM.  150 users, 8 heads of 128, 32 rows, rows of 16
-    // against tiles: up to 100 events 51 and 73 us, up to 1000 105 and 113; 64
-    // users, up to 2000: 101 and 37; 48 rows, up to 400: 90 and 88; heads of 64,
-    // 32 rows, up to 100: 42 and 40.
-    if (cores && (dtype == DLRM_F32 || p.d > 128 || rows <= 16 || (p.d > 64 && rows <= 32 && seen <= 1024)))
-        return launch_kv_attn_few(p, dtype, workspace, st);
-    const AttnKernel kernel = cores ? kAttnTile : kAttnGeneral;
+    const int64_t bound = p.window + (p.causal ? p.max_new : 0);
+    return p.window > 0 && bound < p.max_len ? bound : p.max_len;
+}
+
+// A kernel that goes by tiles of rows and splits of positions, and the join.
+static int launch_planned(AttnParams &p, AttnKernel kernel, int64_t seen, int dtype, void *workspace, cudaStream_t st)
+{
     AttnPlan a = plan(kernel, p.batch.S, p.cache.heads, p.group, p.d, p.max_new, p.max_len);
     if (seen < p.max_len) {  // never more parts than the workspace, whose size knows no window
         const AttnPlan b = plan(kernel, p.batch.S, p.cache.heads, p.group, p.d, p.max_new, seen);
@@ -362,6 +381,25 @@ int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     if (dtype == DLRM_F16)
         return launch_attn_t<__half>(p, a, dtype, st);
     return launch_attn_t<__nv_bfloat16>(p, a, dtype, st);
+}
+
+int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
+{
+    const bool cores = wide_rows(p, dtype);
+    const int64_t rows = p.max_new * p.group, seen = seen_bound(p);
+    // Rows of 16: for few of them a short history's keys and values stay in L2,
+    // and more CTAs fit on an SM.  150 users, 8 heads of 128, 32 rows, rows of 16
+    // against tiles: up to 100 events 51 and 73 us, up to 1000 105 and 113; 64
+    // users, up to 2000: 101 and 37; 48 rows, up to 400: 90 and 88; heads of 64,
+    // 32 rows, up to 100: 42 and 40.
+    if (cores && (dtype == DLRM_F32 || p.d > 128 || rows <= 16 || (p.d > 64 && rows <= 32 && seen <= 1024)))
+        return launch_kv_attn_few(p, dtype, workspace, st);
+    return launch_planned(p, cores ? kAttnTile : kAttnGeneral, seen, dtype, workspace, st);
+}
+
+int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
+{
+    return launch_planned(p, kAttnGeneral, seen_bound(p), dtype, workspace, st);
 }
 
 }  // namespace dlrm

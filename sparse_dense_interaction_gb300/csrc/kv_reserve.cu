@@ -1,0 +1,256 @@
+// Pages and slots for a step's new tokens, from the sequences' counts.
+//
+// Sequence s stores len tokens and gets c more: it needs
+// ceil((len + c) / page) - ceil(len / page) pages.  Prefix sums of the counts are
+// the batch's offsets; prefix sums of the needs say which entries of the free
+// pages' ring a sequence takes, so no page is fought over and the result does
+// not depend on the order in which threads run.  A token's page is then an
+// entry of its table row or of the ring, found without a second pass.
+//
+// What bounds it is the launch and one prefix sum's latency (a step of 2048
+// users writes 130 KB); a batch of prompts is bound by the 16 bytes written a
+// token.  So there is one kernel of one CTA for short steps; for longer ones
+// every CTA takes a run of tokens and sums up the sequences before it by itself
+// (16 bytes a sequence from L2, which costs less than a second kernel that waits for
+// the first), and a last CTA in a launch of its own writes what is in place:
+// lengths and the ring's state, which the others read.
+#include "history.cuh"
+
+namespace dlrm {
+
+constexpr int kResThreads = 1024, kResItems = 2, kResChunk = kResThreads * kResItems;
+constexpr int kResOneCta = 8 * kResThreads;  // tokens that one CTA takes alone
+constexpr int kResMaxCtas = 152;
+
+struct ReserveParams {
+    const int64_t *counts, *lengths;
+    int64_t S, n;
+    int32_t *table;
+    int64_t table_stride, capacity;
+    FastDiv page;
+    int32_t *ring;
+    int64_t pages;
+    const int64_t *state;
+    int64_t *new_state, *offsets, *new_lengths, *slots, *positions;
+    int32_t *err;
+};
+
+// Sums over the sequences before one: new tokens, pages needed, pages given back.
+struct ReserveSums {
+    int64_t tokens, need, gone;
+};
+
+__device__ __forceinline__ ReserveSums operator+(const ReserveSums &a, const ReserveSums &b)
+{
+    return {a.tokens + b.tokens, a.need + b.need, a.gone + b.gone};
+}
+
+__device__ __forceinline__ ReserveSums shfl_up(const ReserveSums &x, int o)
+{
+    return {__shfl_up_sync(0xffffffffu, x.tokens, o), __shfl_up_sync(0xffffffffu, x.need, o),
+            __shfl_up_sync(0xffffffffu, x.gone, o)};
+}
+
+// kTokens: this launch writes slots, positions, table entries and the ring;
+// kSequences: offsets, lengths and the state (one CTA).
+template <bool kTokens, bool kSequences>
+__global__ void __launch_bounds__(kResThreads)
+kv_reserve_kernel(const __grid_constant__ ReserveParams p)
+{
+    __shared__ ReserveSums warp_sums[kResThreads / 32];
+    // of the chunk's sequences: tokens and needs before it (from the chunk's first), stored tokens, and whether
+    // it has its pages (-1: it has left, 0: it is left out)
+    __shared__ uint32_t s_tokens[kResChunk + 1];
+    __shared__ int32_t s_need[kTokens ? kResChunk : 1], s_gone[kTokens ? kResChunk : 1];
+    __shared__ int32_t s_length[kTokens ? kResChunk : 1];
+    __shared__ int8_t s_granted[kTokens ? kResChunk : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t head = p.state[0], tail = p.state[1];
+    const bool sound = tail >= head && tail - head <= p.pages && head >= 0;
+    const int64_t avail = sound ? tail - head : 0;
+    const uint64_t ring_head = sound ? (uint64_t)head % (uint64_t)p.pages : 0;
+    const uint64_t ring_tail = sound ? (uint64_t)tail % (uint64_t)p.pages : 0;
+    // an entry of the ring, k < 2^31 places after one
+    auto place = [&](uint64_t from, int64_t k) {
+        const uint64_t at = from + (uint64_t)k;
+        return at >= (uint64_t)p.pages ? at - (uint64_t)p.pages : at;
+    };
+    const int64_t slice = (p.n + gridDim.x - 1) / gridDim.x;
+    const int64_t t0 = min(blockIdx.x * slice, p.n), t1 = min(t0 + slice, p.n);
+    ReserveSums base = {0, 0, 0};
+    int64_t taken = 0;  // this thread's largest granted sum
+    if (kSequences && threadIdx.x == 0 && !sound)
+        raise_flag(p.err, DLRM_FLAG_BAD_OFFSETS);
+    for (int64_t c0 = 0; c0 < p.S; c0 += kResChunk) {
+        const int64_t s0 = c0 + threadIdx.x * kResItems;
+        int64_t take[kResItems], len[kResItems], need[kResItems], gone[kResItems];
+        bool leaves[kResItems], fits[kResItems];
+        ReserveSums mine = {0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kResItems; i++) {
+            const bool there = s0 + i < p.S;
+            const int64_t count = there ? p.counts[s0 + i] : 0, x = there ? p.lengths[s0 + i] : 0;
+            len[i] = x < 0 ? ~x : x;
+            leaves[i] = count < 0;
+            take[i] = count < 0 ? 0 : min(count, (int64_t)1 << 31);
+            const bool stored = len[i] <= p.capacity;
+            fits[i] = !leaves[i] && stored && take[i] <= p.capacity - len[i];
+            const int64_t held = stored ? (len[i] + p.page.d - 1) / p.page.d : 0;
+            need[i] = fits[i] ? (len[i] + take[i] + p.page.d - 1) / p.page.d - held : 0;
+            gone[i] = leaves[i] ? held : 0;
+            if (kSequences && !stored && leaves[i])
+                raise_flag(p.err, DLRM_FLAG_BAD_OFFSETS);
+            mine = mine + ReserveSums{take[i], need[i], gone[i]};
+        }
+        ReserveSums sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const ReserveSums x = shfl_up(sum, o);
+            if (lane >= o)
+                sum = sum + x;
+        }
+        __syncthreads();  // the chunk before has been read
+        if (lane == 31)
+            warp_sums[warp] = sum;
+        __syncthreads();
+        if (warp == 0) {
+            ReserveSums w = warp_sums[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const ReserveSums x = shfl_up(w, o);
+                if (lane >= o)
+                    w = w + x;
+            }
+            warp_sums[lane] = w;
+        }
+        __syncthreads();
+        ReserveSums at = warp > 0 ? warp_sums[warp - 1] : ReserveSums{0, 0, 0};  // from the chunk's first
+        at = at + ReserveSums{sum.tokens - mine.tokens, sum.need - mine.need, sum.gone - mine.gone};
+        const ReserveSums all = warp_sums[kResThreads / 32 - 1];
+#pragma unroll
+        for (int i = 0; i < kResItems; i++) {
+            const int in = threadIdx.x * kResItems + i;
+            const bool rows = take[i] == 0 || base.tokens + at.tokens + take[i] <= p.n;
+            const bool granted = fits[i] && rows && (need[i] == 0 || base.need + at.need + need[i] <= avail);
+            if (granted && need[i] > 0)
+                taken = max(taken, base.need + at.need + need[i]);
+            if (kTokens) {
+                s_tokens[in] = (uint32_t)min(at.tokens, (int64_t)0xffffffffu);
+                // beyond 2^31 they are past every granted need and every place of the ring
+                s_need[in] = (int)min(at.need, (int64_t)0x7fffffff);
+                s_gone[in] = (int)min(at.gone, (int64_t)0x7fffffff);
+                s_length[in] = (int)min(len[i], (int64_t)0x7fffffff);
+                s_granted[in] = leaves[i] ? -1 : (granted ? 1 : 0);
+            }
+            if (kSequences && s0 + i < p.S) {
+                p.offsets[s0 + i] = base.tokens + at.tokens;
+                p.new_lengths[s0 + i] = leaves[i] ? 0 : (granted ? len[i] + take[i] : ~len[i]);
+                if (!granted && !leaves[i])
+                    raise_flag(p.err, fits[i] && rows ? DLRM_FLAG_CAPACITY : DLRM_FLAG_BAD_OFFSETS);
+            }
+            at = at + ReserveSums{take[i], need[i], gone[i]};
+        }
+        if (kTokens) {
+            if (threadIdx.x == 0)
+                s_tokens[kResChunk] = (uint32_t)min(all.tokens, (int64_t)0xffffffffu);
+            __syncthreads();
+            // pages of those who leave, a warp a sequence, every CTA its share of them
+            const int here = (int)min(p.S - c0, (int64_t)kResChunk);
+            for (int in = blockIdx.x + warp * gridDim.x; in < here; in += (kResThreads / 32) * gridDim.x) {
+                const int length = s_length[in];
+                if (s_granted[in] >= 0 || length > p.capacity)
+                    continue;
+                const int pages = (int)((length + p.page.d - 1) / p.page.d);
+                const int32_t *row = p.table + (c0 + in) * p.table_stride;
+                const int64_t k0 = base.gone + s_gone[in];
+                for (int k = lane; k < pages; k += 32) {
+                    if (!sound || avail + k0 + k >= p.pages) {
+                        raise_flag(p.err, DLRM_FLAG_CAPACITY);
+                        continue;
+                    }
+                    const int32_t page = row[k];
+                    if ((uint32_t)page >= (uint64_t)p.pages)
+                        raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+                    p.ring[place(ring_tail, k0 + k)] = page;
+                }
+            }
+            // this CTA's tokens among the chunk's
+            const int64_t from = max(t0, base.tokens), to = min(t1, base.tokens + all.tokens);
+            for (int64_t t = from + threadIdx.x; t < to; t += kResThreads) {
+                const uint32_t x = (uint32_t)(t - base.tokens);
+                int lo = 0, hi = here;  // the last sequence that starts at or before x: those of no tokens come before
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_tokens[mid] <= x)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                int64_t slot = -1, position = -1;
+                if (s_granted[lo] > 0) {
+                    const int length = s_length[lo], at_token = length + (int)(x - s_tokens[lo]);
+                    const int number = (int)p.page.div((uint32_t)at_token), in_page = at_token - number * (int)p.page.d;
+                    const int held = (int)((length + p.page.d - 1) / p.page.d);
+                    int32_t *entry = p.table + (c0 + lo) * p.table_stride + number;
+                    int32_t page;
+                    if (number < held) {
+                        page = *entry;
+                    } else {
+                        page = p.ring[place(ring_head, base.need + s_need[lo] + number - held)];
+                        if (in_page == 0)
+                            *entry = page;
+                    }
+                    position = at_token;
+                    if ((uint32_t)page < (uint64_t)p.pages)
+                        slot = (int64_t)page * p.page.d + in_page;
+                    else
+                        raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+                }
+                if (p.slots)
+                    p.slots[t] = slot;
+                if (p.positions)
+                    p.positions[t] = position;
+            }
+        }
+        base = base + all;
+    }
+    if (kSequences) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
+        __syncthreads();
+        if (lane == 0)
+            warp_sums[warp].need = taken;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kResThreads / 32; w++)
+                taken = max(taken, warp_sums[w].need);
+            p.offsets[p.S] = base.tokens;
+            p.new_state[0] = head + taken;
+            p.new_state[1] = sound ? tail + min(base.gone, p.pages - avail) : tail;
+        }
+    }
+}
+
+int launch_kv_reserve(const int64_t *counts, const int64_t *lengths, int64_t S, int64_t n, int32_t *table,
+                      int64_t table_stride, int64_t table_width, int page_size, int32_t *ring, int64_t pages,
+                      const int64_t *state, int64_t *new_state, int64_t *offsets, int64_t *new_lengths, int64_t *slots,
+                      int64_t *positions, int32_t *err, cudaStream_t st)
+{
+    const ReserveParams p = {counts, lengths, S, n, table, table_stride, table_width * page_size,
+                             FastDiv::make((uint32_t)page_size), ring, pages, state, new_state, offsets, new_lengths,
+                             slots, positions, err};
+    if (n <= kResOneCta) {
+        kv_reserve_kernel<true, true><<<1, kResThreads, 0, st>>>(p);
+        count_launch(st);
+        return launch_status();
+    }
+    const int64_t ctas = (n + kResThreads - 1) / kResThreads;
+    kv_reserve_kernel<true, false><<<(unsigned)(ctas < kResMaxCtas ? ctas : kResMaxCtas), kResThreads, 0, st>>>(p);
+    count_launch(st);
+    kv_reserve_kernel<false, true><<<1, kResThreads, 0, st>>>(p);
+    count_launch(st);
+    return launch_status();
+}
+
+}  // namespace dlrm
