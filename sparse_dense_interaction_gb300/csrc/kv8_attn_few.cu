@@ -1,0 +1,681 @@
+// Attention over the cache in 8 bits by rows of 16: single tokens and short
+// chunks, and chunks of every length in fp32 or with heads above 128.
+//
+// Memory bounds it, with half the bytes of the 16-bit cache, and the design is
+// that of its rows of 16: items laid end to end in units, equal runs of them to
+// the CTAs, a ring of stages for each warp that bulk tensor copies fill through
+// the page table, the warp's own MMAs with the tokens as their 16 rows.  What 8
+// bits change:
+//  - E4M3's values are fp16 values, so codes become fp16 two at a time by one
+//    conversion each and every product runs in fp16, whatever the queries' type.
+//    bf16 and fp32 queries are lifted by a power of two that takes a row's largest element to 2^14
+//    (exact but for what lies 2^-38 below that element); fp32 ones in two parts,
+//    22 bits, as are their weights.
+//  - A lane's 16-byte chunk of a key row serves four MMA steps, 16 columns of a
+//    value row are a lane's; the codes of two tokens are interleaved by byte
+//    permutes before they are converted, which puts them where the MMA wants pairs.
+//  - The keys' powers multiply the scores, the values' powers the weights, in
+//    fp32: a factor for a token and all rows, so 2 products for a score.
+//    A weight is held relative to the largest power that the warp has seen so far
+//    and rises with it (the output is scaled down when that grows, as it is when a maximum
+//    does), so fp16's range is the row's: what a token gathers is off by at most
+//    2^-39 of the largest weight times the largest power.
+//  - A lane asks for the exponents of one token of the block, a unit or two
+//    ahead, beside the copies; shuffles hand them out.
+// A conversion takes two cycles of a quarter of an SM, a quarter of the time
+// that memory leaves.
+#include <type_traits>
+
+#include "kv8.cuh"
+#include "kv_few.cuh"
+
+namespace dlrm {
+
+template <typename T, int DP, int kGroups>
+struct Few8Shape {
+    static constexpr bool kWide = sizeof(T) == 4;
+    static constexpr int MG = 16;                        // tokens of an MMA group
+    static constexpr int TB = DP <= 128 ? 32 : 16, NB = TB / MG, UT = kFewWarps * TB;
+    static constexpr int KG = DP / 64;                   // a lane's chunks of 16 codes of a key row
+    static constexpr int VB = DP >= 128 ? 16 : 8, VS = DP / (8 * VB);  // codes of its chunks of a value row, and their number
+    static constexpr int kStageBytes = TB * 2 * DP;
+    static constexpr int kStats = 2 * kGroups;           // rows whose statistics a lane holds
+    // Two parts of a weight where fp16's 11 bits are not enough: fp32, and fp16 outputs of narrow tiles
+    static constexpr bool kTwoParts = kWide || (std::is_same<T, __half>::value && kGroups == 1);
+    static constexpr int kOutMmas = VB / 2;              // of a set of output columns
+    static constexpr int kOut = kGroups * VS * kOutMmas * 4;
+    static constexpr int kResident = !kWide && kGroups == 1 && DP <= 128 ? 3 : 2, kStages = DP == 64 ? 4 : kResident == 3 ? 2 : 3;
+    static constexpr int kCtas = kResident * kFewSms;
+    static constexpr int kMerge = kOut < 32 ? kOut : 32;
+    static constexpr int kSmem = 1024 + kFewWarps * kStages * kStageBytes + 2 * kMerge * 32 * 4;
+    static constexpr int kKeyBox = MG * 64, kValueBox = MG * 8 * VB;  // bytes of a column of a group's keys, values
+    static constexpr int kGroupBytes = KG * kKeyBox + VS * kValueBox;
+    static_assert(NB * kGroupBytes == kStageBytes && kCtas <= kFewMaxCtas, "a stage holds whole groups");
+
+    // the row of a lane's statistic i, and the statistic of its output register o
+    __device__ __forceinline__ static int row(int i, int q) { return 2 * q + (i & 1) + 8 * (i >> 1); }
+    __device__ __forceinline__ static constexpr int stat(int o) { return (o & 1) + 2 * (o / (VS * kOutMmas * 4)); }
+};
+
+// 8 query elements as they lie.
+template <typename T>
+struct Few8Query {
+    uint4 x[sizeof(T) / 2];
+
+    __device__ __forceinline__ void load(const T *src, bool there)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; i++)
+            x[i] = there ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ float2 pair(int i) const  // elements 2i, 2i + 1
+    {
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t *w = &x[i / 2].x + 2 * (i & 1);
+            return make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        } else {
+            return unpack2<T>((&x[0].x)[i]);
+        }
+    }
+};
+
+template <typename T, int DP, int kGroups>
+__global__ void __launch_bounds__(kFewWarps * 32, Few8Shape<T, DP, kGroups>::kResident)
+kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FewMaps maps)
+{
+    using Sh = Few8Shape<T, DP, kGroups>;
+    constexpr int KG = Sh::KG, VS = Sh::VS, VB = Sh::VB, NB = Sh::NB, TB = Sh::TB, UT = Sh::UT, kStages = Sh::kStages;
+    constexpr int kParts = Sh::kWide ? 2 : 1;  // of a query
+    constexpr float kTop = kWeightTop<__half>;
+    extern __shared__ uint8_t raw[];
+    __shared__ float s_m[kFewWarps][kFewRows], s_l[kFewWarps][kFewRows];
+    __shared__ uint64_t bars[kFewWarps][kStages];
+    __shared__ int busy[kFewWarps * 32];
+    __shared__ int aborted, died_at[kFewWarps];  // died_at: the unit whose wait ran out
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    uint8_t *smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
+    uint8_t *ring = smem + warp * kStages * Sh::kStageBytes;
+    float *merge = reinterpret_cast<float *>(smem + kFewWarps * kStages * Sh::kStageBytes);  // [2][kMerge][32]
+
+    FewItem it;  // of the unit being computed; `is`: of the unit whose addresses come next
+    int units, quota = 0;  // of this CTA; the items' are counted from its first
+    if (p.splits > 1) {
+        const bool any = few_share(p, it, units, quota, UT, busy);
+        if (threadIdx.x == 0)
+            p.joins[blockIdx.x].rows = 0;  // until an item is left unfinished
+        if (!any)
+            return;
+    } else {
+        const int64_t most = (p.max_new * p.group + kFewRows - 1) / kFewRows, of = blockIdx.x / most;
+        const int64_t s = of / p.cache.heads;
+        if (!read_sequence(p.batch, s, p.max_new, p.max_len, it.seq, p.err) || !few_sequence(p, it, s, 0, UT))
+            return;
+        it.head = (int)(of - s * p.cache.heads);
+        it.tile = (int)(blockIdx.x - of * most);
+        if (it.tile >= it.tiles)
+            return;
+        units = it.last;
+    }
+    FewItem is = it;
+
+    // A lane finds the page and slot of one token of the warp's block (its exponents are the lane's to fetch), and
+    // copies one box, whose place the lane of its first token knows; a box that no query sees anything of is
+    // outside the map: zeros.
+    const int parts = Sh::MG / maps.rows, boxes = parts * (KG + VS);  // of a group: its keys' columns, then its values'
+    const int my_group = lane / boxes, my_box = lane - my_group * boxes;
+    const int my_part = my_box % parts, my_column = my_box / parts;
+    const int my_first = (my_group * Sh::MG + my_part * maps.rows) & 31;
+    const bool copies = my_group < NB;
+    int page_id = -1, page_slot = 0;
+    bool token_seen = false;
+    auto find = [&](int u) {
+        page_id = -1;
+        token_seen = false;
+        if (u >= units)
+            return;
+        while (u >= is.last)
+            few_next(p, is, UT, busy);
+        const int at = is.lo + (u - is.first) * UT + warp * TB + (lane & (TB - 1)), box = at & -maps.rows;
+        if (box < is.hi && box + maps.rows > is.lo_seen) {
+            const uint32_t page = p.cache.page.div((uint32_t)at);
+            page_slot = at - (int)(page * p.cache.page.d);
+            page_id = __ldg(is.pages + page);
+            token_seen = at >= is.lo_seen && at < is.hi;
+        }
+    };
+    const uint32_t ring_at = tc::smem_u32(ring);
+    uint32_t k_exp[kStages], v_exp[kStages];  // of the lane's token of the next units
+    bool dead = false;  // a wait ran out: nothing more is copied, the results are invalid
+    // copies of unit u, whose page numbers were asked for a unit before, into a stage; then asks for the next
+    auto copy = [&](int u, int stage, uint32_t &ke, uint32_t &ve) {
+        ke = ve = 0;
+        if (u < units && !dead) {
+            if (lane == 0)
+                tc::mbar_expect_tx(&bars[warp][stage], Sh::kStageBytes);
+            const bool sound = (uint32_t)page_id < p.cache.pages;
+            if (token_seen && !sound)
+                raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+            const int page = __shfl_sync(0xffffffffu, sound ? page_id : -1, my_first);
+            const int slot = __shfl_sync(0xffffffffu, page_slot, my_first);
+            if (copies) {
+                const uint32_t to = ring_at + stage * Sh::kStageBytes + my_group * Sh::kGroupBytes;
+                if (my_column < KG)
+                    tc::tma_load_4d(to + my_column * Sh::kKeyBox + my_part * maps.rows * 64, &maps.k, my_column * 64,
+                                    slot, is.head, page, &bars[warp][stage]);
+                else
+                    tc::tma_load_4d(to + KG * Sh::kKeyBox + (my_column - KG) * Sh::kValueBox +
+                                        my_part * maps.rows * 8 * VB,
+                                    &maps.v, (my_column - KG) * 8 * VB, slot, is.head, page, &bars[warp][stage]);
+            }
+            if (token_seen && sound) {
+                const int64_t x = exp_offset(p.exp, page_id, page_slot, is.head);
+                ke = p.exp.k[x];
+                ve = p.exp.v[x];
+            }
+        }
+        find(u + 1);
+    };
+    if (lane == 0)
+        for (int i = 0; i < kStages; i++)
+            tc::mbar_init(&bars[warp][i], 1);
+    if (threadIdx.x == 0)
+        aborted = 0;
+    tc::mbar_init_fence();
+    __syncthreads();
+    find(0);
+#pragma unroll
+    for (int i = 0; i < kStages; i++)
+        copy(i, i, k_exp[i], v_exp[i]);
+
+    uint32_t qa[kGroups][KG][kParts][8];  // the queries' chunks of rows g, g + 8 as fp16 (fp32: and the rest)
+    float o[Sh::kOut], m[Sh::kStats], l[Sh::kStats], scale[Sh::kStats];
+    int lo[Sh::kStats], hi[Sh::kStats], rows = 0;  // rows: of the sequence
+    int all_lo = 0, all_hi = 0;  // positions that every row of the tile sees
+    int top_exp = 0;             // the largest exponent of the values so far: weights are relative to its power
+    bool fresh = true, first_item = true;
+    int stage = 0;
+    uint32_t phase = 0;
+#pragma unroll 1
+    for (int u = 0; u < units; u++) {
+        if (fresh) {
+            const int row0 = it.tile * kFewRows;
+            rows = it.seq.count * p.group;
+            all_hi = seen_hi(it.seq, p.causal, row0 / p.group);
+            all_lo = seen_lo(seen_hi(it.seq, p.causal, (min(rows, row0 + kFewRows) - 1) / p.group), p.window);
+            float back[kGroups];  // of rows g, g + 8: what undoes their queries' lifting
+#pragma unroll
+            for (int h = 0; h < kGroups; h++) {
+                const int r = row0 + g + 8 * h, t = r / p.group;
+                const T *src = p.q.row<T>(it.seq.first + (r < rows ? t : 0),
+                                          r < rows ? it.head * p.group + r - t * p.group : 0);
+                Few8Query<T> x[KG][2];
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < KG; i++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        const int e = (4 * i + q) * 16 + 8 * j;
+                        x[i][j].load(src + e, r < rows && e < p.d);
+                        if constexpr (!std::is_same<T, __half>::value)
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const float2 y = x[i][j].pair(k);
+                                top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+                            }
+                    }
+                float lift = 1.f;
+                back[h] = 1.f;
+                if constexpr (!std::is_same<T, __half>::value) {
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
+                    if (top > 0.f && e < 255) {
+                        lift = __uint_as_float((268 - e) << 23);  // 2^(127 + 14 - e)
+                        back[h] = __uint_as_float((e - 14) << 23);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < KG; i++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            uint32_t &w = qa[h][i][0][4 * j + k];
+                            if constexpr (std::is_same<T, __half>::value) {
+                                w = (&x[i][j].x[0].x)[k];
+                            } else {
+                                float2 y = x[i][j].pair(k);
+                                y = make_float2(y.x * lift, y.y * lift);
+                                w = pack2<__half>(y.x, y.y);
+                                if constexpr (Sh::kWide) {
+                                    const float2 z = unpack2<__half>(w);
+                                    qa[h][i][1][4 * j + k] = pack2<__half>(y.x - z.x, y.y - z.y);
+                                }
+                            }
+                        }
+            }
+#pragma unroll
+            for (int i = 0; i < Sh::kStats; i++) {
+                const int r = row0 + Sh::row(i, q);
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+                hi[i] = r < rows ? seen_hi(it.seq, p.causal, r / p.group) : 0;
+                lo[i] = seen_lo(hi[i], p.window);
+                // never 0: a masked score is -infinity
+                scale[i] = fmaxf(p.scale_log2 * __shfl_sync(0xffffffffu, back[i >> 1], (2 * q + (i & 1)) * 4), 1.2e-38f);
+            }
+#pragma unroll
+            for (int i = 0; i < Sh::kOut; i++)
+                o[i] = 0.f;
+            top_exp = 0;
+            fresh = false;
+        }
+        if (!dead && !tc::mbar_wait(&bars[warp][stage], phase, &aborted, p.wait_polls)) {
+            dead = true;
+            died_at[warp] = u;
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        const uint8_t *block = ring + stage * Sh::kStageBytes;
+        const int at = it.lo + (u - it.first) * UT + warp * TB;
+
+        // scores: s[nb][x][j] is of token nb * 16 + g + 8 * (j >> 1) and statistic 2 * x + (j & 1)
+        float s[NB][kGroups][4], weight[NB][2];  // weight: the power of a token's values
+        auto stat_of = [](int x, int j) { return 2 * x + (j & 1); };
+        const int exps = (int)(k_exp[0] | v_exp[0] << 8), new_exp = max(top_exp, __reduce_max_sync(0xffffffffu, (int)v_exp[0]));
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            float other[kGroups][4];  // every second MMA's sum: two chains, half as long
+#pragma unroll
+            for (int x = 0; x < kGroups; x++)
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    s[nb][x][j] = other[x][j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < KG; i++) {
+                uint32_t a[4][4];  // of the chunk's four steps
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    const uint4 k = *reinterpret_cast<const uint4 *>(block + nb * Sh::kGroupBytes + i * Sh::kKeyBox +
+                                                                     (t * 8 + g) * 64 + q * 16);
+                    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        a[e][t] = decode2((uint16_t)w[e]);
+                        a[e][t + 2] = decode2((uint16_t)(w[e] >> 16));
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < kGroups; n++) {
+                    if constexpr (Sh::kWide) {
+                        // The MMA's own sums are cut off, not rounded: two steps, small terms first, then fp32
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int part = 1; part >= 0; part--)
+#pragma unroll
+                                for (int f = e; f < e + 2; f++)
+                                    mma16816<__half>(t, a[f], qa[n][i][part][2 * f], qa[n][i][part][2 * f + 1]);
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                s[nb][n][j] += t[j];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            mma16816<__half>(e & 1 ? other[n] : s[nb][n], a[e], qa[n][i][0][2 * e], qa[n][i][0][2 * e + 1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t mine = (uint32_t)__shfl_sync(0xffffffffu, exps, nb * Sh::MG + g + 8 * h);
+                const float power = exp_power(mine & 255);
+                weight[nb][h] = __uint_as_float((uint32_t)max((int)(mine >> 8) - new_exp + 127, 0) << 23);
+#pragma unroll
+                for (int x = 0; x < kGroups; x++)
+#pragma unroll
+                    for (int j = 2 * h; j < 2 * h + 2; j++)
+                        s[nb][x][j] = (s[nb][x][j] + other[x][j]) * power;
+            }
+        }
+        const bool edge = at < all_lo || at + TB > all_hi;
+        if (edge) {
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int x = 0; x < kGroups; x++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int pos = at + nb * Sh::MG + g + 8 * (j >> 1), i = stat_of(x, j);
+                        s[nb][x][j] = pos >= lo[i] && pos < hi[i] ? s[nb][x][j] : -INFINITY;
+                    }
+        }
+        float top[Sh::kStats], base[Sh::kStats], off[Sh::kStats];
+        bool moved = new_exp > top_exp;
+#pragma unroll
+        for (int i = 0; i < Sh::kStats; i++) {
+            top[i] = -INFINITY;
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int x = 0; x < kGroups; x++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (stat_of(x, j) == i)
+                            top[i] = fmaxf(top[i], s[nb][x][j]);
+#pragma unroll
+            for (int step = 4; step < 32; step *= 2)
+                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], step));
+            top[i] = fmaxf(__fmul_ru(top[i], scale[i]), m[i]);
+            base[i] = top[i] == -INFINITY ? 0.f : top[i];
+            off[i] = __fsub_rd(kTop, base[i]);
+            moved |= top[i] > m[i];
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+            const float down = __uint_as_float((uint32_t)max(127 + top_exp - new_exp, 0) << 23);
+            float f[Sh::kStats];
+#pragma unroll
+            for (int i = 0; i < Sh::kStats; i++) {
+                f[i] = exp2_approx(m[i] - base[i]);
+                l[i] *= f[i];
+                f[i] *= down;
+                m[i] = top[i];
+            }
+#pragma unroll
+            for (int i = 0; i < Sh::kOut; i++)
+                o[i] *= f[Sh::stat(i)];
+            top_exp = new_exp;
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+#pragma unroll
+            for (int x = 0; x < kGroups; x++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int i = stat_of(x, j);
+                    const float e = exp2_approx(fmaf(s[nb][x][j], scale[i], off[i]));
+                    l[i] += e;
+                    s[nb][x][j] = e * weight[nb][j >> 1];
+                }
+            // the weights, rounded to fp16, and in two parts what that leaves of them, rows to columns
+            uint32_t b[kGroups][2], rest[kGroups][2];
+#pragma unroll
+            for (int n = 0; n < kGroups; n++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float x = s[nb][n][2 * h], y = s[nb][n][2 * h + 1];
+                    const uint32_t w = pack2<__half>(x, y);
+                    b[n][h] = transpose8x8(w);
+                    if (Sh::kTwoParts) {
+                        const float2 r = unpack2<__half>(w);
+                        rest[n][h] = transpose8x8(pack2<__half>(x - r.x, y - r.y));
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < VS; i++) {
+                uint32_t v[4][VB / 4];  // the lane's columns of tokens 2q, 2q + 1 and of those + 8
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    const int row = 2 * q + (t & 1) + 8 * (t >> 1);
+                    const uint8_t *from = block + nb * Sh::kGroupBytes + KG * Sh::kKeyBox + i * Sh::kValueBox;
+                    if constexpr (VB == 16) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(from + row * 128 + ((g ^ (row & 7)) << 4));
+                        v[t][0] = x.x, v[t][1] = x.y, v[t][2] = x.z, v[t][3] = x.w;
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(from + row * 64 + (((g >> 1) ^ q) << 4) + (g & 1) * 8);
+                        v[t][0] = x.x, v[t][1] = x.y;
+                    }
+                    // a box's rows that no query sees may hold anything: a zero weight would not do
+                    if (edge) {
+                        const int pos = at + nb * Sh::MG + row;
+                        if (pos < it.lo_seen || pos >= it.hi)
+#pragma unroll
+                            for (int j = 0; j < VB / 4; j++)
+                                v[t][j] = 0;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < VB / 4; j++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {  // columns 4j + 2c and the next of the lane's
+                        const uint32_t x = __byte_perm(v[0][j], v[1][j], c ? 0x7362 : 0x5140);
+                        const uint32_t y = __byte_perm(v[2][j], v[3][j], c ? 0x7362 : 0x5140);
+                        const uint32_t a[4] = {decode2((uint16_t)x), decode2((uint16_t)(x >> 16)), decode2((uint16_t)y),
+                                               decode2((uint16_t)(y >> 16))};
+#pragma unroll
+                        for (int n = 0; n < kGroups; n++) {
+                            float *sum = o + ((n * VS + i) * Sh::kOutMmas + 2 * j + c) * 4;
+                            if constexpr (Sh::kWide) {
+                                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma16816<__half>(t, a, rest[n][0], rest[n][1]);
+                                mma16816<__half>(t, a, b[n][0], b[n][1]);
+#pragma unroll
+                                for (int k = 0; k < 4; k++)
+                                    sum[k] += t[k];
+                            } else {
+                                if (Sh::kTwoParts)
+                                    mma16816<__half>(sum, a, rest[n][0], rest[n][1]);
+                                mma16816<__half>(sum, a, b[n][0], b[n][1]);
+                            }
+                        }
+                    }
+            }
+        }
+        __syncwarp();  // every lane has read the stage that is filled next
+#pragma unroll
+        for (int i = 0; i + 1 < kStages; i++) {
+            k_exp[i] = k_exp[i + 1];
+            v_exp[i] = v_exp[i + 1];
+        }
+        copy(u + kStages, stage, k_exp[kStages - 1], v_exp[kStages - 1]);
+        stage++;
+        if (stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+        if (u + 1 < it.last && u + 1 < units)
+            continue;
+
+        // the item's (or the CTA's) last unit: join the warps
+#pragma unroll
+        for (int i = 0; i < Sh::kStats; i++) {
+#pragma unroll
+            for (int step = 4; step < 32; step *= 2)
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], step);
+            if (g == 0) {
+                s_m[warp][Sh::row(i, q)] = m[i];
+                s_l[warp][Sh::row(i, q)] = l[i];
+            }
+        }
+        __syncthreads();
+        float lse[Sh::kStats], f[Sh::kStats];
+        const float power = exp_power((uint32_t)top_exp);
+#pragma unroll
+        for (int i = 0; i < Sh::kStats; i++) {
+            const int r = Sh::row(i, q);
+            float all = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFewWarps; w++)
+                all = fmaxf(all, s_m[w][r]);
+            const float b = all == -INFINITY ? 0.f : all;
+#pragma unroll
+            for (int w = 0; w < kFewWarps; w++)
+                sum = fmaf(s_l[w][r], exp2_approx(s_m[w][r] - b), sum);
+            // no weight at all: nothing is seen; a sum that is not a number stays one
+            f[i] = sum == 0.f ? 0.f : exp2_approx(m[i] - b) / sum * power;
+            lse[i] = sum == 0.f ? -INFINITY : all + (log2f(sum) - kTop);
+        }
+#pragma unroll
+        for (int i = 0; i < Sh::kOut; i++)
+            o[i] *= f[Sh::stat(i)];
+#pragma unroll
+        for (int r = 0; r < Sh::kOut; r += Sh::kMerge) {
+            if (r > 0)
+                __syncthreads();
+            if (warp >= 2)
+#pragma unroll
+                for (int i = 0; i < Sh::kMerge; i++)
+                    merge[((warp - 2) * Sh::kMerge + i) * 32 + lane] = o[r + i];
+            __syncthreads();
+            if (warp < 2)
+#pragma unroll
+                for (int i = 0; i < Sh::kMerge; i++)
+                    o[r + i] += merge[(warp * Sh::kMerge + i) * 32 + lane];
+            if (warp == 1)
+#pragma unroll
+                for (int i = 0; i < Sh::kMerge; i++)
+                    merge[(Sh::kMerge + i) * 32 + lane] = o[r + i];
+            __syncthreads();
+            if (warp == 0)
+#pragma unroll
+                for (int i = 0; i < Sh::kMerge; i++)
+                    o[r + i] += merge[(Sh::kMerge + i) * 32 + lane];
+        }
+        if (warp == 0) {
+            const bool whole = it.first >= 0 && it.last <= units;
+            const int heads = p.cache.heads * p.group, slot = blockIdx.x * 2 + (first_item ? 0 : 1);
+#pragma unroll
+            for (int i = 0; i < Sh::kStats; i++) {
+                const int in = Sh::row(i, q), r = it.tile * kFewRows + in, t = r / p.group;
+                const int head = it.head * p.group + r - t * p.group;
+                if (r >= rows)
+                    continue;
+                if (g == 0) {
+                    if (!whole)
+                        p.part_lse[slot * p.rows + in] = lse[i];
+                    else if (p.lse)
+                        p.lse[(it.seq.first + t) * heads + head] = lse[i] * kLn2;
+                }
+                // the lane's runs of VB columns of this row, 8 at a time
+#pragma unroll
+                for (int c = 0; c < VS * VB / 8; c++) {
+                    const int set = c / (VB / 8), in_set = c % (VB / 8), e = (8 * set + g) * VB + in_set * 8;
+                    if (e >= p.d)
+                        continue;
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        x[j] = o[(((i >> 1) * VS + set) * Sh::kOutMmas + in_set * 4 + (j >> 1)) * 4 + 2 * (j & 1) + (i & 1)];
+                    T *out = p.out.row<T>(it.seq.first + t, head) + e;
+                    float4 *wide = Sh::kWide && whole ? reinterpret_cast<float4 *>(out)
+                                                      : reinterpret_cast<float4 *>(p.part_o + ((int64_t)slot * p.rows + in) * p.d + e);
+                    if (!whole || Sh::kWide) {
+                        wide[0] = make_float4(x[0], x[1], x[2], x[3]);
+                        wide[1] = make_float4(x[4], x[5], x[6], x[7]);
+                    } else if constexpr (!Sh::kWide) {
+                        *reinterpret_cast<uint4 *>(out) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
+                                                                     pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+                    }
+                }
+            }
+        }
+        if (threadIdx.x == 0 && it.first >= 0 && it.last > units) {  // the CTAs after this one go on with it
+            const int row0 = it.tile * kFewRows;
+            FewJoin j;
+            j.token = it.seq.first;
+            j.head = it.head * p.group;
+            j.row = row0;
+            j.rows = min(rows - row0, kFewRows);
+            j.first = blockIdx.x * 2 + (first_item ? 0 : 1);
+            j.last = blockIdx.x + (it.last - 1) / quota;
+            p.joins[blockIdx.x] = j;
+        }
+        fresh = true;
+        first_item = false;
+        if (u + 1 < units)
+            few_next(p, it, UT, busy);
+    }
+    if (dead) {
+        // that unit and those copied ahead of it may still be in flight: none may be when the memory is given back
+        __syncwarp();
+        const int first = died_at[warp];
+        for (int i = first; i < min(first + kStages, units); i++)
+            tc::mbar_drain(&bars[warp][i % kStages], (i / kStages) & 1);
+        if (lane == 0)
+            raise_flag(p.err, DLRM_FLAG_WAIT_TIMEOUT);
+    }
+}
+
+// Maps of the codes with boxes of `rows` slots; false where they cannot be described so.
+static bool few8_maps(const AttnParams &p, int rows, FewMaps &m)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.d, p.cache.page.d, (cuuint64_t)p.cache.heads, p.cache.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.cache.slot_stride, (cuuint64_t)p.cache.head_stride,
+                                   (cuuint64_t)p.cache.page_stride};
+    const cuuint32_t k_box[4] = {64, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t v_box[4] = {p.d > 64 ? 128u : 64u, (cuuint32_t)rows, 1, 1};
+    // lines of 256 bytes where a head's rows fill them; else they would be its neighbours'
+    const CUtensorMapL2promotion lines = p.cache.slot_stride == p.d ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                                                    : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+    m.rows = rows;
+    return enc(&m.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.cache.k, dims, strides, k_box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, lines,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+           enc(&m.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.cache.v, dims, strides, v_box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, p.d > 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, lines,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int DP, int kGroups>
+static int launch_few8(AttnParams &p, const FewMaps &maps, void *workspace, cudaStream_t st)
+{
+    using Sh = Few8Shape<T, DP, kGroups>;
+    static std::atomic<unsigned long long> done{0};
+    const int s = allow_dynamic_smem((const void *)kv8_attn_few_kernel<T, DP, kGroups>, Sh::kSmem, &done);
+    if (s != DLRM_OK)
+        return s;
+    // a window bounds what an item's rows see, whatever the history's length
+    const int64_t seen = p.window > 0 ? p.window + (p.causal ? p.max_new : 0) : p.max_len;
+    // items, idle sequences' among them; the batch cannot have more busy sequences than tokens
+    const int64_t each = p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows), items = p.batch.S * each;
+    const int64_t busy = (p.batch.S < p.batch.n ? p.batch.S : p.batch.n) * each;
+    const bool split = few_splits(seen < p.max_len ? seen : p.max_len, p.d, 1, busy);
+    p.splits = split ? 2 : 1;
+    p.joins = static_cast<FewJoin *>(workspace);
+    p.part_o = reinterpret_cast<float *>(p.joins + kFewMaxCtas);
+    p.rows = (int)few_rows(p.max_new * p.group);
+    p.part_lse = p.part_o + (size_t)2 * kFewMaxCtas * p.rows * p.d;
+    if (items > 0x7fffffff)
+        return DLRM_ERR_UNSUPPORTED;
+    kv8_attn_few_kernel<T, DP, kGroups>
+        <<<(unsigned)(split ? Sh::kCtas : items), kFewWarps * 32, Sh::kSmem, st>>>(p, maps);
+    count_launch(st);
+    if (split) {
+        const dim3 grid(Sh::kCtas - 1, (unsigned)p.rows);
+        kv_attn_few_join_kernel<T, (DP > 128 ? 2 : 1)><<<grid, kJoinWarps * 32, 0, st>>>(p);
+        count_launch(st);
+    }
+    return launch_status();
+}
+
+template <typename T>
+static int launch_few8_width(AttnParams &p, const FewMaps &maps, void *workspace, cudaStream_t st)
+{
+    const bool narrow = p.max_new * p.group <= 8;
+    if (p.d <= 64)
+        return narrow ? launch_few8<T, 64, 1>(p, maps, workspace, st) : launch_few8<T, 64, 2>(p, maps, workspace, st);
+    if constexpr (sizeof(T) == 2)
+        if (p.d > 128)
+            return narrow ? launch_few8<T, 256, 1>(p, maps, workspace, st)
+                          : launch_few8<T, 256, 2>(p, maps, workspace, st);
+    return narrow ? launch_few8<T, 128, 1>(p, maps, workspace, st) : launch_few8<T, 128, 2>(p, maps, workspace, st);
+}
+
+// False where the codes cannot be copied so (pages that are no multiple of 8 slots, strides or addresses that are
+// none of 16 bytes); else launched, with `status`.
+bool launch_kv8_attn_few(AttnParams &p, int dtype, void *workspace, cudaStream_t st, int &status)
+{
+    FewMaps maps = {};
+    if (p.cache.page.d % 8 != 0 || !few8_maps(p, p.cache.page.d % 16 == 0 ? 16 : 8, maps))
+        return false;
+    status = dtype == DLRM_F32   ? launch_few8_width<float>(p, maps, workspace, st)
+             : dtype == DLRM_F16 ? launch_few8_width<__half>(p, maps, workspace, st)
+                                 : launch_few8_width<__nv_bfloat16>(p, maps, workspace, st);
+    return true;
+}
+
+}  // namespace dlrm

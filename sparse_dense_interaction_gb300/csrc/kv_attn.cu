@@ -18,6 +18,7 @@ namespace dlrm {
 size_t few_workspace(int64_t, int, int64_t);
 int launch_kv_attn_few(AttnParams &, int, void *, cudaStream_t);
 int launch_kv_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
+bool launch_kv8_attn_few(AttnParams &, int, void *, cudaStream_t, int &);
 
 // ---------------------------------------------------------------- general kernel
 
@@ -399,6 +400,14 @@ int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
 
 int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
 {
+    const int e = dtype == DLRM_F32 ? 4 : 8;
+    auto even = [e](const HeadsView &h) {
+        return reinterpret_cast<uintptr_t>(h.ptr) % 16 == 0 && h.ts % e == 0 && h.hs % e == 0;
+    };
+    int status;
+    if (p.d % 8 == 0 && p.d <= (dtype == DLRM_F32 ? 128 : 256) && even(p.q) && even(p.out) &&
+        launch_kv8_attn_few(p, dtype, workspace, st, status))
+        return status;
     return launch_planned(p, kAttnGeneral, seen_bound(p), dtype, workspace, st);
 }
 
