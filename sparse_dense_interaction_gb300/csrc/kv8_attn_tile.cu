@@ -1,0 +1,459 @@
+// Attention over the cache in 8 bits for many rows: tiles of 256 (or 128) rows on
+// the tensor cores, in fp16 whatever the queries' 16-bit type.
+//
+// The tiles, their MMAs and their softmax are those of the 16-bit cache
+// (tensor memory, one warp that issues, a lagging maximum).  What 8 bits change:
+//  - Keys and values are converted on their way into the ring: warps of their own read
+//    16 codes a lane straight from the pages, a tile ahead in registers, and write
+//    them as fp16 into the swizzled tiles that the MMAs read.  The conversion needs
+//    registers anyway, so bulk copies and a ring of raw codes would only add
+//    a trip through shared memory; pages of any size take this path.
+//  - Every code is multiplied by its block's power relative to a power of the tile
+//    (2^7 lifts it to fp16's range; the product is exact but for what lies 2^-41 below the
+//    largest): for keys the tile's largest, which then is part of the tile's
+//    scale, for values the largest so far, and the output is scaled down when it grows, as it
+//    is when a maximum does.  So the softmax does nothing more for an element.
+//  - The softmax's threads fetch the queries, which are idle until then: bf16 rows
+//    are lifted by a power of two each, so that they fit fp16 exactly but for
+//    what lies 2^-38 below a row's largest.
+#include "kv8.cuh"
+#include "kv_tile.cuh"
+
+namespace dlrm {
+
+template <int DP, bool kTwo>
+struct Tile8Shape {
+    using Sh = TileShape<DP, kTwo>;
+    static constexpr int kWarps = kTwo ? 4 : 2;          // that convert
+    static constexpr int kThreads = Sh::kSoftmaxThreads + kWarps * 32 + 32;
+    static constexpr int kRows = kTilePos / kWarps;      // of a tile, a warp's
+    static constexpr int kOwn = kRows / 32;              // whose places a lane finds
+    static constexpr int kStepRows = 32 / (DP / 16);     // rows of which the warp's lanes read a chunk at once
+    static constexpr int kSteps = kRows / kStepRows;
+};
+
+constexpr int kTile8Refs = 8;   // tiles whose powers are kept: more than the ring holds
+constexpr int kTile8Lift = 7;   // log2 of what the codes are lifted by: 448 * 2^7 is near fp16's largest
+constexpr int kConvertBarrier = 9;
+
+struct Tile8Bars : TileBars {
+    int k_ref[kTile8Refs], v_ref[kTile8Refs];  // of a tile: the exponents that its codes are relative to
+    int warp_ref[2][4][2];
+};
+
+// 2^(e + 7) as a pair of fp16, e <= 0; subnormal, at last 0, below 2^-14.
+__device__ __forceinline__ uint32_t relative_power(int e)
+{
+    const int b = e + kTile8Lift + 15;
+    const uint32_t h = b > 0 ? (uint32_t)b << 10 : (b > -10 ? 0x400u >> (1 - b) : 0u);
+    return h | h << 16;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
+{
+    uint32_t c;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
+// The warps that convert.  A tile begins at a multiple of 128 positions.
+template <int DP, bool kTwo>
+__device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *ring, Tile8Bars &b, int tiles)
+{
+    using Sh = TileShape<DP, kTwo>;
+    using S8 = Tile8Shape<DP, kTwo>;
+    constexpr int kOwn = S8::kOwn, kSteps = S8::kSteps, kStepRows = S8::kStepRows;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - Sh::kSoftmaxWarps, row0 = warp * S8::kRows;
+    const int start = w.lo & ~127;
+    const int32_t *pages = p.batch.table + w.s * p.batch.table_stride;
+    // the lane's row and chunk of a step: 8 lanes write to every bank once
+    const int step_row = DP == 128 ? ((lane >> 2) & 1) | (lane >> 4) << 1 : lane >> 2;
+    const int chunk = DP == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
+    const bool inside = chunk * 16 < p.d;
+
+    int32_t page[kOwn], slot[kOwn];     // of the next tile's rows lane, lane + 32
+    int64_t off[kOwn], next_off[kOwn];  // their codes; -1: a row of zeros
+    uint32_t ke[kOwn], ve[kOwn];        // their exponents
+    auto find = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < kOwn; i++) {
+            const int at = start + j * kTilePos + row0 + i * 32 + lane;
+            slot[i] = -1;
+            if (j < tiles && at >= w.lo && at < w.hi) {
+                const uint32_t n = p.cache.page.div((uint32_t)at);
+                slot[i] = at - (int)(n * p.cache.page.d);
+                page[i] = __ldg(pages + n);
+            }
+        }
+    };
+    auto place = [&]() {
+#pragma unroll
+        for (int i = 0; i < kOwn; i++) {
+            next_off[i] = -1;
+            ke[i] = ve[i] = 0;
+            if (slot[i] < 0)
+                continue;
+            if ((uint32_t)page[i] >= p.cache.pages) {
+                raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+                continue;
+            }
+            next_off[i] = page[i] * p.cache.page_stride + slot[i] * p.cache.slot_stride + w.head * p.cache.head_stride;
+            const int64_t x = exp_offset(p.exp, page[i], slot[i], w.head);
+            ke[i] = p.exp.k[x];
+            ve[i] = p.exp.v[x];
+        }
+    };
+    uint4 held[kSteps];
+    auto load = [&](const char *base, const int64_t *from, int i) {
+        const int64_t o = __shfl_sync(0xffffffffu, from[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
+        held[i] = make_uint4(0, 0, 0, 0);
+        if (o >= 0 && inside)
+            asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(held[i].x), "=r"(held[i].y), "=r"(held[i].z), "=r"(held[i].w)
+                         : "l"(base + o + chunk * 16));
+    };
+    auto store = [&](uint8_t *tile, const uint32_t *factor, int i) {
+        const uint32_t f = __shfl_sync(0xffffffffu, factor[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
+        const uint32_t in[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
+        uint32_t x[8];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            x[2 * k] = hmul2(decode2((uint16_t)in[k]), f);
+            x[2 * k + 1] = hmul2(decode2((uint16_t)(in[k] >> 16)), f);
+        }
+        const int r = row0 + i * kStepRows + step_row, unit = 2 * (chunk & 3);
+        uint8_t *to = tile + (chunk >> 2) * Sh::kBlock + r * 128;
+        *reinterpret_cast<uint4 *>(to + ((unit ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4 *>(to + (((unit + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+    };
+    // hands a tile over; after a wait that ran out the warps still meet at their barrier, but write nothing
+    bool dead = false;
+    auto begin = [&](int i) {
+        if (!dead && i >= Sh::kSlots &&
+            !warp_wait(&b.empty[i % Sh::kSlots], (i / Sh::kSlots - 1) & 1, &b.aborted, p.wait_polls))
+            dead = true;
+        return ring + i % Sh::kSlots * Sh::kTileBytes;
+    };
+    auto end = [&](int i) {
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && !dead)
+            tc::mbar_arrive(&b.full[i % Sh::kSlots]);
+    };
+
+    find(0);
+    place();
+#pragma unroll
+    for (int i = 0; i < kSteps; i++)
+        load(p.cache.k, next_off, i);
+    int v_ref = 0;
+#pragma unroll 1
+    for (int j = 0; j < tiles; j++) {
+        // what the tile's codes are relative to
+        uint32_t k_top = 0, v_top = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; i++) {
+            off[i] = next_off[i];
+            k_top = max(k_top, ke[i]);
+            v_top = max(v_top, ve[i]);
+        }
+        k_top = __reduce_max_sync(0xffffffffu, k_top);
+        v_top = __reduce_max_sync(0xffffffffu, v_top);
+        if (lane == 0) {
+            b.warp_ref[j & 1][warp][0] = (int)k_top;
+            b.warp_ref[j & 1][warp][1] = (int)v_top;
+        }
+        tc::named_sync(kConvertBarrier, S8::kWarps * 32);
+        int k_ref = 0;
+#pragma unroll
+        for (int i = 0; i < S8::kWarps; i++) {
+            k_ref = max(k_ref, b.warp_ref[j & 1][i][0]);
+            v_ref = max(v_ref, b.warp_ref[j & 1][i][1]);
+        }
+        if (warp == 0 && lane == 0) {
+            b.k_ref[j % kTile8Refs] = k_ref;
+            b.v_ref[j % kTile8Refs] = v_ref;
+        }
+        uint32_t kf[kOwn], vf[kOwn];
+#pragma unroll
+        for (int i = 0; i < kOwn; i++) {
+            kf[i] = relative_power((int)ke[i] - k_ref);
+            vf[i] = relative_power((int)ve[i] - v_ref);
+        }
+        find(j + 1);
+        uint8_t *tile = begin(2 * j);
+#pragma unroll
+        for (int i = 0; i < kSteps; i++) {
+            if (!dead)
+                store(tile, kf, i);
+            load(p.cache.v, off, i);
+        }
+        end(2 * j);
+        place();
+        tile = begin(2 * j + 1);
+#pragma unroll
+        for (int i = 0; i < kSteps; i++) {
+            if (!dead)
+                store(tile, vf, i);
+            load(p.cache.k, next_off, i);
+        }
+        end(2 * j + 1);
+    }
+}
+
+// A softmax thread's half of its query row, as fp16 in the swizzled tile; returns what undoes the row's lifting.
+template <typename T, int DP, bool kTwo>
+__device__ __forceinline__ float tile8_query(const AttnParams &p, const AttnWork &w, uint8_t *sq, Tile8Bars &b, int t,
+                                             int half, int in, int pair)
+{
+    using Sh = TileShape<DP, kTwo>;
+    constexpr int kChunks = DP / 16;  // of 8 elements, of half a row
+    const int r = t * 128 + in, row = w.row0 + r, token = row / p.group;
+    const bool mine = r < w.rows;
+    const T *src = p.q.row<T>(mine ? w.seq.first + token : 0, mine ? w.head * p.group + row - token * p.group : 0);
+    uint4 x[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; c++) {
+        const int e = half * (DP / 2) + c * 8;
+        x[c] = mine && e < p.d ? *reinterpret_cast<const uint4 *>(src + e) : make_uint4(0, 0, 0, 0);
+    }
+    float back = 1.f;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; c++) {
+            const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 y = unpack2<T>(v[i]);
+                top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+        }
+        b.agree[t][half][in] = top;
+        tc::named_sync(pair, 64);
+        top = fmaxf(top, b.agree[t][1 - half][in]);
+        float lift = 1.f;
+        const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
+        if (top > 0.f && e < 255) {
+            lift = __uint_as_float((268 - e) << 23);  // 2^(127 + 14 - e)
+            back = __uint_as_float((e - 14) << 23);
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; c++) {
+            uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 y = unpack2<T>(v[i]);
+                v[i] = pack2<__half>(y.x * lift, y.y * lift);
+            }
+            x[c] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; c++) {
+        const int e = half * (DP / 2) + c * 8;
+        *reinterpret_cast<uint4 *>(sq + t * Sh::kTileBytes + (e >> 6) * Sh::kBlock + in * 128 +
+                                   ((((e >> 3) & 7) ^ (in & 7)) << 4)) = x[c];
+    }
+    tc::fence_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        tc::mbar_arrive(&b.q_full);
+    return back;
+}
+
+template <typename T, int DP, bool kTwo>
+__device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq, Tile8Bars &b, int tiles)
+{
+    using Sh = TileShape<DP, kTwo>;
+    constexpr int kHalf = kTilePos / 2, kCols = DP / 2;  // scores, output columns of a thread
+    const int warp = threadIdx.x >> 5, t = warp >> 3, half = (warp >> 2) & 1;
+    const int in = (warp & 3) * 32 + (threadIdx.x & 31), r = t * 128 + in, pair = 1 + t * 4 + (warp & 3);
+    const uint32_t lanes = b.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_at = lanes + t * 128 + half * kHalf, p_at = lanes + t * 128 + half * (kHalf / 2);
+    const uint32_t o_at = lanes + Sh::kScoreCols + t * DP + half * kCols;
+    const int row = w.row0 + r, token = row / p.group;
+    const bool mine = r < w.rows;
+    // a row past the last sees everything: it needs no mask, and nothing of it is written
+    const int hi = mine ? min(seen_hi(w.seq, p.causal, token), w.hi) : 0x7fffffff;
+    const int lo = mine ? max(seen_lo(seen_hi(w.seq, p.causal, token), p.window), w.lo) : 0;
+    const float row_scale = p.scale_log2 * tile8_query<T, DP, kTwo>(p, w, sq, b, t, half, in, pair);
+    float m = -INFINITY, l = 0.f;
+    int v_ref = 0;  // the exponent that the output is relative to
+    for (int j = 0; j < tiles; j++) {
+        // a wait that runs out is seen at the end; the pair's barriers below want every warp
+        tc::mbar_wait(&b.s_full[t], j & 1, &b.aborted, p.wait_polls);
+        __syncwarp();
+        tc::fence_after_sync();
+        uint32_t s[kHalf];
+        const int at = (w.lo & ~127) + j * kTilePos + half * kHalf;
+        tc::tmem_ld32_async(s_at, s);
+        tc::tmem_ld32_async(s_at + 32, s + 32);
+        const int k_ref = b.k_ref[j % kTile8Refs], now_ref = b.v_ref[j % kTile8Refs];
+        // never 0: a masked score is -infinity
+        const float scale_log2 = fmaxf(row_scale * exp_power((uint32_t)max(k_ref - kTile8Lift, 0)), 1.2e-38f);
+        tc::tmem_ld_wait(s);
+        tc::tmem_ld_wait(s + 32);
+        if (!__all_sync(0xffffffffu, at >= lo && at + kHalf <= hi)) {
+#pragma unroll
+            for (int i = 0; i < kHalf; i++)
+                s[i] = at + i >= lo && at + i < hi ? s[i] : 0xff800000u;
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kHalf; i += 2)
+            top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+        float now = __fmul_ru(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale_log2);
+        b.agree[t][half][in] = now;
+        tc::named_sync(pair, 64);
+        now = fmaxf(now, b.agree[t][1 - half][in]);
+        if (__any_sync(0xffffffffu, now - m > kTileSlack<__half> || now_ref > v_ref)) {
+            // also from -infinity; the output of the tiles before is complete: the scores' MMA came after it
+            const float next = fmaxf(m, now), f = next == -INFINITY ? 1.f : exp2_approx(m - next);
+            const float down = f * __uint_as_float((uint32_t)max(127 + v_ref - now_ref, 0) << 23);
+            m = next;
+            l *= f;
+            v_ref = now_ref;
+            if (j > 0) {
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 16) {
+                    uint32_t o[16];
+                    tc::tmem_ld16(o_at + c, o);
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * down);
+                    tc::tmem_st16(o_at + c, o);
+                }
+            }
+        }
+        const float lift = __fsub_rd(kTileLift<__half>, m == -INFINITY ? 0.f : m);
+        const float2 scale = make_float2(scale_log2, scale_log2), off = make_float2(lift, lift);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < kHalf / 32; c++) {
+            uint32_t packed[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const int k = c * 32 + 2 * i;
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale, off);
+                const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+                packed[i] = pack2<__half>(e.x, e.y);
+            }
+            tc::tmem_st16(p_at + c * 16, packed);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            tc::mbar_arrive(&b.p_ready[t]);
+    }
+    tc::named_sync(pair, 64);  // the last maxima have been read
+    b.agree[t][half][in] = l;
+    tc::named_sync(pair, 64);
+    l = b.agree[t][0][in] + b.agree[t][1][in];
+    float inv = 0.f, lse = -INFINITY;
+    if (l != 0.f) {  // not a number either: then neither is the row
+        inv = 1.f / l * exp_power((uint32_t)v_ref) * (1.f / (1 << kTile8Lift));
+        lse = m + (log2f(l) - kTileLift<__half>);
+    }
+    if (tiles > 0) {
+        tc::mbar_wait(&b.o_full[t], 0, &b.aborted, p.wait_polls);
+        __syncwarp();
+        tc::fence_after_sync();
+    }
+    tile_write<T, DP, kTwo>(p, w, sq, b.tmem, t, half, tiles, inv, lse);
+}
+
+template <typename T, int DP, bool kTwo>
+__global__ void __launch_bounds__(Tile8Shape<DP, kTwo>::kThreads, kTwo ? 1 : 2)
+kv8_attn_tile_kernel(const __grid_constant__ AttnParams p)
+{
+    using Sh = TileShape<DP, kTwo>;
+    using S8 = Tile8Shape<DP, kTwo>;
+    constexpr int kLast = S8::kThreads / 32 - 1;
+    extern __shared__ __align__(1024) uint8_t sq[];  // query tiles, the ring, then the rest: all that an SM has
+    uint8_t *ring = sq + Sh::kRows / 128 * Sh::kTileBytes;
+    Tile8Bars &b = *reinterpret_cast<Tile8Bars *>(sq + Sh::kTiles);
+    const int warp = threadIdx.x >> 5;
+    AttnWork w;
+    if (!tile_work(p, reinterpret_cast<int *>(sq), w))
+        return;
+    const int tiles = w.hi > w.lo ? (w.hi - (w.lo & ~127) + kTilePos - 1) / kTilePos : 0;  // 0: rows that see nothing
+    const bool two = kTwo && w.rows > 128;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::kSlots; i++) {
+            tc::mbar_init(&b.full[i], S8::kWarps);
+            tc::mbar_init(&b.empty[i], 1);
+        }
+        tc::mbar_init(&b.q_full, two ? 16 : 8);  // the softmax's warps
+        tc::mbar_init(&b.drained, 1);
+        for (int t = 0; t < 2; t++) {
+            tc::mbar_init(&b.s_full[t], 1);
+            tc::mbar_init(&b.p_ready[t], 8);  // the tile's warps
+            tc::mbar_init(&b.o_full[t], 1);
+        }
+        b.aborted = 0;
+        tc::mbar_init_fence();
+    }
+    if (warp == kLast)
+        tc::tmem_alloc<Sh::kTmem>(&b.tmem);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp < Sh::kSoftmaxWarps) {
+        if (warp < 8 || two)
+            tile8_softmax<T, DP, kTwo>(p, w, sq, b, tiles);
+    } else if (warp < kLast) {
+        if (tiles > 0)
+            tile8_convert<DP, kTwo>(p, w, ring, b, tiles);
+    } else if (tiles > 0) {
+        tile_mma<__half, DP, kTwo>(sq, ring, b, tiles, two, p.wait_polls);
+        __syncwarp();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    // Nobody waits any more, so all see the same.  No MMA may be in flight when the memory is given back.
+    if (*reinterpret_cast<volatile int *>(&b.aborted)) {
+        if (threadIdx.x == 0)
+            raise_flag(p.err, DLRM_FLAG_WAIT_TIMEOUT);
+        if (warp == kLast && tiles > 0 && tc::elect_one()) {
+            tc::mma_commit(&b.drained);
+            tc::mbar_drain(&b.drained, 0);
+        }
+        __syncthreads();
+    }
+    if (warp == kLast)
+        tc::tmem_free<Sh::kTmem>(b.tmem);
+}
+
+template <typename T, int DP, bool kTwo>
+static int launch_tile8(const AttnParams &p, int64_t ctas, cudaStream_t st)
+{
+    constexpr int smem = TileShape<DP, kTwo>::kTiles + sizeof(Tile8Bars);
+    static_assert(smem <= 232448, "an SM's shared memory");
+    static std::atomic<unsigned long long> done{0};
+    const int s = allow_dynamic_smem((const void *)kv8_attn_tile_kernel<T, DP, kTwo>, smem, &done);
+    if (s != DLRM_OK)
+        return s;
+    kv8_attn_tile_kernel<T, DP, kTwo><<<(unsigned)ctas, Tile8Shape<DP, kTwo>::kThreads, smem, st>>>(p);
+    count_launch(st);
+    return DLRM_OK;
+}
+
+template <typename T>
+static int launch_tile8_shape(const AttnParams &p, int64_t ctas, cudaStream_t st)
+{
+    if (p.d > 64)
+        return launch_tile8<T, 128, true>(p, ctas, st);
+    return p.rows > 128 ? launch_tile8<T, 64, true>(p, ctas, st) : launch_tile8<T, 64, false>(p, ctas, st);
+}
+
+int launch_kv8_attn_tile(const AttnParams &p, int dtype, int64_t ctas, cudaStream_t st)
+{
+    return dtype == DLRM_F16 ? launch_tile8_shape<__half>(p, ctas, st) : launch_tile8_shape<__nv_bfloat16>(p, ctas, st);
+}
+
+}  // namespace dlrm

@@ -18,6 +18,7 @@ namespace dlrm {
 size_t few_workspace(int64_t, int, int64_t);
 int launch_kv_attn_few(AttnParams &, int, void *, cudaStream_t);
 int launch_kv_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
+int launch_kv8_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
 bool launch_kv8_attn_few(AttnParams &, int, void *, cudaStream_t, int &);
 
 // ---------------------------------------------------------------- general kernel
@@ -327,9 +328,11 @@ static int launch_attn_t(AttnParams &p, const AttnPlan &a, int dtype, cudaStream
     const int64_t ctas = p.batch.S * a.tiles * a.splits * p.cache.heads;
     if (ctas > 0x7fffffff)
         return DLRM_ERR_UNSUPPORTED;
-    const int s = a.kernel == kAttnTile ? launch_kv_attn_tile(p, dtype, ctas, st)
-                  : p.exp.k             ? launch_general<T, true>(p, ctas, st)
-                                        : launch_general<T, false>(p, ctas, st);
+    int s;
+    if (a.kernel == kAttnTile)
+        s = p.exp.k ? launch_kv8_attn_tile(p, dtype, ctas, st) : launch_kv_attn_tile(p, dtype, ctas, st);
+    else
+        s = p.exp.k ? launch_general<T, true>(p, ctas, st) : launch_general<T, false>(p, ctas, st);
     if (s != DLRM_OK)
         return s;
     if (a.splits > 1) {
@@ -404,11 +407,18 @@ int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     auto even = [e](const HeadsView &h) {
         return reinterpret_cast<uintptr_t>(h.ptr) % 16 == 0 && h.ts % e == 0 && h.hs % e == 0;
     };
+    const CacheView &c = p.cache;
+    const bool rows_even = p.d % 8 == 0 && even(p.q) && even(p.out);
+    const bool codes_even = reinterpret_cast<uintptr_t>(c.k) % 16 == 0 && reinterpret_cast<uintptr_t>(c.v) % 16 == 0 &&
+                            c.page_stride % 16 == 0 && c.slot_stride % 16 == 0 && c.head_stride % 16 == 0;
+    const int64_t rows = p.max_new * p.group, seen = seen_bound(p);
+    const bool tile = rows_even && codes_even && p.d % 16 == 0 && dtype != DLRM_F32 && p.d <= 128;
+    const bool few = rows_even && codes_even && p.d <= (dtype == DLRM_F32 ? 128 : 256);
     int status;
-    if (p.d % 8 == 0 && p.d <= (dtype == DLRM_F32 ? 128 : 256) && even(p.q) && even(p.out) &&
+    if (few && (!tile || rows <= 16 || (p.d > 64 && rows <= 32 && seen <= 1024)) &&
         launch_kv8_attn_few(p, dtype, workspace, st, status))
         return status;
-    return launch_planned(p, kAttnGeneral, seen_bound(p), dtype, workspace, st);
+    return launch_planned(p, tile ? kAttnTile : kAttnGeneral, seen, dtype, workspace, st);
 }
 
 }  // namespace dlrm
