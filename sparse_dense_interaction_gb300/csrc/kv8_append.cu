@@ -35,26 +35,52 @@ struct Append8Item {
     int32_t older;  // slots before the token's in the block, all filled
 };
 
-// 8 elements as fp32.
+// 8 elements as they lie; read once.
 template <typename T>
-__device__ __forceinline__ void load8(const T *src, float *x);
-template <>
-__device__ __forceinline__ void load8<float>(const float *src, float *x)
-{
-    const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-template <typename T>
-__device__ __forceinline__ void load8(const T *src, float *x)
-{
-    const uint4 a = *reinterpret_cast<const uint4 *>(src);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Append8Chunk {
+    static constexpr int kWords = sizeof(T) * 2;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 y = unpack2<T>(w[i]);
-        x[2 * i] = y.x;
-        x[2 * i + 1] = y.y;
+        for (int i = 0; i < kWords; i++)
+            w[i] = 0;
     }
+    __device__ __forceinline__ void load(const T *src)
+    {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; i++) {
+            const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
+    }
+    __device__ __forceinline__ float2 pair(int i) const  // elements 2i, 2i + 1
+    {
+        if constexpr (sizeof(T) == 4)
+            return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else
+            return unpack2<T>(w[i]);
+    }
+    // The largest magnitude's bits, as an unsigned number of T's width, in each half or whole of the result and
+    // `top`: magnitudes are ordered like their bits.
+    __device__ __forceinline__ uint32_t largest(uint32_t top) const
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; i++)
+            top = sizeof(T) == 4 ? max(top, w[i] & 0x7fffffffu) : __vmaxu2(top, w[i] & 0x7fff7fffu);
+        return top;
+    }
+};
+
+// The warp's largest magnitude, of what largest() left in every lane; infinity or NaN if any is.
+template <typename T>
+__device__ __forceinline__ float largest_of_warp(uint32_t top)
+{
+    if constexpr (sizeof(T) == 4)
+        return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+    else
+        return unpack2<T>(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16))).x;
 }
 
 // |x| where x is finite, else 0: what is not finite does not count for the exponent.
@@ -114,82 +140,86 @@ __device__ __forceinline__ int append8_items(const Append8Params &p, int64_t i0,
 template <typename T, bool kVec>
 __device__ __forceinline__ void append8_block(const Append8Params &p, const Append8Item &it, int head, bool value)
 {
-    constexpr int kHold = sizeof(T) == 4 ? 4 : 8;  // chunks of a lane that stay in registers
+    constexpr int kHold = kVec ? (sizeof(T) == 4 ? 4 : 8) : 0;  // chunks of a lane that stay in registers
     const int lane = threadIdx.x & 31;
     const HeadsView &in = value ? p.v : p.k;
     uint8_t *exps = (value ? p.exp.v : p.exp.k) + exp_offset(p.exp, it.page, it.slot, head);
     char *codes = (value ? p.cache.v : p.cache.k) + it.page * p.cache.page_stride + head * p.cache.head_stride;
     const int before = it.older > 0 ? *exps : 0;
     const int per_row = kVec ? p.d / 8 : p.d, all = it.fresh * per_row;
-    auto row_of = [&](int c, int &at) {
+    const T *rows = in.row<T>(it.token, head);
+    // where chunk (or element) c lies, and its codes
+    auto source = [&](int c) {
         const int r = (int)p.chunks.div((uint32_t)c);
-        at = (c - r * per_row) * (kVec ? 8 : 1);
-        return r;
+        return rows + r * in.ts + (c - r * per_row) * (kVec ? 8 : 1);
     };
+    auto target = [&](int c) {
+        const int r = (int)p.chunks.div((uint32_t)c);
+        return codes + (it.slot + r) * p.cache.slot_stride + (c - r * per_row) * (kVec ? 8 : 1);
+    };
+    auto size_of = [&](int c) {  // the slow way, past what is not finite
+        float top = 0.f;
+        if constexpr (kVec) {
+            Append8Chunk<T> x;
+            x.load(source(c));
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 y = x.pair(i);
+                top = fmaxf(top, fmaxf(finite_size(y.x), finite_size(y.y)));
+            }
+        } else {
+            top = finite_size(to_f32(*source(c)));
+        }
+        return top;
+    };
+    Append8Chunk<T> held[kHold > 0 ? kHold : 1];
     float top = 0.f;
-    float held[kVec ? kHold : 1][8];
     if constexpr (kVec) {
 #pragma unroll
         for (int i = 0; i < kHold; i++) {
-            const int c = i * 32 + lane;
-            if (c < all) {
-                int at;
-                const int r = row_of(c, at);
-                load8<T>(in.row<T>(it.token + r, head) + at, held[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    held[i][e] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kHold; i++)
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                top = fmaxf(top, finite_size(held[i][e]));
-    }
-    for (int c = (kVec ? kHold * 32 : 0) + lane; c < all; c += 32) {
-        int at;
-        const int r = row_of(c, at);
-        const T *src = in.row<T>(it.token + r, head) + at;
-        if constexpr (kVec) {
-            float x[8];
-            load8<T>(src, x);
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                top = fmaxf(top, finite_size(x[e]));
-        } else {
-            top = fmaxf(top, finite_size(to_f32(*src)));
-        }
-    }
-    const int fresh = exponent_of(warp_max(top)), now = fresh > before ? fresh : before;
-    const float scale = encode_power(now);
-    auto write8 = [&](int c, const float *x) {
-        int at;
-        const int r = row_of(c, at);
-        uint32_t w[2];
-#pragma unroll
-        for (int i = 0; i < 2; i++)
-            w[i] = encode2(x[4 * i] * scale, x[4 * i + 1] * scale) |
-                   (uint32_t)encode2(x[4 * i + 2] * scale, x[4 * i + 3] * scale) << 16;
-        *reinterpret_cast<uint2 *>(codes + (it.slot + r) * p.cache.slot_stride + at) = make_uint2(w[0], w[1]);
-    };
-    if constexpr (kVec) {
-#pragma unroll
-        for (int i = 0; i < kHold; i++)
+            held[i].clear();
             if (i * 32 + lane < all)
-                write8(i * 32 + lane, held[i]);
+                held[i].load(source(i * 32 + lane));
+        }
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < kHold; i++)
+            bits = held[i].largest(bits);
+        for (int c = kHold * 32 + lane; c < all; c += 32) {
+            Append8Chunk<T> x;
+            x.load(source(c));
+            bits = x.largest(bits);
+        }
+        top = largest_of_warp<T>(bits);
     }
-    for (int c = (kVec ? kHold * 32 : 0) + lane; c < all; c += 32) {
-        int at;
-        const int r = row_of(c, at);
-        const T *src = in.row<T>(it.token + r, head) + at;
+    if (!kVec || !(top <= 3.4028234663852886e38f)) {
+        top = 0.f;
+        for (int c = lane; c < all; c += 32)
+            top = fmaxf(top, size_of(c));
+        top = warp_max(top);
+    }
+    const int fresh = exponent_of(top), now = fresh > before ? fresh : before;
+    const float scale = encode_power(now);
+    auto write8 = [&](int c, const Append8Chunk<T> &x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 y = x.pair(i);
+            w[i] = encode2(y.x * scale, y.y * scale);
+        }
+        *reinterpret_cast<uint2 *>(target(c)) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    };
+#pragma unroll
+    for (int i = 0; i < kHold; i++)
+        if (i * 32 + lane < all)
+            write8(i * 32 + lane, held[i]);
+    for (int c = kHold * 32 + lane; c < all; c += 32) {
         if constexpr (kVec) {
-            float x[8];
-            load8<T>(src, x);
+            Append8Chunk<T> x;
+            x.load(source(c));
             write8(c, x);
         } else {
-            codes[(it.slot + r) * p.cache.slot_stride + at] = (char)encode2(to_f32(*src) * scale, 0.f);
+            *target(c) = (char)encode2(to_f32(*source(c)) * scale, 0.f);
         }
     }
     if (it.older > 0 && now > before) {  // older codes under the larger power; below 2^-120 all of them are zeros
@@ -206,7 +236,7 @@ __device__ __forceinline__ void append8_block(const Append8Params &p, const Appe
 }
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kApWarps * 32)
+__global__ void __launch_bounds__(kApWarps * 32, 4)
 kv8_append_kernel(const __grid_constant__ Append8Params p)
 {
     __shared__ Append8Item items[kApMaxSlice];

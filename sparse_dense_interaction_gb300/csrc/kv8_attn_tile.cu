@@ -22,14 +22,16 @@
 namespace dlrm {
 
 template <int DP, bool kTwo>
-struct Tile8Shape {
-    using Sh = TileShape<DP, kTwo>;
+struct Tile8Shape : TileShape<DP, kTwo, DP == 128 || !kTwo ? 4 : 8> {
+    using Sh = TileShape<DP, kTwo, DP == 128 || !kTwo ? 4 : 8>;
     static constexpr int kWarps = kTwo ? 4 : 2;          // that convert
-    static constexpr int kThreads = Sh::kSoftmaxThreads + kWarps * 32 + 32;
-    static constexpr int kRows = kTilePos / kWarps;      // of a tile, a warp's
-    static constexpr int kOwn = kRows / 32;              // whose places a lane finds
-    static constexpr int kStepRows = 32 / (DP / 16);     // rows of which the warp's lanes read a chunk at once
-    static constexpr int kSteps = kRows / kStepRows;
+    static constexpr int kMmaWarp = Sh::kSoftmaxWarps + kWarps, kThreads = kMmaWarp * 32 + 32;
+    static constexpr int kWarpRows = kTilePos / kWarps;  // of a tile, a warp's
+    static constexpr int kOwn = kWarpRows / 32;          // whose places a lane finds
+    static constexpr int kStepRows = 32 / (DP / 16);     // rows of which the warp's lanes take a chunk at once
+    static constexpr int kSteps = kWarpRows / kStepRows;
+    static constexpr int kRawTiles = 2, kRawBytes = kTilePos * DP;  // codes on their way
+    static constexpr int kBars = Sh::kTiles + kRawTiles * kRawBytes;
 };
 
 constexpr int kTile8Refs = 8;   // tiles whose powers are kept: more than the ring holds
@@ -56,24 +58,25 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
     return c;
 }
 
-// The warps that convert.  A tile begins at a multiple of 128 positions.
+// The warps that convert.  A tile begins at a multiple of 128 positions.  A lane reads back the chunks of codes
+// that it copied itself, so a warp waits for nobody's copies but its own.
 template <int DP, bool kTwo>
-__device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *ring, Tile8Bars &b, int tiles)
+__device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *ring, uint8_t *raw, Tile8Bars &b, int tiles)
 {
-    using Sh = TileShape<DP, kTwo>;
-    using S8 = Tile8Shape<DP, kTwo>;
-    constexpr int kOwn = S8::kOwn, kSteps = S8::kSteps, kStepRows = S8::kStepRows;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - Sh::kSoftmaxWarps, row0 = warp * S8::kRows;
+    using Sh = Tile8Shape<DP, kTwo>;
+    constexpr int kOwn = Sh::kOwn, kSteps = Sh::kSteps, kStepRows = Sh::kStepRows;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - Sh::kSoftmaxWarps, row0 = warp * Sh::kWarpRows;
     const int start = w.lo & ~127;
     const int32_t *pages = p.batch.table + w.s * p.batch.table_stride;
     // the lane's row and chunk of a step: 8 lanes write to every bank once
     const int step_row = DP == 128 ? ((lane >> 2) & 1) | (lane >> 4) << 1 : lane >> 2;
     const int chunk = DP == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
     const bool inside = chunk * 16 < p.d;
+    uint8_t *mine = raw + warp * kSteps * 512 + lane * 16;
 
-    int32_t page[kOwn], slot[kOwn];     // of the next tile's rows lane, lane + 32
-    int64_t off[kOwn], next_off[kOwn];  // their codes; -1: a row of zeros
-    uint32_t ke[kOwn], ve[kOwn];        // their exponents
+    int32_t page[kOwn], slot[kOwn];  // of a coming tile's rows lane, lane + 32; slot -1: nothing of it is seen
+    int64_t off[kOwn];               // their codes; -1: a row of zeros
+    uint32_t k_next[kOwn], v_next[kOwn];  // their exponents
     auto find = [&](int j) {
 #pragma unroll
         for (int i = 0; i < kOwn; i++) {
@@ -89,73 +92,80 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
     auto place = [&]() {
 #pragma unroll
         for (int i = 0; i < kOwn; i++) {
-            next_off[i] = -1;
-            ke[i] = ve[i] = 0;
+            off[i] = -1;
+            k_next[i] = v_next[i] = 0;
             if (slot[i] < 0)
                 continue;
             if ((uint32_t)page[i] >= p.cache.pages) {
                 raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
                 continue;
             }
-            next_off[i] = page[i] * p.cache.page_stride + slot[i] * p.cache.slot_stride + w.head * p.cache.head_stride;
+            off[i] = page[i] * p.cache.page_stride + slot[i] * p.cache.slot_stride + w.head * p.cache.head_stride;
             const int64_t x = exp_offset(p.exp, page[i], slot[i], w.head);
-            ke[i] = p.exp.k[x];
-            ve[i] = p.exp.v[x];
+            k_next[i] = p.exp.k[x];
+            v_next[i] = p.exp.v[x];
         }
     };
-    uint4 held[kSteps];
-    auto load = [&](const char *base, const int64_t *from, int i) {
-        const int64_t o = __shfl_sync(0xffffffffu, from[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
-        held[i] = make_uint4(0, 0, 0, 0);
-        if (o >= 0 && inside)
-            asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(held[i].x), "=r"(held[i].y), "=r"(held[i].z), "=r"(held[i].w)
-                         : "l"(base + o + chunk * 16));
-    };
-    auto store = [&](uint8_t *tile, const uint32_t *factor, int i) {
-        const uint32_t f = __shfl_sync(0xffffffffu, factor[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
-        const uint32_t in[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-        uint32_t x[8];
+    auto copy = [&](const char *base, int kv) {
+        uint8_t *to = mine + kv * Sh::kRawBytes;
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            x[2 * k] = hmul2(decode2((uint16_t)in[k]), f);
-            x[2 * k + 1] = hmul2(decode2((uint16_t)(in[k] >> 16)), f);
+        for (int i = 0; i < kSteps; i++) {
+            const int64_t o = __shfl_sync(0xffffffffu, off[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
+            const bool there = o >= 0 && inside;
+            tc::cp_async16(to + i * 512, base + (there ? o + chunk * 16 : 0), there);
         }
-        const int r = row0 + i * kStepRows + step_row, unit = 2 * (chunk & 3);
-        uint8_t *to = tile + (chunk >> 2) * Sh::kBlock + r * 128;
-        *reinterpret_cast<uint4 *>(to + ((unit ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<uint4 *>(to + (((unit + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // hands a tile over; after a wait that ran out the warps still meet at their barrier, but write nothing
+    auto convert = [&](uint8_t *tile, const uint32_t *factor, int kv) {
+#pragma unroll
+        for (int i = 0; i < kSteps; i++) {
+            const uint32_t f = __shfl_sync(0xffffffffu, factor[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
+            const uint4 c = *reinterpret_cast<const uint4 *>(mine + kv * Sh::kRawBytes + i * 512);
+            const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                x[2 * k] = hmul2(decode2((uint16_t)in[k]), f);
+                x[2 * k + 1] = hmul2(decode2((uint16_t)(in[k] >> 16)), f);
+            }
+            const int r = row0 + i * kStepRows + step_row, unit = 2 * (chunk & 3);
+            uint8_t *to = tile + (chunk >> 2) * Sh::kBlock + r * 128;
+            *reinterpret_cast<uint4 *>(to + ((unit ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4 *>(to + (((unit + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+    };
+    // after a wait that ran out the warps still meet at their barrier, but hand nothing over
     bool dead = false;
-    auto begin = [&](int i) {
+    auto hand_over = [&](int i, const uint32_t *factor) {
         if (!dead && i >= Sh::kSlots &&
             !warp_wait(&b.empty[i % Sh::kSlots], (i / Sh::kSlots - 1) & 1, &b.aborted, p.wait_polls))
             dead = true;
-        return ring + i % Sh::kSlots * Sh::kTileBytes;
-    };
-    auto end = [&](int i) {
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0 && !dead)
-            tc::mbar_arrive(&b.full[i % Sh::kSlots]);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (!dead) {
+            convert(ring + i % Sh::kSlots * Sh::kTileBytes, factor, i & 1);
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(&b.full[i % Sh::kSlots]);
+        }
     };
 
     find(0);
     place();
-#pragma unroll
-    for (int i = 0; i < kSteps; i++)
-        load(p.cache.k, next_off, i);
+    copy(p.cache.k, 0);
+    copy(p.cache.v, 1);
+    find(1);
     int v_ref = 0;
 #pragma unroll 1
     for (int j = 0; j < tiles; j++) {
         // what the tile's codes are relative to
-        uint32_t k_top = 0, v_top = 0;
+        uint32_t kf[kOwn], vf[kOwn], k_top = 0, v_top = 0;
 #pragma unroll
         for (int i = 0; i < kOwn; i++) {
-            off[i] = next_off[i];
-            k_top = max(k_top, ke[i]);
-            v_top = max(v_top, ve[i]);
+            kf[i] = k_next[i];
+            vf[i] = v_next[i];
+            k_top = max(k_top, kf[i]);
+            v_top = max(v_top, vf[i]);
         }
         k_top = __reduce_max_sync(0xffffffffu, k_top);
         v_top = __reduce_max_sync(0xffffffffu, v_top);
@@ -163,10 +173,10 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
             b.warp_ref[j & 1][warp][0] = (int)k_top;
             b.warp_ref[j & 1][warp][1] = (int)v_top;
         }
-        tc::named_sync(kConvertBarrier, S8::kWarps * 32);
+        tc::named_sync(kConvertBarrier, Sh::kWarps * 32);
         int k_ref = 0;
 #pragma unroll
-        for (int i = 0; i < S8::kWarps; i++) {
+        for (int i = 0; i < Sh::kWarps; i++) {
             k_ref = max(k_ref, b.warp_ref[j & 1][i][0]);
             v_ref = max(v_ref, b.warp_ref[j & 1][i][1]);
         }
@@ -174,31 +184,19 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
             b.k_ref[j % kTile8Refs] = k_ref;
             b.v_ref[j % kTile8Refs] = v_ref;
         }
-        uint32_t kf[kOwn], vf[kOwn];
 #pragma unroll
         for (int i = 0; i < kOwn; i++) {
-            kf[i] = relative_power((int)ke[i] - k_ref);
-            vf[i] = relative_power((int)ve[i] - v_ref);
+            kf[i] = relative_power((int)kf[i] - k_ref);
+            vf[i] = relative_power((int)vf[i] - v_ref);
         }
-        find(j + 1);
-        uint8_t *tile = begin(2 * j);
-#pragma unroll
-        for (int i = 0; i < kSteps; i++) {
-            if (!dead)
-                store(tile, kf, i);
-            load(p.cache.v, off, i);
-        }
-        end(2 * j);
         place();
-        tile = begin(2 * j + 1);
-#pragma unroll
-        for (int i = 0; i < kSteps; i++) {
-            if (!dead)
-                store(tile, vf, i);
-            load(p.cache.k, next_off, i);
-        }
-        end(2 * j + 1);
+        find(j + 2);
+        hand_over(2 * j, kf);
+        copy(p.cache.k, 0);
+        hand_over(2 * j + 1, vf);
+        copy(p.cache.v, 1);
     }
+    tc::cp_async_wait_all();
 }
 
 // A softmax thread's half of its query row, as fp16 in the swizzled tile; returns what undoes the row's lifting.
@@ -206,7 +204,7 @@ template <typename T, int DP, bool kTwo>
 __device__ __forceinline__ float tile8_query(const AttnParams &p, const AttnWork &w, uint8_t *sq, Tile8Bars &b, int t,
                                              int half, int in, int pair)
 {
-    using Sh = TileShape<DP, kTwo>;
+    using Sh = Tile8Shape<DP, kTwo>;
     constexpr int kChunks = DP / 16;  // of 8 elements, of half a row
     const int r = t * 128 + in, row = w.row0 + r, token = row / p.group;
     const bool mine = r < w.rows;
@@ -265,7 +263,7 @@ __device__ __forceinline__ float tile8_query(const AttnParams &p, const AttnWork
 template <typename T, int DP, bool kTwo>
 __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq, Tile8Bars &b, int tiles)
 {
-    using Sh = TileShape<DP, kTwo>;
+    using Sh = Tile8Shape<DP, kTwo>;
     constexpr int kHalf = kTilePos / 2, kCols = DP / 2;  // scores, output columns of a thread
     const int warp = threadIdx.x >> 5, t = warp >> 3, half = (warp >> 2) & 1;
     const int in = (warp & 3) * 32 + (threadIdx.x & 31), r = t * 128 + in, pair = 1 + t * 4 + (warp & 3);
@@ -285,24 +283,30 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
         tc::mbar_wait(&b.s_full[t], j & 1, &b.aborted, p.wait_polls);
         __syncwarp();
         tc::fence_after_sync();
-        uint32_t s[kHalf];
+        // half of the thread's scores at a time, read twice: all of them and the rest want 96 registers, a fifth more
+        uint32_t s[32];
         const int at = (w.lo & ~127) + j * kTilePos + half * kHalf;
-        tc::tmem_ld32_async(s_at, s);
-        tc::tmem_ld32_async(s_at + 32, s + 32);
+        const bool whole = __all_sync(0xffffffffu, at >= lo && at + kHalf <= hi);
+        auto scores = [&](int c) {
+            tc::tmem_ld32_async(s_at + c, s);
+            tc::tmem_ld_wait(s);
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 32; i++)
+                    s[i] = at + c + i >= lo && at + c + i < hi ? s[i] : 0xff800000u;
+            }
+        };
         const int k_ref = b.k_ref[j % kTile8Refs], now_ref = b.v_ref[j % kTile8Refs];
         // never 0: a masked score is -infinity
         const float scale_log2 = fmaxf(row_scale * exp_power((uint32_t)max(k_ref - kTile8Lift, 0)), 1.2e-38f);
-        tc::tmem_ld_wait(s);
-        tc::tmem_ld_wait(s + 32);
-        if (!__all_sync(0xffffffffu, at >= lo && at + kHalf <= hi)) {
-#pragma unroll
-            for (int i = 0; i < kHalf; i++)
-                s[i] = at + i >= lo && at + i < hi ? s[i] : 0xff800000u;
-        }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kHalf; i += 2)
-            top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+        for (int c = 0; c < kHalf; c += 32) {
+            scores(kHalf - 32 - c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+                top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+        }
         float now = __fmul_ru(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale_log2);
         b.agree[t][half][in] = now;
         tc::named_sync(pair, 64);
@@ -329,19 +333,23 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
         const float lift = __fsub_rd(kTileLift<__half>, m == -INFINITY ? 0.f : m);
         const float2 scale = make_float2(scale_log2, scale_log2), off = make_float2(lift, lift);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t packed[32];
 #pragma unroll
         for (int c = 0; c < kHalf / 32; c++) {
-            uint32_t packed[16];
+            if (c > 0)
+                scores(c * 32);
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                const int k = c * 32 + 2 * i;
+                const int k = 2 * i;
                 const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale, off);
                 const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                 sum[i & 1] = __fadd2_rn(sum[i & 1], e);
-                packed[i] = pack2<__half>(e.x, e.y);
+                packed[c * 16 + i] = pack2<__half>(e.x, e.y);
             }
-            tc::tmem_st16(p_at + c * 16, packed);
         }
+        tc::named_sync(pair, 64);
+        tc::tmem_st16(p_at, packed);
+        tc::tmem_st16(p_at + 16, packed + 16);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::tmem_st_wait();
         tc::fence_before_sync();
@@ -370,12 +378,11 @@ template <typename T, int DP, bool kTwo>
 __global__ void __launch_bounds__(Tile8Shape<DP, kTwo>::kThreads, kTwo ? 1 : 2)
 kv8_attn_tile_kernel(const __grid_constant__ AttnParams p)
 {
-    using Sh = TileShape<DP, kTwo>;
-    using S8 = Tile8Shape<DP, kTwo>;
-    constexpr int kLast = S8::kThreads / 32 - 1;
+    using Sh = Tile8Shape<DP, kTwo>;
+    constexpr int kLast = Sh::kMmaWarp;
     extern __shared__ __align__(1024) uint8_t sq[];  // query tiles, the ring, then the rest: all that an SM has
     uint8_t *ring = sq + Sh::kRows / 128 * Sh::kTileBytes;
-    Tile8Bars &b = *reinterpret_cast<Tile8Bars *>(sq + Sh::kTiles);
+    Tile8Bars &b = *reinterpret_cast<Tile8Bars *>(sq + Sh::kBars);
     const int warp = threadIdx.x >> 5;
     AttnWork w;
     if (!tile_work(p, reinterpret_cast<int *>(sq), w))
@@ -384,7 +391,7 @@ kv8_attn_tile_kernel(const __grid_constant__ AttnParams p)
     const bool two = kTwo && w.rows > 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kSlots; i++) {
-            tc::mbar_init(&b.full[i], S8::kWarps);
+            tc::mbar_init(&b.full[i], Sh::kWarps);
             tc::mbar_init(&b.empty[i], 1);
         }
         tc::mbar_init(&b.q_full, two ? 16 : 8);  // the softmax's warps
@@ -407,9 +414,9 @@ kv8_attn_tile_kernel(const __grid_constant__ AttnParams p)
             tile8_softmax<T, DP, kTwo>(p, w, sq, b, tiles);
     } else if (warp < kLast) {
         if (tiles > 0)
-            tile8_convert<DP, kTwo>(p, w, ring, b, tiles);
+            tile8_convert<DP, kTwo>(p, w, ring, sq + Sh::kTiles, b, tiles);
     } else if (tiles > 0) {
-        tile_mma<__half, DP, kTwo>(sq, ring, b, tiles, two, p.wait_polls);
+        tile_mma<__half, DP, kTwo, typename Sh::Sh>(sq, ring, b, tiles, two, p.wait_polls);
         __syncwarp();
     }
     tc::fence_before_sync();
@@ -432,8 +439,8 @@ kv8_attn_tile_kernel(const __grid_constant__ AttnParams p)
 template <typename T, int DP, bool kTwo>
 static int launch_tile8(const AttnParams &p, int64_t ctas, cudaStream_t st)
 {
-    constexpr int smem = TileShape<DP, kTwo>::kTiles + sizeof(Tile8Bars);
-    static_assert(smem <= 232448, "an SM's shared memory");
+    constexpr int smem = Tile8Shape<DP, kTwo>::kBars + sizeof(Tile8Bars);
+    static_assert(smem <= (kTwo ? 232448 : 115200), "an SM's shared memory");
     static std::atomic<unsigned long long> done{0};
     const int s = allow_dynamic_smem((const void *)kv8_attn_tile_kernel<T, DP, kTwo>, smem, &done);
     if (s != DLRM_OK)

@@ -12,8 +12,8 @@
 // token.  So there is one kernel of one CTA for short steps; for longer ones
 // every CTA takes a run of tokens and sums up the sequences before it by itself
 // (16 bytes a sequence from L2, which costs less than a second kernel that waits for
-// the first), and a last CTA in a launch of its own writes what is in place:
-// lengths and the ring's state, which the others read.
+// the first).  Where lengths or the ring's state, which all CTAs read, are written in place,
+// a launch of its own does that afterwards.
 #include "history.cuh"
 
 namespace dlrm {
@@ -52,7 +52,7 @@ __device__ __forceinline__ ReserveSums shfl_up(const ReserveSums &x, int o)
 }
 
 // kTokens: this launch writes slots, positions, table entries and the ring;
-// kSequences: offsets, lengths and the state (one CTA).
+// kSequences: its first CTA writes offsets, lengths and the state.
 template <bool kTokens, bool kSequences>
 __global__ void __launch_bounds__(kResThreads)
 kv_reserve_kernel(const __grid_constant__ ReserveParams p)
@@ -75,11 +75,14 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
         const uint64_t at = from + (uint64_t)k;
         return at >= (uint64_t)p.pages ? at - (uint64_t)p.pages : at;
     };
+    // pages of so many tokens, at most 2^30
+    auto pages_of = [&](int tokens) { return (int)p.page.div((uint32_t)tokens + p.page.d - 1); };
     const int64_t slice = (p.n + gridDim.x - 1) / gridDim.x;
     const int64_t t0 = min(blockIdx.x * slice, p.n), t1 = min(t0 + slice, p.n);
     ReserveSums base = {0, 0, 0};
     int64_t taken = 0;  // this thread's largest granted sum
-    if (kSequences && threadIdx.x == 0 && !sound)
+    const bool sequences = kSequences && blockIdx.x == 0;
+    if (sequences && threadIdx.x == 0 && !sound)
         raise_flag(p.err, DLRM_FLAG_BAD_OFFSETS);
     for (int64_t c0 = 0; c0 < p.S; c0 += kResChunk) {
         const int64_t s0 = c0 + threadIdx.x * kResItems;
@@ -95,10 +98,10 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
             take[i] = count < 0 ? 0 : min(count, (int64_t)1 << 31);
             const bool stored = len[i] <= p.capacity;
             fits[i] = !leaves[i] && stored && take[i] <= p.capacity - len[i];
-            const int64_t held = stored ? (len[i] + p.page.d - 1) / p.page.d : 0;
-            need[i] = fits[i] ? (len[i] + take[i] + p.page.d - 1) / p.page.d - held : 0;
+            const int64_t held = stored ? pages_of((int)len[i]) : 0;
+            need[i] = fits[i] ? pages_of((int)(len[i] + take[i])) - held : 0;
             gone[i] = leaves[i] ? held : 0;
-            if (kSequences && !stored && leaves[i])
+            if (sequences && !stored && leaves[i])
                 raise_flag(p.err, DLRM_FLAG_BAD_OFFSETS);
             mine = mine + ReserveSums{take[i], need[i], gone[i]};
         }
@@ -142,7 +145,7 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
                 s_length[in] = (int)min(len[i], (int64_t)0x7fffffff);
                 s_granted[in] = leaves[i] ? -1 : (granted ? 1 : 0);
             }
-            if (kSequences && s0 + i < p.S) {
+            if (sequences && s0 + i < p.S) {
                 p.offsets[s0 + i] = base.tokens + at.tokens;
                 p.new_lengths[s0 + i] = leaves[i] ? 0 : (granted ? len[i] + take[i] : ~len[i]);
                 if (!granted && !leaves[i])
@@ -154,43 +157,41 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
             if (threadIdx.x == 0)
                 s_tokens[kResChunk] = (uint32_t)min(all.tokens, (int64_t)0xffffffffu);
             __syncthreads();
-            // pages of those who leave, a warp a sequence, every CTA its share of them
             const int here = (int)min(p.S - c0, (int64_t)kResChunk);
-            for (int in = blockIdx.x + warp * gridDim.x; in < here; in += (kResThreads / 32) * gridDim.x) {
-                const int length = s_length[in];
-                if (s_granted[in] >= 0 || length > p.capacity)
-                    continue;
-                const int pages = (int)((length + p.page.d - 1) / p.page.d);
-                const int32_t *row = p.table + (c0 + in) * p.table_stride;
-                const int64_t k0 = base.gone + s_gone[in];
-                for (int k = lane; k < pages; k += 32) {
-                    if (!sound || avail + k0 + k >= p.pages) {
-                        raise_flag(p.err, DLRM_FLAG_CAPACITY);
-                        continue;
-                    }
-                    const int32_t page = row[k];
-                    if ((uint32_t)page >= (uint64_t)p.pages)
-                        raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
-                    p.ring[place(ring_tail, k0 + k)] = page;
+            // the last of the chunk's sequences whose sum is at most x: those that add nothing come before
+            auto owner = [&](const auto *sums, auto x) {
+                int lo = 0, hi = here;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sums[mid] <= x)
+                        lo = mid;
+                    else
+                        hi = mid;
                 }
+                return lo;
+            };
+            // pages of those who leave, shared out over the CTAs
+            for (int64_t k = (int64_t)blockIdx.x * kResThreads + threadIdx.x; k < all.gone; k += (int64_t)gridDim.x * kResThreads) {
+                if (!sound || avail + base.gone + k >= p.pages) {
+                    raise_flag(p.err, DLRM_FLAG_CAPACITY);
+                    break;
+                }
+                const int in = owner(s_gone, (int)k);
+                const int32_t page = p.table[(c0 + in) * p.table_stride + k - s_gone[in]];
+                if ((uint32_t)page >= (uint64_t)p.pages)
+                    raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+                p.ring[place(ring_tail, base.gone + k)] = page;
             }
             // this CTA's tokens among the chunk's
             const int64_t from = max(t0, base.tokens), to = min(t1, base.tokens + all.tokens);
             for (int64_t t = from + threadIdx.x; t < to; t += kResThreads) {
                 const uint32_t x = (uint32_t)(t - base.tokens);
-                int lo = 0, hi = here;  // the last sequence that starts at or before x: those of no tokens come before
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s_tokens[mid] <= x)
-                        lo = mid;
-                    else
-                        hi = mid;
-                }
+                const int lo = owner(s_tokens, x);
                 int64_t slot = -1, position = -1;
                 if (s_granted[lo] > 0) {
                     const int length = s_length[lo], at_token = length + (int)(x - s_tokens[lo]);
                     const int number = (int)p.page.div((uint32_t)at_token), in_page = at_token - number * (int)p.page.d;
-                    const int held = (int)((length + p.page.d - 1) / p.page.d);
+                    const int held = pages_of(length);
                     int32_t *entry = p.table + (c0 + lo) * p.table_stride + number;
                     int32_t page;
                     if (number < held) {
@@ -214,7 +215,7 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
         }
         base = base + all;
     }
-    if (kSequences) {
+    if (sequences) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
@@ -240,13 +241,15 @@ int launch_kv_reserve(const int64_t *counts, const int64_t *lengths, int64_t S, 
     const ReserveParams p = {counts, lengths, S, n, table, table_stride, table_width * page_size,
                              FastDiv::make((uint32_t)page_size), ring, pages, state, new_state, offsets, new_lengths,
                              slots, positions, err};
-    if (n <= kResOneCta) {
-        kv_reserve_kernel<true, true><<<1, kResThreads, 0, st>>>(p);
+    const int64_t all = (n + kResThreads - 1) / kResThreads;
+    const unsigned ctas = n <= kResOneCta ? 1u : (unsigned)(all < kResMaxCtas ? all : kResMaxCtas);
+    const bool in_place = new_lengths == lengths || new_state == state;
+    if (ctas == 1 || !in_place) {
+        kv_reserve_kernel<true, true><<<ctas, kResThreads, 0, st>>>(p);
         count_launch(st);
         return launch_status();
     }
-    const int64_t ctas = (n + kResThreads - 1) / kResThreads;
-    kv_reserve_kernel<true, false><<<(unsigned)(ctas < kResMaxCtas ? ctas : kResMaxCtas), kResThreads, 0, st>>>(p);
+    kv_reserve_kernel<true, false><<<ctas, kResThreads, 0, st>>>(p);
     count_launch(st);
     kv_reserve_kernel<false, true><<<1, kResThreads, 0, st>>>(p);
     count_launch(st);

@@ -22,14 +22,14 @@ template <typename T>
 constexpr float kTileLift = kWeightTop<T> > 0.f ? kWeightTop<T> - kTileSlack<T> : 0.f;
 
 // kTwo: two query tiles of a CTA that has the SM, else one, and two CTAs share the SM.
-template <int DP, bool kTwo>
+template <int DP, bool kTwo, int kRing = DP == 128 || !kTwo ? 5 : 8>
 struct TileShape {
     static constexpr int kRows = kTwo ? 256 : 128;
     static constexpr int kSoftmaxThreads = 2 * kRows, kSoftmaxWarps = kSoftmaxThreads / 32;
     static constexpr int kScoreCols = kRows, kTmem = 2 * kRows;  // tensor-memory columns: scores, all
     __host__ __device__ static constexpr int threads(bool bulk) { return kSoftmaxThreads + copy_threads(bulk) + 32; }
     static constexpr int kTileBytes = kTilePos * DP * 2;  // of keys or values; a query tile too
-    static constexpr int kSlots = DP == 128 || !kTwo ? 5 : 8;
+    static constexpr int kSlots = kRing;
     static constexpr int kTiles = kRows / 128 * kTileBytes + kSlots * kTileBytes;
     static constexpr int kBlock = kTilePos * 128;         // bytes between 64-column blocks of a tile
     static constexpr int kChunks = DP / 8;                // 16-byte chunks of a row
@@ -49,10 +49,9 @@ struct TileBars {
     float agree[2][2][128];  // [query tile][half][row]: a maximum of half a row's scores; at the end its sum
 };
 
-template <typename T, int DP, bool kTwo>
+template <typename T, int DP, bool kTwo, typename Sh = TileShape<DP, kTwo>>
 __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, bool two, int polls)
 {
-    using Sh = TileShape<DP, kTwo>;
     constexpr int kType = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
     constexpr uint32_t kScores = tc::f16_idesc(kType, 128, kTilePos, false), kOut = tc::f16_idesc(kType, 128, DP, true);
     // all lanes run this; one issues.  Descriptors of a later place are the first plus its distance / 16.
