@@ -17,6 +17,14 @@ __device__ __forceinline__ uint32_t decode2(uint16_t codes)
     return h;
 }
 
+// The same of a word of four.
+__device__ __forceinline__ void decode4(uint32_t codes, uint32_t &lower, uint32_t &upper)
+{
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi; }"
+        : "=r"(lower), "=r"(upper)
+        : "r"(codes));
+}
+
 __device__ __forceinline__ float2 decode2_f32(uint16_t codes) { return unpack2<__half>(decode2(codes)); }
 
 // Two values as codes, x in the lower byte: to nearest, ties to even, beyond 448 the largest.

@@ -31,6 +31,11 @@
 
 namespace dlrm {
 
+// log2 of the growth of a maximum that is let pass before the output is scaled down, and of what weights are
+// lifted by: at most 2^15 in all, fp16's range.  (A tile of 16 rows sees some maximum grow in almost every block of
+// a short history: 96 users with up to 3000, 12 rows of 256: 79 us with a slack of 0, XX.)
+constexpr float kFew8Slack = 4.f, kFew8Lift = kWeightTop<__half> - kFew8Slack;
+
 template <typename T, int DP, int kGroups>
 struct Few8Shape {
     static constexpr bool kWide = sizeof(T) == 4;
@@ -48,9 +53,19 @@ struct Few8Shape {
     static constexpr int kCtas = kResident * kFewSms;
     static constexpr int kMerge = kOut < 32 ? kOut : 32;
     static constexpr int kSmem = 1024 + kFewWarps * kStages * kStageBytes + 2 * kMerge * 32 * 4;
-    static constexpr int kKeyBox = MG * 64, kValueBox = MG * 8 * VB;  // bytes of a column of a group's keys, values
-    static constexpr int kGroupBytes = KG * kKeyBox + VS * kValueBox;
-    static_assert(NB * kGroupBytes == kStageBytes && kCtas <= kFewMaxCtas, "a stage holds whole groups");
+    // a stage: columns of kWidth bytes of the block's keys, then of its values, each TB rows, swizzled over its width
+    static constexpr int kWidth = DP >= 128 ? 128 : 64, kColumns = DP / kWidth, kColumnBytes = TB * kWidth;
+    static_assert(2 * kColumns * kColumnBytes == kStageBytes && kCtas <= kFewMaxCtas, "a stage holds a block");
+
+    // place of 16-byte unit u of row r in a column
+    __device__ __forceinline__ static int at(int r, int u)
+    {
+        return r * kWidth + ((u ^ (kWidth == 128 ? r & 7 : r >> 1 & 3)) << 4);
+    }
+    // the 16 elements that a lane of quarter q takes of chunk i of a row: its column, and unit in it.  (Which are
+    // summed together is free; so 8 lanes of a read meet no bank twice.)
+    __device__ __forceinline__ static constexpr int column(int i) { return kWidth == 128 ? i >> 1 : 0; }
+    __device__ __forceinline__ static constexpr int unit(int i, int q) { return kWidth == 128 ? 2 * q + (i & 1) : q; }
 
     // the row of a lane's statistic i, and the statistic of its output register o
     __device__ __forceinline__ static int row(int i, int q) { return 2 * q + (i & 1) + 8 * (i >> 1); }
@@ -86,7 +101,6 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     using Sh = Few8Shape<T, DP, kGroups>;
     constexpr int KG = Sh::KG, VS = Sh::VS, VB = Sh::VB, NB = Sh::NB, TB = Sh::TB, UT = Sh::UT, kStages = Sh::kStages;
     constexpr int kParts = Sh::kWide ? 2 : 1;  // of a query
-    constexpr float kTop = kWeightTop<__half>;
     extern __shared__ uint8_t raw[];
     __shared__ float s_m[kFewWarps][kFewRows], s_l[kFewWarps][kFewRows];
     __shared__ uint64_t bars[kFewWarps][kStages];
@@ -100,7 +114,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     FewItem it;  // of the unit being computed; `is`: of the unit whose addresses come next
     int units, quota = 0;  // of this CTA; the items' are counted from its first
     if (p.splits > 1) {
-        const bool any = few_share(p, it, units, quota, UT, busy);
+        const bool any = few_share(p, it, units, quota, UT, TB, busy);
         if (threadIdx.x == 0)
             p.joins[blockIdx.x].rows = 0;  // until an item is left unfinished
         if (!any)
@@ -108,7 +122,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     } else {
         const int64_t most = (p.max_new * p.group + kFewRows - 1) / kFewRows, of = blockIdx.x / most;
         const int64_t s = of / p.cache.heads;
-        if (!read_sequence(p.batch, s, p.max_new, p.max_len, it.seq, p.err) || !few_sequence(p, it, s, 0, UT))
+        if (!read_sequence(p.batch, s, p.max_new, p.max_len, it.seq, p.err) || !few_sequence(p, it, s, 0, UT, TB))
             return;
         it.head = (int)(of - s * p.cache.heads);
         it.tile = (int)(blockIdx.x - of * most);
@@ -121,11 +135,8 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     // A lane finds the page and slot of one token of the warp's block (its exponents are the lane's to fetch), and
     // copies one box, whose place the lane of its first token knows; a box that no query sees anything of is
     // outside the map: zeros.
-    const int parts = Sh::MG / maps.rows, boxes = parts * (KG + VS);  // of a group: its keys' columns, then its values'
-    const int my_group = lane / boxes, my_box = lane - my_group * boxes;
-    const int my_part = my_box % parts, my_column = my_box / parts;
-    const int my_first = (my_group * Sh::MG + my_part * maps.rows) & 31;
-    const bool copies = my_group < NB;
+    const int parts = TB / maps.rows, my_column = lane / parts, my_first = (lane - my_column * parts) * maps.rows;
+    const bool copies = my_column < 2 * Sh::kColumns;
     int page_id = -1, page_slot = 0;
     bool token_seen = false;
     auto find = [&](int u) {
@@ -134,7 +145,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         if (u >= units)
             return;
         while (u >= is.last)
-            few_next(p, is, UT, busy);
+            few_next(p, is, UT, TB, busy);
         const int at = is.lo + (u - is.first) * UT + warp * TB + (lane & (TB - 1)), box = at & -maps.rows;
         if (box < is.hi && box + maps.rows > is.lo_seen) {
             const uint32_t page = p.cache.page.div((uint32_t)at);
@@ -158,14 +169,10 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             const int page = __shfl_sync(0xffffffffu, sound ? page_id : -1, my_first);
             const int slot = __shfl_sync(0xffffffffu, page_slot, my_first);
             if (copies) {
-                const uint32_t to = ring_at + stage * Sh::kStageBytes + my_group * Sh::kGroupBytes;
-                if (my_column < KG)
-                    tc::tma_load_4d(to + my_column * Sh::kKeyBox + my_part * maps.rows * 64, &maps.k, my_column * 64,
-                                    slot, is.head, page, &bars[warp][stage]);
-                else
-                    tc::tma_load_4d(to + KG * Sh::kKeyBox + (my_column - KG) * Sh::kValueBox +
-                                        my_part * maps.rows * 8 * VB,
-                                    &maps.v, (my_column - KG) * 8 * VB, slot, is.head, page, &bars[warp][stage]);
+                const bool value = my_column >= Sh::kColumns;
+                tc::tma_load_4d(ring_at + stage * Sh::kStageBytes + my_column * Sh::kColumnBytes + my_first * Sh::kWidth,
+                                value ? &maps.v : &maps.k, (my_column - (value ? Sh::kColumns : 0)) * Sh::kWidth, slot,
+                                is.head, page, &bars[warp][stage]);
             }
             if (token_seen && sound) {
                 const int64_t x = exp_offset(p.exp, page_id, page_slot, is.head);
@@ -214,7 +221,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 for (int i = 0; i < KG; i++)
 #pragma unroll
                     for (int j = 0; j < 2; j++) {
-                        const int e = (4 * i + q) * 16 + 8 * j;
+                        const int e = Sh::column(i) * Sh::kWidth + Sh::unit(i, q) * 16 + 8 * j;
                         x[i][j].load(src + e, r < rows && e < p.d);
                         if constexpr (!std::is_same<T, __half>::value)
 #pragma unroll
@@ -295,14 +302,12 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 uint32_t a[4][4];  // of the chunk's four steps
 #pragma unroll
                 for (int t = 0; t < 2; t++) {
-                    const uint4 k = *reinterpret_cast<const uint4 *>(block + nb * Sh::kGroupBytes + i * Sh::kKeyBox +
-                                                                     (t * 8 + g) * 64 + q * 16);
+                    const uint4 k = *reinterpret_cast<const uint4 *>(
+                        block + Sh::column(i) * Sh::kColumnBytes + Sh::at(nb * Sh::MG + t * 8 + g, Sh::unit(i, q)));
                     const uint32_t w[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        a[e][t] = decode2((uint16_t)w[e]);
-                        a[e][t + 2] = decode2((uint16_t)(w[e] >> 16));
-                    }
+                    for (int e = 0; e < 4; e++)
+                        decode4(w[e], a[e][t], a[e][t + 2]);
                 }
 #pragma unroll
                 for (int n = 0; n < kGroups; n++) {
@@ -350,8 +355,16 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                         const int pos = at + nb * Sh::MG + g + 8 * (j >> 1), i = stat_of(x, j);
                         s[nb][x][j] = pos >= lo[i] && pos < hi[i] ? s[nb][x][j] : -INFINITY;
                     }
+            // values that no query sees may be anything: a zero weight would not do
+            uint8_t *values = ring + stage * Sh::kStageBytes + Sh::kColumns * Sh::kColumnBytes;
+            if (lane < TB && (at + lane < it.lo_seen || at + lane >= it.hi))
+                for (int c = 0; c < 2 * DP / 32; c++)
+                    *reinterpret_cast<uint4 *>(values + c * 16 / Sh::kWidth * Sh::kColumnBytes + lane * Sh::kWidth +
+                                               c * 16 % Sh::kWidth) = make_uint4(0, 0, 0, 0);
+            tc::fence_async_smem();  // the next copies come after
+            __syncwarp();
         }
-        float top[Sh::kStats], base[Sh::kStats], off[Sh::kStats];
+        float top[Sh::kStats], off[Sh::kStats];
         bool moved = new_exp > top_exp;
 #pragma unroll
         for (int i = 0; i < Sh::kStats; i++) {
@@ -367,26 +380,28 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
 #pragma unroll
             for (int step = 4; step < 32; step *= 2)
                 top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], step));
-            top[i] = fmaxf(__fmul_ru(top[i], scale[i]), m[i]);
-            base[i] = top[i] == -INFINITY ? 0.f : top[i];
-            off[i] = __fsub_rd(kTop, base[i]);
-            moved |= top[i] > m[i];
+            top[i] = __fmul_ru(top[i], scale[i]);
+            moved |= top[i] > m[i] + kFew8Slack;
         }
         if (__any_sync(0xffffffffu, moved)) {
             const float down = __uint_as_float((uint32_t)max(127 + top_exp - new_exp, 0) << 23);
             float f[Sh::kStats];
 #pragma unroll
             for (int i = 0; i < Sh::kStats; i++) {
-                f[i] = exp2_approx(m[i] - base[i]);
+                const float next = fmaxf(top[i], m[i]);
+                f[i] = exp2_approx(m[i] - (next == -INFINITY ? 0.f : next));
                 l[i] *= f[i];
                 f[i] *= down;
-                m[i] = top[i];
+                m[i] = next;
             }
 #pragma unroll
             for (int i = 0; i < Sh::kOut; i++)
                 o[i] *= f[Sh::stat(i)];
             top_exp = new_exp;
         }
+#pragma unroll
+        for (int i = 0; i < Sh::kStats; i++)
+            off[i] = __fsub_rd(kFew8Lift, m[i] == -INFINITY ? 0.f : m[i]);
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
 #pragma unroll
@@ -417,22 +432,14 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 uint32_t v[4][VB / 4];  // the lane's columns of tokens 2q, 2q + 1 and of those + 8
 #pragma unroll
                 for (int t = 0; t < 4; t++) {
-                    const int row = 2 * q + (t & 1) + 8 * (t >> 1);
-                    const uint8_t *from = block + nb * Sh::kGroupBytes + KG * Sh::kKeyBox + i * Sh::kValueBox;
+                    const int row = nb * Sh::MG + 2 * q + (t & 1) + 8 * (t >> 1);
+                    const uint8_t *from = block + (Sh::kColumns + i) * Sh::kColumnBytes;
                     if constexpr (VB == 16) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(from + row * 128 + ((g ^ (row & 7)) << 4));
+                        const uint4 x = *reinterpret_cast<const uint4 *>(from + Sh::at(row, g));
                         v[t][0] = x.x, v[t][1] = x.y, v[t][2] = x.z, v[t][3] = x.w;
                     } else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(from + row * 64 + (((g >> 1) ^ q) << 4) + (g & 1) * 8);
+                        const uint2 x = *reinterpret_cast<const uint2 *>(from + Sh::at(row, g >> 1) + (g & 1) * 8);
                         v[t][0] = x.x, v[t][1] = x.y;
-                    }
-                    // a box's rows that no query sees may hold anything: a zero weight would not do
-                    if (edge) {
-                        const int pos = at + nb * Sh::MG + row;
-                        if (pos < it.lo_seen || pos >= it.hi)
-#pragma unroll
-                            for (int j = 0; j < VB / 4; j++)
-                                v[t][j] = 0;
                     }
                 }
 #pragma unroll
@@ -441,8 +448,9 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     for (int c = 0; c < 2; c++) {  // columns 4j + 2c and the next of the lane's
                         const uint32_t x = __byte_perm(v[0][j], v[1][j], c ? 0x7362 : 0x5140);
                         const uint32_t y = __byte_perm(v[2][j], v[3][j], c ? 0x7362 : 0x5140);
-                        const uint32_t a[4] = {decode2((uint16_t)x), decode2((uint16_t)(x >> 16)), decode2((uint16_t)y),
-                                               decode2((uint16_t)(y >> 16))};
+                        uint32_t a[4];
+                        decode4(x, a[0], a[1]);
+                        decode4(y, a[2], a[3]);
 #pragma unroll
                         for (int n = 0; n < kGroups; n++) {
                             float *sum = o + ((n * VS + i) * Sh::kOutMmas + 2 * j + c) * 4;
@@ -504,7 +512,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 sum = fmaf(s_l[w][r], exp2_approx(s_m[w][r] - b), sum);
             // no weight at all: nothing is seen; a sum that is not a number stays one
             f[i] = sum == 0.f ? 0.f : exp2_approx(m[i] - b) / sum * power;
-            lse[i] = sum == 0.f ? -INFINITY : all + (log2f(sum) - kTop);
+            lse[i] = sum == 0.f ? -INFINITY : all + (log2f(sum) - kFew8Lift);
         }
 #pragma unroll
         for (int i = 0; i < Sh::kOut; i++)
@@ -584,7 +592,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         fresh = true;
         first_item = false;
         if (u + 1 < units)
-            few_next(p, it, UT, busy);
+            few_next(p, it, UT, TB, busy);
     }
     if (dead) {
         // that unit and those copied ahead of it may still be in flight: none may be when the memory is given back
@@ -606,18 +614,17 @@ static bool few8_maps(const AttnParams &p, int rows, FewMaps &m)
     const cuuint64_t dims[4] = {(cuuint64_t)p.d, p.cache.page.d, (cuuint64_t)p.cache.heads, p.cache.pages};
     const cuuint64_t strides[3] = {(cuuint64_t)p.cache.slot_stride, (cuuint64_t)p.cache.head_stride,
                                    (cuuint64_t)p.cache.page_stride};
-    const cuuint32_t k_box[4] = {64, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
-    const cuuint32_t v_box[4] = {p.d > 64 ? 128u : 64u, (cuuint32_t)rows, 1, 1};
+    const cuuint32_t box[4] = {p.d > 64 ? 128u : 64u, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUtensorMapSwizzle swizzle = p.d > 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     // lines of 256 bytes where a head's rows fill them; else they would be its neighbours'
     const CUtensorMapL2promotion lines = p.cache.slot_stride == p.d ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                                                     : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
     m.rows = rows;
-    return enc(&m.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.cache.k, dims, strides, k_box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, lines,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
-           enc(&m.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.cache.v, dims, strides, v_box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, p.d > 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, lines,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto encode = [&](CUtensorMap *map, void *codes) {
+        return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle, lines, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return encode(&m.k, p.cache.k) && encode(&m.v, p.cache.v);
 }
 
 template <typename T, int DP, int kGroups>
@@ -670,7 +677,10 @@ static int launch_few8_width(AttnParams &p, const FewMaps &maps, void *workspace
 bool launch_kv8_attn_few(AttnParams &p, int dtype, void *workspace, cudaStream_t st, int &status)
 {
     FewMaps maps = {};
-    if (p.cache.page.d % 8 != 0 || !few8_maps(p, p.cache.page.d % 16 == 0 ? 16 : 8, maps))
+    int rows = p.d > 128 ? 16 : 32;  // of a box: a block's, where it does not cross a page
+    while (rows > 8 && p.cache.page.d % rows != 0)
+        rows /= 2;
+    if (p.cache.page.d % rows != 0 || !few8_maps(p, rows, maps))
         return false;
     status = dtype == DLRM_F32   ? launch_few8_width<float>(p, maps, workspace, st)
              : dtype == DLRM_F16 ? launch_few8_width<__half>(p, maps, workspace, st)

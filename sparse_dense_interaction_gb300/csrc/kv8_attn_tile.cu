@@ -125,8 +125,9 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
             uint32_t x[8];
 #pragma unroll
             for (int k = 0; k < 4; k++) {
-                x[2 * k] = hmul2(decode2((uint16_t)in[k]), f);
-                x[2 * k + 1] = hmul2(decode2((uint16_t)(in[k] >> 16)), f);
+                decode4(in[k], x[2 * k], x[2 * k + 1]);
+                x[2 * k] = hmul2(x[2 * k], f);
+                x[2 * k + 1] = hmul2(x[2 * k + 1], f);
             }
             const int r = row0 + i * kStepRows + step_row, unit = 2 * (chunk & 3);
             uint8_t *to = tile + (chunk >> 2) * Sh::kBlock + r * 128;

@@ -142,7 +142,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     FewItem it;  // of the unit being computed; `is`: of the unit whose addresses come next
     int units, quota = 0;  // of this CTA; the items' are counted from its first
     if (p.splits > 1) {
-        const bool any = few_share(p, it, units, quota, UT, busy);
+        const bool any = few_share(p, it, units, quota, UT, Sh::MG, busy);
         if (threadIdx.x == 0)
             p.joins[blockIdx.x].rows = 0;  // until an item is left unfinished
         if (!any)
@@ -150,7 +150,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     } else {
         const int64_t most = (p.max_new * p.group + kFewRows - 1) / kFewRows, of = blockIdx.x / most;
         const int64_t s = of / p.cache.heads;
-        if (!read_sequence(p.batch, s, p.max_new, p.max_len, it.seq, p.err) || !few_sequence(p, it, s, 0, UT))
+        if (!read_sequence(p.batch, s, p.max_new, p.max_len, it.seq, p.err) || !few_sequence(p, it, s, 0, UT, Sh::MG))
             return;
         it.head = (int)(of - s * p.cache.heads);
         it.tile = (int)(blockIdx.x - of * most);
@@ -174,7 +174,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         if (u >= units)
             return;
         while (u >= is.last)
-            few_next(p, is, UT, busy);
+            few_next(p, is, UT, Sh::MG, busy);
         const int at = is.lo + (u - is.first) * UT + warp * Sh::TB + my_token;
         if (copies && at < is.hi && at + (kBulk ? maps.rows : 1) > is.lo_seen) {
             const uint32_t page = p.cache.page.div((uint32_t)at);
@@ -646,7 +646,7 @@ kv_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         fresh = true;
         first_item = false;
         if (u + 1 < units)
-            few_next(p, it, UT, busy);
+            few_next(p, it, UT, Sh::MG, busy);
     }
     if (kBulk && dead) {
         // that part and those copied ahead of it may still be in flight: none may be when the memory is given back

@@ -39,20 +39,20 @@ struct FewItem {
     int64_t s;
     int first, last;
     int head, tile, tiles;
-    int lo, hi, lo_seen;  // positions that the sequence's queries see, lo down to a multiple of 16
+    int lo, hi, lo_seen;  // positions that the sequence's queries see, lo down to a multiple of `align`
     const int32_t *pages;
 };
 
 // Positions that a sequence's queries see, and the units of one of its items
 // (one at least where there are queries: their rows are written).
-__device__ __forceinline__ int few_units(const AttnParams &p, const Sequence &q, int unit, int &lo, int &hi)
+__device__ __forceinline__ int few_units(const AttnParams &p, const Sequence &q, int unit, int &lo, int &hi, int align)
 {
     lo = hi = 0;
     if (q.count == 0)
         return 0;
     hi = seen_hi(q, p.causal, q.count - 1);
     lo = seen_lo(seen_hi(q, p.causal, 0), p.window);
-    return hi > lo ? (hi - (lo & ~15) + unit - 1) / unit : 1;
+    return hi > lo ? (hi - (lo & -align) + unit - 1) / unit : 1;
 }
 
 __device__ __forceinline__ int few_tiles(const AttnParams &p, const Sequence &q)
@@ -62,12 +62,12 @@ __device__ __forceinline__ int few_tiles(const AttnParams &p, const Sequence &q)
 
 // Sets the item to sequence s's first, from unit `first`; false where the
 // sequence has no units.
-__device__ __forceinline__ bool few_sequence(const AttnParams &p, FewItem &w, int64_t s, int first, int unit)
+__device__ __forceinline__ bool few_sequence(const AttnParams &p, FewItem &w, int64_t s, int first, int unit, int align)
 {
     if (!read_sequence(p.batch, s, p.max_new, p.max_len, w.seq, nullptr))
         return false;
-    const int units = few_units(p, w.seq, unit, w.lo_seen, w.hi);
-    w.lo = w.lo_seen & ~15;
+    const int units = few_units(p, w.seq, unit, w.lo_seen, w.hi, align);
+    w.lo = w.lo_seen & -align;
     w.s = s;
     w.head = w.tile = 0;
     w.tiles = few_tiles(p, w.seq);
@@ -108,7 +108,7 @@ static __device__ __noinline__ int few_busy_after(const AttnParams &p, int s0, c
 }
 
 // The next item, by a whole warp.
-__device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int unit, const int *busy)
+__device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int unit, int align, const int *busy)
 {
     if (++w.tile == w.tiles) {
         w.tile = 0;
@@ -121,7 +121,7 @@ __device__ __forceinline__ void few_next(const AttnParams &p, FewItem &w, int un
         return;
     }
     const int first = w.last, next = few_busy_after(p, (int)w.s, busy);
-    if (next >= 0 && few_sequence(p, w, next, first, unit))
+    if (next >= 0 && few_sequence(p, w, next, first, unit, align))
         return;
     w.last = 0x7fffffff;  // not reached: a CTA's units end with the last item's
 }
@@ -135,7 +135,7 @@ __host__ __device__ __forceinline__ int64_t few_quota(int64_t total, int ctas)
 
 // The CTA's share of all units: sums every sequence's units (each thread a run
 // of sequences), finds the item that holds the first unit of the share.
-static __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int &quota_units, int unit, int *busy)
+static __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, int &quota_units, int unit, int align, int *busy)
 {
     __shared__ int64_t sums[kFewWarps], found[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -146,7 +146,7 @@ static __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, in
     int lo, hi, first = -1;
     for (int64_t s = from; s < to; s++)
         if (read_sequence(p.batch, s, p.max_new, p.max_len, q, blockIdx.x == 0 ? p.err : nullptr)) {
-            mine += (int64_t)few_units(p, q, unit, lo, hi) * few_tiles(p, q) * p.cache.heads;
+            mine += (int64_t)few_units(p, q, unit, lo, hi, align) * few_tiles(p, q) * p.cache.heads;
             first = first < 0 && q.count > 0 ? (int)s : first;
         }
     busy[threadIdx.x] = first;
@@ -173,7 +173,7 @@ static __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, in
     for (int64_t s = from; here && s < to; s++) {
         int64_t here_units = 0;
         if (read_sequence(p.batch, s, p.max_new, p.max_len, q, nullptr))
-            here_units = (int64_t)few_units(p, q, unit, lo, hi) * few_tiles(p, q) * p.cache.heads;
+            here_units = (int64_t)few_units(p, q, unit, lo, hi, align) * few_tiles(p, q) * p.cache.heads;
         if (u0 >= before && u0 < before + here_units) {
             found[0] = s;
             found[1] = before;
@@ -185,7 +185,7 @@ static __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, in
         return false;
     // the sequence's items before it may be many: their units are counted from the share's
     // first in 64 bits, the item's own fit in 32
-    few_sequence(p, w, found[0], 0, unit);
+    few_sequence(p, w, found[0], 0, unit, align);
     const int64_t each = w.last, skip = (u0 - found[1]) / each;
     w.tile = (int)(skip % w.tiles);
     w.head = (int)(skip / w.tiles);
