@@ -17,6 +17,7 @@ int launch_kv_append(const HeadsView &, const HeadsView &, const BatchView &, co
                      const float *, float, const RopeView &, const HeadsView &, const float *, const HeadsView &,
                      int32_t *, cudaStream_t);
 size_t attn_workspace(int64_t, int64_t, int, int, int, int64_t, int64_t);
+size_t attn8_workspace(int64_t, int64_t, int, int, int, int64_t, int64_t);
 int launch_kv_attn(AttnParams &, int, void *, cudaStream_t);
 int launch_kv8_attn(AttnParams &, int, void *, cudaStream_t);
 int launch_kv_reserve(const int64_t *, const int64_t *, int64_t, int64_t, int32_t *, int64_t, int64_t, int, int32_t *,
@@ -153,7 +154,8 @@ static int check_attention(const dlrm_heads *q, const dlrm_kv_batch *batch, int 
         return DLRM_ERR_UNSUPPORTED;
     if (n > 0 && max_new == 0)
         return DLRM_ERR_INVALID_ARG;
-    if (workspace_bytes < attn_workspace(p.batch.S, n, p.q.heads, p.cache.heads, d, max_new, max_len))
+    if (workspace_bytes < (p.exp.k ? attn8_workspace : attn_workspace)(p.batch.S, n, p.q.heads, p.cache.heads, d,
+                                                                       max_new, max_len))
         return DLRM_ERR_WORKSPACE_TOO_SMALL;
     p.max_len = max_len;
     p.d = d;
@@ -262,14 +264,19 @@ int dlrm_kv_append(const dlrm_heads *k, const dlrm_heads *v, const dlrm_kv_batch
                             static_cast<cudaStream_t>(stream));
 }
 
+static bool attn_sizes(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new, int64_t max_len)
+{
+    return S >= 0 && S <= kMaxSequences && n >= 0 && n <= kMaxTokens && kv_heads >= 1 && kv_heads <= kMaxHeads &&
+           q_heads >= 1 && q_heads <= kMaxHeads && q_heads % kv_heads == 0 && d >= 1 && d <= DLRM_MAX_HEAD_DIM &&
+           max_new >= 0 && max_new <= kMaxTokens && max_len >= 0 && max_len <= kMaxPositions;
+}
+
 size_t dlrm_kv_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new,
                                    int64_t max_len)
 {
-    if (S < 0 || S > kMaxSequences || n < 0 || n > kMaxTokens || kv_heads < 1 || kv_heads > kMaxHeads ||
-        q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads != 0 || d < 1 || d > DLRM_MAX_HEAD_DIM ||
-        max_new < 0 || max_new > kMaxTokens || max_len < 0 || max_len > kMaxPositions)
-        return 0;
-    return attn_workspace(S, n, q_heads, kv_heads, d, max_new, max_len);
+    return attn_sizes(S, n, q_heads, kv_heads, d, max_new, max_len)
+               ? attn_workspace(S, n, q_heads, kv_heads, d, max_new, max_len)
+               : 0;
 }
 
 int dlrm_kv_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm_kv_cache *cache, int d, int dtype,
@@ -341,7 +348,9 @@ int dlrm_kv8_append(const dlrm_heads *k, const dlrm_heads *v, const dlrm_kv_batc
 size_t dlrm_kv8_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new,
                                     int64_t max_len)
 {
-    return dlrm_kv_attn_workspace_size(S, n, q_heads, kv_heads, d, max_new, max_len);
+    return attn_sizes(S, n, q_heads, kv_heads, d, max_new, max_len)
+               ? attn8_workspace(S, n, q_heads, kv_heads, d, max_new, max_len)
+               : 0;
 }
 
 int dlrm_kv8_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm_kv_cache8 *cache, int d, int dtype,

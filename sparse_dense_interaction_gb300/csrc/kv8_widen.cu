@@ -1,0 +1,135 @@
+// The part of a cache in 8 bits that a batch sees, as a 16-bit cache in the workspace.
+//
+// Long chunks read every key and value again for each tile of their rows, and
+// converting them each time costs the tiles a third of their time.  bf16 holds every
+// code times its power exactly, so for such batches they are converted once, and
+// the 16-bit cache's tiles do the rest.  Memory bounds the conversion (a byte read, two written,
+// which mostly stay in L2).
+#include "kv8.cuh"
+
+namespace dlrm {
+
+constexpr int kWidenThreads = 256, kWidenPage = 128;
+
+struct WidenParams {
+    AttnParams p;
+    char *k, *v;      // [sequence * pages + page][head][kWidenPage][d], bf16
+    int32_t *table;   // [sequence][pages]
+    int pages;        // of a sequence
+    FastDiv chunks, heads;  // 16 codes of a row; heads
+};
+
+__device__ __forceinline__ void widen16(const char *from, uint32_t e, char *to)
+{
+    const uint4 c = *reinterpret_cast<const uint4 *>(from);
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    const float power = exp_power(e);
+    uint32_t x[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint32_t h[2];
+        decode4(in[i], h[0], h[1]);
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const float2 y = unpack2<__half>(h[k]);
+            x[2 * i + k] = pack2<__nv_bfloat16>(y.x * power, y.y * power);
+        }
+    }
+    reinterpret_cast<uint4 *>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4 *>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+}
+
+// A CTA per sequence, page of the copy and head.
+__global__ void __launch_bounds__(kWidenThreads)
+kv8_widen_kernel(const __grid_constant__ WidenParams w)
+{
+    const AttnParams &p = w.p;
+    __shared__ int64_t row_codes[kWidenPage];  // -1: a row of zeros
+    __shared__ uint8_t row_exps[2][kWidenPage];
+    const uint32_t number = w.heads.div(blockIdx.x);  // of the page
+    const int head = (int)(blockIdx.x - number * w.heads.d), page = (int)(number % (uint32_t)w.pages);
+    const int64_t s = number / (uint32_t)w.pages;
+    if (threadIdx.x == 0 && head == 0)
+        w.table[number] = (int32_t)number;
+    Sequence q;
+    if (!read_sequence(p.batch, s, p.max_new, p.max_len, q, nullptr) || q.count == 0)
+        return;
+    const int start = page * kWidenPage, hi = min(seen_hi(q, p.causal, q.count - 1), start + kWidenPage);
+    const int lo = max(seen_lo(seen_hi(q, p.causal, 0), p.window), start);
+    if (lo >= hi)
+        return;
+    const int r = threadIdx.x;
+    if (r < hi - lo) {
+        const uint32_t at = lo + r, n = p.cache.page.div(at), slot = at - n * p.cache.page.d;
+        const uint32_t id = (uint32_t)p.batch.table[s * p.batch.table_stride + n];
+        row_codes[r] = -1;
+        if (id < p.cache.pages) {
+            row_codes[r] = id * p.cache.page_stride + slot * p.cache.slot_stride + head * p.cache.head_stride;
+            const int64_t x = exp_offset(p.exp, id, slot, head);
+            row_exps[0][r] = p.exp.k[x];
+            row_exps[1][r] = p.exp.v[x];
+        } else {
+            raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+        }
+    }
+    __syncthreads();
+    const int per_row = p.d / 16, all = (hi - lo) * per_row;
+    const int64_t base = ((int64_t)blockIdx.x * kWidenPage + lo - start) * p.d * 2;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < all; i += kWidenThreads) {
+        const int x = (int)w.chunks.div((uint32_t)i), c = i - x * per_row;
+        const int64_t from = row_codes[x] + c * 16, to = base + i * 32;
+        if (row_codes[x] >= 0) {
+            widen16(p.cache.k + from, row_exps[0][x], w.k + to);
+            widen16(p.cache.v + from, row_exps[1][x], w.v + to);
+        } else {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 2; k++) {
+                reinterpret_cast<uint4 *>(w.k + to)[k] = zero;
+                reinterpret_cast<uint4 *>(w.v + to)[k] = zero;
+            }
+        }
+    }
+}
+
+// Bytes of the copy, 0 where there is none.  It pays where tiles of rows read a key and value often, from 4 tiles of
+// 256 rows on with heads above 64 and from 8 on below (converted once and by every tile, us, 16 heads on 4 of 128: 4
+// sequences of 2048 new on 8192 364 and 476; 48 of 512 131 and 181; 16 of 256 on 8192 275 and 287, of
+// 128 229 and 206; 64 of 500 on up to 2000, 8 heads of 64, 131 and 113, of 1000 192 and 188).  It takes four times
+// the bytes of the codes up to max_len, which may be far above the lengths: at most kWidenMost.
+constexpr int64_t kWidenMost = (int64_t)2 << 30;
+
+size_t widen_workspace(int64_t S, int heads, int group, int d, int64_t max_new, int64_t max_len)
+{
+    const int64_t pages = (max_len + kWidenPage - 1) / kWidenPage;
+    if (max_new * group < (d > 64 ? 1024 : 2048) || d > 128 || d % 16 != 0 || pages == 0 || S == 0 ||
+        pages > kWidenMost / (4 * kWidenPage * S * heads * d))
+        return 0;
+    return (size_t)(4 * kWidenPage * S * pages * heads * d + (S * pages * 4 + 255) / 256 * 256);
+}
+
+// Converts, and turns the parameters to the copy; the workspace begins with it.
+int launch_widen(AttnParams &p, void *workspace, cudaStream_t st)
+{
+    WidenParams w;
+    const int64_t pages = (p.max_len + kWidenPage - 1) / kWidenPage, all = p.batch.S * pages;
+    const int64_t bytes = 2 * all * kWidenPage * p.cache.heads * p.d;
+    w.p = p;
+    w.k = static_cast<char *>(workspace);
+    w.v = w.k + bytes;
+    w.table = reinterpret_cast<int32_t *>(w.v + bytes);
+    w.pages = (int)pages;
+    w.chunks = FastDiv::make((uint32_t)p.d / 16);
+    w.heads = FastDiv::make((uint32_t)p.cache.heads);
+    kv8_widen_kernel<<<(unsigned)(all * p.cache.heads), kWidenThreads, 0, st>>>(w);
+    count_launch(st);
+    const int64_t row = p.d, head = kWidenPage * row;
+    p.cache = CacheView{w.k, w.v, head * p.cache.heads, row, head, (uint32_t)all, FastDiv::make(kWidenPage), p.cache.heads};
+    p.batch.table = w.table;
+    p.batch.table_stride = pages;
+    p.batch.capacity = p.batch.capacity < pages * kWidenPage ? p.batch.capacity : pages * kWidenPage;
+    p.exp = ExpView{};
+    return launch_status();
+}
+
+}  // namespace dlrm

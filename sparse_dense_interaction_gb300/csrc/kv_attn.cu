@@ -19,6 +19,8 @@ size_t few_workspace(int64_t, int, int64_t);
 int launch_kv_attn_few(AttnParams &, int, void *, cudaStream_t);
 int launch_kv_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
 int launch_kv8_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
+size_t widen_workspace(int64_t, int, int, int, int64_t, int64_t);
+int launch_widen(AttnParams &, void *, cudaStream_t);
 bool launch_kv8_attn_few(AttnParams &, int, void *, cudaStream_t, int &);
 
 // ---------------------------------------------------------------- general kernel
@@ -310,6 +312,14 @@ size_t attn_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, in
     return most + 16;
 }
 
+// Over a cache in 8 bits: a copy of it in 16 bits may come first.
+size_t attn8_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new, int64_t max_len)
+{
+    const int group = q_heads / kv_heads;
+    return attn_workspace(S, n, q_heads, kv_heads, d, max_new, max_len) +
+           widen_workspace(S, kv_heads, group, d, max_new < n ? max_new : n, max_len);
+}
+
 template <typename T, bool kCodes>
 static int launch_general(const AttnParams &p, int64_t ctas, cudaStream_t st)
 {
@@ -415,6 +425,12 @@ int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     const bool tile = rows_even && codes_even && p.d % 16 == 0 && dtype != DLRM_F32 && p.d <= 128;
     const bool few = rows_even && codes_even && p.d <= (dtype == DLRM_F32 ? 128 : 256);
     int status;
+    // Long chunks of bf16 queries, which hold every value exactly: the codes are converted once.
+    const size_t widened = widen_workspace(p.batch.S, c.heads, p.group, p.d, p.max_new, p.max_len);
+    if (tile && dtype == DLRM_BF16 && widened > 0) {
+        status = launch_widen(p, workspace, st);
+        return status != DLRM_OK ? status : launch_kv_attn(p, dtype, static_cast<char *>(workspace) + widened, st);
+    }
     if (few && (!tile || rows <= 16 || (p.d > 64 && rows <= 32 && seen <= 1024)) &&
         launch_kv8_attn_few(p, dtype, workspace, st, status))
         return status;

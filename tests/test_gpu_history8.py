@@ -202,6 +202,10 @@ ATTN = [
     ([4, 2], [2500, 900], 4, 2, 256, 64, 16, True, True, 0, "f32"),
     ([260, 31], [260, 900], 2, 1, 256, 32, 32, False, True, 0, "f16"),
     ([180], [900], 2, 1, 80, 40, 8, False, False, 0, "f16"),
+    # chunks of many rows, whose codes are converted once
+    ([300, 40, 0], [700, 1000, 33], 16, 4, 64, 16, 8, False, True, 0, "bf16"),
+    ([520], [1300], 4, 2, 128, 24, 24, True, True, 333, "bf16"),
+    ([130, 2], [200, 0], 16, 2, 96, 7, 7, False, False, 0, "bf16"),
 ]
 
 
