@@ -133,10 +133,9 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     FewItem is = it;
 
     // A lane finds the page and slot of one token of the warp's block (its exponents are the lane's to fetch), and
-    // copies one box, whose place the lane of its first token knows; a box that no query sees anything of is
+    // one copies the boxes, whose places the lanes of their first tokens know; a box that no query sees anything of is
     // outside the map: zeros.
-    const int parts = TB / maps.rows, my_column = lane / parts, my_first = (lane - my_column * parts) * maps.rows;
-    const bool copies = my_column < 2 * Sh::kColumns;
+    const int parts = TB / maps.rows;
     int page_id = -1, page_slot = 0;
     bool token_seen = false;
     auto find = [&](int u) {
@@ -161,18 +160,28 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     auto copy = [&](int u, int stage, uint32_t &ke, uint32_t &ve) {
         ke = ve = 0;
         if (u < units && !dead) {
-            if (lane == 0)
-                tc::mbar_expect_tx(&bars[warp][stage], Sh::kStageBytes);
             const bool sound = (uint32_t)page_id < p.cache.pages;
             if (token_seen && !sound)
                 raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
-            const int page = __shfl_sync(0xffffffffu, sound ? page_id : -1, my_first);
-            const int slot = __shfl_sync(0xffffffffu, page_slot, my_first);
-            if (copies) {
-                const bool value = my_column >= Sh::kColumns;
-                tc::tma_load_4d(ring_at + stage * Sh::kStageBytes + my_column * Sh::kColumnBytes + my_first * Sh::kWidth,
-                                value ? &maps.v : &maps.k, (my_column - (value ? Sh::kColumns : 0)) * Sh::kWidth, slot,
-                                is.head, page, &bars[warp][stage]);
+            const int known = sound ? page_id : -1;
+            uint64_t *bar = &bars[warp][stage];
+            // One lane issues them all: a copy's operands are the warp's, and lanes that each issue one take turns.
+#pragma unroll 1
+            for (int i = 0; i < parts; i++) {
+                const int page = __shfl_sync(0xffffffffu, known, i * maps.rows);
+                const int slot = __shfl_sync(0xffffffffu, page_slot, i * maps.rows);
+                if (tc::elect_one()) {
+                    if (i == 0)
+                        tc::mbar_expect_tx(bar, Sh::kStageBytes);
+                    const uint32_t to = ring_at + stage * Sh::kStageBytes + i * maps.rows * Sh::kWidth;
+#pragma unroll
+                    for (int c = 0; c < Sh::kColumns; c++) {
+                        tc::tma_load_4d(to + c * Sh::kColumnBytes, &maps.k, c * Sh::kWidth, slot, is.head, page, bar);
+                        tc::tma_load_4d(to + (Sh::kColumns + c) * Sh::kColumnBytes, &maps.v, c * Sh::kWidth, slot, is.head,
+                                        page, bar);
+                    }
+                }
+                __syncwarp();
             }
             if (token_seen && sound) {
                 const int64_t x = exp_offset(p.exp, page_id, page_slot, is.head);
