@@ -397,7 +397,8 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             float f[Sh::kStats];
 #pragma unroll
             for (int i = 0; i < Sh::kStats; i++) {
-                const float next = fmaxf(top[i], m[i]);
+                // a row's own growth alone, so that its bits do not depend on the other rows'
+                const float next = top[i] > m[i] + kFew8Slack ? top[i] : m[i];
                 f[i] = exp2_approx(m[i] - (next == -INFINITY ? 0.f : next));
                 l[i] *= f[i];
                 f[i] *= down;

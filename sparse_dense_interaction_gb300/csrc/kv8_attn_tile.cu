@@ -314,7 +314,8 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
         now = fmaxf(now, b.agree[t][1 - half][in]);
         if (__any_sync(0xffffffffu, now - m > kTileSlack<__half> || now_ref > v_ref)) {
             // also from -infinity; the output of the tiles before is complete: the scores' MMA came after it
-            const float next = fmaxf(m, now), f = next == -INFINITY ? 1.f : exp2_approx(m - next);
+            // (a row's own growth alone, so that its bits do not depend on the other rows')
+            const float next = now - m > kTileSlack<__half> ? now : m, f = next == -INFINITY ? 1.f : exp2_approx(m - next);
             const float down = f * __uint_as_float((uint32_t)max(127 + v_ref - now_ref, 0) << 23);
             m = next;
             l *= f;
