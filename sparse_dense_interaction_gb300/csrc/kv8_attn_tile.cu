@@ -24,12 +24,13 @@ namespace dlrm {
 template <int DP, bool kTwo>
 struct Tile8Shape : TileShape<DP, kTwo, DP == 128 || !kTwo ? 4 : 8> {
     using Sh = TileShape<DP, kTwo, DP == 128 || !kTwo ? 4 : 8>;
-    static constexpr int kWarps = kTwo ? 4 : 2;          // that convert
+    // that convert: as many as leave the others 80 registers a thread
+    static constexpr int kWarps = kTwo ? 7 : 3;
     static constexpr int kMmaWarp = Sh::kSoftmaxWarps + kWarps, kThreads = kMmaWarp * 32 + 32;
-    static constexpr int kWarpRows = kTilePos / kWarps;  // of a tile, a warp's
-    static constexpr int kOwn = kWarpRows / 32;          // whose places a lane finds
-    static constexpr int kStepRows = 32 / (DP / 16);     // rows of which the warp's lanes take a chunk at once
-    static constexpr int kSteps = kWarpRows / kStepRows;
+    static constexpr int kStepRows = 32 / (DP / 16);     // rows of which a warp's lanes take a chunk at once
+    static constexpr int kGroups = kTilePos / kStepRows;  // of rows, which the warps take in turn
+    static constexpr int kSteps = (kGroups + kWarps - 1) / kWarps;
+    static constexpr int kOwn = (kSteps * kStepRows + 31) / 32;  // rows whose places a lane finds
     static constexpr int kRawTiles = 2, kRawBytes = kTilePos * DP;  // codes on their way
     static constexpr int kBars = Sh::kTiles + kRawTiles * kRawBytes;
 };
@@ -40,7 +41,7 @@ constexpr int kConvertBarrier = 9;
 
 struct Tile8Bars : TileBars {
     int k_ref[kTile8Refs], v_ref[kTile8Refs];  // of a tile: the exponents that its codes are relative to
-    int warp_ref[2][4][2];
+    int warp_ref[2][8][2];
 };
 
 // 2^(e + 7) as a pair of fp16, e <= 0; subnormal, at last 0, below 2^-14.
@@ -65,14 +66,17 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
 {
     using Sh = Tile8Shape<DP, kTwo>;
     constexpr int kOwn = Sh::kOwn, kSteps = Sh::kSteps, kStepRows = Sh::kStepRows;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - Sh::kSoftmaxWarps, row0 = warp * Sh::kWarpRows;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - Sh::kSoftmaxWarps;
     const int start = w.lo & ~127;
     const int32_t *pages = p.batch.table + w.s * p.batch.table_stride;
     // the lane's row and chunk of a step: 8 lanes write to every bank once
     const int step_row = DP == 128 ? ((lane >> 2) & 1) | (lane >> 4) << 1 : lane >> 2;
     const int chunk = DP == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
     const bool inside = chunk * 16 < p.d;
-    uint8_t *mine = raw + warp * kSteps * 512 + lane * 16;
+    uint8_t *mine = raw + lane * 16;
+    // the rows of the warp's step i, and of its own row n: those of a group
+    auto group = [&](int i) { return warp + i * Sh::kWarps; };
+    auto row_of = [&](int n) { return group(n / kStepRows) * kStepRows + n % kStepRows; };
 
     int32_t page[kOwn], slot[kOwn];  // of a coming tile's rows lane, lane + 32; slot -1: nothing of it is seen
     int64_t off[kOwn];               // their codes; -1: a row of zeros
@@ -80,9 +84,9 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
     auto find = [&](int j) {
 #pragma unroll
         for (int i = 0; i < kOwn; i++) {
-            const int at = start + j * kTilePos + row0 + i * 32 + lane;
+            const int row = row_of(i * 32 + lane), at = start + j * kTilePos + row;
             slot[i] = -1;
-            if (j < tiles && at >= w.lo && at < w.hi) {
+            if (j < tiles && row < kTilePos && at >= w.lo && at < w.hi) {
                 const uint32_t n = p.cache.page.div((uint32_t)at);
                 slot[i] = at - (int)(n * p.cache.page.d);
                 page[i] = __ldg(pages + n);
@@ -112,15 +116,18 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
         for (int i = 0; i < kSteps; i++) {
             const int64_t o = __shfl_sync(0xffffffffu, off[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
             const bool there = o >= 0 && inside;
-            tc::cp_async16(to + i * 512, base + (there ? o + chunk * 16 : 0), there);
+            if (group(i) < Sh::kGroups)
+                tc::cp_async16(to + group(i) * 512, base + (there ? o + chunk * 16 : 0), there);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto convert = [&](uint8_t *tile, const uint32_t *factor, int kv) {
 #pragma unroll
         for (int i = 0; i < kSteps; i++) {
+            if (group(i) >= Sh::kGroups)
+                break;
             const uint32_t f = __shfl_sync(0xffffffffu, factor[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
-            const uint4 c = *reinterpret_cast<const uint4 *>(mine + kv * Sh::kRawBytes + i * 512);
+            const uint4 c = *reinterpret_cast<const uint4 *>(mine + kv * Sh::kRawBytes + group(i) * 512);
             const uint32_t in[4] = {c.x, c.y, c.z, c.w};
             uint32_t x[8];
 #pragma unroll
@@ -129,7 +136,7 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
                 x[2 * k] = hmul2(x[2 * k], f);
                 x[2 * k + 1] = hmul2(x[2 * k + 1], f);
             }
-            const int r = row0 + i * kStepRows + step_row, unit = 2 * (chunk & 3);
+            const int r = group(i) * kStepRows + step_row, unit = 2 * (chunk & 3);
             uint8_t *to = tile + (chunk >> 2) * Sh::kBlock + r * 128;
             *reinterpret_cast<uint4 *>(to + ((unit ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<uint4 *>(to + (((unit + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
