@@ -19,7 +19,7 @@
 namespace dlrm {
 
 constexpr int kResThreads = 1024, kResItems = 2, kResChunk = kResThreads * kResItems;
-constexpr int kResOneCta = 8 * kResThreads;  // tokens that one CTA takes alone
+constexpr int kResTokens = kResThreads / 2;  // of a CTA, more where kResMaxCtas would not do
 constexpr int kResMaxCtas = 152;
 
 struct ReserveParams {
@@ -241,9 +241,12 @@ int launch_kv_reserve(const int64_t *counts, const int64_t *lengths, int64_t S, 
     const ReserveParams p = {counts, lengths, S, n, table, table_stride, table_width * page_size,
                              FastDiv::make((uint32_t)page_size), ring, pages, state, new_state, offsets, new_lengths,
                              slots, positions, err};
-    const int64_t all = (n + kResThreads - 1) / kResThreads;
-    const unsigned ctas = n <= kResOneCta ? 1u : (unsigned)(all < kResMaxCtas ? all : kResMaxCtas);
+    // In place the second launch costs 4 us: one CTA takes up to 4096 tokens.  Steps of one event of 2048 users, of
+    // 8192, us (in a graph; one CTA, many, many and a second launch): 12, 8, 12; 41, 21, 28; 64 users' prompts of up
+    // to 200: 11, 7, 9; of one event of 8: 6.
     const bool in_place = new_lengths == lengths || new_state == state;
+    const int64_t all = (n + kResTokens - 1) / kResTokens;
+    const unsigned ctas = n <= (in_place ? 8 : 1) * kResTokens ? 1u : (unsigned)(all < kResMaxCtas ? all : kResMaxCtas);
     if (ctas == 1 || !in_place) {
         kv_reserve_kernel<true, true><<<ctas, kResThreads, 0, st>>>(p);
         count_launch(st);
