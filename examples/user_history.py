@@ -118,13 +118,66 @@ class Histories:
         return self._attend(q_out, batch, counts, False)
 
 
-def serve(model, users=5, seed=1):
+class Histories8:
+    """The same in 8 bits: codes, and an exponent for each block of events and head.  Who has which page is known on
+    the GPU alone; the host keeps only lengths, as bounds for the launches."""
+
+    def __init__(self, model, users, pages=256, page_size=16, pages_of_user=64, block=16):
+        m = self.model = model
+        byte = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=m.device)
+        self.k, self.v = (byte(pages, m.kv_heads, page_size, m.d).transpose(1, 2) for _ in range(2))
+        self.k_exp, self.v_exp = (byte(pages, page_size // block, m.kv_heads) for _ in range(2))
+        self.page_size, self.lengths = page_size, [0] * users
+        self.stored = torch.zeros(users, dtype=torch.int64, device=m.device)  # the lengths on the GPU
+        self.offsets = torch.zeros(users + 1, dtype=torch.int64, device=m.device)
+        self.pages = torch.full((users, pages_of_user), -1, dtype=torch.int32, device=m.device)
+        self.ring = torch.arange(pages, dtype=torch.int32, device=m.device)  # the free pages, and where they begin and end
+        self.state = torch.tensor([0, pages], device=m.device)
+
+    def _cache(self):
+        return self.k, self.v, self.k_exp, self.v_exp
+
+    def _attend(self, q, offsets, counts, causal):
+        m, out = self.model, torch.empty_like(q)
+        sizes = len(counts), q.shape[0], m.q_heads, m.kv_heads, m.d, max(counts), max(self.lengths)
+        workspace = torch.empty(sdi.dlrm_kv8_attn_workspace_size(*sizes), dtype=torch.uint8, device=m.device)
+        sdi.dlrm_kv8_attn_fwd(q, offsets, self.stored, self.pages, *self._cache(), out, m.d ** -0.5, workspace,
+                              max(counts), max(self.lengths), causal=causal, err_flag=m.err)
+        return out
+
+    def append(self, counts, items):
+        """Stores ``counts[u]`` new events of each user (below 0: the user leaves, and their pages are free again);
+        returns what each gathers from those up to itself."""
+        m = self.model
+        self.lengths = [0 if c < 0 else n + c for n, c in zip(self.lengths, counts)]
+        positions = torch.empty(items.numel(), dtype=torch.int64, device=m.device)
+        sdi.dlrm_kv_reserve(torch.tensor(counts, device=m.device), self.stored, self.pages, self.page_size, self.ring,
+                            self.state, self.state, self.offsets, self.stored, positions=positions, err_flag=m.err)
+        q, k, v = m.heads(items)
+        q_out, k_out = (torch.empty(x.shape, dtype=m.dtype, device=m.device) for x in (q, k))
+        sdi.dlrm_qk_norm_rope_fwd(q, k, m.q_weight, m.k_weight, m.eps, m.rope, positions, q_out, k_out, err_flag=m.err)
+        sdi.dlrm_kv8_append(k_out, v, self.offsets, self.stored, self.pages, *self._cache(), err_flag=m.err)
+        return self._attend(q_out, self.offsets, [max(c, 0) for c in counts], True)
+
+    def candidates(self, counts, items):
+        """What ``counts[u]`` candidate items gather from each user's whole history, as the next event would."""
+        m = self.model
+        q = m.heads(items)[0]
+        counts_on = torch.tensor(counts, device=m.device)
+        at = self.stored.repeat_interleave(counts_on, output_size=items.numel())
+        q_out = torch.empty(q.shape, dtype=m.dtype, device=m.device)
+        sdi.dlrm_qk_norm_rope_fwd(q, None, m.q_weight, None, m.eps, m.rope, at, q_out, None, err_flag=m.err)
+        offsets = torch.cat([counts_on.new_zeros(1), counts_on.cumsum(0)])
+        return self._attend(q_out, offsets, counts, False)
+
+
+def serve(model, users=5, seed=1, kind=Histories):
     """Stores histories, an event more for some, then scores candidates; returns
     the histories, their items, the candidates' counts and items, what they
     gather and the interaction's output."""
     g = torch.Generator().manual_seed(seed)
     pick = lambda n: torch.randint(model.table.shape[0], (n,), generator=g).to(model.device)
-    store, past = Histories(model, users), [[] for _ in range(users)]
+    store, past = kind(model, users), [[] for _ in range(users)]
     for counts in ([40 + 37 * u for u in range(users)], [1 - u % 2 for u in range(users)], [1] * users):
         items = pick(sum(counts))
         store.append(counts, items)
@@ -180,6 +233,9 @@ def main():
     store, past, counts, items, gathered, y = serve(model)
     print(f"{len(past)} users with {store.lengths} stored events; {items.numel()} candidates scored, "
           f"interaction output {tuple(y.shape)}")
+    gathered8 = serve(model, kind=Histories8)[4]
+    off = ((gathered8.float() - gathered.float()).norm() / gathered.float().norm()).item()
+    print(f"with histories in 8 bits the candidates gather the same to {off:.3f}")
     losses = train(model)
     print(f"norm weights fitted: loss {losses[0]:.4f} -> {losses[-1]:.4f}")
 
