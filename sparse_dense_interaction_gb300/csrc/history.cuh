@@ -209,8 +209,10 @@ enum AttnKernel { kAttnGeneral, kAttnTile };
 // 256 users of 4 heads and up to 250 events: 48.3 and 50.2, 49.2 and 56.4, 78.9 and 79.0, 127 and 122.  Only
 // where the pairs already fit beside one another is one tile worse at few rows (64 users of 2 heads,
 // 4 query heads each, up to 250 events, 128 rows: 15.8 and 12.5).
-inline int tile_rows(int64_t rows, int d) { return d <= 64 && rows <= 256 ? 128 : 256; }
-__host__ __device__ constexpr int tile_places(int rows) { return rows == 128 ? 2 * 152 : 152; }  // CTAs that run at once
+// Heads above 128 (a cache in 8 bits alone) leave room for one, and for one CTA on an SM.
+inline int tile_rows(int64_t rows, int d) { return d > 128 || (d <= 64 && rows <= 256) ? 128 : 256; }
+// CTAs that run at once
+__host__ __device__ constexpr int tile_places(int rows, int d) { return rows == 128 && d <= 64 ? 2 * 152 : 152; }
 
 struct AttnPlan {
     AttnKernel kernel;

@@ -22,16 +22,19 @@
 namespace dlrm {
 
 template <int DP, bool kTwo>
-struct Tile8Shape : TileShape<DP, kTwo, DP == 128 || !kTwo ? 4 : 8> {
-    using Sh = TileShape<DP, kTwo, DP == 128 || !kTwo ? 4 : 8>;
+struct Tile8Shape : TileShape<DP, kTwo, (DP == 256 ? 2 : DP == 128 || !kTwo ? 4 : 8)> {
+    using Sh = TileShape<DP, kTwo, (DP == 256 ? 2 : DP == 128 || !kTwo ? 4 : 8)>;
+    static constexpr int kResident = kTwo || DP == 256 ? 1 : 2;  // CTAs of an SM
     // that convert: as many as leave the others 80 registers a thread
-    static constexpr int kWarps = kTwo ? 7 : 3;
+    static constexpr int kWarps = kResident == 1 ? 7 : 3;
     static constexpr int kMmaWarp = Sh::kSoftmaxWarps + kWarps, kThreads = kMmaWarp * 32 + 32;
     static constexpr int kStepRows = 32 / (DP / 16);     // rows of which a warp's lanes take a chunk at once
     static constexpr int kGroups = kTilePos / kStepRows;  // of rows, which the warps take in turn
     static constexpr int kSteps = (kGroups + kWarps - 1) / kWarps;
     static constexpr int kOwn = (kSteps * kStepRows + 31) / 32;  // rows whose places a lane finds
-    static constexpr int kRawTiles = 2, kRawBytes = kTilePos * DP;  // codes on their way
+    // Codes on their way: a tile of keys and one of values; with heads of 256, which leave room for one, a step's place is
+    // filled again as soon as it has been read, and L2 is told of the rows a tile ahead.
+    static constexpr int kRawTiles = DP == 256 ? 1 : 2, kRawBytes = kTilePos * DP;
     static constexpr int kBars = Sh::kTiles + kRawTiles * kRawBytes;
 };
 
@@ -70,8 +73,8 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
     const int start = w.lo & ~127;
     const int32_t *pages = p.batch.table + w.s * p.batch.table_stride;
     // the lane's row and chunk of a step: 8 lanes write to every bank once
-    const int step_row = DP == 128 ? ((lane >> 2) & 1) | (lane >> 4) << 1 : lane >> 2;
-    const int chunk = DP == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
+    const int step_row = DP == 256 ? (lane >> 2) & 1 : DP == 128 ? ((lane >> 2) & 1) | (lane >> 4) << 1 : lane >> 2;
+    const int chunk = DP == 256 ? (lane & 3) | (lane >> 3) << 2 : DP == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
     const bool inside = chunk * 16 < p.d;
     uint8_t *mine = raw + lane * 16;
     // the rows of the warp's step i, and of its own row n: those of a group
@@ -79,7 +82,7 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
     auto row_of = [&](int n) { return group(n / kStepRows) * kStepRows + n % kStepRows; };
 
     int32_t page[kOwn], slot[kOwn];  // of a coming tile's rows lane, lane + 32; slot -1: nothing of it is seen
-    int64_t off[kOwn];               // their codes; -1: a row of zeros
+    int64_t off[kOwn], off_now[kOwn];  // codes of the next tile's rows, of this one's; -1: a row of zeros
     uint32_t k_next[kOwn], v_next[kOwn];  // their exponents
     auto find = [&](int j) {
 #pragma unroll
@@ -108,26 +111,36 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
             const int64_t x = exp_offset(p.exp, page[i], slot[i], w.head);
             k_next[i] = p.exp.k[x];
             v_next[i] = p.exp.v[x];
+            if (Sh::kRawTiles == 1) {
+                for (int c = 0; c < p.d; c += 128) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.cache.k + off[i] + c));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.cache.v + off[i] + c));
+                }
+            }
         }
+    };
+    // step i of a tile of keys or values from the rows `from`
+    auto copy_step = [&](const char *base, const int64_t *from, uint8_t *to, int i) {
+        const int64_t o = __shfl_sync(0xffffffffu, from[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
+        const bool there = o >= 0 && inside;
+        if (group(i) < Sh::kGroups)
+            tc::cp_async16(to + group(i) * 512, base + (there ? o + chunk * 16 : 0), there);
     };
     auto copy = [&](const char *base, int kv) {
-        uint8_t *to = mine + kv * Sh::kRawBytes;
 #pragma unroll
-        for (int i = 0; i < kSteps; i++) {
-            const int64_t o = __shfl_sync(0xffffffffu, off[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
-            const bool there = o >= 0 && inside;
-            if (group(i) < Sh::kGroups)
-                tc::cp_async16(to + group(i) * 512, base + (there ? o + chunk * 16 : 0), there);
-        }
+        for (int i = 0; i < kSteps; i++)
+            copy_step(base, off, mine + kv * Sh::kRawBytes, i);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto convert = [&](uint8_t *tile, const uint32_t *factor, int kv) {
+    // `base`, `from`: of the next tile, step by step, where it has no place of its own
+    auto convert = [&](uint8_t *tile, const uint32_t *factor, int kv, const char *base, const int64_t *from) {
+        uint8_t *codes = mine + (Sh::kRawTiles == 1 ? 0 : kv * Sh::kRawBytes);
 #pragma unroll
         for (int i = 0; i < kSteps; i++) {
             if (group(i) >= Sh::kGroups)
                 break;
             const uint32_t f = __shfl_sync(0xffffffffu, factor[i * kStepRows / 32], (i * kStepRows + step_row) & 31);
-            const uint4 c = *reinterpret_cast<const uint4 *>(mine + kv * Sh::kRawBytes + group(i) * 512);
+            const uint4 c = *reinterpret_cast<const uint4 *>(codes + group(i) * 512);
             const uint32_t in[4] = {c.x, c.y, c.z, c.w};
             uint32_t x[8];
 #pragma unroll
@@ -140,28 +153,33 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
             uint8_t *to = tile + (chunk >> 2) * Sh::kBlock + r * 128;
             *reinterpret_cast<uint4 *>(to + ((unit ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<uint4 *>(to + (((unit + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+            if constexpr (Sh::kRawTiles == 1)
+                copy_step(base, from, mine, i);
         }
     };
     // after a wait that ran out the warps still meet at their barrier, but hand nothing over
     bool dead = false;
-    auto hand_over = [&](int i, const uint32_t *factor) {
+    auto hand_over = [&](int i, const uint32_t *factor, const char *base, const int64_t *from) {
         if (!dead && i >= Sh::kSlots &&
             !warp_wait(&b.empty[i % Sh::kSlots], (i / Sh::kSlots - 1) & 1, &b.aborted, p.wait_polls))
             dead = true;
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(Sh::kRawTiles - 1) : "memory");
         if (!dead) {
-            convert(ring + i % Sh::kSlots * Sh::kTileBytes, factor, i & 1);
+            convert(ring + i % Sh::kSlots * Sh::kTileBytes, factor, i & 1, base, from);
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0)
                 tc::mbar_arrive(&b.full[i % Sh::kSlots]);
         }
+        if constexpr (Sh::kRawTiles == 1)
+            asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
     find(0);
     place();
     copy(p.cache.k, 0);
-    copy(p.cache.v, 1);
+    if constexpr (Sh::kRawTiles == 2)
+        copy(p.cache.v, 1);
     find(1);
     int v_ref = 0;
 #pragma unroll 1
@@ -197,12 +215,17 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
             kf[i] = relative_power((int)kf[i] - k_ref);
             vf[i] = relative_power((int)vf[i] - v_ref);
         }
+#pragma unroll
+        for (int i = 0; i < kOwn; i++)
+            off_now[i] = off[i];
         place();
         find(j + 2);
-        hand_over(2 * j, kf);
-        copy(p.cache.k, 0);
-        hand_over(2 * j + 1, vf);
-        copy(p.cache.v, 1);
+        hand_over(2 * j, kf, p.cache.v, off_now);
+        if constexpr (Sh::kRawTiles == 2)
+            copy(p.cache.k, 0);
+        hand_over(2 * j + 1, vf, p.cache.k, off);
+        if constexpr (Sh::kRawTiles == 2)
+            copy(p.cache.v, 1);
     }
     tc::cp_async_wait_all();
 }
@@ -384,7 +407,7 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
 }
 
 template <typename T, int DP, bool kTwo>
-__global__ void __launch_bounds__(Tile8Shape<DP, kTwo>::kThreads, kTwo ? 1 : 2)
+__global__ void __launch_bounds__(Tile8Shape<DP, kTwo>::kThreads, Tile8Shape<DP, kTwo>::kResident)
 kv8_attn_tile_kernel(const __grid_constant__ AttnParams p)
 {
     using Sh = Tile8Shape<DP, kTwo>;
@@ -449,7 +472,7 @@ template <typename T, int DP, bool kTwo>
 static int launch_tile8(const AttnParams &p, int64_t ctas, cudaStream_t st)
 {
     constexpr int smem = Tile8Shape<DP, kTwo>::kBars + sizeof(Tile8Bars);
-    static_assert(smem <= (kTwo ? 232448 : 115200), "an SM's shared memory");
+    static_assert(smem <= (Tile8Shape<DP, kTwo>::kResident == 1 ? 232448 : 115200), "an SM's shared memory");
     static std::atomic<unsigned long long> done{0};
     const int s = allow_dynamic_smem((const void *)kv8_attn_tile_kernel<T, DP, kTwo>, smem, &done);
     if (s != DLRM_OK)
@@ -462,6 +485,8 @@ static int launch_tile8(const AttnParams &p, int64_t ctas, cudaStream_t st)
 template <typename T>
 static int launch_tile8_shape(const AttnParams &p, int64_t ctas, cudaStream_t st)
 {
+    if (p.d > 128)
+        return launch_tile8<T, 256, false>(p, ctas, st);
     if (p.d > 64)
         return launch_tile8<T, 128, true>(p, ctas, st);
     return p.rows > 128 ? launch_tile8<T, 64, true>(p, ctas, st) : launch_tile8<T, 64, false>(p, ctas, st);

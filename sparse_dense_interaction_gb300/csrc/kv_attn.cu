@@ -268,7 +268,7 @@ static AttnPlan plan_tile(int64_t S, int kv_heads, int group, int d, int64_t max
 {
     const int rows = tile_rows(max_new * group, d);
     const int64_t have = S * kv_heads * ceil_div(max_new * group, rows), longest = seen + 127;
-    const int64_t places = tile_places(rows);
+    const int64_t places = tile_places(rows, d);
     int64_t best = 1, least = INT64_MAX;
     // one, or as many as fill 1 to 16 rounds of places
     for (int64_t round = 0, last = 0; round <= (have < 2 * places ? 16 : 0); round++) {
@@ -422,16 +422,19 @@ int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     const bool codes_even = reinterpret_cast<uintptr_t>(c.k) % 16 == 0 && reinterpret_cast<uintptr_t>(c.v) % 16 == 0 &&
                             c.page_stride % 16 == 0 && c.slot_stride % 16 == 0 && c.head_stride % 16 == 0;
     const int64_t rows = p.max_new * p.group, seen = seen_bound(p);
-    const bool tile = rows_even && codes_even && p.d % 16 == 0 && dtype != DLRM_F32 && p.d <= 128;
+    const bool tile = rows_even && codes_even && p.d % 16 == 0 && dtype != DLRM_F32;
     const bool few = rows_even && codes_even && p.d <= (dtype == DLRM_F32 ? 128 : 256);
     int status;
-    // Long chunks of bf16 queries, which hold every value exactly: the codes are converted once.
+    // Long chunks of bf16 queries, which hold every value exactly: the codes are converted once (heads of up to 128).
     const size_t widened = widen_workspace(p.batch.S, c.heads, p.group, p.d, p.max_new, p.max_len);
     if (tile && dtype == DLRM_BF16 && widened > 0) {
         status = launch_widen(p, workspace, st);
         return status != DLRM_OK ? status : launch_kv_attn(p, dtype, static_cast<char *>(workspace) + widened, st);
     }
-    if (few && (!tile || rows <= 16 || (p.d > 64 && rows <= 32 && seen <= 1024)) &&
+    // Rows of 16, as with the 16-bit cache, but for heads above 128 too, rows of 16 against tiles (bf16, 8 heads on
+    // 2 of 256): 96 users with 1500 and 12 rows 61 and 87 us; 16 with up to 4000 and 256 rows 113 and 72; 4 with
+    // 4096 and 8192 rows 1678 and 280.
+    if (few && (!tile || rows <= 16 || (p.d > 64 && p.d <= 128 && rows <= 32 && seen <= 1024)) &&
         launch_kv8_attn_few(p, dtype, workspace, st, status))
         return status;
     return launch_planned(p, tile ? kAttnTile : kAttnGeneral, seen, dtype, workspace, st);

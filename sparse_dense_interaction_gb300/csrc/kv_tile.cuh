@@ -26,7 +26,7 @@ template <int DP, bool kTwo, int kRing = DP == 128 || !kTwo ? 5 : 8>
 struct TileShape {
     static constexpr int kRows = kTwo ? 256 : 128;
     static constexpr int kSoftmaxThreads = 2 * kRows, kSoftmaxWarps = kSoftmaxThreads / 32;
-    static constexpr int kScoreCols = kRows, kTmem = 2 * kRows;  // tensor-memory columns: scores, all
+    static constexpr int kScoreCols = kRows, kTmem = DP > 128 ? 512 : 2 * kRows;  // tensor-memory columns: scores, all
     __host__ __device__ static constexpr int threads(bool bulk) { return kSoftmaxThreads + copy_threads(bulk) + 32; }
     static constexpr int kTileBytes = kTilePos * DP * 2;  // of keys or values; a query tile too
     static constexpr int kSlots = kRing;
@@ -204,7 +204,7 @@ constexpr int kRanked = 256;
 
 static __device__ bool tile_work(const AttnParams &p, int *room, AttnWork &w)
 {
-    if (p.batch.S > kRanked || gridDim.x > 5 * tile_places(p.rows))
+    if (p.batch.S > kRanked || gridDim.x > 5 * tile_places(p.rows, p.d))
         return attn_work(p, blockIdx.x, w);
     int64_t tile;
     const int64_t rank = attn_number(p, blockIdx.x, w, tile);

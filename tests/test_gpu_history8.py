@@ -206,6 +206,10 @@ ATTN = [
     ([300, 40, 0], [700, 1000, 33], 16, 4, 64, 16, 8, False, True, 0, "bf16"),
     ([520], [1300], 4, 2, 128, 24, 24, True, True, 333, "bf16"),
     ([130, 2], [200, 0], 16, 2, 96, 7, 7, False, False, 0, "bf16"),
+    # heads above 128 in tiles: parts, a window, pages that end inside a tile
+    ([50, 0, 9], [3000, 5, 400], 4, 2, 256, 32, 16, True, True, 0, "bf16"),
+    ([40, 33], [500, 700], 2, 2, 144, 7, 1, False, False, 90, "bf16"),
+    ([20], [20000], 2, 1, 192, 64, 8, False, True, 0, "f16"),
 ]
 
 

@@ -39,6 +39,7 @@ KINDS = [
     ([40], [333], 4, 2, 64, 16, 16, True, True, 0, "f16"), ([150], [2000], 4, 2, 64, 16, 2, True, False, 0, "bf16"),
     ([9], [20000], 4, 1, 128, 64, 64, True, True, 0, "bf16"), ([300], [900], 3, 1, 128, 32, 8, False, True, 200, "f16"),
     ([200, 5], [333, 64], 2, 1, 128, 7, 7, False, True, 0, "f16"), ([300, 30], [400, 700], 4, 1, 128, 128, 32, True, True, 0, "bf16"),
+    ([40, 3], [1000, 50], 4, 2, 256, 32, 8, True, True, 0, "bf16"), ([70], [900], 2, 2, 160, 12, 4, False, False, 0, "f16"),
     ([2, 30], [100, 260], 2, 2, 17, 5, 5, False, True, 0, "f32"), ([3], [700], 2, 1, 20, 5, 1, False, True, 0, "bf16"),
 ]
 
@@ -158,7 +159,7 @@ def test_contradictions_are_flagged(case, what):
 
 
 @pytest.mark.parametrize("polls", [0, 1, 40])
-@pytest.mark.parametrize("case", KINDS[:12])
+@pytest.mark.parametrize("case", KINDS[:14])
 def test_waits_that_run_out(case, polls):
     counts, lengths, hq, hk, d, page, block, first, causal, window, dtype = case
     table, given, caches, q = attention_inputs(case)
