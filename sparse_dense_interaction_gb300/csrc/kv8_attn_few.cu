@@ -19,11 +19,19 @@
 //    A weight is held relative to the largest power that the warp has seen so far
 //    and rises with it (the output is scaled down when that grows, as it is when a maximum
 //    does), so fp16's range is the row's: what a token gathers is off by at most
-//    2^-39 of the largest weight times the largest power.
-//  - A lane asks for the exponents of one token of the block, a unit or two
-//    ahead, beside the copies; shuffles hand them out.
-// A conversion takes two cycles of a quarter of an SM, a quarter of the time
-// that memory leaves.
+//    2^-36 of the largest weight times the largest power.
+//  - A lane asks for the exponents of one token of the block beside the copies, two units
+//    ahead; shuffles hand them out.  One lane issues a block's copies.
+//
+// What bounds it: memory, and nearly as much the warps themselves.  Of 8 KB a warp
+// takes 560 instructions, 128 of them conversions, which take two cycles of a
+// quarter of an SM each.  One event each of 256 users with up to 8192 events (16 heads on 4, 128 bf16 elements):
+// 178 us, 5.7 TB/s, 0.86 of a plain copy; the copies alone take 155, the arithmetic alone 135.  One history of
+// 262143: 59 us, of which the join, the launches and the first loads take 12.  12 rows of 8 heads on 2 of 256 of 96
+// users with up to 3000: 74 us, 1.8 TB/s; their registers leave 8 warps an SM, each bound by its own
+// latencies.  Slower: exponents by copies of 4 bytes (193 us for the 256 users), keys and values handed back
+// one by one (188), blocks of 16 tokens with 4 CTAs an SM (247), scores by MMAs of E4M3 with queries in parts (205: the
+// chip composes them of fp16 ones).
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -33,7 +41,7 @@ namespace dlrm {
 
 // log2 of the growth of a maximum that is let pass before the output is scaled down, and of what weights are
 // lifted by: at most 2^15 in all, fp16's range.  (A tile of 16 rows sees some maximum grow in almost every block of
-// a short history: 96 users with up to 3000, 12 rows of 256: 79 us with a slack of 0, XX.)
+// a short history.)
 constexpr float kFew8Slack = 4.f, kFew8Lift = kWeightTop<__half> - kFew8Slack;
 
 template <typename T, int DP, int kGroups>
@@ -637,6 +645,11 @@ static bool few8_maps(const AttnParams &p, int rows, FewMaps &m)
     return encode(&m.k, p.cache.k) && encode(&m.v, p.cache.v);
 }
 
+// Bytes of an item up to which it stays whole.  Whole against runs, us (bf16): 256 users with up to 8192, 4 heads of 128,
+// 187 and 178; 64 with up to 2000 28 and 36; 16 with up to 2000 22 and 25; one with 3000 20 and 18; 96 with 1500, 12
+// rows of 2 heads of 256, 61 and 72.
+constexpr int64_t kFew8WholeBytes = 480 << 10, kFew8WholeBytesPerItem = 1536;
+
 template <typename T, int DP, int kGroups>
 static int launch_few8(AttnParams &p, const FewMaps &maps, void *workspace, cudaStream_t st)
 {
@@ -650,7 +663,7 @@ static int launch_few8(AttnParams &p, const FewMaps &maps, void *workspace, cuda
     // items, idle sequences' among them; the batch cannot have more busy sequences than tokens
     const int64_t each = p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows), items = p.batch.S * each;
     const int64_t busy = (p.batch.S < p.batch.n ? p.batch.S : p.batch.n) * each;
-    const bool split = few_splits(seen < p.max_len ? seen : p.max_len, p.d, 1, busy);
+    const bool split = few_splits(seen < p.max_len ? seen : p.max_len, p.d, 1, busy, kFew8WholeBytes, kFew8WholeBytesPerItem);
     p.splits = split ? 2 : 1;
     p.joins = static_cast<FewJoin *>(workspace);
     p.part_o = reinterpret_cast<float *>(p.joins + kFewMaxCtas);

@@ -294,9 +294,10 @@ kv_attn_few_join_kernel(const __grid_constant__ AttnParams p)
 // up to 8000, 2 heads of 64: 65 and 39; one with 3000: 26 and 16.
 constexpr int64_t kFewWholeBytes = 384 << 10, kFewWholeBytesPerItem = 3 << 10;
 
-inline bool few_splits(int64_t seen, int d, int es, int64_t items)
+inline bool few_splits(int64_t seen, int d, int es, int64_t items, int64_t whole = kFewWholeBytes,
+                       int64_t per_item = kFewWholeBytesPerItem)
 {
-    return seen * d * 2 * es > kFewWholeBytes + items * kFewWholeBytesPerItem;
+    return seen * d * 2 * es > whole + items * per_item;
 }
 
 inline int64_t few_rows(int64_t rows) { return rows < kFewRows ? rows : kFewRows; }
