@@ -20,18 +20,24 @@
 //    and rises with it (the output is scaled down when that grows, as it is when a maximum
 //    does), so fp16's range is the row's: what a token gathers is off by at most
 //    2^-36 of the largest weight times the largest power.
-//  - A lane asks for the exponents of one token of the block beside the copies, two units
-//    ahead; shuffles hand them out.  One lane issues a block's copies.
+//  - A lane asks for the exponents of one token of the block (of two where it has 64) beside
+//    the copies, a ring's length ahead; shuffles hand them out.  One lane issues a block's copies.
+//  - A block is 8 KB where the registers allow: 64 tokens of heads of up to 64, 32 of
+//    up to 128.  What a block costs beside its bytes (the wait, the maximum, the issue of its
+//    copies) is the same for half as many.
 //
 // What bounds it: memory, and nearly as much the warps themselves.  Of 8 KB a warp
 // takes 560 instructions, 128 of them conversions, which take two cycles of a
-// quarter of an SM each.  One event each of 256 users with up to 8192 events (16 heads on 4, 128 bf16 elements):
-// 178 us, 5.7 TB/s, 0.86 of a plain copy; the copies alone take 155, the arithmetic alone 135.  One history of
-// 262143: 59 us, of which the join, the launches and the first loads take 12.  12 rows of 8 heads on 2 of 256 of 96
-// users with up to 3000: 74 us, 1.8 TB/s; their registers leave 8 warps an SM, each bound by its own
-// latencies.  Slower: exponents by copies of 4 bytes (193 us for the 256 users), keys and values handed back
-// one by one (188), blocks of 16 tokens with 4 CTAs an SM (247), scores by MMAs of E4M3 with queries in parts (205: the
-// chip composes them of fp16 ones).
+// quarter of an SM each.  One event each of 256 users with up to 8192 events (16 heads
+// on 4, 128 bf16 elements): 174 us, 5.9 TB/s, 0.87 of a plain copy; the copies alone take
+// 155, the arithmetic alone 135.  With heads of 64 fp16 elements: 111 us, 4.6 TB/s (140
+// with blocks of 32 tokens); there a token's arithmetic, not its bytes, bounds it.  One
+// history of 262143: 59 us, of which the join, the launches and the first loads take 12.
+// 12 rows of 8 heads on 2 of 256 of 96 users with up to 3000: 74 us, 1.8 TB/s; their
+// registers leave 8 warps an SM, each bound by its own latencies.  Slower: exponents by
+// copies of 4 bytes (193 us for the 256 users), keys and values handed back one by one
+// (188), blocks of 16 tokens with 4 CTAs an SM (247), scores by MMAs of E4M3 with
+// queries in parts (205: the chip composes them of fp16 ones).
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -48,7 +54,8 @@ template <typename T, int DP, int kGroups>
 struct Few8Shape {
     static constexpr bool kWide = sizeof(T) == 4;
     static constexpr int MG = 16;                        // tokens of an MMA group
-    static constexpr int TB = DP <= 128 ? 32 : 16, NB = TB / MG, UT = kFewWarps * TB;
+    static constexpr int TB = DP == 64 && !kWide ? 64 : DP <= 128 ? 32 : 16, NB = TB / MG, UT = kFewWarps * TB;
+    static constexpr int kSets = TB > 32 ? 2 : 1;        // tokens of a block that a lane looks after
     static constexpr int KG = DP / 64;                   // a lane's chunks of 16 codes of a key row
     static constexpr int VB = DP >= 128 ? 16 : 8, VS = DP / (8 * VB);  // codes of its chunks of a value row, and their number
     static constexpr int kStageBytes = TB * 2 * DP;
@@ -57,7 +64,8 @@ struct Few8Shape {
     static constexpr bool kTwoParts = kWide || (std::is_same<T, __half>::value && kGroups == 1);
     static constexpr int kOutMmas = VB / 2;              // of a set of output columns
     static constexpr int kOut = kGroups * VS * kOutMmas * 4;
-    static constexpr int kResident = !kWide && kGroups == 1 && DP <= 128 ? 3 : 2, kStages = DP == 64 ? 4 : kResident == 3 ? 2 : 3;
+    static constexpr int kResident = !kWide && kGroups == 1 && DP <= 128 ? 3 : 2;
+    static constexpr int kStages = kResident == 3 ? 2 : kStageBytes < 8192 ? 4 : 3;
     static constexpr int kCtas = kResident * kFewSms;
     static constexpr int kMerge = kOut < 32 ? kOut : 32;
     static constexpr int kSmem = 1024 + kFewWarps * kStages * kStageBytes + 2 * kMerge * 32 * 4;
@@ -140,48 +148,61 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     }
     FewItem is = it;
 
-    // A lane finds the page and slot of one token of the warp's block (its exponents are the lane's to fetch), and
-    // one copies the boxes, whose places the lanes of their first tokens know; a box that no query sees anything of is
+    // A lane finds the page and slot of one token of the warp's block, of two of 64 (their exponents are the lane's to
+    // fetch), and one copies the boxes, whose places the lanes of their first tokens know; a box that no query sees anything of is
     // outside the map: zeros.
     const int parts = TB / maps.rows;
-    int page_id = -1, page_slot = 0;
-    bool token_seen = false;
+    constexpr int kSets = Sh::kSets;
+    int page_id[kSets], page_slot[kSets];  // of the lane's tokens: lane, lane + 32
+    bool token_seen[kSets];
     auto find = [&](int u) {
-        page_id = -1;
-        token_seen = false;
+#pragma unroll
+        for (int i = 0; i < kSets; i++) {
+            page_id[i] = -1;
+            page_slot[i] = 0;
+            token_seen[i] = false;
+        }
         if (u >= units)
             return;
         while (u >= is.last)
             few_next(p, is, UT, TB, busy);
-        const int at = is.lo + (u - is.first) * UT + warp * TB + (lane & (TB - 1)), box = at & -maps.rows;
-        if (box < is.hi && box + maps.rows > is.lo_seen) {
-            const uint32_t page = p.cache.page.div((uint32_t)at);
-            page_slot = at - (int)(page * p.cache.page.d);
-            page_id = __ldg(is.pages + page);
-            token_seen = at >= is.lo_seen && at < is.hi;
+#pragma unroll
+        for (int i = 0; i < kSets; i++) {
+            const int at = is.lo + (u - is.first) * UT + warp * TB + i * 32 + (lane & (TB - 1)), box = at & -maps.rows;
+            if (box < is.hi && box + maps.rows > is.lo_seen) {
+                const uint32_t page = p.cache.page.div((uint32_t)at);
+                page_slot[i] = at - (int)(page * p.cache.page.d);
+                page_id[i] = __ldg(is.pages + page);
+                token_seen[i] = at >= is.lo_seen && at < is.hi;
+            }
         }
     };
     const uint32_t ring_at = tc::smem_u32(ring);
-    uint32_t k_exp[kStages], v_exp[kStages];  // of the lane's token of the next units
+    uint32_t k_exp[kStages][kSets], v_exp[kStages][kSets];  // of the lane's tokens of the next units
     bool dead = false;  // a wait ran out: nothing more is copied, the results are invalid
     // copies of unit u, whose page numbers were asked for a unit before, into a stage; then asks for the next
-    auto copy = [&](int u, int stage, uint32_t &ke, uint32_t &ve) {
-        ke = ve = 0;
+    auto copy = [&](int u, int stage, uint32_t *ke, uint32_t *ve) {
         if (u < units && !dead) {
-            const bool sound = (uint32_t)page_id < p.cache.pages;
-            if (token_seen && !sound)
-                raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
-            const int known = sound ? page_id : -1;
+            int known[kSets];
+#pragma unroll
+            for (int i = 0; i < kSets; i++) {
+                const bool sound = (uint32_t)page_id[i] < p.cache.pages;
+                if (token_seen[i] && !sound)
+                    raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+                known[i] = sound ? page_id[i] : -1;
+            }
             uint64_t *bar = &bars[warp][stage];
             // One lane issues them all: a copy's operands are the warp's, and lanes that each issue one take turns.
 #pragma unroll 1
             for (int i = 0; i < parts; i++) {
-                const int page = __shfl_sync(0xffffffffu, known, i * maps.rows);
-                const int slot = __shfl_sync(0xffffffffu, page_slot, i * maps.rows);
+                const int first = i * maps.rows;  // token
+                const bool second = kSets > 1 && first >= 32;
+                const int page = __shfl_sync(0xffffffffu, second ? known[kSets - 1] : known[0], first & 31);
+                const int slot = __shfl_sync(0xffffffffu, second ? page_slot[kSets - 1] : page_slot[0], first & 31);
                 if (tc::elect_one()) {
                     if (i == 0)
                         tc::mbar_expect_tx(bar, Sh::kStageBytes);
-                    const uint32_t to = ring_at + stage * Sh::kStageBytes + i * maps.rows * Sh::kWidth;
+                    const uint32_t to = ring_at + stage * Sh::kStageBytes + first * Sh::kWidth;
 #pragma unroll
                     for (int c = 0; c < Sh::kColumns; c++) {
                         tc::tma_load_4d(to + c * Sh::kColumnBytes, &maps.k, c * Sh::kWidth, slot, is.head, page, bar);
@@ -191,10 +212,14 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 }
                 __syncwarp();
             }
-            if (token_seen && sound) {
-                const int64_t x = exp_offset(p.exp, page_id, page_slot, is.head);
-                ke = p.exp.k[x];
-                ve = p.exp.v[x];
+        }
+#pragma unroll
+        for (int i = 0; i < kSets; i++) {
+            ke[i] = ve[i] = 0;
+            if (u < units && !dead && token_seen[i] && (uint32_t)page_id[i] < p.cache.pages) {
+                const int64_t x = exp_offset(p.exp, page_id[i], page_slot[i], is.head);
+                ke[i] = p.exp.k[x];
+                ve[i] = p.exp.v[x];
             }
         }
         find(u + 1);
@@ -305,7 +330,13 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         // scores: s[nb][x][j] is of token nb * 16 + g + 8 * (j >> 1) and statistic 2 * x + (j & 1)
         float s[NB][kGroups][4], weight[NB][2];  // weight: the power of a token's values
         auto stat_of = [](int x, int j) { return 2 * x + (j & 1); };
-        const int exps = (int)(k_exp[0] | v_exp[0] << 8), new_exp = max(top_exp, __reduce_max_sync(0xffffffffu, (int)v_exp[0]));
+        int exps[kSets], new_exp = 0;
+#pragma unroll
+        for (int i = 0; i < kSets; i++) {
+            exps[i] = (int)(k_exp[0][i] | v_exp[0][i] << 8);
+            new_exp = max(new_exp, (int)v_exp[0][i]);
+        }
+        new_exp = max(top_exp, __reduce_max_sync(0xffffffffu, new_exp));
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             float other[kGroups][4];  // every second MMA's sum: two chains, half as long
@@ -351,7 +382,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             }
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                const uint32_t mine = (uint32_t)__shfl_sync(0xffffffffu, exps, nb * Sh::MG + g + 8 * h);
+                const uint32_t mine = (uint32_t)__shfl_sync(0xffffffffu, exps[nb / 2 % kSets], (nb & 1) * Sh::MG + g + 8 * h);
                 const float power = exp_power(mine & 255);
                 weight[nb][h] = __uint_as_float((uint32_t)max((int)(mine >> 8) - new_exp + 127, 0) << 23);
 #pragma unroll
@@ -374,10 +405,11 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     }
             // values that no query sees may be anything: a zero weight would not do
             uint8_t *values = ring + stage * Sh::kStageBytes + Sh::kColumns * Sh::kColumnBytes;
-            if (lane < TB && (at + lane < it.lo_seen || at + lane >= it.hi))
-                for (int c = 0; c < 2 * DP / 32; c++)
-                    *reinterpret_cast<uint4 *>(values + c * 16 / Sh::kWidth * Sh::kColumnBytes + lane * Sh::kWidth +
-                                               c * 16 % Sh::kWidth) = make_uint4(0, 0, 0, 0);
+            for (int r = lane; r < TB; r += 32)
+                if (at + r < it.lo_seen || at + r >= it.hi)
+                    for (int c = 0; c < 2 * DP / 32; c++)
+                        *reinterpret_cast<uint4 *>(values + c * 16 / Sh::kWidth * Sh::kColumnBytes + r * Sh::kWidth +
+                                                   c * 16 % Sh::kWidth) = make_uint4(0, 0, 0, 0);
             tc::fence_async_smem();  // the next copies come after
             __syncwarp();
         }
@@ -491,8 +523,11 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         __syncwarp();  // every lane has read the stage that is filled next
 #pragma unroll
         for (int i = 0; i + 1 < kStages; i++) {
-            k_exp[i] = k_exp[i + 1];
-            v_exp[i] = v_exp[i + 1];
+#pragma unroll
+            for (int j = 0; j < kSets; j++) {
+                k_exp[i][j] = k_exp[i + 1][j];
+                v_exp[i][j] = v_exp[i + 1][j];
+            }
         }
         copy(u + kStages, stage, k_exp[kStages - 1], v_exp[kStages - 1]);
         stage++;
@@ -700,7 +735,8 @@ static int launch_few8_width(AttnParams &p, const FewMaps &maps, void *workspace
 bool launch_kv8_attn_few(AttnParams &p, int dtype, void *workspace, cudaStream_t st, int &status)
 {
     FewMaps maps = {};
-    int rows = p.d > 128 ? 16 : 32;  // of a box: a block's, where it does not cross a page
+    // of a box: a block's, where it does not cross a page
+    int rows = p.d > 128 ? 16 : p.d > 64 || dtype == DLRM_F32 ? 32 : 64;
     while (rows > 8 && p.cache.page.d % rows != 0)
         rows /= 2;
     if (p.cache.page.d % rows != 0 || !few8_maps(p, rows, maps))

@@ -405,3 +405,15 @@ def test_reserve_tokens_beyond_n_and_tables():
     assert sdi.dlrm_read_error(f) == _native.ERR_BAD_OFFSETS  # 9 do not fit a row; the rest goes beyond 6 rows
     assert new.tolist() == [3, ~0, ~0, ~0] and offsets.tolist() == [0, 3, 12, 14, 18] and to.tolist() == [1, 9]
     assert slots.tolist() == [0, 1, 2, -1, -1, -1]
+
+
+@pytest.mark.parametrize("page", [8, 16, 24, 40, 64, 128, 192])
+@pytest.mark.parametrize("d,dtype", [(64, "f16"), (48, "bf16"), (64, "f32")])
+def test_narrow_heads_on_pages_of_every_kind(page, d, dtype):
+    """Pages shorter and longer than what a warp reads at a time, none of them dividing the other."""
+    counts, lengths = [1, 2, 0, 1, 2, 1], [1, 63, 40, 64, 130, 1777]
+    for window in (0, 70):
+        case = (counts, lengths, 6, 2, d, page, 8, False, True, window, dtype)
+        table, given, caches, q = attention_inputs(case, seed=page + window)
+        out, lse = attend(case, given, caches, q, 1 / d ** 0.5)
+        check_attention(case, table, caches, q, 1 / d ** 0.5, out, lse)
