@@ -262,16 +262,29 @@ typedef struct dlrm_kv_cache8 {
 int dlrm_kv8_append(const dlrm_heads *k, const dlrm_heads *v, const dlrm_kv_batch *batch,
                     const dlrm_kv_cache8 *cache, int d, int dtype, int32_t *err_flag, dlrm_stream_t stream);
 
-/* Bytes of workspace of dlrm_kv8_attn_fwd for these sizes; 0 for invalid ones. */
+/* Bytes of workspace of dlrm_kv8_attn_fwd for these sizes, of any dtype; 0 for invalid ones. */
 size_t dlrm_kv8_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new,
                                     int64_t max_len);
 
 /*
- * dlrm_kv_attn_fwd over a cache in 8 bits: the same masks, rows, outputs, bounds and errors.
- * dtype is that of q and out.
+ * dlrm_kv_attn_fwd over a cache in 8 bits: the same masks, rows, outputs, bounds and errors;
+ * dtype is that of q and out.  Slots that no query sees may hold any code and any exponent.
  *
- * Codes are read as they are (fp16 holds every one), their powers of two are
- * applied to scores and weights in fp32.
+ * Scores, the softmax's maxima and sums and the output's sums are fp32.  Where widths are multiples of
+ * 8 and the rows of q, out and codes begin on 16 bytes, the products run on the tensor cores, 16-bit
+ * types for heads of at most 256 elements, fp32 for at most 128, but on pages of no multiple of 8 slots
+ * only 16-bit types with widths of multiples of 16.  Others take a general kernel in fp32.  On the tensor cores:
+ * - a code is an fp16 value as it is; the power of its block multiplies scores and weights
+ *   in fp32, or the code where that stays exact but for what lies 2^-41 below the largest value near by;
+ * - 16-bit queries enter exactly (bf16 lifted by a power of two a row, but for what lies 2^-38 below the
+ *   row's largest), fp32 ones in two parts, 22 bits;
+ * - weights are rounded to fp16, in two parts for fp32 and for fp16 with up to 8 rows; relative to the
+ *   largest weight times the largest power of the values so far, what lies below 2^-36 may be lost;
+ * - long chunks in bf16 (of at least 1024 rows of heads of 65 to 128, 2048 of up to 64, widths of multiples of 16) are
+ *   converted once to a bf16 cache in the workspace (four bytes for each code up to max_len, where that is at most
+ *   2 GiB; exact), and go on as dlrm_kv_attn_fwd does: weights are rounded to bf16.
+ * A value or a sum beyond the range of dtype is infinite.  Results are the same bits from run to run of one
+ * batch; a sequence's last bits may depend on which other sequences are in its batch.
  */
 int dlrm_kv8_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlrm_kv_cache8 *cache, int d, int dtype,
                       float scale, int causal, int64_t window, int64_t max_new, int64_t max_len,

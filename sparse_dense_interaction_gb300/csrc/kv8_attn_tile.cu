@@ -3,11 +3,11 @@
 //
 // The tiles, their MMAs and their softmax are those of the 16-bit cache
 // (tensor memory, one warp that issues, a lagging maximum).  What 8 bits change:
-//  - Keys and values are converted on their way into the ring: warps of their own read
-//    16 codes a lane straight from the pages, a tile ahead in registers, and write
-//    them as fp16 into the swizzled tiles that the MMAs read.  The conversion needs
-//    registers anyway, so bulk copies and a ring of raw codes would only add
-//    a trip through shared memory; pages of any size take this path.
+//  - Keys and values are converted on their way into the ring of tiles: warps of their own
+//    copy 16 codes a lane from the pages, asynchronously and two tiles ahead, and
+//    write them as fp16 into the swizzled tiles that the MMAs read; they take groups of rows in
+//    turn.  A lane converts the chunks that it copied, so a warp waits for its own
+//    copies alone, and pages of any size take this path.
 //  - Every code is multiplied by its block's power relative to a power of the tile
 //    (2^7 lifts it to fp16's range; the product is exact but for what lies 2^-41 below the
 //    largest): for keys the tile's largest, which then is part of the tile's
@@ -16,6 +16,18 @@
 //  - The softmax's threads fetch the queries, which are idle until then: bf16 rows
 //    are lifted by a power of two each, so that they fit fp16 exactly but for
 //    what lies 2^-38 below a row's largest.
+//  - The softmax reads half of a thread's scores at a time, twice: that leaves it 80 registers,
+//    and 7 warps (3 where two CTAs share an SM) to convert.
+//
+// What bounds it: shared memory and issue beside the MMAs.  A converted tile is written twice and
+// read back once more than a 16-bit one, and conversions (two values an instruction, two
+// cycles of a quarter of an SM) and multiplications run beside the softmax's exponentials.
+// 4 sequences of 2048 new on 8192 (16 heads on 4, 128 fp16 elements): 452 us, 1063
+// TFLOP/s, 0.56 of a large matrix product's rate (16-bit cache: 341); 64 users' 200
+// candidates on up to 2000, 8 heads of 64: 68 us (16-bit: 55); 4 times 2048 on 4096, 8 heads on 2 of 256: 280 us.
+// Slower: 4 or 8 warps that load a tile ahead into registers (764, 613 us for the
+// first), registers dealt out anew by role (650), bulk copies by a warp
+// of their own (468 against 475 and 75 against 73, so neither better), two query tiles a CTA for heads of 64.
 #include "kv8.cuh"
 #include "kv_tile.cuh"
 
