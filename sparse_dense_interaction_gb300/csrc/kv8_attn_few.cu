@@ -33,9 +33,9 @@
 // 155, the arithmetic alone 135.  With heads of 64 fp16 elements: 111 us, 4.6 TB/s (140
 // with blocks of 32 tokens); there a token's arithmetic, not its bytes, bounds it.  One
 // history of 262143: 59 us, of which the join, the launches and the first loads take 12.
-// 12 rows of 8 heads on 2 of 256 of 96 users with up to 3000: 74 us, 1.8 TB/s; their
-// registers leave 8 warps an SM, each bound by its own latencies.  Slower: exponents by
-// copies of 4 bytes (193 us for the 256 users), keys and values handed back one by one
+// 12 rows of 8 heads on 2 of 256 of 96 users with up to 3000: 65 us, 2.1 TB/s; their
+// outputs' registers leave 8 warps an SM, each bound by its own latencies (75 us with the queries in
+// registers too).  Slower: exponents by copies of 4 bytes (193 us for the 256 users), keys and values handed back one by one
 // (188), blocks of 16 tokens with 4 CTAs an SM (247), scores by MMAs of E4M3 with
 // queries in parts (205: the chip composes them of fp16 ones).
 #include <type_traits>
@@ -68,6 +68,9 @@ struct Few8Shape {
     static constexpr int kStages = kResident == 3 ? 2 : kStageBytes < 8192 ? 4 : 3;
     static constexpr int kCtas = kResident * kFewSms;
     static constexpr int kMerge = kOut < 32 ? kOut : 32;
+    // Beside 128 registers of outputs the queries' 64 are too many: they lie in shared memory, where the warps' outputs
+    // are joined later.  (fp32 heads of 128 on 16 rows, 64 users with up to 4000: 85 us so, 84 in registers.)
+    static constexpr bool kQueryShared = DP == 256 && kGroups == 2;
     static constexpr int kSmem = 1024 + kFewWarps * kStages * kStageBytes + 2 * kMerge * 32 * 4;
     // a stage: columns of kWidth bytes of the block's keys, then of its values, each TB rows, swizzled over its width
     static constexpr int kWidth = DP >= 128 ? 128 : 64, kColumns = DP / kWidth, kColumnBytes = TB * kWidth;
@@ -236,7 +239,9 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     for (int i = 0; i < kStages; i++)
         copy(i, i, k_exp[i], v_exp[i]);
 
-    uint32_t qa[kGroups][KG][kParts][8];  // the queries' chunks of rows g, g + 8 as fp16 (fp32: and the rest)
+    // the queries' chunks of rows g, g + 8 as fp16 (fp32: and the rest)
+    uint32_t qa[Sh::kQueryShared ? 1 : kGroups][KG][kParts][8];
+    uint4 *shared_q = reinterpret_cast<uint4 *>(merge) + lane;  // [group][chunk][part][2][32]
     float o[Sh::kOut], m[Sh::kStats], l[Sh::kStats], scale[Sh::kStats];
     int lo[Sh::kStats], hi[Sh::kStats], rows = 0;  // rows: of the sequence
     int all_lo = 0, all_hi = 0;  // positions that every row of the tile sees
@@ -252,6 +257,8 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             all_hi = seen_hi(it.seq, p.causal, row0 / p.group);
             all_lo = seen_lo(seen_hi(it.seq, p.causal, (min(rows, row0 + kFewRows) - 1) / p.group), p.window);
             float back[kGroups];  // of rows g, g + 8: what undoes their queries' lifting
+            if constexpr (Sh::kQueryShared)
+                __syncthreads();  // the item before has been joined
 #pragma unroll
             for (int h = 0; h < kGroups; h++) {
                 const int r = row0 + g + 8 * h, t = r / p.group;
@@ -289,7 +296,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     for (int j = 0; j < 2; j++)
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
-                            uint32_t &w = qa[h][i][0][4 * j + k];
+                            uint32_t &w = qa[Sh::kQueryShared ? 0 : h][i][0][4 * j + k];
                             if constexpr (std::is_same<T, __half>::value) {
                                 w = (&x[i][j].x[0].x)[k];
                             } else {
@@ -298,11 +305,23 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                                 w = pack2<__half>(y.x, y.y);
                                 if constexpr (Sh::kWide) {
                                     const float2 z = unpack2<__half>(w);
-                                    qa[h][i][1][4 * j + k] = pack2<__half>(y.x - z.x, y.y - z.y);
+                                    qa[Sh::kQueryShared ? 0 : h][i][1][4 * j + k] = pack2<__half>(y.x - z.x, y.y - z.y);
                                 }
                             }
                         }
+                if constexpr (Sh::kQueryShared)
+#pragma unroll
+                    for (int i = 0; i < KG * kParts; i++) {
+                        const uint32_t *w = qa[0][i / kParts][i % kParts];
+                        uint4 *to = shared_q + (h * KG * kParts + i) * 64;
+                        if (i % kFewWarps == warp) {
+                            to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            to[32] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    }
             }
+            if constexpr (Sh::kQueryShared)
+                __syncthreads();
 #pragma unroll
             for (int i = 0; i < Sh::kStats; i++) {
                 const int r = row0 + Sh::row(i, q);
@@ -359,6 +378,20 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 }
 #pragma unroll
                 for (int n = 0; n < kGroups; n++) {
+                    uint32_t b[kParts][8];
+#pragma unroll
+                    for (int part = 0; part < kParts; part++) {
+                        if constexpr (Sh::kQueryShared) {
+                            const uint4 *from = shared_q + ((n * KG + i) * kParts + part) * 64;
+                            const uint4 x = from[0], y = from[32];
+                            b[part][0] = x.x, b[part][1] = x.y, b[part][2] = x.z, b[part][3] = x.w;
+                            b[part][4] = y.x, b[part][5] = y.y, b[part][6] = y.z, b[part][7] = y.w;
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; k++)
+                                b[part][k] = qa[n][i][part][k];
+                        }
+                    }
                     if constexpr (Sh::kWide) {
                         // The MMA's own sums are cut off, not rounded: two steps, small terms first, then fp32
 #pragma unroll
@@ -368,7 +401,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             for (int part = 1; part >= 0; part--)
 #pragma unroll
                                 for (int f = e; f < e + 2; f++)
-                                    mma16816<__half>(t, a[f], qa[n][i][part][2 * f], qa[n][i][part][2 * f + 1]);
+                                    mma16816<__half>(t, a[f], b[part][2 * f], b[part][2 * f + 1]);
 #pragma unroll
                             for (int j = 0; j < 4; j++)
                                 s[nb][n][j] += t[j];
@@ -376,7 +409,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; e++)
-                            mma16816<__half>(e & 1 ? other[n] : s[nb][n], a[e], qa[n][i][0][2 * e], qa[n][i][0][2 * e + 1]);
+                            mma16816<__half>(e & 1 ? other[n] : s[nb][n], a[e], b[0][2 * e], b[0][2 * e + 1]);
                     }
                 }
             }
@@ -682,7 +715,7 @@ static bool few8_maps(const AttnParams &p, int rows, FewMaps &m)
 
 // Bytes of an item up to which it stays whole.  Whole against runs, us (bf16): 256 users with up to 8192, 4 heads of 128,
 // 187 and 178; 64 with up to 2000 28 and 36; 16 with up to 2000 22 and 25; one with 3000 20 and 18; 96 with 1500, 12
-// rows of 2 heads of 256, 61 and 72.
+// rows of 2 heads of 256, 51 and 59.
 constexpr int64_t kFew8WholeBytes = 480 << 10, kFew8WholeBytesPerItem = 1536;
 
 template <typename T, int DP, int kGroups>

@@ -432,7 +432,7 @@ int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
         return status != DLRM_OK ? status : launch_kv_attn(p, dtype, static_cast<char *>(workspace) + widened, st);
     }
     // Rows of 16, as with the 16-bit cache, but for heads above 128 too, rows of 16 against tiles (bf16, 8 heads on
-    // 2 of 256): 96 users with 1500 and 12 rows 61 and 87 us; 16 with up to 4000 and 256 rows 113 and 72; 4 with
+    // 2 of 256): 96 users with 1500 and 12 rows 51 and 87 us; 16 with up to 4000 and 256 rows 113 and 72; 4 with
     // 4096 and 8192 rows 1678 and 280.
     if (few && (!tile || rows <= 16 || (p.d > 64 && p.d <= 128 && rows <= 32 && seen <= 1024)) &&
         launch_kv8_attn_few(p, dtype, workspace, st, status))
