@@ -247,6 +247,9 @@ struct AttnParams {
     int wait_polls;            // of a wait inside a kernel, before it gives up
     int32_t *err;
     ExpView exp;               // of a cache in 8 bits
+    // of an fp16 copy of such a cache, [sequence][page][head]: exponents that a page's keys (low byte) and values are
+    // relative to
+    const uint16_t *refs;
 };
 
 // What one CTA works on: rows of tile `tile` of head `head` of the sequence,

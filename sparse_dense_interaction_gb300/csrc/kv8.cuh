@@ -55,4 +55,23 @@ __device__ __forceinline__ int64_t exp_offset(const ExpView &x, int64_t page, ui
     return page * x.page_stride + (int64_t)x.block.div(slot) * x.block_stride + (int64_t)head * x.head_stride;
 }
 
+// Codes as fp16 times their block's power relative to a larger one, lifted by 2^7: 448 * 2^7 is near fp16's largest.
+// Exact but for what lies 2^-41 below the largest.
+constexpr int kCodeLift = 7;
+
+// 2^(e + 7) as a pair of fp16, e <= 0; subnormal, at last 0, below 2^-14.
+__device__ __forceinline__ uint32_t relative_power(int e)
+{
+    const int b = e + kCodeLift + 15;
+    const uint32_t h = b > 0 ? (uint32_t)b << 10 : (b > -10 ? 0x400u >> (1 - b) : 0u);
+    return h | h << 16;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
+{
+    uint32_t c;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
 }  // namespace dlrm

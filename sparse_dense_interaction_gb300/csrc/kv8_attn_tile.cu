@@ -22,9 +22,10 @@
 // What bounds it: shared memory and issue beside the MMAs.  A converted tile is written twice and
 // read back once more than a 16-bit one, and conversions (two values an instruction, two
 // cycles of a quarter of an SM) and multiplications run beside the softmax's exponentials.
-// 4 sequences of 2048 new on 8192 (16 heads on 4, 128 fp16 elements): 452 us, 1063
-// TFLOP/s, 0.56 of a large matrix product's rate (16-bit cache: 341); 64 users' 200
-// candidates on up to 2000, 8 heads of 64: 68 us (16-bit: 55); 4 times 2048 on 4096, 8 heads on 2 of 256: 280 us.
+// 16 sequences of 256 new on up to 8192 (16 heads on 4, 128 bf16 elements): 142 us; 64 users' 200
+// candidates on up to 2000, 8 heads of 64: 68 us (16-bit cache: 55); 4 times 2048 on 4096, 8 heads
+// on 2 of 256: 280 us.  Longer chunks of narrower heads convert once instead (4 of 2048 on 8192,
+// 16 heads on 4 of 128, would take 452 us here).
 // Slower: 4 or 8 warps that load a tile ahead into registers (764, 613 us for the
 // first), registers dealt out anew by role (650), bulk copies by a warp
 // of their own (468 against 475 and 75 against 73, so neither better), two query tiles a CTA for heads of 64.
@@ -51,28 +52,12 @@ struct Tile8Shape : TileShape<DP, kTwo, (DP == 256 ? 2 : DP == 128 || !kTwo ? 4 
 };
 
 constexpr int kTile8Refs = 8;   // tiles whose powers are kept: more than the ring holds
-constexpr int kTile8Lift = 7;   // log2 of what the codes are lifted by: 448 * 2^7 is near fp16's largest
 constexpr int kConvertBarrier = 9;
 
 struct Tile8Bars : TileBars {
     int k_ref[kTile8Refs], v_ref[kTile8Refs];  // of a tile: the exponents that its codes are relative to
     int warp_ref[2][8][2];
 };
-
-// 2^(e + 7) as a pair of fp16, e <= 0; subnormal, at last 0, below 2^-14.
-__device__ __forceinline__ uint32_t relative_power(int e)
-{
-    const int b = e + kTile8Lift + 15;
-    const uint32_t h = b > 0 ? (uint32_t)b << 10 : (b > -10 ? 0x400u >> (1 - b) : 0u);
-    return h | h << 16;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
-{
-    uint32_t c;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-    return c;
-}
 
 // The warps that convert.  A tile begins at a multiple of 128 positions.  A lane reads back the chunks of codes
 // that it copied itself, so a warp waits for nobody's copies but its own.
@@ -341,7 +326,7 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
         };
         const int k_ref = b.k_ref[j % kTile8Refs], now_ref = b.v_ref[j % kTile8Refs];
         // never 0: a masked score is -infinity
-        const float scale_log2 = fmaxf(row_scale * exp_power((uint32_t)max(k_ref - kTile8Lift, 0)), 1.2e-38f);
+        const float scale_log2 = fmaxf(row_scale * exp_power((uint32_t)max(k_ref - kCodeLift, 0)), 1.2e-38f);
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
@@ -407,7 +392,7 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
     l = b.agree[t][0][in] + b.agree[t][1][in];
     float inv = 0.f, lse = -INFINITY;
     if (l != 0.f) {  // not a number either: then neither is the row
-        inv = 1.f / l * exp_power((uint32_t)v_ref) * (1.f / (1 << kTile8Lift));
+        inv = 1.f / l * exp_power((uint32_t)v_ref) * (1.f / (1 << kCodeLift));
         lse = m + (log2f(l) - kTileLift<__half>);
     }
     if (tiles > 0) {

@@ -1,10 +1,14 @@
 // The part of a cache in 8 bits that a batch sees, as a 16-bit cache in the workspace.
 //
 // Long chunks read every key and value again for each tile of their rows, and
-// converting them each time costs the tiles a third of their time.  bf16 holds every
-// code times its power exactly, so for such batches they are converted once, and
-// the 16-bit cache's tiles do the rest.  Memory bounds the conversion (a byte read, two written,
-// which mostly stay in L2): 4 sequences of 2048 new on 8192, 16 heads on 4 of 128, take 364 us, on a 16-bit cache 341.
+// converting them each time costs the tiles a third of their time.  So for such batches they are
+// converted once, and the 16-bit cache's tiles do the rest.  bf16 holds every code
+// times its power exactly; fp16 holds it relative to the largest power of its page of the
+// copy, which the tiles apply to their scores and weights.  Memory bounds the
+// conversion (a byte read, two written, which mostly stay in L2): 4 sequences of 2048 new on
+// 8192, 16 heads on 4 of 128, take 364 us in bf16, on a 16-bit cache 341.
+#include <type_traits>
+
 #include "kv8.cuh"
 
 namespace dlrm {
@@ -13,17 +17,21 @@ constexpr int kWidenThreads = 256, kWidenPage = 128;
 
 struct WidenParams {
     AttnParams p;
-    char *k, *v;      // [sequence * pages + page][head][kWidenPage][d], bf16
+    char *k, *v;      // [sequence * pages + page][head][kWidenPage][d], bf16 or fp16
     int32_t *table;   // [sequence][pages]
+    uint16_t *refs;   // [sequence][pages][heads], of fp16
     int pages;        // of a sequence
     FastDiv chunks, heads;  // 16 codes of a row; heads
 };
 
-__device__ __forceinline__ void widen16(const char *from, uint32_t e, char *to)
+// 16 codes, times 2^(e - 127), or for fp16 2^(e - ref + 7).
+template <typename T>
+__device__ __forceinline__ void widen16(const char *from, uint32_t e, int ref, char *to)
 {
     const uint4 c = *reinterpret_cast<const uint4 *>(from);
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     const float power = exp_power(e);
+    const uint32_t relative = relative_power((int)e - ref);
     uint32_t x[8];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -31,8 +39,12 @@ __device__ __forceinline__ void widen16(const char *from, uint32_t e, char *to)
         decode4(in[i], h[0], h[1]);
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-            const float2 y = unpack2<__half>(h[k]);
-            x[2 * i + k] = pack2<__nv_bfloat16>(y.x * power, y.y * power);
+            if constexpr (std::is_same<T, __half>::value) {
+                x[2 * i + k] = hmul2(h[k], relative);
+            } else {
+                const float2 y = unpack2<__half>(h[k]);
+                x[2 * i + k] = pack2<T>(y.x * power, y.y * power);
+            }
         }
     }
     reinterpret_cast<uint4 *>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
@@ -40,12 +52,14 @@ __device__ __forceinline__ void widen16(const char *from, uint32_t e, char *to)
 }
 
 // A CTA per sequence, page of the copy and head.
+template <typename T>
 __global__ void __launch_bounds__(kWidenThreads)
 kv8_widen_kernel(const __grid_constant__ WidenParams w)
 {
     const AttnParams &p = w.p;
     __shared__ int64_t row_codes[kWidenPage];  // -1: a row of zeros
     __shared__ uint8_t row_exps[2][kWidenPage];
+    __shared__ uint32_t warp_refs[kWidenThreads / 32];
     const uint32_t number = w.heads.div(blockIdx.x);  // of the page
     const int head = (int)(blockIdx.x - number * w.heads.d), page = (int)(number % (uint32_t)w.pages);
     const int64_t s = number / (uint32_t)w.pages;
@@ -59,6 +73,7 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
     if (lo >= hi)
         return;
     const int r = threadIdx.x;
+    uint32_t k_exp = 0, v_exp = 0;
     if (r < hi - lo) {
         const uint32_t at = lo + r, n = p.cache.page.div(at), slot = at - n * p.cache.page.d;
         const uint32_t id = (uint32_t)p.batch.table[s * p.batch.table_stride + n];
@@ -66,11 +81,26 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
         if (id < p.cache.pages) {
             row_codes[r] = id * p.cache.page_stride + slot * p.cache.slot_stride + head * p.cache.head_stride;
             const int64_t x = exp_offset(p.exp, id, slot, head);
-            row_exps[0][r] = p.exp.k[x];
-            row_exps[1][r] = p.exp.v[x];
+            row_exps[0][r] = k_exp = p.exp.k[x];
+            row_exps[1][r] = v_exp = p.exp.v[x];
         } else {
             raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
         }
+    }
+    int k_ref = 0, v_ref = 0;
+    if constexpr (std::is_same<T, __half>::value) {
+        k_exp = __reduce_max_sync(0xffffffffu, k_exp);
+        v_exp = __reduce_max_sync(0xffffffffu, v_exp);
+        if ((r & 31) == 0)
+            warp_refs[r / 32] = k_exp | v_exp << 16;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWidenPage / 32; i++) {
+            k_ref = max(k_ref, (int)(warp_refs[i] & 0xffff));
+            v_ref = max(v_ref, (int)(warp_refs[i] >> 16));
+        }
+        if (r == 0)
+            w.refs[blockIdx.x] = (uint16_t)(k_ref | v_ref << 8);
     }
     __syncthreads();
     const int per_row = p.d / 16, all = (hi - lo) * per_row;
@@ -80,8 +110,8 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
         const int x = (int)w.chunks.div((uint32_t)i), c = i - x * per_row;
         const int64_t from = row_codes[x] + c * 16, to = base + i * 32;
         if (row_codes[x] >= 0) {
-            widen16(p.cache.k + from, row_exps[0][x], w.k + to);
-            widen16(p.cache.v + from, row_exps[1][x], w.v + to);
+            widen16<T>(p.cache.k + from, row_exps[0][x], k_ref, w.k + to);
+            widen16<T>(p.cache.v + from, row_exps[1][x], v_ref, w.v + to);
         } else {
             const uint4 zero = make_uint4(0, 0, 0, 0);
             for (int k = 0; k < 2; k++) {
@@ -92,24 +122,25 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
     }
 }
 
-// Bytes of the copy, 0 where there is none.  It pays where tiles of rows read a key and value often, from 4 tiles of
+// Bytes of the copy, 0 where there is none.  It pays where tiles of rows read a key and value often, from 6 tiles of
 // 256 rows on with heads above 64 and from 8 on below (converted once and by every tile, us, 16 heads on 4 of 128: 4
-// sequences of 2048 new on 8192 364 and 476; 48 of 512 131 and 181; 16 of 256 on 8192 275 and 287, of
-// 128 229 and 206; 64 of 500 on up to 2000, 8 heads of 64, 131 and 113, of 1000 192 and 188).  It takes four times
+// sequences of 2048 new on 8192 each, bf16 364 and 476, on up to 8192, fp16, 198 and 229; 16 of 512 on up to 4000 106
+// and 111, of 400 91 and 83, on 4000 each 204 and 223; 16 of 256 on up to 8192 154 and 142; 64 of 500 on up to 2000, 8
+// heads of 64, 131 and 113, of 1000 192 and 188).  It takes four times
 // the bytes of the codes up to max_len, which may be far above the lengths: at most kWidenMost.
 constexpr int64_t kWidenMost = (int64_t)2 << 30;
 
 size_t widen_workspace(int64_t S, int heads, int group, int d, int64_t max_new, int64_t max_len)
 {
     const int64_t pages = (max_len + kWidenPage - 1) / kWidenPage;
-    if (max_new * group < (d > 64 ? 1024 : 2048) || d > 128 || d % 16 != 0 || pages == 0 || S == 0 ||
+    if (max_new * group < (d > 64 ? 1536 : 2048) || d > 128 || d % 16 != 0 || pages == 0 || S == 0 ||
         pages > kWidenMost / (4 * kWidenPage * S * heads * d))
         return 0;
-    return (size_t)(4 * kWidenPage * S * pages * heads * d + (S * pages * 4 + 255) / 256 * 256);
+    return (size_t)(4 * kWidenPage * S * pages * heads * d + (S * pages * (4 + 2 * heads) + 255) / 256 * 256);
 }
 
 // Converts, and turns the parameters to the copy; the workspace begins with it.
-int launch_widen(AttnParams &p, void *workspace, cudaStream_t st)
+int launch_widen(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
 {
     WidenParams w;
     const int64_t pages = (p.max_len + kWidenPage - 1) / kWidenPage, all = p.batch.S * pages;
@@ -118,10 +149,15 @@ int launch_widen(AttnParams &p, void *workspace, cudaStream_t st)
     w.k = static_cast<char *>(workspace);
     w.v = w.k + bytes;
     w.table = reinterpret_cast<int32_t *>(w.v + bytes);
+    w.refs = reinterpret_cast<uint16_t *>(w.table + all);
     w.pages = (int)pages;
     w.chunks = FastDiv::make((uint32_t)p.d / 16);
     w.heads = FastDiv::make((uint32_t)p.cache.heads);
-    kv8_widen_kernel<<<(unsigned)(all * p.cache.heads), kWidenThreads, 0, st>>>(w);
+    const unsigned ctas = (unsigned)(all * p.cache.heads);
+    if (dtype == DLRM_F16)
+        kv8_widen_kernel<__half><<<ctas, kWidenThreads, 0, st>>>(w);
+    else
+        kv8_widen_kernel<__nv_bfloat16><<<ctas, kWidenThreads, 0, st>>>(w);
     count_launch(st);
     const int64_t row = p.d, head = kWidenPage * row;
     p.cache = CacheView{w.k, w.v, head * p.cache.heads, row, head, (uint32_t)all, FastDiv::make(kWidenPage), p.cache.heads};
@@ -129,6 +165,7 @@ int launch_widen(AttnParams &p, void *workspace, cudaStream_t st)
     p.batch.table_stride = pages;
     p.batch.capacity = p.batch.capacity < pages * kWidenPage ? p.batch.capacity : pages * kWidenPage;
     p.exp = ExpView{};
+    p.refs = dtype == DLRM_F16 ? w.refs : nullptr;
     return launch_status();
 }
 

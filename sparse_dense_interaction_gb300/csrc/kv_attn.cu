@@ -20,7 +20,7 @@ int launch_kv_attn_few(AttnParams &, int, void *, cudaStream_t);
 int launch_kv_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
 int launch_kv8_attn_tile(const AttnParams &, int, int64_t, cudaStream_t);
 size_t widen_workspace(int64_t, int, int, int, int64_t, int64_t);
-int launch_widen(AttnParams &, void *, cudaStream_t);
+int launch_widen(AttnParams &, int, void *, cudaStream_t);
 bool launch_kv8_attn_few(AttnParams &, int, void *, cudaStream_t, int &);
 
 // ---------------------------------------------------------------- general kernel
@@ -425,10 +425,10 @@ int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     const bool tile = rows_even && codes_even && p.d % 16 == 0 && dtype != DLRM_F32;
     const bool few = rows_even && codes_even && p.d <= (dtype == DLRM_F32 ? 128 : 256);
     int status;
-    // Long chunks of bf16 queries, which hold every value exactly: the codes are converted once (heads of up to 128).
+    // Long chunks: the codes are converted once (heads of up to 128).
     const size_t widened = widen_workspace(p.batch.S, c.heads, p.group, p.d, p.max_new, p.max_len);
-    if (tile && dtype == DLRM_BF16 && widened > 0) {
-        status = launch_widen(p, workspace, st);
+    if (tile && widened > 0) {
+        status = launch_widen(p, dtype, workspace, st);
         return status != DLRM_OK ? status : launch_kv_attn(p, dtype, static_cast<char *>(workspace) + widened, st);
     }
     // Rows of 16, as with the 16-bit cache, but for heads above 128 too, rows of 16 against tiles (bf16, 8 heads on

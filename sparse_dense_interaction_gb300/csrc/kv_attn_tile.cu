@@ -33,6 +33,7 @@
 // each of 64 users with up to 2000 events (8 heads of 64 f16 elements): 53 us,
 // where a CTA lives for 9 tiles of positions and its start, its end and the
 // last CTAs' uneven ends count most.
+#include "kv8.cuh"
 #include "kv_tile.cuh"
 
 namespace dlrm {
@@ -238,7 +239,10 @@ __device__ void tile_copy_rows(const AttnParams &p, const AttnWork &w, uint8_t *
         tc::mbar_arrive(&b.full[done++ % Sh::kSlots]);
 }
 
-template <typename T, int DP, bool kTwo>
+// kPowers: keys and values are those of a cache in 8 bits relative to powers of their page of 128 positions, which is a
+// tile.  The keys' power is part of the tile's scale.  The output is relative to the largest of the values' powers
+// so far; where a tile's is 2^-x of it, its weights are lifted by so much less (x up to 60: no sum loses anything).
+template <typename T, int DP, bool kTwo, bool kPowers>
 __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq, TileBars &b, int tiles)
 {
     using Sh = TileShape<DP, kTwo>;
@@ -254,7 +258,21 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
     const int hi = mine ? min(seen_hi(w.seq, p.causal, token), w.hi) : 0x7fffffff;
     const int lo = mine ? max(seen_lo(seen_hi(w.seq, p.causal, token), p.window), w.lo) : 0;
     float m = -INFINITY, l = 0.f;
+    const uint16_t *refs = nullptr;  // of the tile
+    if constexpr (kPowers)
+        refs = p.refs + (w.s * p.batch.table_stride + (w.lo >> 7)) * p.cache.heads + w.head;
+    int v_ref = 0;  // the exponent that the output is relative to
     for (int j = 0; j < tiles; j++) {
+        float scale_log2 = p.scale_log2;
+        int fall = 0, now_ref = 0;  // how far the tile's values' power lies below the output's
+        if constexpr (kPowers) {
+            const int ref = __ldg(refs);
+            refs += p.cache.heads;
+            // never 0: a masked score is -infinity
+            scale_log2 = fmaxf(scale_log2 * exp_power((uint32_t)max((ref & 255) - kCodeLift, 0)), 1.2e-38f);
+            now_ref = max(v_ref, ref >> 8);
+            fall = min(now_ref - (ref >> 8), 60);
+        }
         // a wait that runs out is seen at the end; the pair's barriers below want every warp
         tc::mbar_wait(&b.s_full[t], j & 1, &b.aborted, p.wait_polls);
         __syncwarp();
@@ -274,15 +292,20 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
 #pragma unroll
         for (int i = 0; i < kHalf; i += 2)
             top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-        float now = __fmul_ru(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), p.scale_log2);
+        float now = __fmul_ru(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale_log2);
         b.agree[t][half][in] = now;
         tc::named_sync(pair, 64);
         now = fmaxf(now, b.agree[t][1 - half][in]);
-        if (__any_sync(0xffffffffu, now - m > kTileSlack<T>)) {
+        if (__any_sync(0xffffffffu, now - m > kTileSlack<T> || (kPowers && now_ref > v_ref))) {
             // also from -infinity; the output of the tiles before is complete: the scores' MMA came after it
-            const float next = fmaxf(m, now), f = next == -INFINITY ? 1.f : exp2_approx(m - next);
+            const float next = fmaxf(m, now);
+            float f = next == -INFINITY ? 1.f : exp2_approx(m - next);
             m = next;
             l *= f;
+            if constexpr (kPowers) {
+                f *= __uint_as_float((uint32_t)max(127 + v_ref - now_ref, 0) << 23);
+                v_ref = now_ref;
+            }
             if (j > 0) {
 #pragma unroll 1
                 for (int c = 0; c < kCols; c += 16) {
@@ -295,8 +318,8 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
                 }
             }
         }
-        const float lift = __fsub_rd(kTileLift<T>, m == -INFINITY ? 0.f : m);
-        const float2 scale = make_float2(p.scale_log2, p.scale_log2), off = make_float2(lift, lift);
+        const float lift = __fsub_rd(kTileLift<T> - (float)fall, m == -INFINITY ? 0.f : m);
+        const float2 scale = make_float2(scale_log2, scale_log2), off = make_float2(lift, lift);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < kHalf / 32; c++) {
@@ -311,7 +334,8 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
             }
             tc::tmem_st16(p_at + c * 16, packed);
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        const float sums = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        l += kPowers ? sums * __uint_as_float((uint32_t)(127 + fall) << 23) : sums;
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
@@ -325,6 +349,8 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
     float inv = 0.f, lse = -INFINITY;
     if (l != 0.f) {  // not a number either: then neither is the row
         inv = 1.f / l;
+        if constexpr (kPowers)
+            inv *= exp_power((uint32_t)v_ref) * (1.f / (1 << kCodeLift));
         lse = m + (log2f(l) - kTileLift<T>);
     }
     if (tiles > 0) {
@@ -335,7 +361,7 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
     tile_write<T, DP, kTwo>(p, w, sq, b.tmem, t, half, tiles, inv, lse);
 }
 
-template <typename T, int DP, bool kBulk, bool kTwo>
+template <typename T, int DP, bool kBulk, bool kTwo, bool kPowers>
 __global__ void __launch_bounds__(TileShape<DP, kTwo>::threads(kBulk), kTwo ? 1 : 2)
 kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TileMaps maps)
 {
@@ -380,7 +406,7 @@ kv_attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     tc::fence_after_sync();
     if (warp < Sh::kSoftmaxWarps) {
         if (warp < 8 || two)
-            tile_softmax<T, DP, kTwo>(p, w, sq, b, tiles);
+            tile_softmax<T, DP, kTwo, kPowers>(p, w, sq, b, tiles);
     } else if (warp < kLast) {
         if (tiles > 0) {
             if constexpr (kBulk) {
@@ -442,16 +468,16 @@ static bool tile_maps(const AttnParams &p, int dtype, TileMaps &m)
     return true;
 }
 
-template <typename T, int DP, bool kBulk, bool kTwo>
+template <typename T, int DP, bool kBulk, bool kTwo, bool kPowers = false>
 static int launch_tile(const AttnParams &p, const TileMaps &maps, int64_t ctas, cudaStream_t st)
 {
     using Sh = TileShape<DP, kTwo>;
     constexpr int smem = Sh::kTiles + sizeof(TileBars);
     static std::atomic<unsigned long long> done{0};
-    const int s = allow_dynamic_smem((const void *)kv_attn_tile_kernel<T, DP, kBulk, kTwo>, smem, &done);
+    const int s = allow_dynamic_smem((const void *)kv_attn_tile_kernel<T, DP, kBulk, kTwo, kPowers>, smem, &done);
     if (s != DLRM_OK)
         return s;
-    kv_attn_tile_kernel<T, DP, kBulk, kTwo><<<(unsigned)ctas, Sh::threads(kBulk), smem, st>>>(p, maps);
+    kv_attn_tile_kernel<T, DP, kBulk, kTwo, kPowers><<<(unsigned)ctas, Sh::threads(kBulk), smem, st>>>(p, maps);
     count_launch(st);
     return DLRM_OK;
 }
@@ -469,8 +495,15 @@ template <typename T>
 static int launch_tile_type(const AttnParams &p, int dtype, int64_t ctas, cudaStream_t st)
 {
     TileMaps maps = {};
-    return tile_maps(p, dtype, maps) ? launch_tile_shape<T, true>(p, maps, ctas, st)
-                                     : launch_tile_shape<T, false>(p, maps, ctas, st);
+    const bool bulk = tile_maps(p, dtype, maps);
+    if constexpr (std::is_same<T, __half>::value)
+        if (p.refs) {  // pages of 128, and more than 256 rows
+            if (!bulk || p.rows != 256)
+                return DLRM_ERR_UNSUPPORTED;
+            return p.d > 64 ? launch_tile<T, 128, true, true, true>(p, maps, ctas, st)
+                            : launch_tile<T, 64, true, true, true>(p, maps, ctas, st);
+        }
+    return bulk ? launch_tile_shape<T, true>(p, maps, ctas, st) : launch_tile_shape<T, false>(p, maps, ctas, st);
 }
 
 int launch_kv_attn_tile(const AttnParams &p, int dtype, int64_t ctas, cudaStream_t st)

@@ -41,6 +41,9 @@ KINDS = [
     ([200, 5], [333, 64], 2, 1, 128, 7, 7, False, True, 0, "f16"), ([300, 30], [400, 700], 4, 1, 128, 128, 32, True, True, 0, "bf16"),
     ([40, 3], [1000, 50], 4, 2, 256, 32, 8, True, True, 0, "bf16"), ([70], [900], 2, 2, 160, 12, 4, False, False, 0, "f16"),
     ([2, 30], [100, 260], 2, 2, 17, 5, 5, False, True, 0, "f32"), ([3], [700], 2, 1, 20, 5, 1, False, True, 0, "bf16"),
+    # chunks for which the codes are converted once
+    ([300, 5], [900, 700], 12, 2, 128, 32, 8, False, True, 0, "f16"), ([700, 1], [1500, 90], 8, 2, 64, 16, 16, True, True, 300, "f16"),
+    ([260, 40], [400, 500], 12, 2, 96, 12, 3, False, True, 0, "bf16"), ([520], [600], 4, 1, 48, 64, 1, True, False, 0, "f16"),
 ]
 
 
