@@ -6,7 +6,7 @@
 // times its power exactly; fp16 holds it relative to the largest power of its page of the
 // copy, which the tiles apply to their scores and weights.  Memory bounds the
 // conversion (a byte read, two written, which mostly stay in L2): 4 sequences of 2048 new on
-// 8192, 16 heads on 4 of 128, take 364 us in bf16, on a 16-bit cache 341.
+// 8192, 16 heads on 4 of 128, take 363 us in bf16 and 378 in fp16, on a 16-bit cache 341.
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -21,20 +21,21 @@ struct WidenParams {
     int32_t *table;   // [sequence][pages]
     uint16_t *refs;   // [sequence][pages][heads], of fp16
     int pages;        // of a sequence
-    FastDiv chunks, heads;  // 16 codes of a row; heads
+    FastDiv chunks, heads;  // 8 codes of a row; heads
 };
 
-// 16 codes, times 2^(e - 127), or for fp16 2^(e - ref + 7).
+// 8 codes, times 2^(e - 127), or for fp16 2^(e - ref + 7).  (16 a lane, in two stores that each write half sectors: 366
+// us for the 4 sequences above instead of 363.)
 template <typename T>
-__device__ __forceinline__ void widen16(const char *from, uint32_t e, int ref, char *to)
+__device__ __forceinline__ void widen8(const char *from, uint32_t e, int ref, char *to)
 {
-    const uint4 c = *reinterpret_cast<const uint4 *>(from);
-    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    const uint2 c = *reinterpret_cast<const uint2 *>(from);
+    const uint32_t in[2] = {c.x, c.y};
     const float power = exp_power(e);
     const uint32_t relative = relative_power((int)e - ref);
-    uint32_t x[8];
+    uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < 2; i++) {
         uint32_t h[2];
         decode4(in[i], h[0], h[1]);
 #pragma unroll
@@ -47,8 +48,7 @@ __device__ __forceinline__ void widen16(const char *from, uint32_t e, int ref, c
             }
         }
     }
-    reinterpret_cast<uint4 *>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<uint4 *>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    *reinterpret_cast<uint4 *>(to) = make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 // A CTA per sequence, page of the copy and head.
@@ -103,28 +103,25 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
             w.refs[blockIdx.x] = (uint16_t)(k_ref | v_ref << 8);
     }
     __syncthreads();
-    const int per_row = p.d / 16, all = (hi - lo) * per_row;
+    const int per_row = p.d / 8, all = (hi - lo) * per_row;
     const int64_t base = ((int64_t)blockIdx.x * kWidenPage + lo - start) * p.d * 2;
 #pragma unroll 4
     for (int i = threadIdx.x; i < all; i += kWidenThreads) {
         const int x = (int)w.chunks.div((uint32_t)i), c = i - x * per_row;
-        const int64_t from = row_codes[x] + c * 16, to = base + i * 32;
+        const int64_t from = row_codes[x] + c * 8, to = base + i * 16;
         if (row_codes[x] >= 0) {
-            widen16<T>(p.cache.k + from, row_exps[0][x], k_ref, w.k + to);
-            widen16<T>(p.cache.v + from, row_exps[1][x], v_ref, w.v + to);
+            widen8<T>(p.cache.k + from, row_exps[0][x], k_ref, w.k + to);
+            widen8<T>(p.cache.v + from, row_exps[1][x], v_ref, w.v + to);
         } else {
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            for (int k = 0; k < 2; k++) {
-                reinterpret_cast<uint4 *>(w.k + to)[k] = zero;
-                reinterpret_cast<uint4 *>(w.v + to)[k] = zero;
-            }
+            *reinterpret_cast<uint4 *>(w.k + to) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(w.v + to) = make_uint4(0, 0, 0, 0);
         }
     }
 }
 
 // Bytes of the copy, 0 where there is none.  It pays where tiles of rows read a key and value often, from 6 tiles of
 // 256 rows on with heads above 64 and from 8 on below (converted once and by every tile, us, 16 heads on 4 of 128: 4
-// sequences of 2048 new on 8192 each, bf16 364 and 476, on up to 8192, fp16, 198 and 229; 16 of 512 on up to 4000 106
+// sequences of 2048 new on 8192 each, bf16 363 and 476, on up to 8192, fp16, 198 and 229; 16 of 512 on up to 4000 106
 // and 111, of 400 91 and 83, on 4000 each 204 and 223; 16 of 256 on up to 8192 154 and 142; 64 of 500 on up to 2000, 8
 // heads of 64, 131 and 113, of 1000 192 and 188).  It takes four times
 // the bytes of the codes up to max_len, which may be far above the lengths: at most kWidenMost.
@@ -151,7 +148,7 @@ int launch_widen(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     w.table = reinterpret_cast<int32_t *>(w.v + bytes);
     w.refs = reinterpret_cast<uint16_t *>(w.table + all);
     w.pages = (int)pages;
-    w.chunks = FastDiv::make((uint32_t)p.d / 16);
+    w.chunks = FastDiv::make((uint32_t)p.d / 8);
     w.heads = FastDiv::make((uint32_t)p.cache.heads);
     const unsigned ctas = (unsigned)(all * p.cache.heads);
     if (dtype == DLRM_F16)
