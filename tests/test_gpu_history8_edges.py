@@ -420,3 +420,18 @@ def test_narrow_heads_on_pages_of_every_kind(page, d, dtype):
         table, given, caches, q = attention_inputs(case, seed=page + window)
         out, lse = attend(case, given, caches, q, 1 / d ** 0.5)
         check_attention(case, table, caches, q, 1 / d ** 0.5, out, lse)
+
+
+@pytest.mark.parametrize("case", KINDS)
+def test_long_runs_of_zeros(case):
+    """Runs longer than any tile whose values, or keys, are zeros: their weights count, wherever they come."""
+    counts, lengths, hq, hk, d, page, block, first, causal, window, dtype = case
+    table, given, caches, q = attention_inputs(case, seed=9)
+    for s, n in enumerate(lengths):
+        for i in range(-(-n // page)):
+            for kind, run in ((0, 300), (1, 280)):
+                if i * page // run % 2 == 0:
+                    caches[kind][0][table[s, i]] = 0
+                    caches[kind][1][table[s, i]] = 0
+    out, lse = attend(case, given, caches, q, 1 / d ** 0.5)
+    check_attention(case, table, caches, q, 1 / d ** 0.5, out, lse)
