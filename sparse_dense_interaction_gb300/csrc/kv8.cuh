@@ -49,6 +49,18 @@ __device__ __forceinline__ int exponent_of(float top)
 // What values are multiplied by before they are encoded: 2^(127 - e), e = 0 .. 247.
 __device__ __forceinline__ float encode_power(int e) { return __uint_as_float((uint32_t)(254 - (e < 1 ? 1 : e)) << 23); }
 
+// 2^x, of x within fp32's normal range.
+__device__ __forceinline__ float power_of(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+
+// What scores that are relative to 2^x are multiplied by.  In two steps, so that it stays a normal number wherever the
+// result is one; never 0 (a masked score is -infinity) and never infinite (a score of 0 stays one).  The scores
+// are below 2^34, so those under the lower bound are 0 but for 2^-92.
+__device__ __forceinline__ float score_scale(float scale_log2, int x)
+{
+    x = min(max(x, -252), 252);
+    return fminf(fmaxf(scale_log2 * power_of(x / 2) * power_of(x - x / 2), 1.2e-38f), 3.4e38f);
+}
+
 // Place of the exponent of a page's slot and head.
 __device__ __forceinline__ int64_t exp_offset(const ExpView &x, int64_t page, uint32_t slot, int head)
 {

@@ -15,7 +15,8 @@
 //    value row are a lane's; the codes of two tokens are interleaved by byte
 //    permutes before they are converted, which puts them where the MMA wants pairs.
 //  - The keys' powers multiply the scores, the values' powers the weights, in
-//    fp32: a factor for a token and all rows, so 2 products for a score.
+//    fp32: a factor for a token and all rows, so 2 products for a score.  The keys' are relative to
+//    the largest that the warp has seen so far, which is part of the scale, so that a lifted sum stays finite.
 //    A weight is held relative to the largest power that the warp has seen so far
 //    and rises with it (the output is scaled down when that grows, as it is when a maximum
 //    does), so fp16's range is the row's: what a token gathers is off by at most
@@ -245,7 +246,15 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     float o[Sh::kOut], m[Sh::kStats], l[Sh::kStats], scale[Sh::kStats];
     int lo[Sh::kStats], hi[Sh::kStats], rows = 0;  // rows: of the sequence
     int all_lo = 0, all_hi = 0;  // positions that every row of the tile sees
-    int top_exp = 0;             // the largest exponent of the values so far: weights are relative to its power
+    int key_exp = 0, top_exp = 0;  // the largest exponents of keys and values so far: scores and weights are relative to them
+    int back[kGroups];             // of rows g, g + 8: 2^back undoes their queries' lifting
+    auto set_scale = [&]() {
+#pragma unroll
+        for (int i = 0; i < Sh::kStats; i++) {
+            const int x = std::is_same<T, __half>::value ? 0 : __shfl_sync(0xffffffffu, back[i >> 1], (2 * q + (i & 1)) * 4);
+            scale[i] = score_scale(p.scale_log2, x + key_exp - 127);
+        }
+    };
     bool fresh = true, first_item = true;
     int stage = 0;
     uint32_t phase = 0;
@@ -256,7 +265,6 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
             rows = it.seq.count * p.group;
             all_hi = seen_hi(it.seq, p.causal, row0 / p.group);
             all_lo = seen_lo(seen_hi(it.seq, p.causal, (min(rows, row0 + kFewRows) - 1) / p.group), p.window);
-            float back[kGroups];  // of rows g, g + 8: what undoes their queries' lifting
             if constexpr (Sh::kQueryShared)
                 __syncthreads();  // the item before has been joined
 #pragma unroll
@@ -280,14 +288,14 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                             }
                     }
                 float lift = 1.f;
-                back[h] = 1.f;
+                back[h] = 0;
                 if constexpr (!std::is_same<T, __half>::value) {
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
                     if (top > 0.f && e < 255) {
                         lift = __uint_as_float((268 - e) << 23);  // 2^(127 + 14 - e)
-                        back[h] = __uint_as_float((e - 14) << 23);
+                        back[h] = (int)e - (127 + 14);
                     }
                 }
 #pragma unroll
@@ -329,9 +337,9 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
                 l[i] = 0.f;
                 hi[i] = r < rows ? seen_hi(it.seq, p.causal, r / p.group) : 0;
                 lo[i] = seen_lo(hi[i], p.window);
-                // never 0: a masked score is -infinity
-                scale[i] = fmaxf(p.scale_log2 * __shfl_sync(0xffffffffu, back[i >> 1], (2 * q + (i & 1)) * 4), 1.2e-38f);
             }
+            key_exp = 0;
+            set_scale();
 #pragma unroll
             for (int i = 0; i < Sh::kOut; i++)
                 o[i] = 0.f;
@@ -349,13 +357,19 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         // scores: s[nb][x][j] is of token nb * 16 + g + 8 * (j >> 1) and statistic 2 * x + (j & 1)
         float s[NB][kGroups][4], weight[NB][2];  // weight: the power of a token's values
         auto stat_of = [](int x, int j) { return 2 * x + (j & 1); };
-        int exps[kSets], new_exp = 0;
+        int exps[kSets], new_key = 0, new_exp = 0;
 #pragma unroll
         for (int i = 0; i < kSets; i++) {
             exps[i] = (int)(k_exp[0][i] | v_exp[0][i] << 8);
+            new_key = max(new_key, (int)k_exp[0][i]);
             new_exp = max(new_exp, (int)v_exp[0][i]);
         }
+        new_key = __reduce_max_sync(0xffffffffu, new_key);
         new_exp = max(top_exp, __reduce_max_sync(0xffffffffu, new_exp));
+        if (new_key > key_exp) {
+            key_exp = new_key;
+            set_scale();
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             float other[kGroups][4];  // every second MMA's sum: two chains, half as long
@@ -416,7 +430,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const uint32_t mine = (uint32_t)__shfl_sync(0xffffffffu, exps[nb / 2 % kSets], (nb & 1) * Sh::MG + g + 8 * h);
-                const float power = exp_power(mine & 255);
+                const float power = exp_power((uint32_t)max((int)(mine & 255) - key_exp + 127, 0));
                 weight[nb][h] = __uint_as_float((uint32_t)max((int)(mine >> 8) - new_exp + 127, 0) << 23);
 #pragma unroll
                 for (int x = 0; x < kGroups; x++)
