@@ -49,17 +49,25 @@ __device__ __forceinline__ int exponent_of(float top)
 // What values are multiplied by before they are encoded: 2^(127 - e), e = 0 .. 247.
 __device__ __forceinline__ float encode_power(int e) { return __uint_as_float((uint32_t)(254 - (e < 1 ? 1 : e)) << 23); }
 
-// 2^x, of x within fp32's normal range.
-__device__ __forceinline__ float power_of(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+// What scores that are relative to a power of two are multiplied by, where that power changes from block to block.
+// Never 0 (a masked score is -infinity) and never infinite (a score of 0 stays one): the exponent stops at fp32's
+// smallest and largest.  The scores are below 2^34, so those under the smallest are 0 but for 2^-91.
+struct ScoreScale {
+    uint32_t bits;  // of a value from 1 to 2
+    int exponent;   // and the power of two that it is to be multiplied by
 
-// What scores that are relative to 2^x are multiplied by.  In two steps, so that it stays a normal number wherever the
-// result is one; never 0 (a masked score is -infinity) and never infinite (a score of 0 stays one).  The scores
-// are below 2^34, so those under the lower bound are 0 but for 2^-92.
-__device__ __forceinline__ float score_scale(float scale_log2, int x)
-{
-    x = min(max(x, -252), 252);
-    return fminf(fmaxf(scale_log2 * power_of(x / 2) * power_of(x - x / 2), 1.2e-38f), 3.4e38f);
-}
+    __device__ __forceinline__ ScoreScale(float x, int power)  // x * 2^power, x > 0
+    {
+        const bool small = x < 1.1754943508222875e-38f;  // subnormal
+        const uint32_t b = __float_as_uint(small ? x * 16777216.f : x);
+        bits = (b & 0x7fffffu) | 0x3f800000u;
+        exponent = (int)(b >> 23) - 127 - (small ? 24 : 0) + power;
+    }
+    __device__ __forceinline__ float times(int power) const  // times 2^power
+    {
+        return __uint_as_float(bits + (uint32_t)min(max(exponent + power, -126), 127) * 0x800000u);
+    }
+};
 
 // Place of the exponent of a page's slot and head.
 __device__ __forceinline__ int64_t exp_offset(const ExpView &x, int64_t page, uint32_t slot, int head)

@@ -249,11 +249,12 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
     int key_exp = 0, top_exp = 0;  // the largest exponents of keys and values so far: scores and weights are relative to them
     int back[kGroups];             // of rows g, g + 8: 2^back undoes their queries' lifting
     auto set_scale = [&]() {
+        const ScoreScale all(p.scale_log2, key_exp - 127);
 #pragma unroll
-        for (int i = 0; i < Sh::kStats; i++) {
-            const int x = std::is_same<T, __half>::value ? 0 : __shfl_sync(0xffffffffu, back[i >> 1], (2 * q + (i & 1)) * 4);
-            scale[i] = score_scale(p.scale_log2, x + key_exp - 127);
-        }
+        for (int i = 0; i < Sh::kStats; i++)
+            scale[i] = all.times(std::is_same<T, __half>::value
+                                     ? 0
+                                     : __shfl_sync(0xffffffffu, back[i >> 1], (2 * q + (i & 1)) * 4));
     };
     bool fresh = true, first_item = true;
     int stage = 0;

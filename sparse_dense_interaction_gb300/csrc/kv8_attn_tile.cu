@@ -228,9 +228,10 @@ __device__ void tile8_convert(const AttnParams &p, const AttnWork &w, uint8_t *r
     tc::cp_async_wait_all();
 }
 
-// A softmax thread's half of its query row, as fp16 in the swizzled tile; returns what undoes the row's lifting.
+// A softmax thread's half of its query row, as fp16 in the swizzled tile; 2 to the power of what it returns undoes the
+// row's lifting.
 template <typename T, int DP, bool kTwo>
-__device__ __forceinline__ float tile8_query(const AttnParams &p, const AttnWork &w, uint8_t *sq, Tile8Bars &b, int t,
+__device__ __forceinline__ int tile8_query(const AttnParams &p, const AttnWork &w, uint8_t *sq, Tile8Bars &b, int t,
                                              int half, int in, int pair)
 {
     using Sh = Tile8Shape<DP, kTwo>;
@@ -244,7 +245,7 @@ __device__ __forceinline__ float tile8_query(const AttnParams &p, const AttnWork
         const int e = half * (DP / 2) + c * 8;
         x[c] = mine && e < p.d ? *reinterpret_cast<const uint4 *>(src + e) : make_uint4(0, 0, 0, 0);
     }
-    float back = 1.f;
+    int back = 0;
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
         float top = 0.f;
 #pragma unroll
@@ -263,7 +264,7 @@ __device__ __forceinline__ float tile8_query(const AttnParams &p, const AttnWork
         const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
         if (top > 0.f && e < 255) {
             lift = __uint_as_float((268 - e) << 23);  // 2^(127 + 14 - e)
-            back = __uint_as_float((e - 14) << 23);
+            back = (int)e - (127 + 14);
         }
 #pragma unroll
         for (int c = 0; c < kChunks; c++) {
@@ -304,7 +305,7 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
     // a row past the last sees everything: it needs no mask, and nothing of it is written
     const int hi = mine ? min(seen_hi(w.seq, p.causal, token), w.hi) : 0x7fffffff;
     const int lo = mine ? max(seen_lo(seen_hi(w.seq, p.causal, token), p.window), w.lo) : 0;
-    const float row_scale = p.scale_log2 * tile8_query<T, DP, kTwo>(p, w, sq, b, t, half, in, pair);
+    const ScoreScale scale_of(p.scale_log2, tile8_query<T, DP, kTwo>(p, w, sq, b, t, half, in, pair) - kCodeLift - 127);
     float m = -INFINITY, l = 0.f;
     int v_ref = 0;  // the exponent that the output is relative to
     for (int j = 0; j < tiles; j++) {
@@ -326,8 +327,7 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
             }
         };
         const int k_ref = b.k_ref[j % kTile8Refs], now_ref = b.v_ref[j % kTile8Refs];
-        // never 0: a masked score is -infinity
-        const float scale_log2 = fmaxf(row_scale * exp_power((uint32_t)max(k_ref - kCodeLift, 0)), 1.2e-38f);
+        const float scale_log2 = scale_of.times(k_ref);
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {

@@ -261,6 +261,7 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
     const uint16_t *refs = nullptr;  // of the tile
     if constexpr (kPowers)
         refs = p.refs + (w.s * p.batch.table_stride + (w.lo >> 7)) * p.cache.heads + w.head;
+    const ScoreScale scale_of(p.scale_log2, -kCodeLift - 127);
     int v_ref = 0;  // the exponent that the output is relative to
     for (int j = 0; j < tiles; j++) {
         float scale_log2 = p.scale_log2;
@@ -268,8 +269,7 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
         if constexpr (kPowers) {
             const int ref = __ldg(refs);
             refs += p.cache.heads;
-            // never 0: a masked score is -infinity
-            scale_log2 = fmaxf(scale_log2 * exp_power((uint32_t)max((ref & 255) - kCodeLift, 0)), 1.2e-38f);
+            scale_log2 = scale_of.times(ref & 255);
             now_ref = max(v_ref, ref >> 8);
             fall = min(now_ref - (ref >> 8), 60);
         }

@@ -20,7 +20,7 @@ def lse_check(case, table, caches, q, scale, lse):
 
 # Keys of up to 2^8 * 2^(e - 127), queries of up to 4 or so and sums of 256: below 2^127 to e = 235.  Lifted
 # queries (2^15) make that 2^141.  The scale takes the scores back to a few.
-@pytest.mark.parametrize("low,high", [(228, 233), (150, 233)])
+@pytest.mark.parametrize("low,high", [(228, 233), (150, 233), (2, 8)])
 @pytest.mark.parametrize("case", KINDS)
 def test_keys_near_the_ends_of_the_range(case, low, high):
     d = case[4]
@@ -48,3 +48,15 @@ def test_queries_and_keys_at_opposite_ends(case, size, low, high):
     scale = float(np.float32(2.0 ** (119 - high) / size / d ** 0.5))
     out, lse = attend(case, given, caches, q, scale)
     check_attention(case, table, caches, q, scale, out, lse)
+
+
+# A row of zeros scores 0 against every key, however large scale and keys are: the mean of the values.
+@pytest.mark.parametrize("case", KINDS)
+def test_a_query_of_zeros_under_a_large_scale(case):
+    counts, lengths, hq, hk, d, page, block, first, causal, window, dtype = case
+    table, given, caches, q = attention_inputs(case, seed=13)
+    exps = caches[0][1]
+    exps[exps < 255] = 200
+    q[:] = 0
+    out, lse = attend(case, given, caches, q, 1e38)
+    check_attention(case, table, caches, q, 1e38, out, lse)
