@@ -317,7 +317,8 @@ int dlrm_kv8_attn_fwd(const dlrm_heads *q, const dlrm_kv_batch *batch, const dlr
  * A sequence whose pages, with those that the sequences before it need, are more than the ring has is left
  * out (DLRM_FLAG_CAPACITY), and so is every later one that needs a page; so is one that does not fit its row
  * of the table, which takes no pages, or whose tokens go beyond n (DLRM_FLAG_BAD_OFFSETS).  A page number outside 0 .. pages - 1 raises
- * DLRM_FLAG_INDEX_OOB (its tokens' slots are -1).  A state that is not 0 <= state[0] <= state[1] <=
+ * DLRM_FLAG_INDEX_OOB: of a sequence that has ended it is passed over, so it does not become a free page; of one that
+ * goes on, in its row or in the ring as the caller filled it, its tokens' slots are -1.  A state that is not 0 <= state[0] <= state[1] <=
  * state[0] + pages raises DLRM_FLAG_BAD_OFFSETS: no page is taken or given back.  More pages given back than the
  * ring has room for raise DLRM_FLAG_CAPACITY and are dropped.
  * Every launch sums up all S sequences in each of its CTAs: made for steps of some thousands of them.

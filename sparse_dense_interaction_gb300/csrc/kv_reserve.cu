@@ -13,8 +13,8 @@
 // every CTA takes a run of tokens and sums up the sequences before it by itself
 // (16 bytes a sequence from L2, which costs less than a second kernel that waits for
 // the first).  Where lengths or the ring's state, which all CTAs read, are written in place,
-// a launch of its own does that afterwards.  One event of each of 2048 users: 10 us from
-// call to call, 8 in a graph; 512 users with up to 4096 new (14.4 MB): 14 and 12.
+// a launch of its own does that afterwards.  One event of each of 2048 users: 11 us from
+// call to call, 9.5 in a graph; 512 users with up to 4096 new (14.4 MB): 16 and 13.5.
 #include "history.cuh"
 
 namespace dlrm {
@@ -22,6 +22,7 @@ namespace dlrm {
 constexpr int kResThreads = 1024, kResItems = 2, kResChunk = kResThreads * kResItems;
 constexpr int kResTokens = kResThreads / 2;  // of a CTA, more where kResMaxCtas would not do
 constexpr int kResMaxCtas = 152;
+constexpr int kResLanes = 16, kResRun = 4;  // threads that look at a row given back; numbers that each asks for at once
 
 struct ReserveParams {
     const int64_t *counts, *lengths;
@@ -60,11 +61,15 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
 {
     __shared__ ReserveSums warp_sums[kResThreads / 32];
     // of the chunk's sequences: tokens and needs before it (from the chunk's first), stored tokens, and whether
-    // it has its pages (-1: it has left, 0: it is left out)
+    // it has its pages (0: it is left out, -1: it has left, -2: and some numbers of its row are no pages)
     __shared__ uint32_t s_tokens[kResChunk + 1];
     __shared__ int32_t s_need[kTokens ? kResChunk : 1], s_gone[kTokens ? kResChunk : 1];
     __shared__ int32_t s_length[kTokens ? kResChunk : 1];
     __shared__ int8_t s_granted[kTokens ? kResChunk : 1];
+    // those who give pages back, in any order, and how many (of this chunk, of the next)
+    __shared__ uint16_t s_leavers[kResChunk];
+    __shared__ int32_t s_held[kResChunk];
+    __shared__ int s_leaving[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t head = p.state[0], tail = p.state[1];
     const bool sound = tail >= head && tail - head <= p.pages && head >= 0;
@@ -85,7 +90,11 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
     const bool sequences = kSequences && blockIdx.x == 0;
     if (sequences && threadIdx.x == 0 && !sound)
         raise_flag(p.err, DLRM_FLAG_BAD_OFFSETS);
+    auto is_page = [&](int32_t page) { return (uint32_t)page < (uint64_t)p.pages; };
+    if (threadIdx.x < 2)
+        s_leaving[threadIdx.x] = 0;
     for (int64_t c0 = 0; c0 < p.S; c0 += kResChunk) {
+        int &leaving = s_leaving[c0 / kResChunk & 1], &next_leaving = s_leaving[~(c0 / kResChunk) & 1];
         const int64_t s0 = c0 + threadIdx.x * kResItems;
         int64_t take[kResItems], len[kResItems], need[kResItems], gone[kResItems];
         bool leaves[kResItems], fits[kResItems];
@@ -106,28 +115,79 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
                 raise_flag(p.err, DLRM_FLAG_BAD_OFFSETS);
             mine = mine + ReserveSums{take[i], need[i], gone[i]};
         }
-        ReserveSums sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const ReserveSums x = shfl_up(sum, o);
-            if (lane >= o)
-                sum = sum + x;
-        }
-        __syncthreads();  // the chunk before has been read
-        if (lane == 31)
-            warp_sums[warp] = sum;
-        __syncthreads();
-        if (warp == 0) {
-            ReserveSums w = warp_sums[lane];
+        // Sums over the chunk.  Meanwhile 16 threads a row look for numbers that are no pages among those given back; they
+        // are passed over, which moves all after them, so where there are any, the rows' pages are counted and summed up
+        // again.  (One event of each of 2048 users, 128 of whom leave, and prompts of 512, of whom 64 leave, in a graph:
+        // 9.5 and 13.5 us, without looking 8.2 and 12.5; where nobody leaves the same.  8 threads a row 9.5 and 14.0,
+        // whole warps, before the sums, 10.3 and 16.7.)
+        bool odd[kResItems] = {};
+        ReserveSums sum;
+        for (bool counted = false;; counted = true) {
+            sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const ReserveSums x = shfl_up(w, o);
+                const ReserveSums x = shfl_up(sum, o);
                 if (lane >= o)
-                    w = w + x;
+                    sum = sum + x;
             }
-            warp_sums[lane] = w;
+            __syncthreads();  // the chunk before has been read
+            if (lane == 31)
+                warp_sums[warp] = sum;
+#pragma unroll
+            for (int i = 0; i < kResItems; i++)
+                if (!counted && gone[i] > 0) {
+                    const int in = threadIdx.x * kResItems + i;
+                    s_held[in] = (int)gone[i];
+                    s_leavers[atomicAdd(&leaving, 1)] = (uint16_t)in;
+                }
+            __syncthreads();
+            if (warp == 0) {
+                ReserveSums w = warp_sums[lane];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const ReserveSums x = shfl_up(w, o);
+                    if (lane >= o)
+                        w = w + x;
+                }
+                warp_sums[lane] = w;
+            }
+            bool bad = false;
+            for (int r = threadIdx.x / kResLanes; !counted && r < leaving; r += kResThreads / kResLanes) {
+                const int in = s_leavers[r], held = s_held[in];
+                const int32_t *row = p.table + (c0 + in) * p.table_stride;
+                for (int k = threadIdx.x % kResLanes; k < held; k += kResLanes * kResRun) {
+                    int32_t page[kResRun];
+#pragma unroll
+                    for (int j = 0; j < kResRun; j++)
+                        page[j] = k + j * kResLanes < held ? row[k + j * kResLanes] : 0;
+#pragma unroll
+                    for (int j = 0; j < kResRun; j++)
+                        bad |= !is_page(page[j]);
+                }
+            }
+            if (!__syncthreads_or(bad))
+                break;
+#pragma unroll
+            for (int i = 0; i < kResItems; i++) {
+                for (uint32_t left = __ballot_sync(0xffffffffu, gone[i] > 0); left != 0; left &= left - 1) {
+                    const int who = __ffs(left) - 1, held = __shfl_sync(0xffffffffu, (int)gone[i], who);
+                    const int32_t *row = p.table + (c0 + (warp * 32 + who) * kResItems + i) * p.table_stride;
+                    int pages = 0;
+                    for (int k = lane; k < held; k += 32)
+                        pages += is_page(row[k]);
+                    pages = __reduce_add_sync(0xffffffffu, pages);
+                    if (lane == who && pages < held) {
+                        odd[i] = true;
+                        mine.gone -= held - pages;
+                        gone[i] = pages;
+                        if (sequences)
+                            raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
+                    }
+                }
+            }
         }
-        __syncthreads();
+        if (threadIdx.x == 0)
+            next_leaving = 0;
         ReserveSums at = warp > 0 ? warp_sums[warp - 1] : ReserveSums{0, 0, 0};  // from the chunk's first
         at = at + ReserveSums{sum.tokens - mine.tokens, sum.need - mine.need, sum.gone - mine.gone};
         const ReserveSums all = warp_sums[kResThreads / 32 - 1];
@@ -144,7 +204,7 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
                 s_need[in] = (int)min(at.need, (int64_t)0x7fffffff);
                 s_gone[in] = (int)min(at.gone, (int64_t)0x7fffffff);
                 s_length[in] = (int)min(len[i], (int64_t)0x7fffffff);
-                s_granted[in] = leaves[i] ? -1 : (granted ? 1 : 0);
+                s_granted[in] = leaves[i] ? (odd[i] ? -2 : -1) : (granted ? 1 : 0);
             }
             if (sequences && s0 + i < p.S) {
                 p.offsets[s0 + i] = base.tokens + at.tokens;
@@ -178,10 +238,16 @@ kv_reserve_kernel(const __grid_constant__ ReserveParams p)
                     break;
                 }
                 const int in = owner(s_gone, (int)k);
-                const int32_t page = p.table[(c0 + in) * p.table_stride + k - s_gone[in]];
-                if ((uint32_t)page >= (uint64_t)p.pages)
-                    raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
-                p.ring[place(ring_tail, base.gone + k)] = page;
+                const int32_t *row = p.table + (c0 + in) * p.table_stride;
+                int number = (int)k - s_gone[in];
+                if (s_granted[in] == -2) {  // among those that are pages
+                    int before = number;
+                    const int last = pages_of(s_length[in]) - 1;
+                    for (number = 0; number < last; number++)
+                        if (is_page(row[number]) && before-- == 0)
+                            break;
+                }
+                p.ring[place(ring_tail, base.gone + k)] = row[number];
             }
             // this CTA's tokens among the chunk's
             const int64_t from = max(t0, base.tokens), to = min(t1, base.tokens + all.tokens);
