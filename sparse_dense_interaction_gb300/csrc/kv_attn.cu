@@ -299,24 +299,33 @@ static size_t part_floats(const AttnPlan &a, int64_t n, int heads, int d)
     return a.splits > 1 ? (size_t)a.splits * n * heads * (d + 1) : 0;
 }
 
-// The largest of the kernels' needs: which one runs depends on types and alignment too.
-size_t attn_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new, int64_t max_len)
+// The largest of the kernels' needs: which one runs depends on types and alignment too.  (Heads above 128 take tiles
+// over a cache in 8 bits alone.)
+static size_t workspace_of(bool codes, int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new,
+                           int64_t max_len)
 {
     const int group = q_heads / kv_heads;
     max_new = max_new < n ? max_new : n;
     size_t most = few_workspace(max_new * group, d, max_len);
     for (AttnKernel k : {kAttnGeneral, kAttnTile}) {
+        if (k == kAttnTile && d > 128 && !codes)
+            continue;
         const size_t b = part_floats(plan(k, S, kv_heads, group, d, max_new, max_len), n, q_heads, d) * sizeof(float);
         most = b > most ? b : most;
     }
     return most + 16;
 }
 
+size_t attn_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new, int64_t max_len)
+{
+    return workspace_of(false, S, n, q_heads, kv_heads, d, max_new, max_len);
+}
+
 // Over a cache in 8 bits: a copy of it in 16 bits may come first.
 size_t attn8_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new, int64_t max_len)
 {
     const int group = q_heads / kv_heads;
-    return attn_workspace(S, n, q_heads, kv_heads, d, max_new, max_len) +
+    return workspace_of(true, S, n, q_heads, kv_heads, d, max_new, max_len) +
            widen_workspace(S, kv_heads, group, d, max_new < n ? max_new : n, max_len);
 }
 
