@@ -247,8 +247,8 @@ struct AttnParams {
     int wait_polls;            // of a wait inside a kernel, before it gives up
     int32_t *err;
     ExpView exp;               // of a cache in 8 bits
-    // of an fp16 copy of such a cache, [sequence][page][head]: exponents that a page's keys (low byte) and values are
-    // relative to
+    // of a 16-bit copy of such a cache, [sequence][page][head]: exponents that a page's keys (low byte; bf16 keys are
+    // as they are) and values are relative to
     const uint16_t *refs;
 };
 

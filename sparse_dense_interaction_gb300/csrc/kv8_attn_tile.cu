@@ -446,7 +446,7 @@ kv8_attn_tile_kernel(const __grid_constant__ AttnParams p)
         if (tiles > 0)
             tile8_convert<DP, kTwo>(p, w, ring, sq + Sh::kTiles, b, tiles);
     } else if (tiles > 0) {
-        tile_mma<__half, DP, kTwo, typename Sh::Sh>(sq, ring, b, tiles, two, p.wait_polls);
+        tile_mma<__half, __half, DP, kTwo, typename Sh::Sh>(sq, ring, b, tiles, two, p.wait_polls);
         __syncwarp();
     }
     tc::fence_before_sync();

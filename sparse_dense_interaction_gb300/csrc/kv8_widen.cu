@@ -2,11 +2,13 @@
 //
 // Long chunks read every key and value again for each tile of their rows, and
 // converting them each time costs the tiles a third of their time.  So for such batches they are
-// converted once, and the 16-bit cache's tiles do the rest.  bf16 holds every code
-// times its power exactly; fp16 holds it relative to the largest power of its page of the
-// copy, which the tiles apply to their scores and weights.  Memory bounds the
+// converted once, and the 16-bit cache's tiles do the rest.  Values become fp16 relative to the largest power of
+// their page of the copy, which the tiles apply to their weights; fp16 weights have as many bits as everywhere else over
+// this cache.  Keys are of the queries' type: so in fp16, which the tiles apply to their scores; in bf16, which holds
+// every code times its power, as they are.  (Values in bf16 would make the weights bf16: 363 us for the
+// sequences below, but 1.35 times the error against 64 bits.)  Memory bounds the
 // conversion (a byte read, two written, which mostly stay in L2): 4 sequences of 2048 new on
-// 8192, 16 heads on 4 of 128, take 363 us in bf16 and 378 in fp16, on a 16-bit cache 341.
+// 8192, 16 heads on 4 of 128, take 372 us in bf16 and 378 in fp16, on a 16-bit cache 341.
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -17,9 +19,9 @@ constexpr int kWidenThreads = 256, kWidenPage = 128;
 
 struct WidenParams {
     AttnParams p;
-    char *k, *v;      // [sequence * pages + page][head][kWidenPage][d], bf16 or fp16
+    char *k, *v;      // [sequence * pages + page][head][kWidenPage][d]; keys bf16 or fp16, values fp16
     int32_t *table;   // [sequence][pages]
-    uint16_t *refs;   // [sequence][pages][heads], of fp16
+    uint16_t *refs;   // [sequence][pages][heads]
     int pages;        // of a sequence
     FastDiv chunks, heads;  // 8 codes of a row; heads
 };
@@ -87,22 +89,19 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
             raise_flag(p.err, DLRM_FLAG_INDEX_OOB);
         }
     }
-    int k_ref = 0, v_ref = 0;
-    if constexpr (std::is_same<T, __half>::value) {
-        k_exp = __reduce_max_sync(0xffffffffu, k_exp);
-        v_exp = __reduce_max_sync(0xffffffffu, v_exp);
-        if ((r & 31) == 0)
-            warp_refs[r / 32] = k_exp | v_exp << 16;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kWidenPage / 32; i++) {
-            k_ref = max(k_ref, (int)(warp_refs[i] & 0xffff));
-            v_ref = max(v_ref, (int)(warp_refs[i] >> 16));
-        }
-        if (r == 0)
-            w.refs[blockIdx.x] = (uint16_t)(k_ref | v_ref << 8);
-    }
+    k_exp = __reduce_max_sync(0xffffffffu, k_exp);
+    v_exp = __reduce_max_sync(0xffffffffu, v_exp);
+    if ((r & 31) == 0)
+        warp_refs[r / 32] = k_exp | v_exp << 16;
     __syncthreads();
+    int k_ref = 0, v_ref = 0;
+#pragma unroll
+    for (int i = 0; i < kWidenPage / 32; i++) {
+        k_ref = max(k_ref, (int)(warp_refs[i] & 0xffff));
+        v_ref = max(v_ref, (int)(warp_refs[i] >> 16));
+    }
+    if (r == 0)
+        w.refs[blockIdx.x] = (uint16_t)(k_ref | v_ref << 8);
     const int per_row = p.d / 8, all = (hi - lo) * per_row;
     const int64_t base = ((int64_t)blockIdx.x * kWidenPage + lo - start) * p.d * 2;
 #pragma unroll 4
@@ -111,7 +110,7 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
         const int64_t from = row_codes[x] + c * 8, to = base + i * 16;
         if (row_codes[x] >= 0) {
             widen8<T>(p.cache.k + from, row_exps[0][x], k_ref, w.k + to);
-            widen8<T>(p.cache.v + from, row_exps[1][x], v_ref, w.v + to);
+            widen8<__half>(p.cache.v + from, row_exps[1][x], v_ref, w.v + to);
         } else {
             *reinterpret_cast<uint4 *>(w.k + to) = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4 *>(w.v + to) = make_uint4(0, 0, 0, 0);
@@ -162,7 +161,7 @@ int launch_widen(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     p.batch.table_stride = pages;
     p.batch.capacity = p.batch.capacity < pages * kWidenPage ? p.batch.capacity : pages * kWidenPage;
     p.exp = ExpView{};
-    p.refs = dtype == DLRM_F16 ? w.refs : nullptr;
+    p.refs = w.refs;
     return launch_status();
 }
 

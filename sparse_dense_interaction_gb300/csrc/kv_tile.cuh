@@ -49,11 +49,12 @@ struct TileBars {
     float agree[2][2][128];  // [query tile][half][row]: a maximum of half a row's scores; at the end its sum
 };
 
-template <typename T, int DP, bool kTwo, typename Sh = TileShape<DP, kTwo>>
+// T: the type of queries and keys; W: of weights and values.
+template <typename T, typename W, int DP, bool kTwo, typename Sh = TileShape<DP, kTwo>>
 __device__ void tile_mma(uint8_t *sq, uint8_t *ring, TileBars &b, int tiles, bool two, int polls)
 {
-    constexpr int kType = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
-    constexpr uint32_t kScores = tc::f16_idesc(kType, 128, kTilePos, false), kOut = tc::f16_idesc(kType, 128, DP, true);
+    constexpr int kType = std::is_same<T, __nv_bfloat16>::value ? 1 : 0, kTypeW = std::is_same<W, __nv_bfloat16>::value ? 1 : 0;
+    constexpr uint32_t kScores = tc::f16_idesc(kType, 128, kTilePos, false), kOut = tc::f16_idesc(kTypeW, 128, DP, true);
     // all lanes run this; one issues.  Descriptors of a later place are the first plus its distance / 16.
     const uint32_t tmem = __shfl_sync(0xffffffffu, b.tmem, 0);
     tiles = __shfl_sync(0xffffffffu, tiles, 0);  // known to be the warp's: the loop's values are uniform
