@@ -309,7 +309,8 @@ __device__ void tile_softmax(const AttnParams &p, const AttnWork &w, uint8_t *sq
         now = fmaxf(now, b.agree[t][1 - half][in]);
         if (__any_sync(0xffffffffu, now - m > kTileSlack<W> || (kPowers && now_ref > v_ref))) {
             // also from -infinity; the output of the tiles before is complete: the scores' MMA came after it
-            const float next = fmaxf(m, now);
+            // (over codes a row goes by its own growth alone, so that its bits do not depend on the other rows')
+            const float next = !kPowers || now - m > kTileSlack<W> ? fmaxf(m, now) : m;
             float f = next == -INFINITY ? 1.f : exp2_approx(m - next);
             m = next;
             l *= f;

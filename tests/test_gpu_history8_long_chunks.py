@@ -38,3 +38,24 @@ def test_weights_have_eleven_bits(case):
     tol = R.attention_tolerance(want, absout, smax, flat, d, "f32") + 2.0 ** -11 * 1.01 * absout
     tol = tol + R.U[dtype] * 1.01 * np.abs(want) + R.TINY[dtype] * (1 + flat)
     close(out, want, tol + 2.0 ** -36 * np.abs(v).max() * max(lengths), case)
+
+
+# One row's scores grow by much along the history, those of the others by less than a maximum is let lag: with the one
+# row gone (NaN) the others keep their bits.
+@pytest.mark.parametrize("case", KINDS)
+def test_bits_do_not_depend_on_other_rows(case):
+    counts, lengths, hq, hk, d, page, block, first, causal, window, dtype = case
+    table, given, caches, q = attention_inputs(case, seed=22)
+    for s, n in enumerate(lengths):
+        own = -(-n // page)
+        for i in range(own):  # keys grow by 2^6 in all
+            caches[0][1][table[s, i]] = 114 + int(6 * i / max(own - 1, 1))
+    one = torch.zeros(q.shape[:2], dtype=torch.bool, device=q.device)
+    one[-1, hq - 1] = True  # the last row of the batch
+    q = q * 0.25
+    q[one] *= 64
+    with_one, lse_with = attend(case, given, caches, q, 0.5 / d ** 0.5)
+    q[one] = float("nan")
+    out, lse = attend(case, given, caches, q, 0.5 / d ** 0.5)
+    assert out[one].isnan().all() and lse[one].isnan().all()
+    assert torch.equal(out[~one], with_one[~one]) and torch.equal(lse[~one], lse_with[~one])
