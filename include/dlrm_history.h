@@ -282,7 +282,9 @@ size_t dlrm_kv8_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_he
  *   largest weight times the largest power of the values so far, what lies below 2^-36 may be lost;
  * - long chunks of 16-bit types (of at least 1536 rows of heads of 65 to 128, 2048 of up to 64, widths of multiples
  *   of 16) are converted once to a 16-bit cache in the workspace (four bytes for each code up to max_len, where that
- *   is at most 2 GiB; exact as above), and go on in the tiles of dlrm_kv_attn_fwd, bf16 with fp16 weights too.
+ *   is at most 2 GiB; exact as above), and go on in the tiles of dlrm_kv_attn_fwd, bf16 with fp16 weights too.  Where
+ *   the batch has fewer than 512 rows a sequence, sequences of up to 16 rows beside them do not: they go as single
+ *   tokens do.
  * A value or a sum beyond the range of dtype is infinite.  Results are the same bits from run to run of one
  * batch; a sequence's last bits may depend on which other sequences are in its batch.
  */

@@ -235,6 +235,7 @@ struct AttnParams {
     BatchView batch;
     CacheView cache;
     int64_t max_new, max_len;
+    int from_new, most_new;  // this launch takes the sequences of so many new tokens, and leaves the others to another
     int d, group;       // group: query heads of a cache head
     float scale_log2;   // scale * log2(e)
     bool causal;
@@ -251,6 +252,11 @@ struct AttnParams {
     // as they are) and values are relative to
     const uint16_t *refs;
 };
+
+__device__ __forceinline__ bool attn_takes(const AttnParams &p, const Sequence &q)
+{
+    return q.count >= p.from_new && q.count <= p.most_new;
+}
 
 // What one CTA works on: rows of tile `tile` of head `head` of the sequence,
 // positions [lo, hi) of split `split`; whole: the tile needs no other split.
@@ -306,7 +312,8 @@ __device__ __forceinline__ bool attn_work(const AttnParams &p, uint32_t cta, Att
 {
     int64_t tile;
     w.s = attn_number(p, cta, w, tile);
-    return read_sequence(p.batch, w.s, p.max_new, p.max_len, w.seq, p.err) && attn_rows(p, tile, w);
+    return read_sequence(p.batch, w.s, p.max_new, p.max_len, w.seq, p.err) && attn_takes(p, w.seq) &&
+           attn_rows(p, tile, w);
 }
 
 // Byte offset of a position's slot row in the cache (head's own offset

@@ -158,6 +158,8 @@ static int check_attention(const dlrm_heads *q, const dlrm_kv_batch *batch, int 
                                                                        max_new, max_len))
         return DLRM_ERR_WORKSPACE_TOO_SMALL;
     p.max_len = max_len;
+    p.from_new = 0;
+    p.most_new = 0x7fffffff;
     p.d = d;
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.causal = causal != 0;

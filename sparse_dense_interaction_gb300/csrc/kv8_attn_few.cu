@@ -140,7 +140,7 @@ kv8_attn_few_kernel(const __grid_constant__ AttnParams p, const __grid_constant_
         if (!any)
             return;
     } else {
-        const int64_t most = (p.max_new * p.group + kFewRows - 1) / kFewRows, of = blockIdx.x / most;
+        const int64_t most = (few_new(p) * p.group + kFewRows - 1) / kFewRows, of = blockIdx.x / most;
         const int64_t s = of / p.cache.heads;
         if (!read_sequence(p.batch, s, p.max_new, p.max_len, it.seq, p.err) || !few_sequence(p, it, s, 0, UT, TB))
             return;
@@ -742,15 +742,15 @@ static int launch_few8(AttnParams &p, const FewMaps &maps, void *workspace, cuda
     if (s != DLRM_OK)
         return s;
     // a window bounds what an item's rows see, whatever the history's length
-    const int64_t seen = p.window > 0 ? p.window + (p.causal ? p.max_new : 0) : p.max_len;
+    const int64_t seen = p.window > 0 ? p.window + (p.causal ? few_new(p) : 0) : p.max_len;
     // items, idle sequences' among them; the batch cannot have more busy sequences than tokens
-    const int64_t each = p.cache.heads * ((p.max_new * p.group + kFewRows - 1) / kFewRows), items = p.batch.S * each;
+    const int64_t each = p.cache.heads * ((few_new(p) * p.group + kFewRows - 1) / kFewRows), items = p.batch.S * each;
     const int64_t busy = (p.batch.S < p.batch.n ? p.batch.S : p.batch.n) * each;
     const bool split = few_splits(seen < p.max_len ? seen : p.max_len, p.d, 1, busy, kFew8WholeBytes, kFew8WholeBytesPerItem);
     p.splits = split ? 2 : 1;
     p.joins = static_cast<FewJoin *>(workspace);
     p.part_o = reinterpret_cast<float *>(p.joins + kFewMaxCtas);
-    p.rows = (int)few_rows(p.max_new * p.group);
+    p.rows = (int)few_rows(few_new(p) * p.group);
     p.part_lse = p.part_o + (size_t)2 * kFewMaxCtas * p.rows * p.d;
     if (items > 0x7fffffff)
         return DLRM_ERR_UNSUPPORTED;
@@ -768,7 +768,7 @@ static int launch_few8(AttnParams &p, const FewMaps &maps, void *workspace, cuda
 template <typename T>
 static int launch_few8_width(AttnParams &p, const FewMaps &maps, void *workspace, cudaStream_t st)
 {
-    const bool narrow = p.max_new * p.group <= 8;
+    const bool narrow = few_new(p) * p.group <= 8;
     if (p.d <= 64)
         return narrow ? launch_few8<T, 64, 1>(p, maps, workspace, st) : launch_few8<T, 64, 2>(p, maps, workspace, st);
     if constexpr (sizeof(T) == 2)

@@ -68,7 +68,7 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
     if (threadIdx.x == 0 && head == 0)
         w.table[number] = (int32_t)number;
     Sequence q;
-    if (!read_sequence(p.batch, s, p.max_new, p.max_len, q, nullptr) || q.count == 0)
+    if (!read_sequence(p.batch, s, p.max_new, p.max_len, q, nullptr) || q.count == 0 || !attn_takes(p, q))
         return;
     const int start = page * kWidenPage, hi = min(seen_hi(q, p.causal, q.count - 1), start + kWidenPage);
     const int lo = max(seen_lo(seen_hi(q, p.causal, 0), p.window), start);

@@ -186,7 +186,8 @@ kv_attn_join_kernel(const __grid_constant__ AttnParams p)
         const int64_t token = i / heads, s = find_sequence(p.batch, token);
         const int h = (int)(i - token * heads);
         Sequence seq;
-        if (s < 0 || !read_sequence(p.batch, s, p.max_new, p.max_len, seq, nullptr) || !seq.has(token))
+        if (s < 0 || !read_sequence(p.batch, s, p.max_new, p.max_len, seq, nullptr) || !seq.has(token) ||
+            !attn_takes(p, seq))
             continue;
         // the tile that held this row, and whether it was split
         const int t = (int)(token - seq.first), row = t * p.group + h % p.group, row0 = row / p.rows * p.rows;
@@ -434,9 +435,21 @@ int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     const bool tile = rows_even && codes_even && p.d % 16 == 0 && dtype != DLRM_F32;
     const bool few = rows_even && codes_even && p.d <= (dtype == DLRM_F32 ? 128 : 256);
     int status;
-    // Long chunks: the codes are converted once (heads of up to 128).
+    // Long chunks: the codes are converted once (heads of up to 128).  Sequences beside them that have up to 16 rows go in
+    // rows of 16 instead, in a launch of their own, where the batch has fewer than 512 rows a sequence, so that there may be
+    // many of them.  With that launch and without, us (bf16, 16 heads on 4 of 128, histories of 8192): one chunk of 2048
+    // and 99 single events 352 and 870, and 31 192 and 367; 4 of 2048 and 60 users without new events (512 rows a
+    // sequence) 397 and 392; 8 of up to 2048 on up to 8192 361 and 348; 16 of 300 to 500 on up to 4000 174 and 164.
     const size_t widened = widen_workspace(p.batch.S, c.heads, p.group, p.d, p.max_new, p.max_len);
     if (tile && widened > 0) {
+        AttnParams others = p;
+        others.most_new = 16 / p.group;
+        if (others.most_new > 0 && p.batch.n * p.group < 512 * p.batch.S &&
+            launch_kv8_attn_few(others, dtype, workspace, st, status)) {
+            if (status != DLRM_OK)
+                return status;
+            p.from_new = others.most_new + 1;
+        }
         status = launch_widen(p, dtype, workspace, st);
         return status != DLRM_OK ? status : launch_kv_attn(p, dtype, static_cast<char *>(workspace) + widened, st);
     }

@@ -43,12 +43,18 @@ struct FewItem {
     const int32_t *pages;
 };
 
+// New tokens of a sequence that this launch takes, at most.
+__host__ __device__ __forceinline__ int64_t few_new(const AttnParams &p)
+{
+    return p.max_new < p.most_new ? p.max_new : p.most_new;
+}
+
 // Positions that a sequence's queries see, and the units of one of its items
 // (one at least where there are queries: their rows are written).
 __device__ __forceinline__ int few_units(const AttnParams &p, const Sequence &q, int unit, int &lo, int &hi, int align)
 {
     lo = hi = 0;
-    if (q.count == 0)
+    if (q.count == 0 || !attn_takes(p, q))
         return 0;
     hi = seen_hi(q, p.causal, q.count - 1);
     lo = seen_lo(seen_hi(q, p.causal, 0), p.window);
@@ -95,7 +101,7 @@ static __device__ __noinline__ int few_busy_after(const AttnParams &p, int s0, c
     for (int s = s0 + 1; s < end && next < 0; s += 32) {
         Sequence mine;
         const bool some = s + lane < end && read_sequence(p.batch, s + lane, p.max_new, p.max_len, mine, nullptr) &&
-                          mine.count > 0;
+                          mine.count > 0 && attn_takes(p, mine);
         const uint32_t found = __ballot_sync(0xffffffffu, some);
         next = found ? s + __ffs(found) - 1 : -1;
     }
@@ -147,7 +153,7 @@ static __device__ bool few_share(const AttnParams &p, FewItem &w, int &units, in
     for (int64_t s = from; s < to; s++)
         if (read_sequence(p.batch, s, p.max_new, p.max_len, q, blockIdx.x == 0 ? p.err : nullptr)) {
             mine += (int64_t)few_units(p, q, unit, lo, hi, align) * few_tiles(p, q) * p.cache.heads;
-            first = first < 0 && q.count > 0 ? (int)s : first;
+            first = first < 0 && q.count > 0 && attn_takes(p, q) ? (int)s : first;
         }
     busy[threadIdx.x] = first;
     int64_t before = mine;

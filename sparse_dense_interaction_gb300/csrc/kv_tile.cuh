@@ -214,7 +214,7 @@ static __device__ bool tile_work(const AttnParams &p, int *room, AttnWork &w)
     Sequence seq = {0, 0, 0};
     int key = -1;  // of a sequence without work, and past the last
     if (t < S && read_sequence(p.batch, t, p.max_new, p.max_len, seq, blockIdx.x == 0 ? p.err : nullptr) &&
-        seq.count > 0)
+        seq.count > 0 && attn_takes(p, seq))
         key = seq.length;
     if (t < padded)
         room[t] = key;
