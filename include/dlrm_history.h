@@ -262,7 +262,10 @@ typedef struct dlrm_kv_cache8 {
 int dlrm_kv8_append(const dlrm_heads *k, const dlrm_heads *v, const dlrm_kv_batch *batch,
                     const dlrm_kv_cache8 *cache, int d, int dtype, int32_t *err_flag, dlrm_stream_t stream);
 
-/* Bytes of workspace of dlrm_kv8_attn_fwd for these sizes, of any dtype; 0 for invalid ones. */
+/* Bytes of workspace of dlrm_kv8_attn_fwd for these sizes, of any dtype; 0 for invalid ones.  The copy of long chunks'
+ * codes (below) is among them, which may be large.  Calls that cannot make it (fp32, heads that are no multiple of 16 or
+ * above 128, rows or codes that do not lie on 16 bytes) do without: for heads of up to 128 they need
+ * dlrm_kv_attn_workspace_size bytes alone. */
 size_t dlrm_kv8_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new,
                                     int64_t max_len);
 

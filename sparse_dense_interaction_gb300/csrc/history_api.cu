@@ -17,7 +17,8 @@ int launch_kv_append(const HeadsView &, const HeadsView &, const BatchView &, co
                      const float *, float, const RopeView &, const HeadsView &, const float *, const HeadsView &,
                      int32_t *, cudaStream_t);
 size_t attn_workspace(int64_t, int64_t, int, int, int, int64_t, int64_t);
-size_t attn8_workspace(int64_t, int64_t, int, int, int, int64_t, int64_t);
+size_t attn8_workspace(int64_t, int64_t, int, int, int, int64_t, int64_t, bool);
+bool kv8_tiles(const AttnParams &, int);
 int launch_kv_attn(AttnParams &, int, void *, cudaStream_t);
 int launch_kv8_attn(AttnParams &, int, void *, cudaStream_t);
 int launch_kv_reserve(const int64_t *, const int64_t *, int64_t, int64_t, int32_t *, int64_t, int64_t, int, int32_t *,
@@ -154,13 +155,15 @@ static int check_attention(const dlrm_heads *q, const dlrm_kv_batch *batch, int 
         return DLRM_ERR_UNSUPPORTED;
     if (n > 0 && max_new == 0)
         return DLRM_ERR_INVALID_ARG;
-    if (workspace_bytes < (p.exp.k ? attn8_workspace : attn_workspace)(p.batch.S, n, p.q.heads, p.cache.heads, d,
-                                                                       max_new, max_len))
-        return DLRM_ERR_WORKSPACE_TOO_SMALL;
     p.max_len = max_len;
     p.from_new = 0;
     p.most_new = 0x7fffffff;
     p.d = d;
+    const int64_t S = p.batch.S;
+    const size_t need = p.exp.k ? attn8_workspace(S, n, p.q.heads, p.cache.heads, d, max_new, max_len, kv8_tiles(p, dtype))
+                                : attn_workspace(S, n, p.q.heads, p.cache.heads, d, max_new, max_len);
+    if (workspace_bytes < need)
+        return DLRM_ERR_WORKSPACE_TOO_SMALL;
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.causal = causal != 0;
     p.window = window < kMaxPositions ? (int)window : 0;  // as wide as any history: none
@@ -351,7 +354,7 @@ size_t dlrm_kv8_attn_workspace_size(int64_t S, int64_t n, int q_heads, int kv_he
                                     int64_t max_len)
 {
     return attn_sizes(S, n, q_heads, kv_heads, d, max_new, max_len)
-               ? attn8_workspace(S, n, q_heads, kv_heads, d, max_new, max_len)
+               ? attn8_workspace(S, n, q_heads, kv_heads, d, max_new, max_len, true)
                : 0;
 }
 

@@ -322,12 +322,13 @@ size_t attn_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, in
     return workspace_of(false, S, n, q_heads, kv_heads, d, max_new, max_len);
 }
 
-// Over a cache in 8 bits: a copy of it in 16 bits may come first.
-size_t attn8_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new, int64_t max_len)
+// Over a cache in 8 bits: a copy of it in 16 bits may come first, if the call may take tiles.
+size_t attn8_workspace(int64_t S, int64_t n, int q_heads, int kv_heads, int d, int64_t max_new, int64_t max_len,
+                       bool tiles)
 {
     const int group = q_heads / kv_heads;
     return workspace_of(true, S, n, q_heads, kv_heads, d, max_new, max_len) +
-           widen_workspace(S, kv_heads, group, d, max_new < n ? max_new : n, max_len);
+           (tiles ? widen_workspace(S, kv_heads, group, d, max_new < n ? max_new : n, max_len) : 0);
 }
 
 template <typename T, bool kCodes>
@@ -421,19 +422,29 @@ int launch_kv_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
     return launch_planned(p, cores ? kAttnTile : kAttnGeneral, seen, dtype, workspace, st);
 }
 
-int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
+static bool even_rows(const HeadsView &h, int dtype)
 {
     const int e = dtype == DLRM_F32 ? 4 : 8;
-    auto even = [e](const HeadsView &h) {
-        return reinterpret_cast<uintptr_t>(h.ptr) % 16 == 0 && h.ts % e == 0 && h.hs % e == 0;
-    };
+    return reinterpret_cast<uintptr_t>(h.ptr) % 16 == 0 && h.ts % e == 0 && h.hs % e == 0;
+}
+
+// What the tensor-core kernels over codes ask of rows and codes.
+static bool kv8_even(const AttnParams &p, int dtype)
+{
     const CacheView &c = p.cache;
-    const bool rows_even = p.d % 8 == 0 && even(p.q) && even(p.out);
-    const bool codes_even = reinterpret_cast<uintptr_t>(c.k) % 16 == 0 && reinterpret_cast<uintptr_t>(c.v) % 16 == 0 &&
-                            c.page_stride % 16 == 0 && c.slot_stride % 16 == 0 && c.head_stride % 16 == 0;
+    return p.d % 8 == 0 && even_rows(p.q, dtype) && even_rows(p.out, dtype) &&
+           reinterpret_cast<uintptr_t>(c.k) % 16 == 0 && reinterpret_cast<uintptr_t>(c.v) % 16 == 0 &&
+           c.page_stride % 16 == 0 && c.slot_stride % 16 == 0 && c.head_stride % 16 == 0;
+}
+
+// Whether a call may take tiles, and convert codes of long chunks.
+bool kv8_tiles(const AttnParams &p, int dtype) { return dtype != DLRM_F32 && p.d % 16 == 0 && kv8_even(p, dtype); }
+
+int launch_kv8_attn(AttnParams &p, int dtype, void *workspace, cudaStream_t st)
+{
+    const CacheView &c = p.cache;
     const int64_t rows = p.max_new * p.group, seen = seen_bound(p);
-    const bool tile = rows_even && codes_even && p.d % 16 == 0 && dtype != DLRM_F32;
-    const bool few = rows_even && codes_even && p.d <= (dtype == DLRM_F32 ? 128 : 256);
+    const bool tile = kv8_tiles(p, dtype), few = kv8_even(p, dtype) && p.d <= (dtype == DLRM_F32 ? 128 : 256);
     int status;
     // Long chunks: the codes are converted once (heads of up to 128).  Sequences beside them that have up to 16 rows go in
     // rows of 16 instead, in a launch of their own, where the batch has fewer than 512 rows a sequence, so that there may be
