@@ -305,7 +305,9 @@ __device__ void tile8_softmax(const AttnParams &p, const AttnWork &w, uint8_t *s
     // a row past the last sees everything: it needs no mask, and nothing of it is written
     const int hi = mine ? min(seen_hi(w.seq, p.causal, token), w.hi) : 0x7fffffff;
     const int lo = mine ? max(seen_lo(seen_hi(w.seq, p.causal, token), p.window), w.lo) : 0;
-    const ScoreScale scale_of(p.scale_log2, tile8_query<T, DP, kTwo>(p, w, sq, b, t, half, in, pair) - kCodeLift - 127);
+    // Rows that see nothing want no query: the warps' outputs go through the queries' tiles, and no MMA comes between
+    const int back = tiles > 0 ? tile8_query<T, DP, kTwo>(p, w, sq, b, t, half, in, pair) : 0;
+    const ScoreScale scale_of(p.scale_log2, back - kCodeLift - 127);
     float m = -INFINITY, l = 0.f;
     int v_ref = 0;  // the exponent that the output is relative to
     for (int j = 0; j < tiles; j++) {
