@@ -10,8 +10,11 @@
 // Memory bounds long prompts: rows are read once into registers, a chunk of
 // 8 elements each, as they lie, and written as a byte an element.  98000 new tokens of 48
 // users (8 heads of 128 bf16 elements): 98 us, 554 MB, 5.6 TB/s, 0.84 of a plain copy.
-// One event of each of 2048 users moves 1.6 MB: 12 us from call to call, launch and a
-// chain of dependent reads (offsets, table, exponent, codes).
+// That is with blocks of 16 rows, all that a warp's registers hold (fp32: 8 rows); of larger ones it reads the rest
+// twice.  With a cold L2, blocks of 8, 16, 32, 64 and 128: 130, 101, 148, 193 and 253 us; 24 of these users in
+// fp32 (490 MB) 91, 121, 148, 183 and 185.  Rows off the vector path (heads of 68) 224.
+// One event of each of 2048 users moves 1.6 MB: 12 us from call to call, 9.7 in a graph: a
+// chain of dependent reads (offsets, table, exponent, codes) in each of 1024 CTAs, of which 608 run at once.
 #include "kv8.cuh"
 
 namespace dlrm {

@@ -17,15 +17,15 @@
 //    are lifted by a power of two each, so that they fit fp16 exactly but for
 //    what lies 2^-38 below a row's largest.
 //  - The softmax reads half of a thread's scores at a time, twice: that leaves it 80 registers,
-//    and 7 warps (3 where two CTAs share an SM) to convert.
+//    and 7 warps (3 where two CTAs share an SM) to convert.  (Nothing spills but bf16 heads above 128, 176 bytes.)
 //
 // What bounds it: the converting warps' own path (copies, conversion, hand-over).  49 users' 56 rows
 // on up to 51630 (8 heads on 4 of 80) take 685 us, without the softmax 652, without converting 522, without both and
 // the copies 300.  16 sequences of 256 new on up to 8192 (16 heads on 4, 128 bf16
 // elements): 142 us; 64 users' 200
 // candidates on up to 2000, 8 heads of 64: 68 us (16-bit cache: 55); 4 times 2048 on 4096, 8 heads
-// on 2 of 256: 280 us.  Longer chunks of narrower heads convert once instead (4 of 2048 on 8192,
-// 16 heads on 4 of 128, would take 452 us here).
+// on 2 of 256: 282 us.  Longer chunks of narrower heads convert once instead (4 of 2048 on 8192,
+// 16 heads on 4 of 128, would take 461 us here in fp16, 470 in bf16).
 // Slower: 15 such warps for one query tile (714 us for the 56 rows); 4 or 8 warps that load a
 // tile ahead into registers (764, 613 us for those 4 of 2048, then 476); registers dealt out anew by
 // role (650); bulk copies by a warp of their own (468, and 75 against 73 for the candidates,

@@ -5,10 +5,10 @@
 // converted once, and the 16-bit cache's tiles do the rest.  Values become fp16 relative to the largest power of
 // their page of the copy, which the tiles apply to their weights; fp16 weights have as many bits as everywhere else over
 // this cache.  Keys are of the queries' type: so in fp16, which the tiles apply to their scores; in bf16, which holds
-// every code times its power, as they are.  (Values in bf16 would make the weights bf16: 363 us for the
-// sequences below, but 1.35 times the error against 64 bits.)  Memory bounds the
-// conversion (a byte read, two written, which mostly stay in L2): 4 sequences of 2048 new on
-// 8192, 16 heads on 4 of 128, take 372 us in bf16 and 378 in fp16, on a 16-bit cache 341.
+// every code times its power, as they are.  (Values in bf16 would make the weights bf16: 369 us for the sequences below,
+// but 1.35 times the error against 64 bits.)  Memory bounds the conversion (a byte read, two written, which mostly stay
+// in L2).  With a cold L2 4 sequences of 2048 new on 8192, 16 heads on 4 of 128, take 384 us in bf16 and 392 in fp16,
+// on a 16-bit cache 345 and 349.
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -119,11 +119,12 @@ kv8_widen_kernel(const __grid_constant__ WidenParams w)
 }
 
 // Bytes of the copy, 0 where there is none.  It pays where tiles of rows read a key and value often, from 6 tiles of
-// 256 rows on with heads above 64 and from 8 on below (converted once and by every tile, us, 16 heads on 4 of 128: 4
-// sequences of 2048 new on 8192 each, bf16 363 and 476, on up to 8192, fp16, 198 and 229; 16 of 512 on up to 4000 106
-// and 111, of 400 91 and 83, on 4000 each 204 and 223; 16 of 256 on up to 8192 154 and 142; 64 of 500 on up to 2000, 8
-// heads of 64, 131 and 113, of 1000 192 and 188).  It takes four times
-// the bytes of the codes up to max_len, which may be far above the lengths: at most kWidenMost.
+// 256 rows on with heads above 64 and from 8 on below.  Converted once and by every tile, us, cold L2, 16 heads on 4 of
+// 128, bf16 and fp16: 4 sequences of 2048 new on 8192 each 382 and 470, 394 and 461; on up to 8192 201 and 236, 205 and
+// 232; 16 of 512 on up to 4000 109 and 113, 110 and 109; of 400 91 and 89, 93 and 85, on 4000 each 220 and 230, 224 and
+// 225; 16 of 600 on up to 4000, heads of 64, 113 and 113, 115 and 113.  (Fewer rows, warm: 16 of 256 on up to 8192 154 and
+// 142; 64 of 500 on up to 2000, 8 heads of 64, 131 and 113.)  It takes four times the bytes of the codes up to max_len,
+// which may be far above the lengths: at most kWidenMost.
 constexpr int64_t kWidenMost = (int64_t)2 << 30;
 
 size_t widen_workspace(int64_t S, int heads, int group, int d, int64_t max_new, int64_t max_len)
