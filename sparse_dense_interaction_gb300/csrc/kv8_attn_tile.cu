@@ -17,7 +17,7 @@
 //    are lifted by a power of two each, so that they fit fp16 exactly but for
 //    what lies 2^-38 below a row's largest.
 //  - Weights are rounded to fp16 once: 2^-11 of each, as much as an fp16 output's own rounding and an eighth of a bf16
-//    one's (candidates, fp16: error against 64 bits 2.6e-4, the plain form's 2.1e-4).  A second part would be a second
+//    one's (candidates, fp16: error against 64 bits 2.5 to 2.8e-4, the plain form's 2.1e-4).  A second part would be a second
 //    MMA for each tile of values.
 //  - The softmax reads half of a thread's scores at a time, twice: that leaves it 80 registers,
 //    and 7 warps (3 where two CTAs share an SM) to convert.  (Nothing spills but bf16 heads above 128, 176 bytes.)
